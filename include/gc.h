@@ -446,6 +446,163 @@ gc_status gc_partition_at(const void *d_in, void *d_out, size_t out_capacity,
                           cudaStream_t stream);
 
 /*
+ * ---------------------------------------------------------------- rows
+ *
+ * Partition, sort and selection with rows or scores attached: the forms in
+ * which a language model meets them.  They have no counterpart on the pages
+ * this library follows; each declaration states its formula.
+ *
+ *   - A row array holds rows of `width` elements of a gc_row_dtype; element
+ *     (r, c) is at r * stride + c, stride in elements, stride >= width,
+ *     1 <= width <= GC_MAX_ROW_WIDTH, at most GC_MAX_ELEMENTS rows.  Row
+ *     pointers need only the element's own alignment; arrays whose pointer
+ *     and strides are multiples of 16 bytes move in 16-byte pieces.
+ *   - Sums are held in float32 (double where stated) and rounded once to the
+ *     output's type.  The order of every sum is fixed by the arguments, so
+ *     the same call gives the same bits.
+ *   - Index arrays are read on the device: an index outside its range
+ *     selects nothing (a zero row, or no contribution) and is never
+ *     followed.  No index array is read on the host.
+ *   - Calls are asynchronous on `stream`, allocate nothing and can be
+ *     captured in a CUDA graph.  A workspace (256-byte aligned, contents
+ *     immaterial, no initialisation needed) is scratch of that one call.
+ *   - Inputs must not overlap outputs, nor outputs one another, except where
+ *     stated (GC_ERR_INVALID_VALUE).
+ */
+typedef enum { GC_ROW_F32 = 0, GC_ROW_BF16 = 1, GC_ROW_F16 = 2 } gc_row_dtype;
+typedef enum { GC_ID_I32 = 0, GC_ID_I64 = 1 } gc_id_type;
+
+#define GC_MAX_EXPERTS 2048u
+#define GC_MAX_TOPK 64u
+#define GC_MAX_EXPERT_ALIGN 65536u
+#define GC_MAX_SAMPLE_VOCAB 4194304u
+#define GC_MAX_ROW_WIDTH 16777216u
+
+/*
+ * Rows that hold any routing of tokens * topk pairs to `experts` experts,
+ * each expert's block starting at a multiple of `align`: pairs + min(experts,
+ * pairs) * (align - 1).  0 for arguments out of range (below) or a result
+ * above GC_MAX_ELEMENTS; also 0 for tokens == 0.
+ */
+size_t gc_expert_rows(size_t tokens, size_t topk, uint32_t experts, uint32_t align);
+
+/* Workspace bytes of gc_expert_dispatch; 0 for arguments out of range. */
+size_t gc_expert_workspace_bytes(size_t tokens, size_t topk, uint32_t experts);
+
+/*
+ * Tokens sorted by expert: the stable partition into `experts` blocks of the
+ * pairs p = t * topk + j, by the expert e(p) = ids[p] that token t names as
+ * its choice j.  A pair whose id is outside [0, experts) is dropped.
+ *
+ *   counts[e]      = pairs with e(p) == e
+ *   offsets[0]     = 0, offsets[e + 1] = offsets[e] + counts[e] rounded up
+ *                    to a multiple of align
+ *   slots[p]       = offsets[e(p)] + (pairs q < p with e(q) == e(p)), or -1
+ *                    for a dropped pair
+ *   pairs[slots[p]] = p, and -1 for every other row of [0, rows)
+ *   out[slots[p]]  = x[t], and zeros for every other row
+ *
+ * d_ids: tokens * topk ids.  d_x: tokens rows; NULL (with d_out NULL) makes
+ * the plan alone.  d_out: `rows` rows, rows >= gc_expert_rows(...).
+ * d_offsets: experts + 1, d_counts: experts, d_slots: tokens * topk,
+ * d_pairs: rows.  1 <= topk <= GC_MAX_TOPK, 1 <= experts <= GC_MAX_EXPERTS,
+ * 1 <= align <= GC_MAX_EXPERT_ALIGN.
+ */
+gc_status gc_expert_dispatch(const void *d_ids, gc_id_type id_type, size_t tokens, size_t topk,
+                             uint32_t experts, uint32_t align, const void *d_x, size_t x_stride,
+                             size_t width, gc_row_dtype dtype, void *d_out, size_t out_stride,
+                             size_t rows, int32_t *d_offsets, int32_t *d_counts, int32_t *d_slots,
+                             int32_t *d_pairs, void *d_ws, size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * The experts' rows back to their tokens: out[t] = sum over j, in order, of
+ * weights[t * topk + j] * y[slots[t * topk + j]], skipping slots outside
+ * [0, rows).  d_weights (float32, tokens * topk) may be NULL: all weights 1,
+ * which is also the gradient of gc_expert_dispatch with respect to x, y
+ * being the gradient of its rows.
+ */
+gc_status gc_expert_combine(const void *d_y, size_t y_stride, size_t rows, const int32_t *d_slots,
+                            const float *d_weights, size_t tokens, size_t topk, size_t width,
+                            gc_row_dtype dtype, void *d_out, size_t out_stride,
+                            cudaStream_t stream);
+
+/*
+ * Gradient of gc_expert_combine, g = the gradient of its output (tokens
+ * rows):
+ *   dy[slots[p]]   = weights[p] * g[t], zeros for every row that pairs marks
+ *                    with -1 (or with a pair outside [0, tokens * topk))
+ *   dweights[p]    = <g[t], y[slots[p]]>, 0 for a slot outside [0, rows)
+ * slots and pairs are gc_expert_dispatch's.  d_dweights may be NULL; then
+ * d_y is not read and may be NULL.  d_weights may be NULL (all 1).
+ */
+gc_status gc_expert_combine_grad(const void *d_g, size_t g_stride, const void *d_y,
+                                 size_t y_stride, size_t rows, const int32_t *d_slots,
+                                 const int32_t *d_pairs, const float *d_weights, size_t tokens,
+                                 size_t topk, size_t width, gc_row_dtype dtype, void *d_dy,
+                                 size_t dy_stride, float *d_dweights, cudaStream_t stream);
+
+/*
+ * Embedding lookup: out[i] = scale * table[ids[i]], zeros for an id outside
+ * [0, vocab).  d_table: vocab rows, d_out: n rows of the same type.
+ */
+gc_status gc_embedding(const void *d_table, size_t table_stride, size_t vocab, size_t width,
+                       gc_row_dtype dtype, const void *d_ids, gc_id_type id_type, size_t n,
+                       float scale, void *d_out, size_t out_stride, cudaStream_t stream);
+
+/* Workspace bytes of gc_embedding_grad; 0 for arguments out of range. */
+size_t gc_embedding_grad_workspace_bytes(size_t n, size_t vocab, size_t width);
+
+/*
+ * Gradient of gc_embedding with respect to the table, by tokens sorted
+ * stably: dtable[v] = scale * sum over i with ids[i] == v of g[i], in a fixed
+ * order of float32 additions.  accumulate == 0: every row is written, rows
+ * of absent tokens with zeros.  accumulate != 0: the sum is added to the
+ * row, and rows of absent tokens are neither read nor written.  d_g: n rows
+ * of g_dtype; d_dtable: vocab rows of out_dtype, which is g_dtype or
+ * GC_ROW_F32.  vocab < GC_MAX_ELEMENTS.
+ */
+gc_status gc_embedding_grad(const void *d_g, size_t g_stride, gc_row_dtype g_dtype,
+                            const void *d_ids, gc_id_type id_type, size_t n, size_t vocab,
+                            size_t width, float scale, void *d_dtable, size_t dtable_stride,
+                            gc_row_dtype out_dtype, int accumulate, void *d_ws, size_t ws_bytes,
+                            cudaStream_t stream);
+
+/*
+ * One token per row of logits, drawn with given uniform random numbers.  Per
+ * row, with x the logits (float32 of them; +inf counts as the largest finite
+ * float32, NaN and -inf as forbidden tokens), m = max x, z = (x - m) / T and
+ * w = exp(z):
+ *
+ *   order      by x descending, equal values by index ascending
+ *   top-k      the first top_k of the order (top_k <= 0: all)
+ *   top-p      of those, each whose predecessors weigh less than top_p times
+ *              the top-k set's sum of w; always the first (top_p >= 1 or NaN: all)
+ *   min-p      of those, each with w >= min_p (min_p <= 0 or NaN: all; min_p > 1
+ *              counts as 1)
+ *   token      of those, the largest z - log(-log u), equal values: the
+ *              lowest index (the Gumbel-max form of drawing with
+ *              probability w / sum of kept w); u is clamped to
+ *              [2^-25, 1 - 2^-24], NaN counts as 2^-25
+ *   logprob    z of the token - log(sum of kept w)
+ *
+ * T <= 0 or NaN: the first of the order, logprob 0; u is not read.  Every
+ * token forbidden: token -1, logprob -inf.
+ * z - log(-log u) of a token 20 below the maximum cannot be the largest, so
+ * such tokens' u are not read; tokens whose w underflows to 0 are never kept.
+ *
+ * d_logits: rows x vocab of dtype, vocab <= GC_MAX_SAMPLE_VOCAB.  d_uniform:
+ * float32, same shape, its own stride; NULL draws every row with T = 0.
+ * d_temperature, d_top_p, d_min_p (float32) and d_top_k (int32): one value
+ * per row, each may be NULL (1, 1, 0, 0).  d_tokens: int32 per row;
+ * d_logprobs: float32 per row, may be NULL.
+ */
+gc_status gc_sample(const void *d_logits, size_t logits_stride, size_t rows, size_t vocab,
+                    gc_row_dtype dtype, const float *d_uniform, size_t uniform_stride,
+                    const float *d_temperature, const int32_t *d_top_k, const float *d_top_p,
+                    const float *d_min_p, int32_t *d_tokens, float *d_logprobs,
+                    cudaStream_t stream);
+
+/*
  * SYNCHRONOUS.  Waits for `stream`, then reads and clears the device-side
  * error word of the workspace.  Returns GC_OK, GC_ERR_TIMEOUT if a kernel's
  * bounded wait (a look-back, a staged load, or the start barrier at which a

@@ -1,0 +1,242 @@
+// experts.cu -- tokens sorted by expert and back (gc_expert_dispatch,
+// gc_expert_combine, gc_expert_combine_grad).
+//
+// The plan is a stable partition of the tokens * topk pairs into one bin per
+// expert (gc_binsort.cuh); the rest moves rows: one row per pair out, a
+// weighted sum of topk rows per token back, and for the gradient one scaled
+// row and one dot product per pair.  All of it is bound by HBM traffic.
+#include "gc_binsort.cuh"
+#include "gc_internal.h"
+#include "gc_rows.cuh"
+
+namespace {
+
+using namespace gcd;
+
+struct ExpertSource {
+    const void *ids;
+    bool wide;
+    uint32_t experts;
+    __device__ __forceinline__ uint32_t bin(uint32_t i) const { return load_id(ids, wide, i, experts); }
+};
+
+struct ExpertSink {
+    int32_t *offsets, *counts, *slots, *pairs;
+    uint32_t experts;
+    __device__ __forceinline__ void start(uint32_t b, uint32_t start, uint32_t count) const
+    {
+        offsets[b] = int32_t(start);
+        counts[b] = int32_t(count);
+    }
+    __device__ __forceinline__ void end(uint32_t total) const { offsets[experts] = int32_t(total); }
+    __device__ __forceinline__ void place(uint32_t p, uint32_t row) const
+    {
+        slots[p] = int32_t(row);
+        pairs[row] = int32_t(p);
+    }
+    __device__ __forceinline__ void drop(uint32_t p) const { slots[p] = -1; }
+};
+
+// Threads of a row kernel: `tx` across one row's pieces, kRowThreads / tx rows.
+constexpr int kRowThreads = 256;
+
+dim3 row_block(size_t pieces)
+{
+    int tx = 32;
+    while (tx < kRowThreads && size_t(tx) < pieces) tx <<= 1;
+    return dim3(tx, kRowThreads / tx);
+}
+
+// out[r] = x[pairs[r] / topk], or zeros.  E: an integer of the element's size.
+template <class E, int N>
+__global__ void __launch_bounds__(kRowThreads)
+expert_rows_kernel(const E *__restrict__ x, size_t x_stride, uint32_t pieces, uint32_t topk, uint32_t pair_limit,
+                   const int32_t *__restrict__ pairs, uint32_t rows, E *__restrict__ out, size_t out_stride)
+{
+    const uint32_t r = blockIdx.x * blockDim.y + threadIdx.y;
+    if (r >= rows) return;
+    const uint32_t p = uint32_t(pairs[r]);
+    const E *src = x + size_t(p / topk) * x_stride;
+    E *dst = out + size_t(r) * out_stride;
+    for (uint32_t c = threadIdx.x; c < pieces; c += blockDim.x) {
+        Piece<E, N> v{};
+        if (p < pair_limit) v = load_piece<E, N>(src + size_t(c) * N);
+        store_piece<E, N>(dst + size_t(c) * N, v);
+    }
+}
+
+template <class T, int N>
+__global__ void __launch_bounds__(kRowThreads)
+expert_combine_kernel(const T *__restrict__ y, size_t y_stride, uint32_t rows, const int32_t *__restrict__ slots,
+                      const float *__restrict__ weights, uint32_t tokens, uint32_t topk, uint32_t pieces,
+                      T *__restrict__ out, size_t out_stride)
+{
+    const uint32_t t = blockIdx.x * blockDim.y + threadIdx.y;
+    if (t >= tokens) return;
+    for (uint32_t c = threadIdx.x; c < pieces; c += blockDim.x) {
+        float acc[N] = {};
+        for (uint32_t j = 0; j < topk; ++j) {
+            const uint32_t slot = uint32_t(slots[size_t(t) * topk + j]);
+            if (slot >= rows) continue;
+            const float w = weights ? weights[size_t(t) * topk + j] : 1.0f;
+            const Piece<T, N> v = load_piece<T, N>(y + size_t(slot) * y_stride + size_t(c) * N);
+#pragma unroll
+            for (int i = 0; i < N; ++i) acc[i] = fmaf(w, row_to_float(v.v[i]), acc[i]);
+        }
+        Piece<T, N> o;
+#pragma unroll
+        for (int i = 0; i < N; ++i) o.v[i] = row_from_float<T>(acc[i]);
+        store_piece<T, N>(out + size_t(t) * out_stride + size_t(c) * N, o);
+    }
+}
+
+// One warp per pair: the scaled gradient row and the dot product; then one
+// warp per row without a pair: zeros.
+template <class T, int N>
+__global__ void __launch_bounds__(kRowThreads)
+expert_combine_grad_kernel(const T *__restrict__ g, size_t g_stride, const T *__restrict__ y, size_t y_stride,
+                           uint32_t rows, const int32_t *__restrict__ slots, const int32_t *__restrict__ pairs,
+                           const float *__restrict__ weights, uint32_t npairs, uint32_t topk, uint32_t pieces,
+                           T *__restrict__ dy, size_t dy_stride, float *__restrict__ dweights)
+{
+    const uint64_t unit = uint64_t(blockIdx.x) * (kRowThreads / 32) + (threadIdx.x >> 5);
+    const uint32_t lane = threadIdx.x & 31;
+    if (unit < npairs) {
+        const uint32_t p = uint32_t(unit);
+        const uint32_t slot = uint32_t(slots[p]);
+        float dot = 0.0f;
+        if (slot < rows) {
+            const float w = weights ? weights[p] : 1.0f;
+            const T *gr = g + size_t(p / topk) * g_stride;
+            for (uint32_t c = lane; c < pieces; c += 32) {
+                const Piece<T, N> a = load_piece<T, N>(gr + size_t(c) * N);
+                Piece<T, N> o;
+#pragma unroll
+                for (int i = 0; i < N; ++i) o.v[i] = row_from_float<T>(w * row_to_float(a.v[i]));
+                store_piece<T, N>(dy + size_t(slot) * dy_stride + size_t(c) * N, o);
+                if (dweights) {
+                    const Piece<T, N> b = load_piece<T, N>(y + size_t(slot) * y_stride + size_t(c) * N);
+#pragma unroll
+                    for (int i = 0; i < N; ++i) dot = fmaf(row_to_float(a.v[i]), row_to_float(b.v[i]), dot);
+                }
+            }
+        }
+        if (dweights) {
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+            if (lane == 0) dweights[p] = dot;
+        }
+    } else if (unit - npairs < rows) {
+        const uint32_t r = uint32_t(unit - npairs);
+        if (uint32_t(pairs[r]) < npairs) return;
+        for (uint32_t c = lane; c < pieces; c += 32)
+            store_piece<T, N>(dy + size_t(r) * dy_stride + size_t(c) * N, zero_piece<T, N>());
+    }
+}
+
+template <class T, int N>
+void run_combine(const void *y, size_t y_stride, uint32_t rows, const int32_t *slots, const float *weights,
+                 uint32_t tokens, uint32_t topk, size_t width, void *out, size_t out_stride, cudaStream_t s)
+{
+    const uint32_t pieces = uint32_t(width / N);
+    const dim3 block = row_block(pieces);
+    expert_combine_kernel<T, N><<<uint32_t(gch::ceil_div(tokens, block.y)), block, 0, s>>>(
+        static_cast<const T *>(y), y_stride, rows, slots, weights, tokens, topk, pieces, static_cast<T *>(out),
+        out_stride);
+}
+
+template <class T, int N>
+void run_combine_grad(const void *g, size_t g_stride, const void *y, size_t y_stride, uint32_t rows,
+                      const int32_t *slots, const int32_t *pairs, const float *weights, uint32_t npairs,
+                      uint32_t topk, size_t width, void *dy, size_t dy_stride, float *dweights, cudaStream_t s)
+{
+    const uint64_t units = uint64_t(npairs) + rows;
+    expert_combine_grad_kernel<T, N><<<uint32_t(gch::ceil_div(units, kRowThreads / 32)), kRowThreads, 0, s>>>(
+        static_cast<const T *>(g), g_stride, static_cast<const T *>(y), y_stride, rows, slots, pairs, weights,
+        npairs, topk, uint32_t(width / N), static_cast<T *>(dy), dy_stride, dweights);
+}
+
+template <class E, int N>
+void run_rows(const void *x, size_t x_stride, size_t width, uint32_t topk, uint32_t npairs, const int32_t *pairs,
+              uint32_t rows, void *out, size_t out_stride, cudaStream_t s)
+{
+    const uint32_t pieces = uint32_t(width / N);
+    const dim3 block = row_block(pieces);
+    expert_rows_kernel<E, N><<<uint32_t(gch::ceil_div(rows, block.y)), block, 0, s>>>(
+        static_cast<const E *>(x), x_stride, pieces, topk, npairs, pairs, rows, static_cast<E *>(out), out_stride);
+}
+
+// Row kernels by piece size: 16 bytes down to one element.
+#define GC_BY_PIECE(T, n, CALL)                                     \
+    switch (n) {                                                    \
+    case 1: CALL(T, 1); break;                                      \
+    case 2: CALL(T, 2); break;                                      \
+    case 4: CALL(T, 4); break;                                      \
+    default: CALL(T, (16 / int(sizeof(T)))); break;                 \
+    }
+#define GC_BY_DTYPE(dt, n, CALL)                                    \
+    if (dt == GC_ROW_F32) { GC_BY_PIECE(float, n, CALL) }           \
+    else if (dt == GC_ROW_BF16) { GC_BY_PIECE(__nv_bfloat16, n, CALL) } \
+    else { GC_BY_PIECE(__half, n, CALL) }
+
+}  // namespace
+
+namespace gch {
+
+size_t expert_workspace_bytes(size_t npairs, uint32_t experts)
+{
+    return align_up(size_t(gcd::bin_chunks(npairs)) * experts * sizeof(uint32_t), 256) + 256;
+}
+
+cudaError_t launch_expert_dispatch(const void *ids, bool wide, uint32_t npairs, uint32_t topk, uint32_t experts,
+                                   uint32_t align, const void *x, size_t x_stride, size_t width, gc_row_dtype dt,
+                                   void *out, size_t out_stride, uint32_t rows, int32_t *offsets, int32_t *counts,
+                                   int32_t *slots, int32_t *pairs, uint8_t *ws, cudaStream_t s)
+{
+    uint32_t *table = reinterpret_cast<uint32_t *>(ws);
+    const ExpertSource src{ids, wide, experts};
+    const ExpertSink sink{offsets, counts, slots, pairs, experts};
+    cudaError_t e = rows ? cudaMemsetAsync(pairs, 0xff, size_t(rows) * sizeof(int32_t), s) : cudaSuccess;
+    if (npairs == 0) {
+        if (e == cudaSuccess) e = cudaMemsetAsync(offsets, 0, (size_t(experts) + 1) * sizeof(int32_t), s);
+        if (e == cudaSuccess) e = cudaMemsetAsync(counts, 0, size_t(experts) * sizeof(int32_t), s);
+    } else {
+        if (e == cudaSuccess) e = gcd::launch_bin_count(src, npairs, experts, table, s);
+        if (e == cudaSuccess) e = gcd::launch_bin_place(src, sink, npairs, experts, align, table, s);
+    }
+    if (e != cudaSuccess || out == nullptr || rows == 0) return e;
+    const int elem = dt == GC_ROW_F32 ? 4 : 2;
+    const int n = piece_elems(uint64_t(uintptr_t(x)) | uintptr_t(out) | elem * (x_stride | out_stride | width), elem);
+#define GC_ROWS_CALL(E, N) run_rows<E, N>(x, x_stride, width, topk, npairs, pairs, rows, out, out_stride, s)
+    if (elem == 4) { GC_BY_PIECE(uint32_t, n, GC_ROWS_CALL) }
+    else { GC_BY_PIECE(uint16_t, n, GC_ROWS_CALL) }
+    return cudaGetLastError();
+}
+
+cudaError_t launch_expert_combine(const void *y, size_t y_stride, uint32_t rows, const int32_t *slots,
+                                  const float *weights, uint32_t tokens, uint32_t topk, size_t width,
+                                  gc_row_dtype dt, void *out, size_t out_stride, cudaStream_t s)
+{
+    const int elem = dt == GC_ROW_F32 ? 4 : 2;
+    const int n = piece_elems(uint64_t(uintptr_t(y)) | uintptr_t(out) | elem * (y_stride | out_stride | width), elem);
+#define GC_COMBINE_CALL(T, N) run_combine<T, N>(y, y_stride, rows, slots, weights, tokens, topk, width, out, out_stride, s)
+    GC_BY_DTYPE(dt, n, GC_COMBINE_CALL)
+    return cudaGetLastError();
+}
+
+cudaError_t launch_expert_combine_grad(const void *g, size_t g_stride, const void *y, size_t y_stride, uint32_t rows,
+                                       const int32_t *slots, const int32_t *pairs, const float *weights,
+                                       uint32_t tokens, uint32_t topk, size_t width, gc_row_dtype dt, void *dy,
+                                       size_t dy_stride, float *dweights, cudaStream_t s)
+{
+    const int elem = dt == GC_ROW_F32 ? 4 : 2;
+    uint64_t bits = uint64_t(uintptr_t(g)) | uintptr_t(dy) | elem * (g_stride | dy_stride | width);
+    if (dweights) bits |= uintptr_t(y) | elem * y_stride;
+    const int n = piece_elems(bits, elem);
+#define GC_GRAD_CALL(T, N) run_combine_grad<T, N>(g, g_stride, y, y_stride, rows, slots, pairs, weights, tokens * topk, \
+                                                  topk, width, dy, dy_stride, dweights, s)
+    GC_BY_DTYPE(dt, n, GC_GRAD_CALL)
+    return cudaGetLastError();
+}
+
+}  // namespace gch

@@ -1,0 +1,78 @@
+// gc_rows.cuh -- device building blocks of the row operators (experts.cu,
+// embedding.cu, sample.cu): element types, pieces of 2 to 16 bytes of a row
+// with their float32 values, and ids of either width.
+#pragma once
+
+#include <cstdint>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+namespace gcd {
+
+__device__ __forceinline__ float row_to_float(float x) { return x; }
+__device__ __forceinline__ float row_to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float row_to_float(__half x) { return __half2float(x); }
+
+// One rounding, to nearest even.
+template <class T>
+__device__ __forceinline__ T row_from_float(float x);
+template <>
+__device__ __forceinline__ float row_from_float<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 row_from_float<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+template <>
+__device__ __forceinline__ __half row_from_float<__half>(float x) { return __float2half_rn(x); }
+
+// N consecutive elements of a row, loaded and stored as one access of
+// sizeof(Piece) bytes; the address is a multiple of that.
+template <class T, int N>
+struct alignas(sizeof(T) * N) Piece {
+    T v[N];
+};
+
+template <class T, int N>
+__device__ __forceinline__ Piece<T, N> load_piece(const T *p)
+{
+    return *reinterpret_cast<const Piece<T, N> *>(p);
+}
+
+template <class T, int N>
+__device__ __forceinline__ void store_piece(T *p, const Piece<T, N> &x)
+{
+    *reinterpret_cast<Piece<T, N> *>(p) = x;
+}
+
+template <class T, int N>
+__device__ __forceinline__ Piece<T, N> zero_piece()
+{
+    Piece<T, N> z;
+#pragma unroll
+    for (int i = 0; i < N; ++i) z.v[i] = row_from_float<T>(0.0f);
+    return z;
+}
+
+// Id i of an int32 or int64 array; any value outside [0, limit) becomes limit
+// (limit <= 2^31 - 1).
+__device__ __forceinline__ uint32_t load_id(const void *ids, bool wide, uint64_t i, uint32_t limit)
+{
+    const int64_t v = wide ? static_cast<const int64_t *>(ids)[i]
+                           : int64_t(static_cast<const int32_t *>(ids)[i]);
+    return v >= 0 && v < int64_t(limit) ? uint32_t(v) : limit;
+}
+
+}  // namespace gcd
+
+namespace gch {
+
+// Elements per access for rows of `elem`-byte elements: the largest piece of
+// at most 16 bytes that divides every address and length in `bits` (the
+// bitwise or of pointers, stride bytes and width bytes).
+inline int piece_elems(uint64_t bits, int elem)
+{
+    int bytes = 16;
+    while (bytes > elem && (bits & uint64_t(bytes - 1)) != 0) bytes >>= 1;
+    return bytes / elem;
+}
+
+}  // namespace gch

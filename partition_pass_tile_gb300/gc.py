@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import ctypes
 from pathlib import Path
+from typing import NamedTuple
 
 import torch
 
@@ -29,6 +30,8 @@ OP_RADIX_SORT = 6
 OP_REDUCE = 7
 OP_COUNT_IF = 8
 LT, LE, GT, GE, EQ, NE, MASK_EQ, MASK_NE = range(8)
+ROW_F32, ROW_BF16, ROW_F16 = 0, 1, 2
+ID_I32, ID_I64 = 0, 1
 CMP_NAMES = {"<": LT, "<=": LE, ">": GT, ">=": GE, "==": EQ, "!=": NE,
              "mask==": MASK_EQ, "mask!=": MASK_NE}
 
@@ -61,7 +64,7 @@ def load(path: str | Path | None = None) -> ctypes.CDLL:
                            "(python -m partition_pass_tile_gb300.build)")
     lib = ctypes.CDLL(str(p))
     V, Z, I, U64 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int, ctypes.c_uint64
-    S = ctypes.c_int
+    S, U32T, F = ctypes.c_int, ctypes.c_uint32, ctypes.c_float
     sig = {
         "gc_status_string": ([S], ctypes.c_char_p),
         "gc_version": ([], ctypes.c_char_p),
@@ -87,6 +90,15 @@ def load(path: str | Path | None = None) -> ctypes.CDLL:
         "gc_exclusive_scan_carry": ([V, V, V, Z, I, V, V, Z, V], S),
         "gc_select_if_at": ([V, V, Z, V, V, Z, I, I, V, Z, V], S),
         "gc_partition_at": ([V, V, Z, V, V, Z, I, I, V, Z, V], S),
+        "gc_expert_rows": ([Z, Z, U32T, U32T], Z),
+        "gc_expert_workspace_bytes": ([Z, Z, U32T], Z),
+        "gc_expert_dispatch": ([V, I, Z, Z, U32T, U32T, V, Z, Z, I, V, Z, Z, V, V, V, V, V, Z, V], S),
+        "gc_expert_combine": ([V, Z, Z, V, V, Z, Z, Z, I, V, Z, V], S),
+        "gc_expert_combine_grad": ([V, Z, V, Z, Z, V, V, V, Z, Z, Z, I, V, Z, V, V], S),
+        "gc_embedding": ([V, Z, Z, Z, I, V, I, Z, F, V, Z, V], S),
+        "gc_embedding_grad_workspace_bytes": ([Z, Z, Z], Z),
+        "gc_embedding_grad": ([V, Z, I, V, I, Z, Z, Z, F, V, Z, I, I, V, Z, V], S),
+        "gc_sample": ([V, Z, Z, Z, I, V, Z, V, V, V, V, V, V, V], S),
     }
     for name, (args, res) in sig.items():
         f = getattr(lib, name)
@@ -483,3 +495,255 @@ def partition_at(x: torch.Tensor, pred, out: torch.Tensor, offsets: torch.Tensor
                                   n, dt, pred_code(pred), _ptr(ws), ws.numel(), _stream(stream)),
            "gc_partition_at")
     return out, count_true
+
+
+# ---------------------------------------------------------------- rows
+
+ROW_DTYPES = {torch.float32: ROW_F32, torch.bfloat16: ROW_BF16, torch.float16: ROW_F16}
+
+
+class ExpertPlan(NamedTuple):
+    """Where gc_expert_dispatch put the pairs (token, choice); int32 tensors."""
+    offsets: torch.Tensor  # [experts + 1] first row of each expert's block
+    counts: torch.Tensor   # [experts] rows of the block that hold a pair
+    slots: torch.Tensor    # [tokens, topk] row of each pair, -1 if dropped
+    pairs: torch.Tensor    # [rows] pair of each row, -1 if none
+
+
+def row_dtype_code(dtype: torch.dtype) -> int:
+    code = ROW_DTYPES.get(dtype)
+    if code is None:
+        raise TypeError(f"libgc handles rows of float32, bfloat16 and float16, not {dtype}")
+    return code
+
+
+def _rows(t: torch.Tensor) -> tuple[int, int]:
+    """(pointer, row stride) of a 2-D tensor whose rows are contiguous."""
+    if not t.is_cuda:
+        raise ValueError("libgc takes CUDA tensors (device pointers)")
+    if t.dim() != 2 or (t.size(1) > 1 and t.stride(1) != 1):
+        raise ValueError("libgc takes 2-D row arrays whose rows are contiguous")
+    return t.data_ptr(), t.stride(0) if t.size(0) > 1 else t.size(1)
+
+
+def _ids(t: torch.Tensor) -> int:
+    if t.dtype == torch.int64:
+        return ID_I64
+    if t.dtype == torch.int32:
+        return ID_I32
+    raise TypeError(f"libgc takes int32 or int64 ids, not {t.dtype}")
+
+
+def _typed(t: torch.Tensor | None, dtype: torch.dtype, n: int, what: str) -> int | None:
+    """Pointer of a contiguous tensor of n elements of dtype (None stays None)."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise TypeError(f"{what} is a {dtype} tensor, not {t.dtype}")
+    if t.numel() != n:
+        raise ValueError(f"{what} has {t.numel()} elements, not {n}")
+    return _ptr(t)
+
+
+def _new(shape, dtype: torch.dtype, device, stream, value=None) -> torch.Tensor:
+    """A tensor whose memory belongs to the stream that the call runs on."""
+    if stream is not None:
+        s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))
+        with torch.cuda.stream(s):
+            return _new(shape, dtype, device, None, value)
+    if value is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    return torch.full(shape, value, dtype=dtype, device=device)
+
+
+def _like(t: torch.Tensor | None, shape, dtype: torch.dtype, device, stream, what: str) -> torch.Tensor:
+    """The caller's output, checked, or a new one."""
+    if t is None:
+        return _new(shape, dtype, device, stream)
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+        raise ValueError(f"{what} is a {dtype} tensor of shape {tuple(shape)}")
+    return t
+
+
+def _scratch(ws: torch.Tensor | None, nbytes: int, device, stream) -> torch.Tensor:
+    return ws if ws is not None else _new(max(nbytes, 256), torch.uint8, device, stream)
+
+
+def expert_rows(tokens: int, topk: int, experts: int, align: int = 1) -> int:
+    """gc_expert_rows: rows that hold any routing (0 for arguments out of range)."""
+    return int(load().gc_expert_rows(tokens, topk, experts, align))
+
+
+def expert_workspace_bytes(tokens: int, topk: int, experts: int) -> int:
+    return int(load().gc_expert_workspace_bytes(tokens, topk, experts))
+
+
+def expert_dispatch(x: torch.Tensor | None, ids: torch.Tensor, experts: int, align: int = 1,
+                    out: torch.Tensor | None = None, plan: ExpertPlan | None = None,
+                    ws: torch.Tensor | None = None, stream=None):
+    """Tokens' rows sorted by expert -> (rows, plan).
+
+    x: [tokens, width] rows; ids: [tokens, topk] int32 or int64, ids outside
+    [0, experts) are dropped.  rows: [expert_rows(...), width], each expert's
+    block starting at a multiple of `align`; rows without a pair are zeros.
+    x None makes the plan alone (rows None).
+    """
+    if ids.dim() != 2:
+        raise ValueError("ids is [tokens, topk]")
+    tokens, topk = ids.shape
+    lib = load()
+    rows = plan.pairs.numel() if plan is not None else lib.gc_expert_rows(tokens, topk, experts, align)
+    dev = ids.device
+    if plan is None:
+        plan = ExpertPlan(*(_new(shape, torch.int32, dev, stream)
+                            for shape in ((experts + 1,), (experts,), (tokens, topk), (rows,))))
+    xp, xs, op, os, width, dt = None, 0, None, 0, 0, ROW_F32
+    if x is not None:
+        xp, xs = _rows(x)
+        if x.size(0) != tokens:
+            raise ValueError(f"x has {x.size(0)} rows, ids has {tokens} tokens")
+        width, dt = x.size(1), row_dtype_code(x.dtype)
+        out = _like(out, (rows, width), x.dtype, dev, stream, "out")
+        op, os = _rows(out)
+    ws = _scratch(ws, lib.gc_expert_workspace_bytes(tokens, topk, experts), dev, stream)
+    _check(lib.gc_expert_dispatch(
+        _ptr(ids), _ids(ids), tokens, topk, experts, align, xp, xs, width, dt, op, os, rows,
+        _typed(plan.offsets, torch.int32, experts + 1, "plan.offsets"),
+        _typed(plan.counts, torch.int32, experts, "plan.counts"),
+        _typed(plan.slots, torch.int32, tokens * topk, "plan.slots"),
+        _typed(plan.pairs, torch.int32, rows, "plan.pairs"), _ptr(ws), ws.numel(), _stream(stream)),
+        "gc_expert_dispatch")
+    return out, plan
+
+
+def expert_combine(y: torch.Tensor, slots: torch.Tensor, weights: torch.Tensor | None = None,
+                   out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """out[t] = sum_j weights[t, j] * y[slots[t, j]] (weights None: all 1; slot -1: nothing)."""
+    if slots.dim() != 2:
+        raise ValueError("slots is [tokens, topk]")
+    tokens, topk = slots.shape
+    yp, ys = _rows(y)
+    rows, width = y.shape
+    out = _like(out, (tokens, width), y.dtype, y.device, stream, "out")
+    op, os = _rows(out)
+    _check(load().gc_expert_combine(
+        yp, ys, rows, _typed(slots, torch.int32, tokens * topk, "slots"),
+        _typed(weights, torch.float32, tokens * topk, "weights"), tokens, topk, width,
+        row_dtype_code(y.dtype), op, os, _stream(stream)), "gc_expert_combine")
+    return out
+
+
+def expert_dispatch_grad(d_rows: torch.Tensor, slots: torch.Tensor, out: torch.Tensor | None = None,
+                         stream=None) -> torch.Tensor:
+    """Gradient of expert_dispatch with respect to x: the sum of the gradients of each token's rows."""
+    return expert_combine(d_rows, slots, None, out=out, stream=stream)
+
+
+def expert_combine_grad(g: torch.Tensor, y: torch.Tensor | None, slots: torch.Tensor, pairs: torch.Tensor,
+                        weights: torch.Tensor | None = None, dy: torch.Tensor | None = None,
+                        dweights: torch.Tensor | None = None, stream=None):
+    """Gradient of expert_combine -> (dy, dweights).
+
+    g: [tokens, width], the gradient of its output.  y None: only dy is
+    computed and dweights is None.
+    """
+    if slots.dim() != 2:
+        raise ValueError("slots is [tokens, topk]")
+    tokens, topk = slots.shape
+    rows = pairs.numel()
+    gp, gs = _rows(g)
+    if g.size(0) != tokens:
+        raise ValueError(f"g has {g.size(0)} rows, slots has {tokens} tokens")
+    width = g.size(1)
+    dy = _like(dy, (rows, width), g.dtype, g.device, stream, "dy")
+    dp, ds = _rows(dy)
+    yp, ys, wp = None, 0, None
+    if y is not None:
+        if tuple(y.shape) != (rows, width) or y.dtype != g.dtype:
+            raise ValueError(f"y is a {g.dtype} tensor of shape {(rows, width)}")
+        yp, ys = _rows(y)
+        dweights = _like(dweights, (tokens, topk), torch.float32, g.device, stream, "dweights")
+        wp = _ptr(dweights)
+    _check(load().gc_expert_combine_grad(
+        gp, gs, yp, ys, rows, _typed(slots, torch.int32, tokens * topk, "slots"),
+        _typed(pairs, torch.int32, rows, "pairs"), _typed(weights, torch.float32, tokens * topk, "weights"),
+        tokens, topk, width, row_dtype_code(g.dtype), dp, ds, wp, _stream(stream)), "gc_expert_combine_grad")
+    return dy, dweights if y is not None else None
+
+
+def embedding(table: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, out: torch.Tensor | None = None,
+              stream=None) -> torch.Tensor:
+    """scale * table[ids], zeros for ids outside the table -> ids.shape + (width,)."""
+    n = ids.numel()
+    tp, ts = _rows(table)
+    vocab, width = table.shape
+    out = _like(out, (*ids.shape, width), table.dtype, table.device, stream, "out")
+    op, os = _rows(out if out.dim() == 2 else out.view(n, width))
+    _check(load().gc_embedding(tp, ts, vocab, width, row_dtype_code(table.dtype), _ptr(ids), _ids(ids), n,
+                               scale, op, os, _stream(stream)), "gc_embedding")
+    return out
+
+
+def embedding_grad_workspace_bytes(n: int, vocab: int, width: int) -> int:
+    return int(load().gc_embedding_grad_workspace_bytes(n, vocab, width))
+
+
+def embedding_grad(g: torch.Tensor, ids: torch.Tensor, vocab: int, scale: float = 1.0,
+                   out_dtype: torch.dtype | None = None, out: torch.Tensor | None = None,
+                   accumulate: bool = False, ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Gradient of embedding with respect to its table -> [vocab, width].
+
+    g: the gradient of embedding's output, ids.shape + (width,).  out_dtype:
+    g's type (the default) or float32.  accumulate adds to `out`, leaving the
+    rows of absent tokens alone.
+    """
+    n, width = ids.numel(), g.size(-1)
+    if accumulate and out is None:
+        raise ValueError("accumulate adds to the caller's out")
+    if g.numel() != n * width:
+        raise ValueError(f"g has {g.numel()} elements for {n} ids of width {width}")
+    gp, gs = _rows(g if g.dim() == 2 else g.view(n, width))
+    dt = out_dtype or (out.dtype if out is not None else g.dtype)
+    out = _like(out, (vocab, width), dt, g.device, stream, "out")
+    op, os = _rows(out)
+    lib = load()
+    ws = _scratch(ws, lib.gc_embedding_grad_workspace_bytes(n, vocab, width), g.device, stream)
+    _check(lib.gc_embedding_grad(gp, gs, row_dtype_code(g.dtype), _ptr(ids), _ids(ids), n, vocab, width, scale,
+                                 op, os, row_dtype_code(dt), int(accumulate), _ptr(ws), ws.numel(),
+                                 _stream(stream)), "gc_embedding_grad")
+    return out
+
+
+def _per_row(v, dtype: torch.dtype, rows: int, device, stream) -> torch.Tensor | None:
+    return v if v is None or isinstance(v, torch.Tensor) else _new((rows,), dtype, device, stream, v)
+
+
+def sample(logits: torch.Tensor, uniform: torch.Tensor | None = None, temperature=None, top_k=None, top_p=None,
+           min_p=None, tokens: torch.Tensor | None = None, logprobs: torch.Tensor | None = None, stream=None):
+    """One token per row of logits -> (tokens int32, logprobs float32).
+
+    uniform: float32 random numbers of [0, 1), logits' shape; None takes the
+    largest logit of every row.  temperature, top_k (int32), top_p, min_p: a
+    number or one value per row; None leaves the filter out.
+    """
+    lp, ls = _rows(logits)
+    rows, vocab = logits.shape
+    up, us = None, 0
+    if uniform is not None:
+        if uniform.dtype != torch.float32 or tuple(uniform.shape) != (rows, vocab):
+            raise ValueError("uniform is a float32 tensor of logits' shape")
+        up, us = _rows(uniform)
+    dev = logits.device
+    temperature = _per_row(temperature, torch.float32, rows, dev, stream)
+    top_k = _per_row(top_k, torch.int32, rows, dev, stream)
+    top_p = _per_row(top_p, torch.float32, rows, dev, stream)
+    min_p = _per_row(min_p, torch.float32, rows, dev, stream)
+    tokens = _like(tokens, (rows,), torch.int32, dev, stream, "tokens")
+    logprobs = _like(logprobs, (rows,), torch.float32, dev, stream, "logprobs")
+    _check(load().gc_sample(lp, ls, rows, vocab, row_dtype_code(logits.dtype), up, us,
+                            _typed(temperature, torch.float32, rows, "temperature"),
+                            _typed(top_k, torch.int32, rows, "top_k"),
+                            _typed(top_p, torch.float32, rows, "top_p"),
+                            _typed(min_p, torch.float32, rows, "min_p"), _ptr(tokens), _ptr(logprobs),
+                            _stream(stream)), "gc_sample")
+    return tokens, logprobs
