@@ -31,19 +31,22 @@ namespace cg = cooperative_groups;
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxTeam = 8;
-constexpr uint32_t kList = 4096;            // candidates that the leader can hold
+constexpr uint32_t kMaxTeam = 8;
+constexpr uint32_t kList = 8192;            // candidates that the leader can hold
 constexpr int kBins = 2048;                 // histogram of z, 64 bins to a unit
 constexpr float kBinsPerUnit = 64.0f;
-constexpr int kLoads = 4;                   // 16-byte loads in flight per thread
+constexpr int kSubBins = 1024;              // histogram of the list
+constexpr uint32_t kFew = 1024;             // of the list's tokens near a cut
+constexpr int kLoads = 4;                   // pieces of 16 bytes that a thread loads at a time
 constexpr float kFixed = 1099511627776.0f;  // 2^40
 constexpr float kUniformLo = 0x1p-25f, kUniformHi = 1.0f - 0x1p-24f;
+// -log u lies in [2^-24, 17.4] and the largest token weighs 1, so a token
+// lighter than 2^-24 / 17.4 cannot be drawn; this is exp(-20).
+constexpr float kLightest = 2.0611536e-9f;
+constexpr uint32_t kFull = 0xffffffffu;
 
 // x as the operator reads it: NaN is -inf, +inf the largest finite value.
-__device__ __forceinline__ float sample_value(float x)
-{
-    return x != x ? -INFINITY : fminf(x, 3.402823466e38f);
-}
+__device__ __forceinline__ float sample_value(float x) { return fminf(fmaxf(x, -INFINITY), 3.402823466e38f); }
 
 // Ascends with x; -0 and +0 are one value.
 __device__ __forceinline__ uint32_t order_bits(float x)
@@ -57,45 +60,52 @@ __device__ __forceinline__ uint64_t order_key(float x, uint32_t i)
     return (uint64_t(order_bits(x)) << 32) | uint32_t(~i);
 }
 
-__device__ __forceinline__ float key_value(uint64_t key)
+__device__ __forceinline__ float order_value(uint32_t o)
 {
-    const uint32_t o = uint32_t(key >> 32);
     return __uint_as_float((o & 0x80000000u) ? o ^ 0x80000000u : ~o);
 }
 
+__device__ __forceinline__ float key_value(uint64_t key) { return order_value(uint32_t(key >> 32)); }
 __device__ __forceinline__ uint32_t key_index(uint64_t key) { return ~uint32_t(key); }
 
-__device__ __forceinline__ float scaled(float x, float m, float t)
-{
-    const float d = x - m;
-    return d == -INFINITY ? d : d / t;
-}
-
-__device__ __forceinline__ uint64_t fixed_weight(float w) { return __float2ull_rn(w * kFixed); }
-
-__device__ __forceinline__ float draw_score(float z, float u)
-{
-    return z - logf(-logf(fminf(fmaxf(u, kUniformLo), kUniformHi)));
-}
-
-struct Larger {
-    template <class V>
-    __device__ __forceinline__ V operator()(V a, V b) const { return a > b ? a : b; }
+// Tokens whose key is at least a cut, decided on the value: 0 keeps all.
+struct Cut {
+    float value;
+    uint32_t index;
+    __device__ __forceinline__ explicit Cut(uint64_t key)
+        : value(key ? key_value(key) : -INFINITY), index(key ? key_index(key) : ~0u) {}
+    __device__ __forceinline__ bool keeps(float x, uint32_t i) const { return x > value || (x == value && i <= index); }
 };
-struct Plus {
-    template <class V>
-    __device__ __forceinline__ V operator()(V a, V b) const { return a + b; }
+
+// z = (x - m) / t and w = exp(z) of a row; the quotient as a product with
+// 1 / t, one rounding more, and no division per token.
+struct Scale {
+    float m, inv;
+    __device__ __forceinline__ Scale(float m_, float t) : m(m_), inv(fminf(fmaxf(1.0f / t, 1.17549435e-38f), 3.402823466e38f)) {}
+    __device__ __forceinline__ float z(float x) const { return (x - m) * inv; }
+    __device__ __forceinline__ float w(float x) const { return expf(z(x)); }
+    __device__ __forceinline__ uint64_t fixed(float x) const { return __float2ull_rn(w(x) * kFixed); }
+};
+
+// A key to find the largest of and a weight to add up, reduced together.
+struct KeySum {
+    uint64_t key;
+    float sum;
 };
 
 struct Smem {
     uint64_t list[kList];
-    uint32_t hist[kBins];
-    uint64_t warp[kWarps];
-    uint64_t slot[2][kMaxTeam];  // team reductions, two in turn
+    alignas(16) uint32_t hist[kBins];
+    union {
+        uint64_t sub[kSubBins];
+        uint64_t few[kFew];
+    };
+    KeySum warp[2][kWarps];      // reductions, two in turn
+    KeySum slot[2][kMaxTeam];
+    uint64_t scan[kWarps];
     uint64_t cut, above;
     uint32_t count;              // candidates appended (may pass kList)
-    uint32_t bin;
-    float threshold;
+    uint32_t bin, state;
     bool found;
 };
 
@@ -106,15 +116,18 @@ template <class T>
 struct Row {
     static constexpr uint32_t kVec = 16 / sizeof(T);
     const T *x;
+    const float *u;
     uint32_t vocab, head, pieces, me, team;  // this thread and the threads of the team
+    uint32_t shift;                          // elements of u between a 16-byte boundary and a piece's first
 
-    __device__ __forceinline__ Row(const T *x_, uint32_t vocab_, uint32_t rank, uint32_t size)
-        : x(x_), vocab(vocab_), team(size * kThreads)
+    __device__ __forceinline__ Row(const T *x_, const float *u_, uint32_t vocab_, uint32_t rank, uint32_t size)
+        : x(x_), u(u_), vocab(vocab_), team(size * kThreads)
     {
         const uint32_t lead = uint32_t((16u - (reinterpret_cast<uintptr_t>(x) & 15u)) & 15u) / uint32_t(sizeof(T));
         head = min(lead, vocab);
         pieces = (vocab - head) / kVec;
         me = rank * kThreads + threadIdx.x;
+        shift = uint32_t(reinterpret_cast<uintptr_t>(u + head) >> 2) & 3u;
     }
     __device__ __forceinline__ float value(uint32_t i) const { return sample_value(row_to_float(x[i])); }
     // Single elements outside the pieces; this thread's, or vocab.
@@ -124,43 +137,64 @@ struct Row {
         if (me < head) return me;
         return me - head < vocab - tail ? tail + (me - head) : vocab;
     }
-    // Piece q of the batch that starts at `base`, -inf past the end.
-    __device__ __forceinline__ void load(uint32_t base, Piece<T, kVec> (&p)[kLoads]) const
+    __device__ __forceinline__ void load(uint32_t j, Piece<T, kVec> &p) const
     {
+        if (j < pieces) {
+            p = load_piece<T, kVec>(x + head + size_t(j) * kVec);
+        } else {
 #pragma unroll
-        for (int q = 0; q < kLoads; ++q) {
-            const uint32_t j = base + uint32_t(q) * team + me;
-            if (j < pieces) {
-                p[q] = load_piece<T, kVec>(x + head + size_t(j) * kVec);
-            } else {
+            for (uint32_t e = 0; e < kVec; ++e) p.v[e] = row_from_float<T>(-INFINITY);
+        }
+    }
+    // f(values, index of the first) for this thread's pieces and, as a piece
+    // of one value, its single element; -inf where there is no token.  All
+    // threads of a warp call f together.  N pieces are loaded while the N
+    // before them are in work.
+    template <int N, class F>
+    __device__ __forceinline__ void each(const F &f) const
+    {
+        float v[kVec];
+        {
+            const uint32_t s = single();
 #pragma unroll
-                for (uint32_t e = 0; e < kVec; ++e) p[q].v[e] = row_from_float<T>(-INFINITY);
+            for (uint32_t e = 1; e < kVec; ++e) v[e] = -INFINITY;
+            v[0] = s < vocab ? row_to_float(x[s]) : -INFINITY;
+            if (__any_sync(kFull, s < vocab)) f(v, s);
+        }
+        Piece<T, kVec> now[N], next[N];
+#pragma unroll
+        for (int q = 0; q < N; ++q) load(q * team + me, now[q]);
+        for (uint32_t base = 0; base < pieces; base += N * team) {
+#pragma unroll
+            for (int q = 0; q < N; ++q) load(base + (N + q) * team + me, next[q]);
+#pragma unroll
+            for (int q = 0; q < N; ++q) {
+#pragma unroll
+                for (uint32_t e = 0; e < kVec; ++e) v[e] = row_to_float(now[q].v[e]);
+                f(v, head + (base + q * team + me) * kVec);
+                now[q] = next[q];
             }
         }
     }
-    __device__ __forceinline__ uint32_t index(uint32_t base, int q, uint32_t e) const
+    // u of the tokens of a piece, 0 past the end.  Rows of u that are aligned
+    // otherwise than the pieces are read as the 16-byte words around them.
+    __device__ __forceinline__ void uniforms(uint32_t i, float (&r)[kVec]) const
     {
-        return head + (base + uint32_t(q) * team + me) * kVec + e;
-    }
-    // f(value, index) for each of this thread's tokens that is not forbidden.
-    template <class F>
-    __device__ __forceinline__ void each(const F &f) const
-    {
-        const uint32_t s = single();
-        if (s < vocab) {
-            const float v = value(s);
-            if (v > -INFINITY) f(v, s);
-        }
-        for (uint32_t base = 0; base < pieces; base += kLoads * team) {
-            Piece<T, kVec> p[kLoads];
-            load(base, p);
+        if (i >= 4u && i + kVec + 4u <= vocab && i >= head) {
+            const float4 *p = reinterpret_cast<const float4 *>(u + i - shift);
+            float w[kVec + 4];
 #pragma unroll
-            for (int q = 0; q < kLoads; ++q)
+            for (uint32_t e = 0; e < kVec; e += 4) *reinterpret_cast<float4 *>(&w[e]) = __ldcs(p + e / 4);
+            if (shift) {
+                const float4 a = __ldcs(p + kVec / 4);
+                w[kVec] = a.x, w[kVec + 1] = a.y, w[kVec + 2] = a.z;
+            }
 #pragma unroll
-                for (uint32_t e = 0; e < kVec; ++e) {
-                    const float v = sample_value(row_to_float(p[q].v[e]));
-                    if (v > -INFINITY) f(v, index(base, q, e));
-                }
+            for (uint32_t e = 0; e < kVec; ++e)
+                r[e] = shift == 0 ? w[e] : shift == 1 ? w[e + 1] : shift == 2 ? w[e + 2] : w[e + 3];
+        } else {
+#pragma unroll
+            for (uint32_t e = 0; e < kVec; ++e) r[e] = i + e < vocab ? u[i + e] : 0.0f;
         }
     }
 };
@@ -188,86 +222,248 @@ struct Team {
         if (size == 1) __syncthreads();
         else cg::this_cluster().sync();
     }
-    // The same value to every thread of the team.
-    template <class Op>
-    __device__ __forceinline__ uint64_t reduce(uint64_t v, Op op)
+    // The same value to every thread of the team: the largest key and the sum,
+    // added in a fixed order.  Buffers alternate: one is written again two
+    // reductions later, past a barrier that follows every read of it.
+    __device__ __noinline__ KeySum reduce(KeySum v)
     {
+        auto join = [&](int o) {
+            const uint64_t k = __shfl_xor_sync(kFull, v.key, o);
+            v.key = k > v.key ? k : v.key;
+            v.sum += __shfl_xor_sync(kFull, v.sum, o);
+        };
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) v = op(v, __shfl_xor_sync(0xffffffffu, v, o));
-        __syncthreads();  // the previous use of sm.warp
-        if ((threadIdx.x & 31) == 0) sm.warp[threadIdx.x >> 5] = v;
+        for (int o = 16; o > 0; o >>= 1) join(o);
+        if ((threadIdx.x & 31) == 0) sm.warp[turn][threadIdx.x >> 5] = v;
         __syncthreads();
-        v = sm.warp[0];
+        v = sm.warp[turn][threadIdx.x & (kWarps - 1)];
 #pragma unroll
-        for (int w = 1; w < kWarps; ++w) v = op(v, sm.warp[w]);
+        for (int o = kWarps / 2; o > 0; o >>= 1) join(o);
         if (size > 1) {
-            // Slots alternate: a CTA writes a turn's slots again only two
-            // reductions later, past a sync that follows every read.
             if (threadIdx.x < size) peer(threadIdx.x)->slot[turn][rank] = v;
             sync();
-            v = sm.slot[turn][0];
-            for (uint32_t c = 1; c < size; ++c) v = op(v, sm.slot[turn][c]);
-            turn ^= 1;
+            v = sm.slot[turn][threadIdx.x & (size - 1)];
+            for (int o = int(size) / 2; o > 0; o >>= 1) join(o);
         }
+        turn ^= 1;
         return v;
     }
+    __device__ __forceinline__ uint64_t largest(uint64_t key) { return reduce(KeySum{key, 0.0f}).key; }
+    __device__ __forceinline__ float sum(float v) { return reduce(KeySum{0u, v}).sum; }
     // Adds this warp's keys to the leader's list; every lane calls it.
     __device__ __forceinline__ void append(bool mine, uint64_t key) const
     {
-        const uint32_t who = __ballot_sync(0xffffffffu, mine);
+        const uint32_t who = __ballot_sync(kFull, mine);
         if (who == 0u) return;
         uint32_t at = 0u;
         const int first = __ffs(who) - 1, lane = threadIdx.x & 31;
         if (lane == first) at = atomicAdd(&lead->count, uint32_t(__popc(who)));
-        at = __shfl_sync(0xffffffffu, at, first) + __popc(who & ((1u << lane) - 1u));
+        at = __shfl_sync(kFull, at, first) + __popc(who & ((1u << lane) - 1u));
         if (mine && at < kList) lead->list[at] = key;
     }
 };
 
-// Exclusive scan over the CTA (u64), total to every thread.
-__device__ __forceinline__ uint64_t block_scan(uint64_t v, Smem &sm, uint64_t &total)
+// The draw: of the tokens offered, the largest w / -log u, which orders them
+// as z - log(-log u) does.  A token can only be it if -log u < w / bound for
+// any ratio `bound` already seen, so u > 1 - w / bound: one multiply-add
+// spares most tokens the logarithm.
+struct Draw {
+    float best = -1.0f;
+    uint32_t index = ~0u;
+    float bound = 0.0f, slope = -INFINITY;  // bound: the warp's; slope: -1 / bound and a little more
+
+    __device__ __forceinline__ bool open(float w, float u) const { return u >= fmaf(w, slope, 0.9999995f); }
+    __device__ __forceinline__ void take(float w, float u, uint32_t i)
+    {
+        const float r = w / -logf(fminf(fmaxf(u, kUniformLo), kUniformHi));
+        if (r > best || (r == best && i < index)) {
+            best = r;
+            index = i;
+        }
+    }
+    // All lanes together: the bound of the warp.
+    __device__ __forceinline__ void share()
+    {
+        float b = best;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) b = fmaxf(b, __shfl_xor_sync(kFull, b, o));
+        if (b > bound) {
+            bound = b;
+            slope = -1.00001f / b;
+        }
+    }
+    // Offers the tokens of a piece with kept[e]; all lanes together.
+    template <uint32_t N>
+    __device__ __forceinline__ void offer(const float (&w)[N], const bool (&kept)[N], const float (&u)[N], uint32_t i)
+    {
+        bool any = false;
+#pragma unroll
+        for (uint32_t e = 0; e < N; ++e) any |= kept[e] && w[e] >= kLightest && open(w[e], fmaxf(u[e], kUniformLo));
+        if (!__any_sync(kFull, any)) return;
+#pragma unroll
+        for (uint32_t e = 0; e < N; ++e)
+            if (kept[e] && w[e] >= kLightest && open(w[e], fmaxf(u[e], kUniformLo))) take(w[e], u[e], i + e);
+        share();
+    }
+    __device__ __forceinline__ uint64_t key() const { return best > 0.0f ? order_key(best, index) : 0u; }
+};
+
+// Exclusive scan over the CTA (u64), total to every thread.  Between two uses
+// lies a barrier.
+__device__ __noinline__ uint64_t block_scan(uint64_t v, Smem &sm, uint64_t &total)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     uint64_t incl = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const uint64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+        const uint64_t y = __shfl_up_sync(kFull, incl, o);
         if (lane >= o) incl += y;
     }
+    if (lane == 31) sm.scan[warp] = incl;
     __syncthreads();
-    if (lane == 31) sm.warp[warp] = incl;
-    __syncthreads();
-    uint64_t before = 0u;
-    total = 0u;
+    uint64_t c = lane < kWarps ? sm.scan[lane] : 0u;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        const uint64_t c = sm.warp[w];
-        if (w < warp) before += c;
-        total += c;
+    for (int o = 1; o < kWarps; o <<= 1) {
+        const uint64_t y = __shfl_up_sync(kFull, c, o);
+        if (lane >= o) c += y;
     }
-    return before + incl - v;
+    total = __shfl_sync(kFull, c, kWarps - 1);
+    const uint64_t before = __shfl_sync(kFull, c, warp > 0 ? warp - 1 : 0);
+    return (warp > 0 ? before : 0u) + incl - v;
 }
 
-// Sorts list[0, n) descending (n <= kList; the list is padded with zeros,
-// below every key), by the leader's CTA.
-__device__ __forceinline__ void sort_list(Smem &sm, uint32_t n)
+// Sorts up to 64 keys descending, two to a lane of one warp.
+__device__ __forceinline__ void sort_warp(uint64_t *list, uint32_t n)
 {
-    uint32_t size = 2;
-    while (size < n) size <<= 1;
-    for (uint32_t i = n + threadIdx.x; i < size; i += kThreads) sm.list[i] = 0u;
-    for (uint32_t run = 2; run <= size; run <<= 1)
-        for (uint32_t step = run >> 1; step > 0; step >>= 1) {
-            __syncthreads();
-            for (uint32_t p = threadIdx.x; p < size / 2; p += kThreads) {
-                const uint32_t i = 2 * p - (p & (step - 1)), j = i + step;
-                const uint64_t a = sm.list[i], b = sm.list[j];
-                if ((a < b) == ((i & run) == 0)) {
-                    sm.list[i] = b;
-                    sm.list[j] = a;
+    const uint32_t lane = threadIdx.x & 31;
+    uint64_t a = lane < n ? list[lane] : 0u, b = lane + 32 < n ? list[lane + 32] : 0u;
+#pragma unroll
+    for (uint32_t run = 2; run <= 64; run <<= 1) {
+        if (run == 64) {
+            const uint64_t hi = a > b ? a : b;
+            b = a > b ? b : a;
+            a = hi;
+        }
+#pragma unroll
+        for (uint32_t step = run >> 1 > 16 ? 16 : run >> 1; step > 0; step >>= 1) {
+            const uint64_t x = __shfl_xor_sync(kFull, a, step), y = __shfl_xor_sync(kFull, b, step);
+            const bool low = (lane & step) == 0;
+            // Key i = lane (a) or lane + 32 (b) goes down in runs with i & run == 0.
+            a = (a > x) == (low == ((lane & run) == 0)) ? a : x;
+            b = (b > y) == (low == (((lane + 32) & run) == 0)) ? b : y;
+        }
+    }
+    if (lane < n) list[lane] = a;
+    if (lane + 32 < n) list[lane + 32] = b;
+}
+
+// Sorts list[0, n) descending, by one CTA; the list has room for the next
+// power of two and is padded with zeros, below every key.
+__device__ __noinline__ void sort_list(uint64_t *list, uint32_t n)
+{
+    __syncthreads();
+    if (n <= 64) {
+        if (threadIdx.x < 32) sort_warp(list, n);
+    } else {
+        uint32_t size = 128;
+        while (size < n) size <<= 1;
+        for (uint32_t i = n + threadIdx.x; i < size; i += kThreads) list[i] = 0u;
+        for (uint32_t run = 2; run <= size; run <<= 1)
+            for (uint32_t step = run >> 1; step > 0; step >>= 1) {
+                __syncthreads();
+                for (uint32_t p = threadIdx.x; p < size / 2; p += kThreads) {
+                    const uint32_t i = 2 * p - (p & (step - 1)), j = i + step;
+                    const uint64_t a = list[i], b = list[j];
+                    if ((a < b) == ((i & run) == 0)) {
+                        list[i] = b;
+                        list[j] = a;
+                    }
                 }
             }
-        }
+    }
     __syncthreads();
+}
+
+// Where of the list a cut falls, by one CTA: the bin of a histogram over
+// (top - x) * rate, and the amounts of the bins before it and of the tokens
+// `before` the list; kSubBins where the list does not reach the target.
+struct SubBin {
+    float top, rate;
+    uint32_t at;
+    uint64_t before;
+    __device__ __forceinline__ uint32_t of(uint64_t key) const
+    {
+        return uint32_t(fminf(fmaxf((top - key_value(key)) * rate, 0.0f), float(kSubBins - 1)));
+    }
+};
+
+template <class Amount>
+__device__ __forceinline__ SubBin sub_bin(Smem &sm, uint32_t n, float top, float span, uint64_t before, uint64_t target,
+                                          const Amount &amount)
+{
+    SubBin r{top, float(kSubBins) / fmaxf(span, 1e-30f), kSubBins, 0u};
+    __syncthreads();
+    for (int b = threadIdx.x; b < kSubBins; b += kThreads) sm.sub[b] = 0u;
+    if (threadIdx.x == 0) sm.bin = kSubBins;
+    __syncthreads();
+    for (uint32_t j = threadIdx.x; j < n; j += kThreads)
+        atomicAdd(reinterpret_cast<unsigned long long *>(&sm.sub[r.of(sm.list[j])]),
+                  static_cast<unsigned long long>(amount(sm.list[j])));
+    __syncthreads();
+    constexpr int kPer = kSubBins / kThreads;
+    uint64_t part[kPer], sum = 0u, all;
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) sum += part[q] = sm.sub[threadIdx.x * kPer + q];
+    uint64_t at = before + block_scan(sum, sm, all);
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) {
+        if (at < target && at + part[q] >= target) {
+            sm.bin = threadIdx.x * kPer + q;
+            sm.above = at;
+        }
+        at += part[q];
+    }
+    __syncthreads();
+    r.at = sm.bin;
+    r.before = sm.above;
+    return r;
+}
+
+// The list's keys with pick(key) to sm.few; how many there are (may pass kFew).
+template <class Pick>
+__device__ __forceinline__ uint32_t pick_few(Smem &sm, uint32_t n, const Pick &pick)
+{
+    __syncthreads();
+    if (threadIdx.x == 0) sm.count = 0u;
+    __syncthreads();
+    const int lane = threadIdx.x & 31;
+    for (uint32_t base = 0; base < n; base += kThreads) {
+        const uint32_t j = base + threadIdx.x;
+        const uint64_t key = j < n ? sm.list[j] : 0u;
+        const bool mine = j < n && pick(key);
+        const uint32_t who = __ballot_sync(kFull, mine);
+        if (who == 0u) continue;
+        uint32_t at = 0u;
+        const int first = __ffs(who) - 1;
+        if (lane == first) at = atomicAdd(&sm.count, uint32_t(__popc(who)));
+        at = __shfl_sync(kFull, at, first) + __popc(who & ((1u << lane) - 1u));
+        if (mine && at < kFew) sm.few[at] = key;
+    }
+    __syncthreads();
+    return sm.count;
+}
+
+// The largest K of 16 leading bits such that at least k of the CTA's order
+// bits, one per thread, are >= K, the bits below them 0; 0 if there are fewer.
+__device__ __forceinline__ uint32_t kth_largest(uint32_t o, uint32_t k)
+{
+    uint32_t at = 0u;
+#pragma unroll 1
+    for (int b = 31; b >= 16; --b) {
+        const uint32_t mid = at | (1u << b);
+        if (uint32_t(__syncthreads_count(o >= mid)) >= k) at = mid;
+    }
+    return at;
 }
 
 // The largest key K such that the amounts of all keys >= K sum to at least
@@ -297,7 +493,7 @@ __device__ __noinline__ uint64_t select_cut(uint64_t target, Smem &sm, const Eac
             for (int k = 0; k < 8; ++k) sum += hist[top - k];
             uint64_t incl = sum;
             for (int o = 1; o < 32; o <<= 1) {
-                const uint64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+                const uint64_t y = __shfl_up_sync(kFull, incl, o);
                 if (int(threadIdx.x) >= o) incl += y;
             }
             uint64_t before = above + incl - sum;
@@ -321,187 +517,282 @@ __device__ __noinline__ uint64_t select_cut(uint64_t target, Smem &sm, const Eac
     return prefix;
 }
 
-// Bin of a token: its distance below the maximum in steps of 1/64; kBins for
-// tokens 32 or more below, whose weights round to 0 of 2^-40.
-__device__ __forceinline__ uint32_t z_bin(float z)
+// x rounded to a whole number, 0 <= x < 2^22: an addition that leaves it in the
+// low bits; a conversion instruction takes eight times its issue slots.
+__device__ __forceinline__ uint32_t round_small(float x) { return __float_as_uint(x + 8388608.0f) & 0x7fffffu; }
+
+// Bin of a token: its distance below the maximum in steps of 1/64, rounded;
+// kBins for tokens 32 or more below, whose weights round to 0 of 2^-40.
+__device__ __forceinline__ uint32_t z_bin(float z) { return round_small(fminf(-z * kBinsPerUnit, float(kBins))); }
+
+// A bin's weights, all below 2^(1 - e) for e = bin_power, are counted in units
+// of 2^-(e + bits), 2^bits times the vocabulary at most 2^31, so that a bin of
+// all tokens fits 32 bits.
+__device__ __forceinline__ int bin_power(uint32_t bin) { return int((bin * 1477u) >> 16); }  // 1477 / 2^16 < log2(e) / 64
+
+__device__ __forceinline__ uint64_t share_of(float p, double fixed_sum)
 {
-    const float b = -z * kBinsPerUnit;
-    return b < float(kBins) ? uint32_t(b) : uint32_t(kBins);
+    const double s = ceil(double(fmaxf(p, 0.0f)) * fixed_sum);
+    return s < 1.0 ? 1u : uint64_t(s);
 }
 
-// Amounts of a bin are counted in units of 2^shift, so that `bits` bits hold
-// the largest weight of the bin and a bin of all tokens fits 32 bits.
-__device__ __forceinline__ int bin_shift(uint32_t bin, int bits)
-{
-    const int top = 41 - int((bin * 1477u) >> 16);  // weights of the bin are below 2^top: 1477 / 2^16 < log2(e) / 64
-    return max(0, top - bits);
-}
+// Whether find_cut found the cut, may find it with other bins, or cannot.
+enum : uint32_t { kMissed, kFound, kAgain };
+
+// What the row keeps so far: the sum of the weights and the draw.
+struct Kept {
+    float sum = 0.0f;
+    Draw draw;
+};
 
 // The cut at `target` (select_cut's) found by the team.  MASS: amounts are
-// fixed-point weights and target is a share p of their sum; else each token
-// counts 1 and target is k.  Only keys >= floor count.
+// weights and the target is a share p of their sum; else each token counts 1
+// and the target is k.  Only the tokens of `floor` count.  With `kept`, the
+// tokens above the cut's bins are added to it on the way and the leader adds
+// the rest; returns whether it did.
 template <bool MASS, class T>
-__device__ __noinline__ uint64_t find_cut(Team &team, const Row<T> &row, float m, float t, uint64_t floor, uint64_t k,
-                                          float p)
+__device__ __noinline__ bool find_cut(Team &team, const Row<T> &row, const Scale &scale, uint64_t floor_key, uint32_t k,
+                                      float p, float q, Kept *kept, uint64_t &cut_key)
 {
+    constexpr uint32_t kVec = Row<T>::kVec;
     Smem &sm = team.sm;
-    const int bits = 32 - (32 - __clz(int(row.vocab)));
-    team.sync();
+    const Cut floor(floor_key);
+    const int bits = min(14, __clz(int(row.vocab)) - 1);
     for (int b = threadIdx.x; b < kBins; b += kThreads) sm.hist[b] = 0u;
     if (threadIdx.x == 0) sm.count = 0u;
     team.sync();
-    uint64_t total = 0u;
-    row.each([&](float v, uint32_t i) {
-        if (order_key(v, i) < floor) return;
-        const float z = scaled(v, m, t);
-        const uint32_t b = z_bin(z);
-        if (b >= kBins) return;
-        if (MASS) {
-            const uint64_t w = fixed_weight(expf(z));
-            const int s = bin_shift(b, bits);
-            total += w;
-            atomicAdd(&sm.hist[b], uint32_t((w + ((uint64_t(1) << s) >> 1)) >> s));
-        } else {
-            total += 1u;
-            atomicAdd(&sm.hist[b], 1u);
+    float mass = 0.0f;
+    row.template each<2>([&](const float (&x)[kVec], uint32_t i) {
+#pragma unroll
+        for (uint32_t e = 0; e < kVec; ++e) {
+            const float v = sample_value(x[e]), z = scale.z(v);
+            const uint32_t b = z_bin(z);
+            if (b >= uint32_t(kBins) || !floor.keeps(v, i + e)) continue;
+            if (MASS) {
+                const float w = expf(z);
+                mass += w;
+                atomicAdd(&sm.hist[b], round_small(w * __int_as_float((127 + bits + bin_power(b)) << 23)));
+            } else {
+                mass += 1.0f;
+                atomicAdd(&sm.hist[b], 1u);
+            }
         }
     });
-    total = team.reduce(total, Plus());
+    mass = team.sum(mass);
     uint64_t target = k;
     if (MASS) {
-        const double share = ceil(double(fmaxf(p, 0.0f)) * double(total));
-        target = share < 1.0 ? 1u : uint64_t(share);
-    } else if (total < k) {
-        return 0u;  // the cut lies 32 below the maximum or more, where no weight is left
+        target = share_of(p, double(mass) * double(kFixed));
+    } else if (mass < float(k)) {
+        cut_key = floor_key;  // the cut lies 32 below the maximum or more, where no weight is left
+        return false;
     }
-    team.sync();  // every CTA's histogram is complete
-    if (team.rank == 0) {
-        // Thread j owns bins 4 j to 4 j + 3.
-        constexpr int kPer = kBins / kThreads;
-        uint64_t part[kPer], sum = 0u;
-        for (int q = 0; q < kPer; ++q) {
-            const uint32_t b = threadIdx.x * kPer + q;
-            uint64_t h = 0u;
-            for (uint32_t c = 0; c < team.size; ++c) h += team.peer(c)->hist[b];
-            part[q] = MASS ? h << bin_shift(b, bits) : h;
-            sum += part[q];
-        }
-        uint64_t all;
-        uint64_t before = block_scan(sum, sm, all);
-        const uint64_t aim = all < target ? all : target;  // rounding may leave the sum short
-        if (before < aim && before + sum >= aim)
-            for (int q = 0; q < kPer; ++q) {
-                if (before < aim && before + part[q] >= aim) sm.bin = threadIdx.x * kPer + q;
-                before += part[q];
-            }
-    }
-    team.sync();
-    // Tokens of the cut's bin and its neighbours to the list, those above added up.
-    const uint32_t bin = team.lead->bin, lo = bin > 0 ? bin - 1 : 0;
-    uint64_t above = 0u;
-    {
-        auto one = [&](float v, uint32_t i, bool in) {
-            const uint64_t key = order_key(v, i);
-            float z = 0.0f;
-            uint32_t b = kBins;
-            if (in && v > -INFINITY && key >= floor) {
-                z = scaled(v, m, t);
-                b = z_bin(z);
-            }
-            if (b < lo) above += MASS ? fixed_weight(expf(z)) : 1u;
-            team.append(b >= lo && b <= bin + 1 && b < kBins, key);
-        };
-        const uint32_t s = row.single();
-        one(s < row.vocab ? row.value(s) : -INFINITY, s, s < row.vocab);
-        for (uint32_t base = 0; base < row.pieces; base += kLoads * row.team) {
-            Piece<T, Row<T>::kVec> pc[kLoads];
-            row.load(base, pc);
+    // The rounded amounts may miss the cut's bin where the bins about it hold
+    // next to nothing; the exact sum above the bins tried puts that right.
+    int64_t error = 0;
+    Kept mine;
+    uint32_t state = kAgain;
+    for (int tries = 0; state == kAgain && tries < 4; ++tries) {
+        uint64_t rough = 0u;
+        if (team.rank == 0) {
+            // Thread j owns bins 4 j to 4 j + 3.
+            constexpr int kPer = kBins / kThreads;
+            uint64_t part[kPer], sum = 0u, all;
 #pragma unroll
-            for (int q = 0; q < kLoads; ++q)
+            for (int j = 0; j < kPer; ++j) part[j] = 0u;
+            for (uint32_t c = 0; c < team.size; ++c) {
+                const uint4 h = reinterpret_cast<const uint4 *>(team.peer(c)->hist)[threadIdx.x];
+                part[0] += h.x, part[1] += h.y, part[2] += h.z, part[3] += h.w;
+            }
 #pragma unroll
-                for (uint32_t e = 0; e < Row<T>::kVec; ++e)
-                    one(sample_value(row_to_float(pc[q].v[e])), row.index(base, q, e), true);
+            for (int j = 0; j < kPer; ++j) {
+                // in units of 2^-40 where that is the finer, and cut off there elsewhere
+                const int up = 40 - bits - bin_power(threadIdx.x * kPer + j);
+                if (MASS) part[j] = up >= 0 ? part[j] << up : part[j] >> -up;
+                sum += part[j];
+            }
+            const uint64_t before = block_scan(sum, sm, all);
+            const int64_t want = int64_t(target) - error;
+            const uint64_t aim = want < 1 ? 1u : all < uint64_t(want) ? all : uint64_t(want);
+            uint64_t at = before;
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) {
+                if (at < aim && at + part[j] >= aim) sm.bin = threadIdx.x * kPer + j;
+                at += part[j];
+            }
+            if (threadIdx.x == 0) sm.count = 0u;
+            __syncthreads();
+            const uint32_t lo = sm.bin > 0 ? sm.bin - 1 : 0;
+            if (lo / kPer == threadIdx.x) {
+                at = before;
+#pragma unroll
+                for (int j = 0; j < kPer; ++j)
+                    if (uint32_t(j) < lo % kPer) at += part[j];
+                sm.above = at;
+            }
+            __syncthreads();
+            rough = sm.above;
         }
-    }
-    above = team.reduce(above, Plus());
-    team.sync();  // the list is complete
-    if (team.rank == 0) {
-        const uint32_t n = sm.count;
-        if (threadIdx.x == 0) sm.found = false;
-        if (n <= kList && above < target) {
-            sort_list(sm, n);
-            const uint32_t per = (n + kThreads - 1) / kThreads;
-            const uint32_t first = min(n, threadIdx.x * per), last = min(n, first + per);
-            auto amount = [&](uint32_t j) {
-                return MASS ? fixed_weight(expf(scaled(key_value(sm.list[j]), m, t))) : uint64_t(1);
+        team.sync();
+        // Tokens of the cut's bin and its neighbours to the list, those above added up.
+        const uint32_t bin = team.lead->bin, lo = bin > 0 ? bin - 1 : 0, hi = min(bin + 1, uint32_t(kBins - 1));
+        mass = 0.0f;
+        mine = Kept();
+        row.template each<2>([&](const float (&x)[kVec], uint32_t i) {
+            float most = -INFINITY;
+#pragma unroll
+            for (uint32_t e = 0; e < kVec; ++e) most = fmaxf(most, sample_value(x[e]));
+            if (!__any_sync(kFull, z_bin(scale.z(most)) <= hi)) return;
+            float w[kVec];
+            bool sure[kVec];
+            bool some = false;
+            uint32_t list = 0u;
+#pragma unroll
+            for (uint32_t e = 0; e < kVec; ++e) {
+                const float v = sample_value(x[e]), z = scale.z(v);
+                const uint32_t b = z_bin(z);
+                const bool in = b <= hi && floor.keeps(v, i + e);
+                w[e] = expf(z);
+                if (in && b >= lo) list |= 1u << e;
+                sure[e] = in && b < lo;
+                mass += sure[e] ? (MASS ? w[e] : 1.0f) : 0.0f;
+                sure[e] = sure[e] && w[e] >= q;
+                mine.sum += sure[e] ? w[e] : 0.0f;
+                some |= sure[e];
+            }
+            if (__any_sync(kFull, list != 0u)) {
+#pragma unroll
+                for (uint32_t e = 0; e < kVec; ++e)
+                    team.append((list >> e) & 1u, order_key(sample_value(x[e]), i + e));
+            }
+            if (kept && __any_sync(kFull, some)) {
+                float u[kVec];
+                row.uniforms(i, u);
+                mine.draw.offer(w, sure, u, i);
+            }
+        });
+        mass = team.sum(mass);
+        if (team.rank == 0) {
+            // The cut is in the list if the tokens above it stay below the
+            // target and the list reaches it.  A histogram leaves few to sort.
+            const uint32_t n = sm.count;
+            const uint64_t above = MASS ? uint64_t(double(mass) * double(kFixed) + 0.5) : uint64_t(mass);
+            error = int64_t(above) - int64_t(rough);
+            auto amount = [&](uint64_t key) { return MASS ? scale.fixed(key_value(key)) : uint64_t(1); };
+            auto keep = [&](uint64_t key) {
+                const float w = scale.w(key_value(key));
+                if (!kept || w < q) return;
+                mine.sum += w;
+                if (w >= kLightest) mine.draw.take(w, row.u[key_index(key)], key_index(key));
             };
-            uint64_t sum = 0u, all;
-            for (uint32_t j = first; j < last; ++j) sum += amount(j);
-            uint64_t before = above + block_scan(sum, sm, all);
-            for (uint32_t j = first; j < last; ++j) {
-                const uint64_t a = amount(j);
-                if (before < target && before + a >= target) {
-                    sm.cut = sm.list[j];
-                    sm.found = true;
+            SubBin sub{0.0f, 0.0f, uint32_t(kSubBins), 0u};
+            if (n <= kList && above < target) {
+                const float step = 1.0f / (kBinsPerUnit * scale.inv);
+                sub = sub_bin(sm, n, scale.m - (float(lo) - 0.5f) * step, 3.0f * step, above, target, amount);
+            }
+            if (threadIdx.x == 0) sm.state = n <= kList ? kAgain : kMissed;
+            if (sub.at < uint32_t(kSubBins)) {
+                uint32_t few = pick_few(sm, n, [&](uint64_t key) { return sub.of(key) == sub.at; });
+                const bool fits = few <= kFew;
+                if (fits)
+                    for (uint32_t j = threadIdx.x; j < n; j += kThreads)
+                        if (sub.of(sm.list[j]) < sub.at) keep(sm.list[j]);
+                uint64_t *list = fits ? sm.few : sm.list;
+                few = fits ? few : n;
+                sort_list(list, few);
+                const uint32_t per = (few + kThreads - 1) / kThreads;
+                const uint32_t first = min(few, threadIdx.x * per), last = min(few, first + per);
+                uint64_t sum = 0u, all;
+                for (uint32_t j = first; j < last; ++j) sum += amount(list[j]);
+                uint64_t before = (fits ? sub.before : above) + block_scan(sum, sm, all);
+                for (uint32_t j = first; j < last && before < target; ++j) {
+                    keep(list[j]);
+                    before += amount(list[j]);
+                    if (before >= target) {
+                        sm.cut = list[j];
+                        sm.state = kFound;
+                    }
                 }
-                before += a;
             }
         }
-        __syncthreads();
-        if (!sm.found) {
-            const Row<T> whole(row.x, row.vocab, 0, 1);
+        team.sync();
+        state = team.lead->state;
+        team.sync();  // everyone has read it, and the list may be filled anew
+    }
+    if (kept) *kept = mine;
+    if (state != kFound) {
+        if (team.rank == 0) {
+            const Row<T> whole(row.x, row.u, row.vocab, 0, 1);
             const uint64_t cut = select_cut(target, sm, [&](auto add) {
-                whole.each([&](float v, uint32_t i) {
-                    const uint64_t key = order_key(v, i);
-                    if (key >= floor) add(key, MASS ? fixed_weight(expf(scaled(v, m, t))) : uint64_t(1));
+                whole.template each<1>([&](const float (&x)[kVec], uint32_t i) {
+#pragma unroll
+                    for (uint32_t e = 0; e < kVec; ++e) {
+                        const float v = sample_value(x[e]);
+                        if (v > -INFINITY && floor.keeps(v, i + e))
+                            add(order_key(v, i + e), MASS ? scale.fixed(v) : uint64_t(1));
+                    }
                 });
             });
             __syncthreads();
             if (threadIdx.x == 0) sm.cut = cut;
         }
+        team.sync();
     }
+    cut_key = floor_key > team.lead->cut ? floor_key : team.lead->cut;
     team.sync();
-    return team.lead->cut;
+    return state == kFound && kept != nullptr;
 }
 
-// The rest of a row whose candidates are all in the leader's list, by the
-// leader's CTA: sort, top-k, top-p, min-p, draw.
-__device__ __forceinline__ void finish_list(Smem &sm, uint32_t k, float t, float p, float q,
-                                            const float *__restrict__ u, int32_t *token, float *logprob)
+// The rest of a row whose candidates, all tokens not below `threshold`, are in
+// the leader's list, by the leader's CTA: top-k, sort, top-p, min-p, draw.
+__device__ __noinline__ void finish_list(Smem &sm, uint32_t k, float t, float p, float q, float threshold,
+                                         const float *__restrict__ u, int32_t *token, float *logprob)
 {
-    const uint32_t n = min(k, sm.count);
-    sort_list(sm, sm.count);
-    const float m = key_value(sm.list[0]);
+    uint32_t n = sm.count;
+    uint64_t *list = sm.list;
+    Team alone(sm, 1);
+    if (n > 64) {
+        // A histogram of the values leaves k and a few to sort.
+        uint64_t most = 0u;
+        for (uint32_t j = threadIdx.x; j < n; j += kThreads) most = sm.list[j] > most ? sm.list[j] : most;
+        const float m = key_value(alone.largest(most));
+        const SubBin sub = sub_bin(sm, n, m, m - fmaxf(threshold, m - 32.0f * t), 0u, min(k, n),
+                                   [](uint64_t) { return uint64_t(1); });
+        // The last bin of a span of 32 t holds tokens without weight, which may go.
+        const uint32_t last = m - 32.0f * t > threshold ? min(sub.at, uint32_t(kSubBins - 2)) : sub.at;
+        const uint32_t few = pick_few(sm, n, [&](uint64_t key) { return sub.of(key) <= last; });
+        if (few <= kFew) {
+            list = sm.few;
+            n = few;
+        }
+    }
+    for (uint32_t j = threadIdx.x; j < n; j += kThreads)  // on their way while the list is sorted
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(u + key_index(list[j])));
+    sort_list(list, n);
+    n = min(k, n);
+    const Scale scale(key_value(list[0]), t);
     const uint32_t per = (n + kThreads - 1) / kThreads;
     const uint32_t first = min(n, threadIdx.x * per), last = min(n, first + per);
     uint64_t before = 0u, target = ~uint64_t(0);
     if (p < 1.0f) {
         uint64_t sum = 0u, all;
-        for (uint32_t j = first; j < last; ++j) sum += fixed_weight(expf(scaled(key_value(sm.list[j]), m, t)));
+        for (uint32_t j = first; j < last; ++j) sum += scale.fixed(key_value(list[j]));
         before = block_scan(sum, sm, all);
-        const double share = ceil(double(fmaxf(p, 0.0f)) * double(all));
-        target = share < 1.0 ? 1u : uint64_t(share);
+        target = share_of(p, double(all));
     }
-    float sum = 0.0f;
-    uint64_t best = 0u;
+    Kept kept;
     for (uint32_t j = first; j < last && before < target; ++j) {
-        const uint32_t i = key_index(sm.list[j]);
-        const float z = scaled(key_value(sm.list[j]), m, t), w = expf(z);
-        if (p < 1.0f) before += fixed_weight(w);
-        if (w < q || w == 0.0f) continue;
-        sum += w;
-        if (z >= -20.0f) best = Larger()(best, order_key(draw_score(z, u[i]), i));
+        const uint32_t i = key_index(list[j]);
+        const float w = scale.w(key_value(list[j]));
+        if (p < 1.0f) before += scale.fixed(key_value(list[j]));
+        if (w < q) continue;
+        kept.sum += w;
+        if (w >= kLightest) kept.draw.take(w, u[i], i);
     }
-    Team alone(sm, 1);
-    best = alone.reduce(best, Larger());
-    const uint64_t mass = alone.reduce(uint64_t(__double_as_longlong(double(sum))), [](uint64_t a, uint64_t b) {
-        return uint64_t(__double_as_longlong(__longlong_as_double(int64_t(a)) + __longlong_as_double(int64_t(b))));
-    });
-    for (uint32_t j = threadIdx.x; j < n; j += kThreads)
-        if (key_index(sm.list[j]) == key_index(best)) {
-            *token = int32_t(key_index(best));
-            if (logprob)
-                *logprob = scaled(key_value(sm.list[j]), m, t) - logf(float(__longlong_as_double(int64_t(mass))));
+    const KeySum end = alone.reduce(KeySum{kept.draw.key(), kept.sum});
+    for (uint32_t j = first; j < last; ++j)
+        if (key_index(list[j]) == key_index(end.key)) {
+            *token = int32_t(key_index(end.key));
+            if (logprob) *logprob = scale.z(key_value(list[j])) - logf(end.sum);
         }
 }
 
@@ -512,11 +803,13 @@ sample_kernel(const T *__restrict__ logits, size_t logits_stride, uint32_t vocab
               const int32_t *__restrict__ top_k, const float *__restrict__ top_p, const float *__restrict__ min_p,
               int32_t *__restrict__ tokens, float *__restrict__ logprobs)
 {
-    __shared__ Smem sm;
+    extern __shared__ __align__(16) uint8_t sample_smem[];
+    Smem &sm = *reinterpret_cast<Smem *>(sample_smem);
+    constexpr uint32_t kVec = Row<T>::kVec;
     Team team(sm, cg::this_cluster().num_blocks());
     const uint32_t r = blockIdx.x / team.size;
-    const Row<T> row(logits + size_t(r) * logits_stride, vocab, team.rank, team.size);
-    const float *u = uniform + size_t(r) * uniform_stride;
+    const Row<T> row(logits + size_t(r) * logits_stride, uniform + size_t(r) * uniform_stride, vocab, team.rank,
+                     team.size);
     const float t = temperature ? temperature[r] : 1.0f;
     const float p = top_p ? top_p[r] : 1.0f;
     const float q0 = min_p ? min_p[r] : 0.0f, q = q0 > 0.0f ? fminf(q0, 1.0f) : 0.0f;
@@ -525,113 +818,114 @@ sample_kernel(const T *__restrict__ logits, size_t logits_stride, uint32_t vocab
     int32_t *token = tokens + r;
     float *logprob = logprobs ? logprobs + r : nullptr;
 
-    // Candidates by one pass: the whole row if it fits the list; else the
-    // k-th largest of the threads' maxima over each CTA's first batch bounds
-    // the k-th largest value from below, and about k in kBatch tokens get in.
-    constexpr uint32_t kBatch = kLoads * kThreads * Row<T>::kVec;
-    const bool shortcut = !greedy && (k < vocab || p < 1.0f) &&
-                          (vocab <= kList || (k <= uint32_t(kThreads) && uint64_t(k) * vocab <= uint64_t(kBatch) * (kList * 3 / 4)));
-    if (shortcut) {
-        if (threadIdx.x == 0) {
-            sm.count = 0u;
-            sm.threshold = -INFINITY;
-        }
+    // Top-k by one pass that collects candidates: all tokens of a short row;
+    // else the k-th largest of the threads' maxima over each CTA's first batch, rounded
+    // down to 16 bits, bounds the k-th largest value from below, and about k
+    // in kBatch tokens get in.
+    constexpr uint32_t kBatch = kLoads * kThreads * kVec;
+    const bool brief = vocab <= kList / 2;
+    if (!greedy && k < vocab &&
+        (brief || (k <= uint32_t(kThreads) && uint64_t(k) * vocab <= uint64_t(kBatch) * (kList / 2)))) {
+        if (threadIdx.x == 0) sm.count = 0u;
         float threshold = -INFINITY;
         team.sync();
-        Piece<T, Row<T>::kVec> pc[kLoads];
-        row.load(0, pc);
-        if (vocab > kList) {
-            float top = -INFINITY;
+        if (!brief) {
+            float best = -INFINITY;
 #pragma unroll
-            for (int b = 0; b < kLoads; ++b)
+            for (int j = 0; j < kLoads; ++j) {
+                Piece<T, kVec> pc;
+                row.load(j * row.team + row.me, pc);
 #pragma unroll
-                for (uint32_t e = 0; e < Row<T>::kVec; ++e) top = fmaxf(top, sample_value(row_to_float(pc[b].v[e])));
-            float *tops = reinterpret_cast<float *>(sm.hist);
-            tops[threadIdx.x] = top;
-            __syncthreads();
-            uint32_t above = 0u;
-            for (int j = 0; j < kThreads; j += 4) {
-                const float4 o = *reinterpret_cast<const float4 *>(tops + j);
-                above += (o.x > top || (o.x == top && j < int(threadIdx.x))) +
-                         (o.y > top || (o.y == top && j + 1 < int(threadIdx.x))) +
-                         (o.z > top || (o.z == top && j + 2 < int(threadIdx.x))) +
-                         (o.w > top || (o.w == top && j + 3 < int(threadIdx.x)));
+                for (uint32_t e = 0; e < kVec; ++e) best = fmaxf(best, row_to_float(pc.v[e]));
             }
-            if (above == k - 1) sm.threshold = top;
-            __syncthreads();
-            threshold = sm.threshold;
+            const uint32_t least = kth_largest(best > -INFINITY ? order_bits(sample_value(best)) : 0u, k);
+            if (least) threshold = order_value(least);
         }
-        const uint32_t s = row.single();
-        const float sv = s < vocab ? row.value(s) : -INFINITY;
-        team.append(sv > -INFINITY && sv >= threshold, order_key(sv, s));
-        for (uint32_t base = 0; base < row.pieces;) {
+        row.template each<kLoads>([&](const float (&x)[kVec], uint32_t i) {
+            float best = -INFINITY;
 #pragma unroll
-            for (int b = 0; b < kLoads; ++b) {
-                float top = -INFINITY;
+            for (uint32_t e = 0; e < kVec; ++e) best = fmaxf(best, x[e]);
+            if (!__any_sync(kFull, best > -INFINITY && best >= threshold)) return;
 #pragma unroll
-                for (uint32_t e = 0; e < Row<T>::kVec; ++e) top = fmaxf(top, sample_value(row_to_float(pc[b].v[e])));
-                if (!__any_sync(0xffffffffu, top > -INFINITY && top >= threshold)) continue;
-#pragma unroll
-                for (uint32_t e = 0; e < Row<T>::kVec; ++e) {
-                    const float v = sample_value(row_to_float(pc[b].v[e]));
-                    team.append(v > -INFINITY && v >= threshold, order_key(v, row.index(base, b, e)));
-                }
+            for (uint32_t e = 0; e < kVec; ++e) {
+                const float v = sample_value(x[e]);
+                team.append(v > -INFINITY && v >= threshold, order_key(v, i + e));
             }
-            base += kLoads * row.team;
-            if (base < row.pieces) row.load(base, pc);
-        }
+        });
         team.sync();
         const uint32_t n = team.lead->count;
+        team.sync();  // finish_list counts anew
         if (n <= kList) {
             if (team.rank == 0) {
                 if (n > 0) {
-                    finish_list(sm, k, t, p, q, u, token, logprob);
+                    finish_list(sm, k, t, p, q, threshold, row.u, token, logprob);
                 } else if (threadIdx.x == 0) {
                     *token = -1;
                     if (logprob) *logprob = -INFINITY;
                 }
             }
-            team.sync();
-            return;
+            return;  // nobody reads another CTA's shared memory any more
         }
     }
 
-    uint64_t best = 0u;
-    row.each([&](float v, uint32_t i) { best = Larger()(best, order_key(v, i)); });
-    best = team.reduce(best, Larger());
-    if (best == 0u || greedy) {
-        if (team.rank == 0 && threadIdx.x == 0) {
-            *token = best == 0u ? -1 : int32_t(key_index(best));
-            if (logprob) *logprob = best == 0u ? -INFINITY : 0.0f;
+    // The first of the order.
+    float best = -INFINITY;
+    uint32_t at = ~0u;
+    row.template each<kLoads>([&](const float (&x)[kVec], uint32_t i) {
+        float top = -INFINITY;
+#pragma unroll
+        for (uint32_t e = 0; e < kVec; ++e) top = fmaxf(top, sample_value(x[e]));
+        if (top > best || (top == best && i < at)) {
+            best = top;
+#pragma unroll
+            for (int e = int(kVec) - 1; e >= 0; --e)
+                if (sample_value(x[e]) == top) at = i + e;
         }
-        team.sync();
+    });
+    const uint64_t first = team.largest(best > -INFINITY ? order_key(best, at) : 0u);
+    if (first == 0u || greedy) {
+        if (team.rank == 0 && threadIdx.x == 0) {
+            *token = first == 0u ? -1 : int32_t(key_index(first));
+            if (logprob) *logprob = first == 0u ? -INFINITY : 0.0f;
+        }
+        team.sync();  // no CTA leaves while another may write to its slots
         return;
     }
-    const float m = key_value(best);
-    uint64_t cut = 0u;
-    if (k < vocab) cut = find_cut<false>(team, row, m, t, 0u, k, 1.0f);
-    if (p < 1.0f) cut = Larger()(cut, find_cut<true>(team, row, m, t, cut, 0u, p));
-
-    // What is kept: its weight, and the draw.
-    float sum = 0.0f;
-    best = 0u;
-    row.each([&](float v, uint32_t i) {
-        if (order_key(v, i) < cut) return;
-        const float z = scaled(v, m, t), w = expf(z);
-        if (w < q || w == 0.0f) return;
-        sum += w;
-        if (z >= -20.0f) best = Larger()(best, order_key(draw_score(z, u[i]), i));
-    });
-    best = team.reduce(best, Larger());
-    const uint64_t mass = team.reduce(uint64_t(__double_as_longlong(double(sum))), [](uint64_t a, uint64_t b) {
-        return uint64_t(__double_as_longlong(__longlong_as_double(int64_t(a)) + __longlong_as_double(int64_t(b))));
-    });
-    if (team.rank == 0 && threadIdx.x == 0) {
-        const uint32_t i = key_index(best);
-        *token = int32_t(i);
-        if (logprob) *logprob = scaled(row.value(i), m, t) - logf(float(__longlong_as_double(int64_t(mass))));
+    const Scale scale(key_value(first), t);
+    Kept kept;
+    uint64_t cut_key = 0u;
+    bool done = false;
+    if (k < vocab) done = find_cut<false>(team, row, scale, 0u, k, 1.0f, q, p < 1.0f ? nullptr : &kept, cut_key);
+    if (p < 1.0f) done = find_cut<true>(team, row, scale, cut_key, 0u, p, q, &kept, cut_key);
+    if (!done) {
+        kept = Kept();
+        const Cut cut(cut_key);
+        row.template each<2>([&](const float (&x)[kVec], uint32_t i) {
+            float w[kVec];
+            bool in[kVec];
+            bool some = false;
+#pragma unroll
+            for (uint32_t e = 0; e < kVec; ++e) {
+                const float v = sample_value(x[e]);
+                w[e] = scale.w(v);
+                in[e] = cut.keeps(v, i + e) && w[e] >= q;
+                kept.sum += in[e] ? w[e] : 0.0f;
+                in[e] = in[e] && w[e] >= kLightest;
+                some |= in[e];
+            }
+            if (!__any_sync(kFull, some)) return;
+            float u[kVec];
+            row.uniforms(i, u);
+            kept.draw.offer(w, in, u, i);
+        });
     }
-    team.sync();  // no CTA leaves while another may read its shared memory
+    const KeySum end = team.reduce(KeySum{kept.draw.key(), kept.sum});
+    if (team.rank == 0 && threadIdx.x == 0) {
+        const uint32_t i = key_index(end.key);
+        *token = int32_t(i);
+        if (logprob) *logprob = scale.z(row.value(i)) - logf(end.sum);
+    }
+    team.sync();  // no CTA leaves while another may write to its slots
 }
 
 template <class T, class... A>
@@ -643,9 +937,14 @@ cudaError_t run_sample(const void *logits, uint32_t rows, uint32_t vocab, cudaSt
     while (team < kMaxTeam && uint64_t(rows) * (2 * team) <= slots &&
            vocab >= 2 * team * (kThreads * kLoads * uint32_t(16 / sizeof(T))))
         team *= 2;
+    // Raises the kernel's shared-memory limit, once per device.
+    auto kernel = sample_kernel<T>;
+    if (gch::persistent_grid(reinterpret_cast<const void *>(kernel), kThreads, sizeof(Smem), 1) <= 0)
+        return cudaErrorInvalidConfiguration;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(rows * team);
     cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = sizeof(Smem);
     cfg.stream = s;
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeClusterDimension;
@@ -654,7 +953,7 @@ cudaError_t run_sample(const void *logits, uint32_t rows, uint32_t vocab, cudaSt
     attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, sample_kernel<T>, static_cast<const T *>(logits), stride, vocab, args...);
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<const T *>(logits), stride, vocab, args...);
 }
 
 }  // namespace
