@@ -3,10 +3,12 @@
 //
 // The gradient sorts (token, position) pairs by LSD passes of the stable bin
 // partition (gc_binsort.cuh), up to 9 bits each, so that every table row's
-// positions are contiguous and ascending; then each table row is the sum of
-// its positions' rows.  A frequent token's positions are summed in fixed
-// blocks first, so that no CTA walks them alone.  Every sum's order depends
-// on the ids alone.
+// positions are contiguous and ascending.  Blocks of kBlock sorted positions
+// are then summed run by run, whatever tokens they hold, so that a frequent
+// token's thousands of rows are spread over the GPU: a run that lies within
+// its block is a row of the result, the ends of one that does not are kept
+// and joined by a last kernel.  Rows of absent tokens are zeroed beside the
+// sums.  Every sum's order depends on the ids alone.
 #include "gc_binsort.cuh"
 #include "gc_internal.h"
 #include "gc_rows.cuh"
@@ -16,7 +18,12 @@ namespace {
 using namespace gcd;
 
 constexpr int kRowThreads = 256;
+constexpr uint32_t kBlock = 32;     // sorted positions per block
+constexpr int kAhead = 8;           // rows loaded at a time
+constexpr int kLookups = 4;         // rows per thread of a lookup
+constexpr size_t kZeroBytes = 32768;  // zeroed per CTA, about
 
+// tx threads across a row's pieces, kRowThreads / tx rows.
 dim3 row_block(size_t pieces)
 {
     int tx = 32;
@@ -24,34 +31,42 @@ dim3 row_block(size_t pieces)
     return dim3(tx, kRowThreads / tx);
 }
 
+// A thread moves the same piece of kLookups rows, whose ids and then whose
+// pieces are loaded together.
 template <class T, int N>
 __global__ void __launch_bounds__(kRowThreads)
 embedding_kernel(const T *__restrict__ table, size_t table_stride, uint32_t vocab, uint32_t pieces,
                  const void *__restrict__ ids, bool wide, uint32_t n, float scale, T *__restrict__ out,
                  size_t out_stride)
 {
-    const uint32_t i = blockIdx.x * blockDim.y + threadIdx.y;
-    if (i >= n) return;
-    const uint32_t id = load_id(ids, wide, i, vocab);
-    const T *src = table + size_t(id) * table_stride;
-    T *dst = out + size_t(i) * out_stride;
-    for (uint32_t c = threadIdx.x; c < pieces; c += blockDim.x) {
-        Piece<T, N> v = zero_piece<T, N>();
-        if (id < vocab) {
-            v = load_piece<T, N>(src + size_t(c) * N);
+    const uint32_t first = (blockIdx.x * blockDim.y + threadIdx.y) * kLookups;
+    uint32_t id[kLookups];
 #pragma unroll
-            for (int k = 0; k < N; ++k) v.v[k] = row_from_float<T>(scale * row_to_float(v.v[k]));
+    for (int r = 0; r < kLookups; ++r) id[r] = first + r < n ? load_id(ids, wide, first + r, vocab) : vocab;
+    for (uint32_t c = threadIdx.x; c < pieces; c += blockDim.x) {
+        Piece<T, N> v[kLookups];
+#pragma unroll
+        for (int r = 0; r < kLookups; ++r) {
+            v[r] = zero_piece<T, N>();
+            if (id[r] < vocab) v[r] = load_piece<T, N>(table + size_t(id[r]) * table_stride + size_t(c) * N);
         }
-        store_piece<T, N>(dst + size_t(c) * N, v);
+#pragma unroll
+        for (int r = 0; r < kLookups; ++r) {
+            if (id[r] < vocab)  // zeros stay zeros whatever the scale
+#pragma unroll
+                for (int k = 0; k < N; ++k) v[r].v[k] = row_from_float<T>(scale * row_to_float(v[r].v[k]));
+            if (first + r < n) store_piece<T, N>(out + size_t(first + r) * out_stride + size_t(c) * N, v[r]);
+        }
     }
 }
 
 // A pass's items: (key, position) pairs, or in the first pass the ids
 // themselves; an id outside the vocabulary is the key `vocab`, which sorts
-// last.
+// last.  The first pass marks the tokens that occur.
 struct TokenPass {
     const void *ids;        // first pass
     const uint2 *in;        // later passes
+    uint8_t *seen;          // may be null
     bool first, wide;
     uint32_t vocab, shift, mask;
     __device__ __forceinline__ uint2 item(uint32_t i) const
@@ -59,6 +74,12 @@ struct TokenPass {
         return first ? make_uint2(load_id(ids, wide, i, vocab), i) : in[i];
     }
     __device__ __forceinline__ uint32_t bin(uint32_t i) const { return (item(i).x >> shift) & mask; }
+    __device__ __forceinline__ void visit(uint32_t i) const
+    {
+        if (!first || seen == nullptr) return;
+        const uint32_t key = load_id(ids, wide, i, vocab);
+        if (key < vocab) seen[key] = 1;
+    }
 };
 
 struct TokenSink {
@@ -70,82 +91,158 @@ struct TokenSink {
     __device__ __forceinline__ void drop(uint32_t) const {}
 };
 
-// [start, end) of every token that occurs, in bounds (zeroed before).
-__global__ void __launch_bounds__(256)
-token_bounds_kernel(const uint2 *__restrict__ sorted, uint32_t n, uint32_t vocab, uint2 *__restrict__ bounds)
+// All passes of a short sort, and the clearing of `seen`, by one CTA.
+__global__ void __launch_bounds__(kBinThreads)
+token_sort_kernel(const void *ids, bool wide, uint32_t n, uint32_t vocab, uint32_t digit, int passes, uint2 *a,
+                  uint2 *b, uint8_t *seen)
 {
-    const uint32_t i = blockIdx.x * 256u + threadIdx.x;
-    if (i >= n) return;
-    const uint32_t key = sorted[i].x;
-    if (key >= vocab) return;
-    if (i == 0 || sorted[i - 1].x != key) bounds[key].x = i;
-    if (i + 1 == n || sorted[i + 1].x != key) bounds[key].y = i + 1;
-}
-
-// Sums of the blocks of `block` sorted positions that hold one token only.
-template <class T, int N>
-__global__ void __launch_bounds__(kRowThreads)
-token_blocks_kernel(const uint2 *__restrict__ sorted, uint32_t vocab, uint32_t block, const T *__restrict__ g,
-                    size_t g_stride, uint32_t width, float *__restrict__ partial)
-{
-    const uint32_t first = blockIdx.x * block;
-    const uint32_t key = sorted[first].x;
-    if (key >= vocab || sorted[first + block - 1].x != key) return;
-    const uint32_t c = (blockIdx.y * kRowThreads + threadIdx.x) * N;
-    if (c >= width) return;
-    float acc[N] = {};
-    for (uint32_t i = first; i < first + block; ++i) {
-        const Piece<T, N> v = load_piece<T, N>(g + size_t(sorted[i].y) * g_stride + c);
-#pragma unroll
-        for (int k = 0; k < N; ++k) acc[k] += row_to_float(v.v[k]);
+    extern __shared__ uint32_t s_cnt[];
+    __shared__ BinSmem sm;
+    if (seen != nullptr) {
+        // `seen` has room for whole words.
+        for (uint32_t i = threadIdx.x; i < (vocab + 15u) / 16u; i += kBinThreads)
+            reinterpret_cast<uint4 *>(seen)[i] = make_uint4(0u, 0u, 0u, 0u);
+        __syncthreads();
     }
-    for (int k = 0; k < N; ++k) partial[size_t(blockIdx.x) * width + c + k] = acc[k];
+    for (int p = 0; p < passes; ++p) {
+        const TokenPass src{ids, a, seen, p == 0, wide, vocab, uint32_t(p) * digit, (1u << digit) - 1u};
+        const TokenSink sink{src, b};
+        bin_place_chunk(src, sink, n, n, 1, 0, 1u << digit, 1u, nullptr, s_cnt, sm);
+        __syncthreads();
+        uint2 *t = a;
+        a = b;
+        b = t;
+    }
 }
 
-// dtable[v] (+)= scale * (sum of v's rows).
+template <class O, int N>
+__device__ __forceinline__ void put_sum(O *dst, const float (&sum)[N], float scale, bool accumulate)
+{
+    Piece<O, N> o;
+    if (accumulate) o = load_piece<O, N>(dst);
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        const float r = scale * sum[k];
+        o.v[k] = row_from_float<O>(accumulate ? r + row_to_float(o.v[k]) : r);
+    }
+    store_piece<O, N>(dst, o);
+}
+
+struct GradOut {
+    void *rows;
+    size_t stride;
+    float scale;
+    bool accumulate;
+    const uint8_t *seen;
+    uint32_t vocab;
+};
+
+// CTAs below `sums`: blocks of kBlock sorted positions, one to a row of
+// threads, summed run by run.  edges: two rows per block, the sum of its
+// first run where that began before the block, and of its last where that
+// began in the block and goes on.  The other CTAs zero rows of absent tokens.
 template <class T, class O, int N>
 __global__ void __launch_bounds__(kRowThreads)
-token_rows_kernel(const uint2 *__restrict__ sorted, const uint2 *__restrict__ bounds, uint32_t vocab,
-                  uint32_t block, const T *__restrict__ g, size_t g_stride, uint32_t width,
-                  const float *__restrict__ partial, float scale, O *__restrict__ out, size_t out_stride,
-                  bool accumulate)
+token_sums_kernel(const uint2 *__restrict__ sorted, uint32_t n, const T *__restrict__ g, size_t g_stride,
+                  uint32_t width, float *__restrict__ edges, GradOut out, uint32_t sums, uint32_t zero_rows)
 {
-    const uint32_t v = blockIdx.x * blockDim.y + threadIdx.y;
-    if (v >= vocab) return;
-    const uint2 range = bounds[v];
-    if (accumulate && range.x == range.y) return;
-    for (uint32_t c = threadIdx.x * N; c < width; c += blockDim.x * N) {
-        float acc[N] = {};
-        for (uint32_t i = range.x; i < range.y;) {
-            if (i % block == 0 && i + block <= range.y) {
-                const float *p = partial + size_t(i / block) * width + c;
-#pragma unroll
-                for (int k = 0; k < N; ++k) acc[k] += p[k];
-                i += block;
-            } else {
-                const Piece<T, N> x = load_piece<T, N>(g + size_t(sorted[i].y) * g_stride + c);
-#pragma unroll
-                for (int k = 0; k < N; ++k) acc[k] += row_to_float(x.v[k]);
-                ++i;
-            }
+    O *rows = static_cast<O *>(out.rows);
+    const uint32_t columns = blockDim.x * N;
+    if (blockIdx.x >= sums) {
+        const uint32_t first = (blockIdx.x - sums) * zero_rows, last = min(out.vocab, first + zero_rows);
+        for (uint32_t v = first + threadIdx.y; v < last; v += blockDim.y) {
+            if (out.seen[v]) continue;
+            for (uint32_t c = threadIdx.x * N; c < width; c += columns)
+                store_piece<O, N>(rows + size_t(v) * out.stride + c, zero_piece<O, N>());
         }
-        O *dst = out + size_t(v) * out_stride + c;
+        return;
+    }
+    const uint32_t parts = (width + columns - 1) / columns;  // of a row, neighbours in the grid
+    const uint32_t block = blockIdx.x / parts * blockDim.y + threadIdx.y;
+    const uint32_t c = (blockIdx.x % parts) * columns + threadIdx.x * N;
+    if (block >= (n + kBlock - 1) / kBlock || c >= width) return;
+    const uint32_t first = block * kBlock, last = min(n, first + kBlock);
+    const uint32_t none = ~0u;
+    const uint32_t prev = first > 0 ? sorted[first - 1].x : none, next = last < n ? sorted[last].x : none;
+    float sum[N] = {};
+    uint32_t key = sorted[first].x;
+    bool began = key != prev;
+    auto flush = [&](bool goes_on) {
+        if (key >= out.vocab) return;
+        if (began && !goes_on) {
+            put_sum<O, N>(rows + size_t(key) * out.stride + c, sum, out.scale, out.accumulate);
+        } else {
+            Piece<float, N> e;
 #pragma unroll
-        for (int k = 0; k < N; ++k) {
-            float r = scale * acc[k];
-            if (accumulate) r += row_to_float(dst[k]);
-            dst[k] = row_from_float<O>(r);
+            for (int k = 0; k < N; ++k) e.v[k] = sum[k];
+            store_piece<float, N>(edges + (size_t(block) * 2 + (began ? 1 : 0)) * width + c, e);
+        }
+    };
+    for (uint32_t base = first; base < last; base += kAhead) {
+        uint2 item[kAhead];
+        Piece<T, N> x[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) item[j] = base + j < last ? sorted[base + j] : make_uint2(out.vocab, 0u);
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+            if (item[j].x < out.vocab) x[j] = load_piece<T, N>(g + size_t(item[j].y) * g_stride + c);
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            if (base + j >= last) break;
+            if (item[j].x != key) {
+                flush(false);
+                key = item[j].x;
+                began = true;
+#pragma unroll
+                for (int k = 0; k < N; ++k) sum[k] = 0.0f;
+            }
+            if (key < out.vocab)
+#pragma unroll
+                for (int k = 0; k < N; ++k) sum[k] += row_to_float(x[j].v[k]);
         }
     }
+    flush(key == next);
 }
 
-// Sorted positions per block: about sqrt(n), so that the longest token's sum
-// is about sqrt(n) steps in both kernels.
-uint32_t token_block(size_t n)
+// Tokens whose run crosses blocks: the block in which it began adds up its
+// parts.
+template <class O, int N>
+__global__ void __launch_bounds__(kRowThreads)
+token_join_kernel(const uint2 *__restrict__ sorted, uint32_t n, uint32_t width, const float *__restrict__ edges,
+                  GradOut out)
 {
-    uint32_t b = 32;
-    while (size_t(b) * b < n && b < 4096) b <<= 1;
-    return b;
+    const uint32_t columns = blockDim.x * N, parts = (width + columns - 1) / columns;
+    const uint32_t block = blockIdx.x / parts * blockDim.y + threadIdx.y;
+    const uint32_t c = (blockIdx.x % parts) * columns + threadIdx.x * N;
+    const uint32_t blocks = (n + kBlock - 1) / kBlock;
+    if (block + 1 >= blocks || c >= width) return;
+    const uint32_t first = block * kBlock, next = first + kBlock;
+    const uint32_t key = sorted[next - 1].x;
+    if (key >= out.vocab || sorted[next].x != key || (first > 0 && sorted[first - 1].x == key)) return;
+    // The last block that the run reaches: the last whose first key is it.
+    uint32_t lo = block + 1, hi = blocks;
+    while (hi - lo > 1) {
+        const uint32_t mid = (lo + hi) / 2;
+        if (sorted[mid * kBlock].x == key) lo = mid;
+        else hi = mid;
+    }
+    const float *e = edges + (size_t(block) * 2 + 1) * width + c;
+    Piece<float, N> sum = load_piece<float, N>(e);
+    e += width;
+    for (uint32_t b = block + 1; b <= lo; b += kAhead) {
+        Piece<float, N> x[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            x[j] = Piece<float, N>{};
+            if (b + j <= lo) x[j] = load_piece<float, N>(e + size_t(j) * 2 * width);
+        }
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+#pragma unroll
+            for (int k = 0; k < N; ++k) sum.v[k] += x[j].v[k];
+        e += size_t(kAhead) * 2 * width;
+    }
+    put_sum<O, N>(static_cast<O *>(out.rows) + size_t(key) * out.stride + c, sum.v, out.scale, out.accumulate);
 }
 
 int key_bits(size_t vocab)
@@ -156,7 +253,7 @@ int key_bits(size_t vocab)
 }
 
 struct GradLayout {
-    size_t items_a, items_b, table, bounds, partial, total;
+    size_t items_a, items_b, table, seen, edges, total;
 };
 
 GradLayout grad_layout(size_t n, size_t vocab, size_t width)
@@ -166,27 +263,49 @@ GradLayout grad_layout(size_t n, size_t vocab, size_t width)
     l.items_a = 0;
     l.items_b = items;
     l.table = 2 * items;
-    l.bounds = l.table + gch::align_up(size_t(bin_chunks(n)) * 512 * 4, 256);
-    l.partial = l.bounds + gch::align_up(8 * vocab, 256);
-    l.total = l.partial + gch::align_up(n / token_block(n) * width * 4, 256) + 256;
+    l.seen = l.table + gch::align_up(size_t(bin_chunks(n)) * 512 * 4, 256);
+    l.edges = l.seen + gch::align_up(vocab, 256);
+    l.total = l.edges + gch::align_up(gch::ceil_div(n, size_t(kBlock)) * 2 * width * 4, 256) + 256;
     return l;
 }
 
 template <class T, class O, int N>
-cudaError_t run_grad_rows(const uint2 *sorted, const uint2 *bounds, uint32_t n, uint32_t vocab, const void *g,
-                          size_t g_stride, size_t width, float *partial, float scale, void *out,
-                          size_t out_stride, bool accumulate, cudaStream_t s)
+cudaError_t run_grad_rows(const uint2 *sorted, uint32_t n, const void *g, size_t g_stride, size_t width,
+                          float *edges, const GradOut &out, cudaStream_t s)
 {
-    const uint32_t block = token_block(n);
-    const uint32_t pieces = uint32_t(width / N);
-    if (n / block > 0)
-        token_blocks_kernel<T, N><<<dim3(n / block, uint32_t(gch::ceil_div(pieces, kRowThreads))), kRowThreads, 0, s>>>(
-            sorted, vocab, block, static_cast<const T *>(g), g_stride, uint32_t(width), partial);
-    const dim3 threads = row_block(pieces);
-    token_rows_kernel<T, O, N><<<uint32_t(gch::ceil_div(vocab, threads.y)), threads, 0, s>>>(
-        sorted, bounds, vocab, block, static_cast<const T *>(g), g_stride, uint32_t(width), partial, scale,
-        static_cast<O *>(out), out_stride, accumulate);
+    const dim3 threads = row_block(width / N);
+    const uint32_t blocks = uint32_t(gch::ceil_div(n, kBlock));
+    const size_t parts = gch::ceil_div(width / N, threads.x);
+    const size_t sums = gch::ceil_div(blocks, threads.y) * parts;
+    const size_t zero_rows = gch::align_up(gch::ceil_div(kZeroBytes, width * sizeof(O)), threads.y);
+    const size_t zeros = out.accumulate ? 0 : gch::ceil_div(out.vocab, zero_rows);
+    if (sums + zeros > 0x7fffffffu) return cudaErrorInvalidConfiguration;
+    if (sums + zeros > 0)
+        token_sums_kernel<T, O, N><<<uint32_t(sums + zeros), threads, 0, s>>>(
+            sorted, n, static_cast<const T *>(g), g_stride, uint32_t(width), edges, out, uint32_t(sums),
+            uint32_t(zero_rows));
+    if (blocks > 1)
+        token_join_kernel<O, N><<<uint32_t(sums), threads, 0, s>>>(sorted, n, uint32_t(width), edges, out);
     return cudaGetLastError();
+}
+
+// Pieces of N elements, N a power of two that both rows allow and that fills
+// 16 bytes of the result at most.
+#define GC_GRAD_BY_PIECE(T, O, n)                                                   \
+    switch (n) {                                                                    \
+    case 1: return run_grad_rows<T, O, 1>(sorted, n_, g, g_stride, width, edges, out, s); \
+    case 2: return run_grad_rows<T, O, 2>(sorted, n_, g, g_stride, width, edges, out, s); \
+    case 4: return run_grad_rows<T, O, 4>(sorted, n_, g, g_stride, width, edges, out, s); \
+    default: return run_grad_rows<T, O, 16 / int(sizeof(O))>(sorted, n_, g, g_stride, width, edges, out, s); \
+    }
+
+template <class T, class O>
+cudaError_t grad_rows(const uint2 *sorted, uint32_t n_, const void *g, size_t g_stride, size_t width, float *edges,
+                      const GradOut &out, cudaStream_t s)
+{
+    const int in = gch::piece_elems(uint64_t(uintptr_t(g)) | sizeof(T) * (g_stride | width), sizeof(T));
+    const int to = gch::piece_elems(uint64_t(uintptr_t(out.rows)) | sizeof(O) * (out.stride | width), sizeof(O));
+    GC_GRAD_BY_PIECE(T, O, (in < to ? in : to))
 }
 
 #define GC_BY_PIECE(T, n, CALL)                                     \
@@ -214,7 +333,7 @@ cudaError_t launch_embedding(const void *table, size_t table_stride, uint32_t vo
     {                                                                                                            \
         const uint32_t pieces = uint32_t(width / (N));                                                           \
         const dim3 block = row_block(pieces);                                                                    \
-        embedding_kernel<T, N><<<uint32_t(ceil_div(n, block.y)), block, 0, s>>>(                                 \
+        embedding_kernel<T, N><<<uint32_t(ceil_div(n, size_t(block.y) * kLookups)), block, 0, s>>>(              \
             static_cast<const T *>(table), table_stride, vocab, pieces, ids, wide, n, scale, static_cast<T *>(out), \
             out_stride);                                                                                         \
     }
@@ -225,40 +344,39 @@ cudaError_t launch_embedding(const void *table, size_t table_stride, uint32_t vo
 }
 
 cudaError_t launch_embedding_grad(const void *g, size_t g_stride, gc_row_dtype gdt, const void *ids, bool wide,
-                                  uint32_t n, uint32_t vocab, size_t width, float scale, void *out,
-                                  size_t out_stride, gc_row_dtype odt, bool accumulate, uint8_t *ws, cudaStream_t s)
+                                  uint32_t n, uint32_t vocab, size_t width, float scale, void *dtable,
+                                  size_t dtable_stride, gc_row_dtype odt, bool accumulate, uint8_t *ws, cudaStream_t s)
 {
     const GradLayout l = grad_layout(n, vocab, width);
     uint2 *items[2] = {reinterpret_cast<uint2 *>(ws + l.items_a), reinterpret_cast<uint2 *>(ws + l.items_b)};
     uint32_t *table = reinterpret_cast<uint32_t *>(ws + l.table);
-    uint2 *bounds = reinterpret_cast<uint2 *>(ws + l.bounds);
-    float *partial = reinterpret_cast<float *>(ws + l.partial);
-    cudaError_t e = cudaMemsetAsync(bounds, 0, size_t(vocab) * 8, s);
-    if (e != cudaSuccess) return e;
-    int at = 0;
-    if (n > 0) {
-        const int bits = key_bits(vocab), passes = int(ceil_div(bits, 9)), digit = int(ceil_div(bits, passes));
-        for (int p = 0; p < passes; ++p) {
-            const TokenPass src{ids, items[at], p == 0, wide, vocab, uint32_t(p * digit), (1u << digit) - 1u};
-            const TokenSink sink{src, items[at ^ 1]};
-            if ((e = gcd::launch_bin_count(src, n, 1u << digit, table, s)) != cudaSuccess) return e;
-            if ((e = gcd::launch_bin_place(src, sink, n, 1u << digit, 1u, table, s)) != cudaSuccess) return e;
-            at ^= 1;
+    uint8_t *seen = accumulate ? nullptr : ws + l.seen;
+    float *edges = reinterpret_cast<float *>(ws + l.edges);
+    const int bits = key_bits(vocab), passes = int(ceil_div(bits, 9)), digit = int(ceil_div(bits, passes));
+    cudaError_t e = cudaSuccess;
+    if (n > 0 && gcd::bin_chunks(n) == 1) {
+        if (!gcd::bin_place_smem(reinterpret_cast<const void *>(token_sort_kernel))) return cudaErrorInvalidConfiguration;
+        token_sort_kernel<<<1, gcd::kBinThreads, (sizeof(uint32_t) * gcd::kBinWarps) << digit, s>>>(
+            ids, wide, n, vocab, uint32_t(digit), passes, items[0], items[1], seen);
+        e = cudaGetLastError();
+    } else {
+        if (seen) e = cudaMemsetAsync(seen, 0, vocab, s);
+        for (int p = 0; n > 0 && p < passes && e == cudaSuccess; ++p) {
+            const TokenPass src{ids, items[p & 1], seen, p == 0, wide, vocab, uint32_t(p * digit), (1u << digit) - 1u};
+            const TokenSink sink{src, items[(p & 1) ^ 1]};
+            e = gcd::launch_bin_count(src, n, 1u << digit, table, s);
+            if (e == cudaSuccess) e = gcd::launch_bin_place(src, sink, n, 1u << digit, 1u, table, s);
         }
-        token_bounds_kernel<<<uint32_t(ceil_div(n, 256)), 256, 0, s>>>(items[at], n, vocab, bounds);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
-    const int elem = gdt == GC_ROW_F32 ? 4 : 2;
-    const int m = piece_elems(uint64_t(uintptr_t(g)) | elem * (g_stride | width), elem);
-#define GC_GRAD_ARGS items[at], bounds, n, vocab, g, g_stride, width, partial, scale, out, out_stride, accumulate, s
-#define GC_GRAD_WIDE(T, N) e = run_grad_rows<T, float, N>(GC_GRAD_ARGS)
-#define GC_GRAD_SAME(T, N) e = run_grad_rows<T, T, N>(GC_GRAD_ARGS)
-    if (gdt == GC_ROW_F32) { GC_BY_PIECE(float, m, GC_GRAD_WIDE) }
-    else if (gdt == GC_ROW_BF16 && odt == GC_ROW_F32) { GC_BY_PIECE(__nv_bfloat16, m, GC_GRAD_WIDE) }
-    else if (gdt == GC_ROW_BF16) { GC_BY_PIECE(__nv_bfloat16, m, GC_GRAD_SAME) }
-    else if (odt == GC_ROW_F32) { GC_BY_PIECE(__half, m, GC_GRAD_WIDE) }
-    else { GC_BY_PIECE(__half, m, GC_GRAD_SAME) }
-    return e;
+    if (e != cudaSuccess) return e;
+    const uint2 *sorted = items[passes & 1];
+    const GradOut out{dtable, dtable_stride, scale, accumulate, seen, vocab};
+    if (gdt == GC_ROW_F32) return grad_rows<float, float>(sorted, n, g, g_stride, width, edges, out, s);
+    if (gdt == GC_ROW_BF16)
+        return odt == GC_ROW_F32 ? grad_rows<__nv_bfloat16, float>(sorted, n, g, g_stride, width, edges, out, s)
+                                 : grad_rows<__nv_bfloat16, __nv_bfloat16>(sorted, n, g, g_stride, width, edges, out, s);
+    return odt == GC_ROW_F32 ? grad_rows<__half, float>(sorted, n, g, g_stride, width, edges, out, s)
+                             : grad_rows<__half, __half>(sorted, n, g, g_stride, width, edges, out, s);
 }
 
 }  // namespace gch

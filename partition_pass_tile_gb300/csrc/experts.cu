@@ -18,6 +18,7 @@ struct ExpertSource {
     bool wide;
     uint32_t experts;
     __device__ __forceinline__ uint32_t bin(uint32_t i) const { return load_id(ids, wide, i, experts); }
+    __device__ __forceinline__ void visit(uint32_t) const {}
 };
 
 struct ExpertSink {
@@ -47,23 +48,145 @@ dim3 row_block(size_t pieces)
     return dim3(tx, kRowThreads / tx);
 }
 
-// out[r] = x[pairs[r] / topk], or zeros.  E: an integer of the element's size.
+// Rows without a pair: -1 in pairs and zeros.  One warp takes 32 rows, each
+// lane looks one up in the experts' blocks.
 template <class E, int N>
-__global__ void __launch_bounds__(kRowThreads)
-expert_rows_kernel(const E *__restrict__ x, size_t x_stride, uint32_t pieces, uint32_t topk, uint32_t pair_limit,
-                   const int32_t *__restrict__ pairs, uint32_t rows, E *__restrict__ out, size_t out_stride)
+__device__ __forceinline__ void expert_pad_rows(uint32_t first, uint32_t rows, uint32_t experts,
+                                                const int32_t *__restrict__ offsets,
+                                                const int32_t *__restrict__ counts, int32_t *__restrict__ pairs,
+                                                E *__restrict__ out, size_t out_stride, uint32_t pieces)
 {
-    const uint32_t r = blockIdx.x * blockDim.y + threadIdx.y;
-    if (r >= rows) return;
-    const uint32_t p = uint32_t(pairs[r]);
-    const E *src = x + size_t(p / topk) * x_stride;
-    E *dst = out + size_t(r) * out_stride;
-    for (uint32_t c = threadIdx.x; c < pieces; c += blockDim.x) {
-        Piece<E, N> v{};
-        if (p < pair_limit) v = load_piece<E, N>(src + size_t(c) * N);
-        store_piece<E, N>(dst + size_t(c) * N, v);
+    const uint32_t lane = threadIdx.x & 31, r = first + lane;
+    bool pad = false;
+    if (r < rows) {
+        pad = r >= uint32_t(offsets[experts]);
+        if (!pad) {
+            // the last block that starts at or before r, which is not an empty one
+            uint32_t lo = 0, hi = experts;
+            while (hi - lo > 1) {
+                const uint32_t mid = (lo + hi) / 2;
+                if (uint32_t(offsets[mid]) <= r) lo = mid;
+                else hi = mid;
+            }
+            pad = r - uint32_t(offsets[lo]) >= uint32_t(counts[lo]);
+        }
+        if (pad) pairs[r] = -1;
+    }
+    uint32_t left = __ballot_sync(0xffffffffu, pad);
+    if (out == nullptr) return;
+    for (; left; left &= left - 1) {
+        E *dst = out + size_t(first + __ffs(left) - 1) * out_stride;
+        for (uint32_t c = lane; c < pieces; c += 32) store_piece<E, N>(dst + size_t(c) * N, Piece<E, N>{});
     }
 }
+
+// One token's row to its slots: read once, written up to topk times.
+template <class E, int N>
+__device__ __forceinline__ void expert_spread_row(const E *__restrict__ src, const uint32_t *slots, uint32_t topk,
+                                                  uint32_t rows, E *__restrict__ out, size_t out_stride,
+                                                  uint32_t pieces)
+{
+    for (uint32_t c = threadIdx.x; c < pieces; c += blockDim.x) {
+        const Piece<E, N> v = load_piece<E, N>(src + size_t(c) * N);
+        for (uint32_t j = 0; j < topk; ++j)
+            if (slots[j] < rows) store_piece<E, N>(out + size_t(slots[j]) * out_stride + size_t(c) * N, v);
+    }
+}
+
+// E: an integer of the element's size.  CTAs below `spread` move tokens, one
+// to a row of threads; the others take 32 rows per warp.
+template <class E, int N>
+__global__ void __launch_bounds__(kRowThreads)
+expert_rows_kernel(const E *__restrict__ x, size_t x_stride, uint32_t tokens, uint32_t topk, uint32_t experts,
+                   const int32_t *__restrict__ offsets, const int32_t *__restrict__ counts,
+                   const int32_t *__restrict__ slots, int32_t *__restrict__ pairs, uint32_t rows,
+                   E *__restrict__ out, size_t out_stride, uint32_t pieces, uint32_t spread)
+{
+    if (blockIdx.x >= spread) {
+        const uint32_t warp = (threadIdx.y * blockDim.x + threadIdx.x) >> 5;
+        const uint64_t first = (uint64_t(blockIdx.x - spread) * (kRowThreads / 32) + warp) * 32u;
+        if (first < rows)
+            expert_pad_rows<E, N>(uint32_t(first), rows, experts, offsets, counts, pairs, out, out_stride, pieces);
+        return;
+    }
+    __shared__ uint32_t s_slots[kRowThreads / 32][GC_MAX_TOPK];
+    const uint32_t t = blockIdx.x * blockDim.y + threadIdx.y;
+    if (t < tokens && threadIdx.x < topk) {
+        // 32 threads at least to a row, 64 choices at most
+        s_slots[threadIdx.y][threadIdx.x] = uint32_t(slots[size_t(t) * topk + threadIdx.x]);
+        if (threadIdx.x + 32 < topk && blockDim.x == 32)
+            s_slots[threadIdx.y][threadIdx.x + 32] = uint32_t(slots[size_t(t) * topk + threadIdx.x + 32]);
+    }
+    __syncthreads();
+    if (t < tokens)
+        expert_spread_row<E, N>(x + size_t(t) * x_stride, s_slots[threadIdx.y], topk, rows, out, out_stride, pieces);
+}
+
+// The whole dispatch of up to kSmallPairs pairs in one launch: every CTA counts
+// all pairs itself, which takes less than a second launch.  CTAs below tokens
+// move one token each, the others 32 rows per warp.
+constexpr uint32_t kSmallPairs = 1024;
+
+template <class E, int N>
+__global__ void __launch_bounds__(kRowThreads)
+expert_small_kernel(ExpertSource src, ExpertSink sink, uint32_t npairs, uint32_t topk, uint32_t align,
+                    const E *__restrict__ x, size_t x_stride, uint32_t rows, E *__restrict__ out, size_t out_stride,
+                    uint32_t pieces)
+{
+    __shared__ uint32_t s_ids[kSmallPairs];
+    __shared__ int32_t s_counts[GC_MAX_EXPERTS], s_offsets[GC_MAX_EXPERTS + 1];
+    __shared__ uint32_t s_slots[GC_MAX_TOPK], s_warp[kRowThreads / 32];
+    const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, experts = src.experts;
+    for (uint32_t e = tid; e < experts; e += kRowThreads) s_counts[e] = 0;
+    __syncthreads();
+    for (uint32_t p = tid; p < npairs; p += kRowThreads) {
+        const uint32_t e = src.bin(p);
+        s_ids[p] = e;
+        if (e < experts) atomicAdd(&s_counts[e], 1);
+    }
+    __syncthreads();
+    const uint32_t per = (experts + kRowThreads - 1) / kRowThreads;
+    const uint32_t lo = min(experts, tid * per), hi = min(experts, lo + per);
+    uint32_t sum = 0u, total;
+    for (uint32_t e = lo; e < hi; ++e) sum += (uint32_t(s_counts[e]) + align - 1u) / align * align;
+    uint32_t start = bin_block_scan<kRowThreads>(sum, s_warp, total);
+    for (uint32_t e = lo; e < hi; ++e) {
+        s_offsets[e] = int32_t(start);
+        if (blockIdx.x == 0) sink.start(e, start, uint32_t(s_counts[e]));
+        start += (uint32_t(s_counts[e]) + align - 1u) / align * align;
+    }
+    if (tid == 0) {
+        s_offsets[experts] = int32_t(total);
+        if (blockIdx.x == 0) sink.end(total);
+    }
+    __syncthreads();
+    const uint32_t t = blockIdx.x, tokens = npairs / topk;
+    if (t >= tokens) {
+        const uint32_t first = ((t - tokens) * (kRowThreads / 32) + warp) * 32u;
+        if (first < rows)
+            expert_pad_rows<E, N>(first, rows, experts, s_offsets, s_counts, sink.pairs, out, out_stride, pieces);
+        return;
+    }
+    // A warp per choice: the earlier pairs of the same expert.
+    for (uint32_t j = warp; j < topk; j += kRowThreads / 32) {
+        const uint32_t p = t * topk + j, e = s_ids[p];
+        uint32_t rank = 0u;
+        for (uint32_t q = lane; q < p; q += 32) rank += s_ids[q] == e;
+        rank = __reduce_add_sync(0xffffffffu, rank);
+        const uint32_t row = e < experts ? uint32_t(s_offsets[e]) + rank : ~0u;
+        if (lane == 0) {
+            s_slots[j] = row;
+            if (e < experts) sink.place(p, row);
+            else sink.drop(p);
+        }
+    }
+    __syncthreads();
+    if (out != nullptr)
+        expert_spread_row<E, N>(x + size_t(t) * x_stride, s_slots, topk, rows, out, out_stride, pieces);
+}
+
+// The rows of kAhead choices are loaded together.
+constexpr int kAhead = 8;
 
 template <class T, int N>
 __global__ void __launch_bounds__(kRowThreads)
@@ -75,13 +198,24 @@ expert_combine_kernel(const T *__restrict__ y, size_t y_stride, uint32_t rows, c
     if (t >= tokens) return;
     for (uint32_t c = threadIdx.x; c < pieces; c += blockDim.x) {
         float acc[N] = {};
-        for (uint32_t j = 0; j < topk; ++j) {
-            const uint32_t slot = uint32_t(slots[size_t(t) * topk + j]);
-            if (slot >= rows) continue;
-            const float w = weights ? weights[size_t(t) * topk + j] : 1.0f;
-            const Piece<T, N> v = load_piece<T, N>(y + size_t(slot) * y_stride + size_t(c) * N);
+        for (uint32_t base = 0; base < topk; base += kAhead) {
+            uint32_t slot[kAhead];
+            float w[kAhead];
+            Piece<T, N> v[kAhead];
 #pragma unroll
-            for (int i = 0; i < N; ++i) acc[i] = fmaf(w, row_to_float(v.v[i]), acc[i]);
+            for (int j = 0; j < kAhead; ++j) {
+                const uint64_t p = uint64_t(t) * topk + base + j;
+                slot[j] = base + j < topk ? uint32_t(slots[p]) : ~0u;
+                w[j] = weights && base + j < topk ? weights[p] : 1.0f;
+            }
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j)
+                if (slot[j] < rows) v[j] = load_piece<T, N>(y + size_t(slot[j]) * y_stride + size_t(c) * N);
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j)
+                if (slot[j] < rows)
+#pragma unroll
+                    for (int i = 0; i < N; ++i) acc[i] = fmaf(w[j], row_to_float(v[j].v[i]), acc[i]);
         }
         Piece<T, N> o;
 #pragma unroll
@@ -157,13 +291,22 @@ void run_combine_grad(const void *g, size_t g_stride, const void *y, size_t y_st
 }
 
 template <class E, int N>
-void run_rows(const void *x, size_t x_stride, size_t width, uint32_t topk, uint32_t npairs, const int32_t *pairs,
-              uint32_t rows, void *out, size_t out_stride, cudaStream_t s)
+void run_rows(const void *x, size_t x_stride, size_t width, uint32_t tokens, uint32_t topk, const ExpertSource &src,
+              const ExpertSink &sink, uint32_t align, uint32_t rows, void *out, size_t out_stride, cudaStream_t s)
 {
-    const uint32_t pieces = uint32_t(width / N);
+    const uint32_t pieces = uint32_t(width / N), pads = uint32_t(gch::ceil_div(rows, kRowThreads));
+    const E *from = static_cast<const E *>(x);
+    E *to = static_cast<E *>(out);
+    if (tokens * topk <= kSmallPairs) {
+        expert_small_kernel<E, N><<<tokens + pads, kRowThreads, 0, s>>>(src, sink, tokens * topk, topk, align, from,
+                                                                        x_stride, rows, to, out_stride, pieces);
+        return;
+    }
     const dim3 block = row_block(pieces);
-    expert_rows_kernel<E, N><<<uint32_t(gch::ceil_div(rows, block.y)), block, 0, s>>>(
-        static_cast<const E *>(x), x_stride, pieces, topk, npairs, pairs, rows, static_cast<E *>(out), out_stride);
+    const uint32_t spread = out ? uint32_t(gch::ceil_div(tokens, block.y)) : 0;
+    expert_rows_kernel<E, N><<<spread + pads, block, 0, s>>>(from, x_stride, tokens, topk, src.experts, sink.offsets,
+                                                             sink.counts, sink.slots, sink.pairs, rows, to, out_stride,
+                                                             pieces, spread);
 }
 
 // Row kernels by piece size: 16 bytes down to one element.
@@ -185,7 +328,7 @@ namespace gch {
 
 size_t expert_workspace_bytes(size_t npairs, uint32_t experts)
 {
-    return align_up(size_t(gcd::bin_chunks(npairs)) * experts * sizeof(uint32_t), 256) + 256;
+    return npairs > kSmallPairs ? align_up(size_t(gcd::bin_chunks(npairs)) * experts * sizeof(uint32_t), 256) : 256;
 }
 
 cudaError_t launch_expert_dispatch(const void *ids, bool wide, uint32_t npairs, uint32_t topk, uint32_t experts,
@@ -196,18 +339,21 @@ cudaError_t launch_expert_dispatch(const void *ids, bool wide, uint32_t npairs, 
     uint32_t *table = reinterpret_cast<uint32_t *>(ws);
     const ExpertSource src{ids, wide, experts};
     const ExpertSink sink{offsets, counts, slots, pairs, experts};
-    cudaError_t e = rows ? cudaMemsetAsync(pairs, 0xff, size_t(rows) * sizeof(int32_t), s) : cudaSuccess;
-    if (npairs == 0) {
-        if (e == cudaSuccess) e = cudaMemsetAsync(offsets, 0, (size_t(experts) + 1) * sizeof(int32_t), s);
-        if (e == cudaSuccess) e = cudaMemsetAsync(counts, 0, size_t(experts) * sizeof(int32_t), s);
-    } else {
-        if (e == cudaSuccess) e = gcd::launch_bin_count(src, npairs, experts, table, s);
+    cudaError_t e = cudaSuccess;
+    if (npairs > kSmallPairs) {
+        e = gcd::launch_bin_count(src, npairs, experts, table, s);
         if (e == cudaSuccess) e = gcd::launch_bin_place(src, sink, npairs, experts, align, table, s);
+    } else if (rows == 0) {  // no pairs either
+        e = cudaMemsetAsync(offsets, 0, (size_t(experts) + 1) * sizeof(int32_t), s);
+        if (e == cudaSuccess) e = cudaMemsetAsync(counts, 0, size_t(experts) * sizeof(int32_t), s);
+        return e;
     }
-    if (e != cudaSuccess || out == nullptr || rows == 0) return e;
+    if (e != cudaSuccess) return e;
     const int elem = dt == GC_ROW_F32 ? 4 : 2;
-    const int n = piece_elems(uint64_t(uintptr_t(x)) | uintptr_t(out) | elem * (x_stride | out_stride | width), elem);
-#define GC_ROWS_CALL(E, N) run_rows<E, N>(x, x_stride, width, topk, npairs, pairs, rows, out, out_stride, s)
+    const int n = out ? piece_elems(uint64_t(uintptr_t(x)) | uintptr_t(out) | elem * (x_stride | out_stride | width), elem)
+                      : 1;
+#define GC_ROWS_CALL(E, N) run_rows<E, N>(x, x_stride, out ? width : 0, npairs / topk, topk, src, sink, align, rows, out, \
+                                          out_stride, s)
     if (elem == 4) { GC_BY_PIECE(uint32_t, n, GC_ROWS_CALL) }
     else { GC_BY_PIECE(uint16_t, n, GC_ROWS_CALL) }
     return cudaGetLastError();

@@ -6,9 +6,10 @@
 // bin; bin_place_kernel adds the counts of the chunks before its own and of
 // the smaller bins (each bin's total rounded up to `align`) to get where its
 // first item of each bin goes, ranks its own items, and hands every item's
-// destination to a sink.  Within a chunk a warp owns a contiguous segment and
-// takes 32 items at a time, so the rank is: earlier warps' counts of the bin
-// + this warp's count so far + the earlier lanes with the same bin.
+// destination to a sink.  A single chunk (up to kBinSingle items) needs no
+// count kernel.  Within a chunk a warp owns a contiguous segment and takes 32
+// items at a time, so the rank is: earlier warps' counts of the bin + this
+// warp's count so far + the earlier lanes with the same bin.
 #pragma once
 
 #include "gc_internal.h"
@@ -21,15 +22,19 @@ constexpr int kBinWarps = kBinThreads / 32;
 constexpr uint32_t kMaxBins = 2048;
 constexpr uint32_t kBinChunks = 128;   // most chunks: every CTA reads all chunks' counts
 constexpr uint32_t kBinMinChunk = 1024;
+constexpr uint32_t kBinSingle = 4096;  // items that one CTA places alone
 
 inline uint32_t bin_chunk_elems(size_t n)
 {
+    if (n <= kBinSingle) return kBinSingle;
     const size_t even = gch::align_up(gch::ceil_div(n, size_t(kBinChunks)), size_t(kBinThreads));
     return uint32_t(even > kBinMinChunk ? even : kBinMinChunk);
 }
 inline uint32_t bin_chunks(size_t n) { return uint32_t(gch::ceil_div(n, size_t(bin_chunk_elems(n)))); }
 
-// Exclusive scan of one value per thread over the CTA; total to every thread.
+// Exclusive scan of one value per thread over THREADS threads; total to every
+// thread.  Between two uses lies a barrier.
+template <int THREADS>
 __device__ __forceinline__ uint32_t bin_block_scan(uint32_t v, uint32_t *s_warp, uint32_t &total)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -44,16 +49,16 @@ __device__ __forceinline__ uint32_t bin_block_scan(uint32_t v, uint32_t *s_warp,
     uint32_t before = 0u;
     total = 0u;
 #pragma unroll
-    for (int w = 0; w < kBinWarps; ++w) {
+    for (int w = 0; w < THREADS / 32; ++w) {
         const uint32_t c = s_warp[w];
         if (w < warp) before += c;
         total += c;
     }
-    __syncthreads();
     return before + incl - v;
 }
 
 // Source: bin(i) in [0, bins], where `bins` marks an item that goes nowhere.
+// Counts are written bin-major, counts[b * chunks + c].
 template <class Source>
 __global__ void __launch_bounds__(kBinThreads)
 bin_count_kernel(Source src, uint32_t n, uint32_t chunk, uint32_t bins, uint32_t *__restrict__ counts)
@@ -64,67 +69,96 @@ bin_count_kernel(Source src, uint32_t n, uint32_t chunk, uint32_t bins, uint32_t
     const uint32_t first = blockIdx.x * chunk, last = min(n - first, chunk) + first;
     for (uint32_t i = first + threadIdx.x; i < last; i += kBinThreads) {
         const uint32_t b = src.bin(i);
+        src.visit(i);
         if (b < bins) atomicAdd(&s_hist[b], 1u);
     }
     __syncthreads();
     for (uint32_t b = threadIdx.x; b < bins; b += kBinThreads)
-        counts[size_t(blockIdx.x) * bins + b] = s_hist[b];
+        counts[size_t(b) * gridDim.x + blockIdx.x] = s_hist[b];
 }
 
-// Sink: place(i, destination), drop(i); starts(b, start, count) once per bin
-// and end(total) once, by CTA 0.  Dynamic shared memory: kBinWarps * bins
-// words.
+struct BinSmem {
+    uint32_t all[kMaxBins];     // items of each bin, then where the chunk's first goes
+    uint32_t before[kMaxBins];  // of those, in earlier chunks
+    uint32_t warp[kBinWarps];
+};
+
+// Places chunk `index` of `chunks` (bin_place_kernel); s_cnt: kBinWarps * bins
+// words of shared memory.
 template <class Source, class Sink>
-__global__ void __launch_bounds__(kBinThreads)
-bin_place_kernel(Source src, Sink sink, uint32_t n, uint32_t chunk, uint32_t chunks, uint32_t bins,
-                 uint32_t align, const uint32_t *__restrict__ counts)
+__device__ __forceinline__ void bin_place_chunk(const Source &src, const Sink &sink, uint32_t n, uint32_t chunk,
+                                                uint32_t chunks, uint32_t index, uint32_t bins, uint32_t align,
+                                                const uint32_t *counts, uint32_t *s_cnt, BinSmem &sm)
 {
-    extern __shared__ uint32_t s_cnt[];  // [kBinWarps][bins]
-    __shared__ uint32_t s_warp[kBinWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     for (uint32_t i = tid; i < kBinWarps * bins; i += kBinThreads) s_cnt[i] = 0u;
     __syncthreads();
 
-    const uint32_t first = blockIdx.x * chunk, size = n > first ? min(n - first, chunk) : 0u;
-    const uint32_t segment = chunk / kBinWarps;  // a multiple of 32
+    const uint32_t first = index * chunk, size = n > first ? min(n - first, chunk) : 0u;
+    const uint32_t segment = ((size + kBinThreads - 1) / kBinThreads) * 32u;  // per warp
     const uint32_t seg_lo = min(size, uint32_t(warp) * segment), seg_hi = min(size, seg_lo + segment);
     uint32_t *mine = s_cnt + size_t(warp) * bins;
     for (uint32_t i = seg_lo + lane; i < seg_hi; i += 32) {
         const uint32_t b = src.bin(first + i);
+        if (chunks == 1) src.visit(first + i);
         if (b < bins) atomicAdd(&mine[b], 1u);
     }
     __syncthreads();
 
-    // Per bin: items in earlier chunks and in all chunks; starts of the bins
-    // by a scan over their rounded-up totals; then each warp's first
-    // destination.
+    // Per bin: items in all chunks and in earlier ones.  A warp reads one
+    // bin's counts at a time, consecutive chunks on consecutive lanes.
+    if (chunks == 1) {
+        for (uint32_t b = tid; b < bins; b += kBinThreads) {
+            uint32_t all = 0u;
+#pragma unroll
+            for (int w = 0; w < kBinWarps; ++w) all += s_cnt[size_t(w) * bins + b];
+            sm.all[b] = all;
+            sm.before[b] = 0u;
+        }
+    } else {
+        for (uint32_t b = warp; b < bins; b += kBinWarps) {
+            uint32_t all = 0u, before = 0u;
+#pragma unroll
+            for (uint32_t c = 0; c < kBinChunks; c += 32) {
+                const uint32_t at = c + lane;
+                const uint32_t v = at < chunks ? counts[size_t(b) * chunks + at] : 0u;
+                all += v;
+                before += at < index ? v : 0u;
+            }
+            all = __reduce_add_sync(0xffffffffu, all);
+            before = __reduce_add_sync(0xffffffffu, before);
+            if (lane == 0) {
+                sm.all[b] = all;
+                sm.before[b] = before;
+            }
+        }
+    }
+    __syncthreads();
+
+    // Starts of the bins by a scan over their rounded-up totals, then each
+    // warp's first destination.
     const uint32_t per = (bins + kBinThreads - 1) / kBinThreads;
     const uint32_t lo = min(bins, uint32_t(tid) * per), hi = min(bins, lo + per);
-    uint32_t sum = 0u;
+    uint32_t sum = 0u, total;
+    for (uint32_t b = lo; b < hi; ++b) sum += (sm.all[b] + align - 1u) / align * align;
+    uint32_t start = bin_block_scan<kBinThreads>(sum, sm.warp, total);
     for (uint32_t b = lo; b < hi; ++b) {
-        uint32_t all = 0u;
-        for (uint32_t c = 0; c < chunks; ++c) all += counts[size_t(c) * bins + b];
-        sum += (all + align - 1u) / align * align;
+        const uint32_t all = sm.all[b];
+        if (index == 0) sink.start(b, start, all);
+        sm.all[b] = start + sm.before[b];
+        start += (all + align - 1u) / align * align;
     }
-    uint32_t total;
-    uint32_t start = bin_block_scan(sum, s_warp, total);
-    for (uint32_t b = lo; b < hi; ++b) {
-        uint32_t all = 0u, before = 0u;
-        for (uint32_t c = 0; c < chunks; ++c) {
-            const uint32_t v = counts[size_t(c) * bins + b];
-            if (c < blockIdx.x) before += v;
-            all += v;
-        }
-        if (blockIdx.x == 0) sink.start(b, start, all);
-        uint32_t at = start + before;
+    if (index == 0 && tid == 0) sink.end(total);
+    __syncthreads();
+    for (uint32_t b = tid; b < bins; b += kBinThreads) {
+        uint32_t at = sm.all[b];
+#pragma unroll
         for (int w = 0; w < kBinWarps; ++w) {
             const uint32_t v = s_cnt[size_t(w) * bins + b];
             s_cnt[size_t(w) * bins + b] = at;
             at += v;
         }
-        start += (all + align - 1u) / align * align;
     }
-    if (blockIdx.x == 0 && tid == 0) sink.end(total);
     __syncthreads();
 
     for (uint32_t base = seg_lo; base < seg_hi; base += 32) {
@@ -147,11 +181,31 @@ bin_place_kernel(Source src, Sink sink, uint32_t n, uint32_t chunk, uint32_t chu
     }
 }
 
+// Sink: place(i, destination), drop(i); start(b, start, count) once per bin
+// and end(total) once, by CTA 0.  Dynamic shared memory: kBinWarps * bins
+// words.
+template <class Source, class Sink>
+__global__ void __launch_bounds__(kBinThreads)
+bin_place_kernel(Source src, Sink sink, uint32_t n, uint32_t chunk, uint32_t bins, uint32_t align,
+                 const uint32_t *__restrict__ counts)
+{
+    extern __shared__ uint32_t s_cnt[];
+    __shared__ BinSmem sm;
+    bin_place_chunk(src, sink, n, chunk, gridDim.x, blockIdx.x, bins, align, counts, s_cnt, sm);
+}
+
 template <class Source>
 cudaError_t launch_bin_count(const Source &src, uint32_t n, uint32_t bins, uint32_t *counts, cudaStream_t s)
 {
+    if (bin_chunks(n) == 1) return cudaSuccess;
     bin_count_kernel<Source><<<bin_chunks(n), kBinThreads, 0, s>>>(src, n, bin_chunk_elems(n), bins, counts);
     return cudaGetLastError();
+}
+
+// Raises a kernel's shared-memory limit to what the most bins need, once per device.
+inline bool bin_place_smem(const void *kernel)
+{
+    return gch::persistent_grid(kernel, kBinThreads, size_t(kBinWarps) * kMaxBins * sizeof(uint32_t), 1) > 0;
 }
 
 template <class Source, class Sink>
@@ -159,13 +213,9 @@ cudaError_t launch_bin_place(const Source &src, const Sink &sink, uint32_t n, ui
                              uint32_t align, const uint32_t *counts, cudaStream_t s)
 {
     auto kernel = bin_place_kernel<Source, Sink>;
-    const size_t smem = size_t(kBinWarps) * bins * sizeof(uint32_t);
-    const size_t most = size_t(kBinWarps) * kMaxBins * sizeof(uint32_t);
-    // Raises the kernel's shared-memory limit, once per device.
-    if (gch::persistent_grid(reinterpret_cast<const void *>(kernel), kBinThreads, most, 1) <= 0)
-        return cudaErrorInvalidConfiguration;
-    kernel<<<bin_chunks(n), kBinThreads, smem, s>>>(src, sink, n, bin_chunk_elems(n), bin_chunks(n), bins,
-                                                   align, counts);
+    if (!bin_place_smem(reinterpret_cast<const void *>(kernel))) return cudaErrorInvalidConfiguration;
+    kernel<<<bin_chunks(n), kBinThreads, size_t(kBinWarps) * bins * sizeof(uint32_t), s>>>(
+        src, sink, n, bin_chunk_elems(n), bins, align, counts);
     return cudaGetLastError();
 }
 
