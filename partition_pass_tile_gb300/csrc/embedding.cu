@@ -18,8 +18,11 @@ namespace {
 using namespace gcd;
 
 constexpr int kRowThreads = 256;
+constexpr uint32_t kFull = 0xffffffffu;
 constexpr uint32_t kBlock = 32;     // sorted positions per block
-constexpr int kAhead = 8;           // rows loaded at a time
+#ifndef GC_SUMS_CTAS
+#define GC_SUMS_CTAS 4
+#endif
 constexpr int kLookups = 4;         // rows per thread of a lookup
 constexpr size_t kZeroBytes = 32768;  // zeroed per CTA, about
 
@@ -91,27 +94,34 @@ struct TokenSink {
     __device__ __forceinline__ void drop(uint32_t) const {}
 };
 
-// All passes of a short sort, and the clearing of `seen`, by one CTA.
+// A short sort, and the clearing of `seen`, by one CTA: the items stay in
+// shared memory between the passes.
+struct TokenSortSmem {
+    BinSmem bins;
+    uint2 items[2][kBinSingle];
+    uint32_t cnt[kBinWarps << 9];
+};
+
 __global__ void __launch_bounds__(kBinThreads)
-token_sort_kernel(const void *ids, bool wide, uint32_t n, uint32_t vocab, uint32_t digit, int passes, uint2 *a,
-                  uint2 *b, uint8_t *seen)
+token_sort_kernel(const void *ids, bool wide, uint32_t n, uint32_t vocab, uint32_t digit, int passes, uint2 *sorted,
+                  uint8_t *seen)
 {
-    extern __shared__ uint32_t s_cnt[];
-    __shared__ BinSmem sm;
-    if (seen != nullptr) {
-        // `seen` has room for whole words.
-        for (uint32_t i = threadIdx.x; i < (vocab + 15u) / 16u; i += kBinThreads)
+    extern __shared__ __align__(16) uint8_t token_smem[];
+    TokenSortSmem &sm = *reinterpret_cast<TokenSortSmem *>(token_smem);
+    if (seen != nullptr)
+        for (uint32_t i = threadIdx.x; i < (vocab + 15u) / 16u; i += kBinThreads)  // `seen` has room for whole words
             reinterpret_cast<uint4 *>(seen)[i] = make_uint4(0u, 0u, 0u, 0u);
-        __syncthreads();
-    }
+    for (uint32_t i = threadIdx.x; i < n; i += kBinThreads) sm.items[0][i] = make_uint2(load_id(ids, wide, i, vocab), i);
+    __syncthreads();
+    if (seen != nullptr)
+        for (uint32_t i = threadIdx.x; i < n; i += kBinThreads)
+            if (sm.items[0][i].x < vocab) seen[sm.items[0][i].x] = 1;
     for (int p = 0; p < passes; ++p) {
-        const TokenPass src{ids, a, seen, p == 0, wide, vocab, uint32_t(p) * digit, (1u << digit) - 1u};
-        const TokenSink sink{src, b};
-        bin_place_chunk(src, sink, n, n, 1, 0, 1u << digit, 1u, nullptr, s_cnt, sm);
+        const TokenPass src{nullptr, sm.items[p & 1], nullptr, false, wide, vocab, uint32_t(p) * digit,
+                            (1u << digit) - 1u};
+        const TokenSink sink{src, p + 1 < passes ? sm.items[(p & 1) ^ 1] : sorted};
+        bin_place_chunk(src, sink, n, n, 1, 0, 1u << digit, 1u, nullptr, sm.cnt, sm.bins);
         __syncthreads();
-        uint2 *t = a;
-        a = b;
-        b = t;
     }
 }
 
@@ -141,8 +151,10 @@ struct GradOut {
 // threads, summed run by run.  edges: two rows per block, the sum of its
 // first run where that began before the block, and of its last where that
 // began in the block and goes on.  The other CTAs zero rows of absent tokens.
-template <class T, class O, int N>
-__global__ void __launch_bounds__(kRowThreads)
+// The rows of the next kAhead positions, and what they are added to, are
+// loaded while the ones before are summed.
+template <class T, class O, int N, bool ADD>
+__global__ void __launch_bounds__(kRowThreads, GC_SUMS_CTAS)
 token_sums_kernel(const uint2 *__restrict__ sorted, uint32_t n, const T *__restrict__ g, size_t g_stride,
                   uint32_t width, float *__restrict__ edges, GradOut out, uint32_t sums, uint32_t zero_rows)
 {
@@ -157,51 +169,70 @@ token_sums_kernel(const uint2 *__restrict__ sorted, uint32_t n, const T *__restr
         }
         return;
     }
+    // Keys of the block's positions between those of its neighbours, and the
+    // positions; none: the end of the tokens in range.
+    __shared__ uint32_t s_key[kRowThreads / 32][kBlock + 2], s_at[kRowThreads / 32][kBlock];
     const uint32_t parts = (width + columns - 1) / columns;  // of a row, neighbours in the grid
-    const uint32_t block = blockIdx.x / parts * blockDim.y + threadIdx.y;
+    const uint32_t block = blockIdx.x / parts * blockDim.y + threadIdx.y, first = block * kBlock;
+    const uint32_t none = out.vocab;
+    uint32_t *key = s_key[threadIdx.y], *at = s_at[threadIdx.y];
+    for (uint32_t j = threadIdx.x; j < kBlock + 2; j += blockDim.x) {
+        const uint32_t i = first + j - 1;  // wraps before the first
+        const uint2 item = i < n ? sorted[i] : make_uint2(none, 0u);
+        key[j] = item.x;
+        if (j >= 1 && j <= kBlock) at[j - 1] = item.y;
+    }
+    __syncthreads();
     const uint32_t c = (blockIdx.x % parts) * columns + threadIdx.x * N;
-    if (block >= (n + kBlock - 1) / kBlock || c >= width) return;
-    const uint32_t first = block * kBlock, last = min(n, first + kBlock);
-    const uint32_t none = ~0u;
-    const uint32_t prev = first > 0 ? sorted[first - 1].x : none, next = last < n ? sorted[last].x : none;
-    float sum[N] = {};
-    uint32_t key = sorted[first].x;
-    bool began = key != prev;
-    auto flush = [&](bool goes_on) {
-        if (key >= out.vocab) return;
-        if (began && !goes_on) {
-            put_sum<O, N>(rows + size_t(key) * out.stride + c, sum, out.scale, out.accumulate);
-        } else {
-            Piece<float, N> e;
-#pragma unroll
-            for (int k = 0; k < N; ++k) e.v[k] = sum[k];
-            store_piece<float, N>(edges + (size_t(block) * 2 + (began ? 1 : 0)) * width + c, e);
-        }
-    };
-    for (uint32_t base = first; base < last; base += kAhead) {
-        uint2 item[kAhead];
-        Piece<T, N> x[kAhead];
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j) item[j] = base + j < last ? sorted[base + j] : make_uint2(out.vocab, 0u);
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j)
-            if (item[j].x < out.vocab) x[j] = load_piece<T, N>(g + size_t(item[j].y) * g_stride + c);
+    if (key[1] == none || c >= width) return;
+    constexpr int kAhead = ADD ? 4 : 8;
+    Piece<T, N> x[kAhead];
+    Piece<O, N> old[ADD ? kAhead : 1];
+    auto load = [&](uint32_t base) {
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
-            if (base + j >= last) break;
-            if (item[j].x != key) {
-                flush(false);
-                key = item[j].x;
-                began = true;
+            const uint32_t k = base + j < kBlock ? key[base + j + 1] : none;
+            if (k == none) continue;
+            x[j] = load_piece<T, N>(g + size_t(at[base + j]) * g_stride + c);
+            if (ADD && key[base + j + 2] != k) old[ADD ? j : 0] = load_piece<O, N>(rows + size_t(k) * out.stride + c);
+        }
+    };
+    Piece<float, N> sum{};
+    bool began = key[0] != key[1];
+    load(0);
+    for (uint32_t base = 0; base < kBlock; base += kAhead) {
+        Piece<T, N> now[kAhead];
+        Piece<O, N> add[ADD ? kAhead : 1];
 #pragma unroll
-                for (int k = 0; k < N; ++k) sum[k] = 0.0f;
+        for (int j = 0; j < kAhead; ++j) {
+            now[j] = x[j];
+            if (ADD) add[j] = old[j];
+        }
+        load(base + kAhead);
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            const uint32_t k = key[base + j + 1];
+            if (k == none) return;
+#pragma unroll
+            for (int e = 0; e < N; ++e) sum.v[e] += row_to_float(now[j].v[e]);
+            const bool ends = key[base + j + 2] != k;
+            if (ends && began) {
+                Piece<O, N> o;
+#pragma unroll
+                for (int e = 0; e < N; ++e) {
+                    const float r = out.scale * sum.v[e];
+                    o.v[e] = row_from_float<O>(ADD ? r + row_to_float(add[ADD ? j : 0].v[e]) : r);
+                }
+                store_piece<O, N>(rows + size_t(k) * out.stride + c, o);
+            } else if (ends || base + j + 1 == kBlock) {
+                store_piece<float, N>(edges + (size_t(block) * 2 + (began ? 1 : 0)) * width + c, sum);
             }
-            if (key < out.vocab)
-#pragma unroll
-                for (int k = 0; k < N; ++k) sum[k] += row_to_float(x[j].v[k]);
+            if (ends) {
+                sum = Piece<float, N>{};
+                began = true;
+            }
         }
     }
-    flush(key == next);
 }
 
 // Tokens whose run crosses blocks: the block in which it began adds up its
@@ -215,17 +246,21 @@ token_join_kernel(const uint2 *__restrict__ sorted, uint32_t n, uint32_t width, 
     const uint32_t block = blockIdx.x / parts * blockDim.y + threadIdx.y;
     const uint32_t c = (blockIdx.x % parts) * columns + threadIdx.x * N;
     const uint32_t blocks = (n + kBlock - 1) / kBlock;
-    if (block + 1 >= blocks || c >= width) return;
+    if (block + 1 >= blocks) return;  // as does its whole warp
     const uint32_t first = block * kBlock, next = first + kBlock;
     const uint32_t key = sorted[next - 1].x;
     if (key >= out.vocab || sorted[next].x != key || (first > 0 && sorted[first - 1].x == key)) return;
-    // The last block that the run reaches: the last whose first key is it.
-    uint32_t lo = block + 1, hi = blocks;
-    while (hi - lo > 1) {
-        const uint32_t mid = (lo + hi) / 2;
-        if (sorted[mid * kBlock].x == key) lo = mid;
-        else hi = mid;
+    // The blocks whose first key is it: the run reaches them.
+    uint32_t more = 1;
+    for (bool on = true; on; ) {
+        const uint32_t b = block + more + 1 + (threadIdx.x & 31);
+        const uint32_t same = __ballot_sync(kFull, b < blocks && sorted[size_t(min(b, blocks - 1)) * kBlock].x == key);
+        more += uint32_t(__ffs(~same) == 0 ? 32 : __ffs(~same) - 1);
+        on = same == kFull;
     }
+    if (c >= width) return;
+    const uint32_t lo = block + more;
+    constexpr int kAhead = 8;
     const float *e = edges + (size_t(block) * 2 + 1) * width + c;
     Piece<float, N> sum = load_piece<float, N>(e);
     e += width;
@@ -263,7 +298,7 @@ GradLayout grad_layout(size_t n, size_t vocab, size_t width)
     l.items_a = 0;
     l.items_b = items;
     l.table = 2 * items;
-    l.seen = l.table + gch::align_up(size_t(bin_chunks(n)) * 512 * 4, 256);
+    l.seen = l.table + gch::align_up(bin_table_bytes(n, 512), 256);
     l.edges = l.seen + gch::align_up(vocab, 256);
     l.total = l.edges + gch::align_up(gch::ceil_div(n, size_t(kBlock)) * 2 * width * 4, 256) + 256;
     return l;
@@ -280,10 +315,11 @@ cudaError_t run_grad_rows(const uint2 *sorted, uint32_t n, const void *g, size_t
     const size_t zero_rows = gch::align_up(gch::ceil_div(kZeroBytes, width * sizeof(O)), threads.y);
     const size_t zeros = out.accumulate ? 0 : gch::ceil_div(out.vocab, zero_rows);
     if (sums + zeros > 0x7fffffffu) return cudaErrorInvalidConfiguration;
+    auto kernel = out.accumulate ? token_sums_kernel<T, O, N, true> : token_sums_kernel<T, O, N, false>;
     if (sums + zeros > 0)
-        token_sums_kernel<T, O, N><<<uint32_t(sums + zeros), threads, 0, s>>>(
-            sorted, n, static_cast<const T *>(g), g_stride, uint32_t(width), edges, out, uint32_t(sums),
-            uint32_t(zero_rows));
+        kernel<<<uint32_t(sums + zeros), threads, 0, s>>>(sorted, n, static_cast<const T *>(g), g_stride,
+                                                          uint32_t(width), edges, out, uint32_t(sums),
+                                                          uint32_t(zero_rows));
     if (blocks > 1)
         token_join_kernel<O, N><<<uint32_t(sums), threads, 0, s>>>(sorted, n, uint32_t(width), edges, out);
     return cudaGetLastError();
@@ -355,9 +391,11 @@ cudaError_t launch_embedding_grad(const void *g, size_t g_stride, gc_row_dtype g
     const int bits = key_bits(vocab), passes = int(ceil_div(bits, 9)), digit = int(ceil_div(bits, passes));
     cudaError_t e = cudaSuccess;
     if (n > 0 && gcd::bin_chunks(n) == 1) {
-        if (!gcd::bin_place_smem(reinterpret_cast<const void *>(token_sort_kernel))) return cudaErrorInvalidConfiguration;
-        token_sort_kernel<<<1, gcd::kBinThreads, (sizeof(uint32_t) * gcd::kBinWarps) << digit, s>>>(
-            ids, wide, n, vocab, uint32_t(digit), passes, items[0], items[1], seen);
+        if (persistent_grid(reinterpret_cast<const void *>(token_sort_kernel), gcd::kBinThreads, sizeof(TokenSortSmem),
+                            1) <= 0)
+            return cudaErrorInvalidConfiguration;
+        token_sort_kernel<<<1, gcd::kBinThreads, sizeof(TokenSortSmem), s>>>(
+            ids, wide, n, vocab, uint32_t(digit), passes, items[passes & 1], seen);
         e = cudaGetLastError();
     } else {
         if (seen) e = cudaMemsetAsync(seen, 0, vocab, s);

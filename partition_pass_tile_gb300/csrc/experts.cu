@@ -186,10 +186,16 @@ expert_small_kernel(ExpertSource src, ExpertSink sink, uint32_t npairs, uint32_t
 }
 
 // The rows of kAhead choices are loaded together.
-constexpr int kAhead = 8;
+#ifndef GC_COMBINE_AHEAD
+#define GC_COMBINE_AHEAD 4
+#endif
+#ifndef GC_COMBINE_CTAS
+#define GC_COMBINE_CTAS 4
+#endif
+constexpr int kAhead = GC_COMBINE_AHEAD;
 
 template <class T, int N>
-__global__ void __launch_bounds__(kRowThreads)
+__global__ void __launch_bounds__(kRowThreads, GC_COMBINE_CTAS)
 expert_combine_kernel(const T *__restrict__ y, size_t y_stride, uint32_t rows, const int32_t *__restrict__ slots,
                       const float *__restrict__ weights, uint32_t tokens, uint32_t topk, uint32_t pieces,
                       T *__restrict__ out, size_t out_stride)
@@ -328,7 +334,7 @@ namespace gch {
 
 size_t expert_workspace_bytes(size_t npairs, uint32_t experts)
 {
-    return npairs > kSmallPairs ? align_up(size_t(gcd::bin_chunks(npairs)) * experts * sizeof(uint32_t), 256) : 256;
+    return npairs > kSmallPairs ? align_up(gcd::bin_table_bytes(npairs, experts), 256) : 256;
 }
 
 cudaError_t launch_expert_dispatch(const void *ids, bool wide, uint32_t npairs, uint32_t topk, uint32_t experts,

@@ -31,6 +31,8 @@ inline uint32_t bin_chunk_elems(size_t n)
     return uint32_t(even > kBinMinChunk ? even : kBinMinChunk);
 }
 inline uint32_t bin_chunks(size_t n) { return uint32_t(gch::ceil_div(n, size_t(bin_chunk_elems(n)))); }
+__host__ __device__ inline uint32_t bin_count_stride(uint32_t chunks) { return (chunks + 3u) / 4u * 4u; }
+inline size_t bin_table_bytes(size_t n, size_t bins) { return size_t(bin_count_stride(bin_chunks(n))) * bins * 4; }
 
 // Exclusive scan of one value per thread over THREADS threads; total to every
 // thread.  Between two uses lies a barrier.
@@ -58,7 +60,8 @@ __device__ __forceinline__ uint32_t bin_block_scan(uint32_t v, uint32_t *s_warp,
 }
 
 // Source: bin(i) in [0, bins], where `bins` marks an item that goes nowhere.
-// Counts are written bin-major, counts[b * chunks + c].
+// Counts are written bin-major, counts[b * bin_count_stride(chunks) + c], with
+// zeros up to the stride.
 template <class Source>
 __global__ void __launch_bounds__(kBinThreads)
 bin_count_kernel(Source src, uint32_t n, uint32_t chunk, uint32_t bins, uint32_t *__restrict__ counts)
@@ -73,8 +76,12 @@ bin_count_kernel(Source src, uint32_t n, uint32_t chunk, uint32_t bins, uint32_t
         if (b < bins) atomicAdd(&s_hist[b], 1u);
     }
     __syncthreads();
-    for (uint32_t b = threadIdx.x; b < bins; b += kBinThreads)
-        counts[size_t(b) * gridDim.x + blockIdx.x] = s_hist[b];
+    const uint32_t stride = bin_count_stride(gridDim.x);
+    for (uint32_t b = threadIdx.x; b < bins; b += kBinThreads) {
+        counts[size_t(b) * stride + blockIdx.x] = s_hist[b];
+        if (blockIdx.x == 0)
+            for (uint32_t c = gridDim.x; c < stride; ++c) counts[size_t(b) * stride + c] = 0u;
+    }
 }
 
 struct BinSmem {
@@ -105,8 +112,8 @@ __device__ __forceinline__ void bin_place_chunk(const Source &src, const Sink &s
     }
     __syncthreads();
 
-    // Per bin: items in all chunks and in earlier ones.  A warp reads one
-    // bin's counts at a time, consecutive chunks on consecutive lanes.
+    // Per bin: items in all chunks and in earlier ones.  A group of lanes
+    // reads one bin's counts, four chunks to a lane at a time.
     if (chunks == 1) {
         for (uint32_t b = tid; b < bins; b += kBinThreads) {
             uint32_t all = 0u;
@@ -116,18 +123,27 @@ __device__ __forceinline__ void bin_place_chunk(const Source &src, const Sink &s
             sm.before[b] = 0u;
         }
     } else {
-        for (uint32_t b = warp; b < bins; b += kBinWarps) {
+        uint32_t group = 1;
+        while (group < 32 && bins * group * 2 <= kBinThreads) group <<= 1;
+        const uint32_t quads = bin_count_stride(chunks) / 4, part = uint32_t(tid) & (group - 1);
+        for (uint32_t base = 0; base < bins; base += kBinThreads / group) {  // the same for all lanes
+            const uint32_t b = base + uint32_t(tid) / group;
+            const uint4 *row = reinterpret_cast<const uint4 *>(counts) + size_t(b) * quads;
             uint32_t all = 0u, before = 0u;
-#pragma unroll
-            for (uint32_t c = 0; c < kBinChunks; c += 32) {
-                const uint32_t at = c + lane;
-                const uint32_t v = at < chunks ? counts[size_t(b) * chunks + at] : 0u;
-                all += v;
-                before += at < index ? v : 0u;
+            if (b < bins)
+#pragma unroll 8
+                for (uint32_t c = part; c < quads; c += group) {
+                    const uint4 v = row[c];
+                    all += v.x + v.y + v.z + v.w;
+                    const uint32_t left = index > 4 * c ? index - 4 * c : 0u;  // chunks of the four before mine
+                    before += (left > 0 ? v.x : 0u) + (left > 1 ? v.y : 0u) + (left > 2 ? v.z : 0u) +
+                              (left > 3 ? v.w : 0u);
+                }
+            for (uint32_t o = 1; o < group; o <<= 1) {
+                all += __shfl_xor_sync(0xffffffffu, all, o);
+                before += __shfl_xor_sync(0xffffffffu, before, o);
             }
-            all = __reduce_add_sync(0xffffffffu, all);
-            before = __reduce_add_sync(0xffffffffu, before);
-            if (lane == 0) {
+            if (b < bins && part == 0) {
                 sm.all[b] = all;
                 sm.before[b] = before;
             }
