@@ -9,8 +9,11 @@
 // its block is a row of the result, the ends of one that does not are kept
 // and joined by a last kernel.  Rows of absent tokens are zeroed beside the
 // sums.  Every sum's order depends on the ids alone.
+#include <algorithm>
+
 #include "gc_binsort.cuh"
 #include "gc_internal.h"
+#include "gc_pipe.cuh"
 #include "gc_rows.cuh"
 
 namespace {
@@ -18,13 +21,19 @@ namespace {
 using namespace gcd;
 
 constexpr int kRowThreads = 256;
-constexpr uint32_t kFull = 0xffffffffu;
 constexpr uint32_t kBlock = 32;     // sorted positions per block
 #ifndef GC_SUMS_CTAS
 #define GC_SUMS_CTAS 4
 #endif
 constexpr int kLookups = 4;         // rows per thread of a lookup
-constexpr size_t kZeroBytes = 32768;  // zeroed per CTA, about
+constexpr size_t kZeroBytes = 32768;  // zeroed per CTA of the sums, about
+// A bulk sum's CTA holds kBlock rows of up to this many bytes per row of
+// threads, 64 KiB in all: three CTAs to an SM.
+constexpr uint32_t kSliceBytes = 2048;
+// Zeroed beside a count and a place kernel, whose CTAs wait for memory most
+// of the time: about what an idle GPU writes meanwhile.
+constexpr size_t kCountZeros = size_t(20) << 20, kPlaceZeros = size_t(44) << 20;
+constexpr uint32_t kZeroCtas = 300;
 
 // tx threads across a row's pieces, kRowThreads / tx rows.
 dim3 row_block(size_t pieces)
@@ -94,8 +103,36 @@ struct TokenSink {
     __device__ __forceinline__ void drop(uint32_t) const {}
 };
 
-// A short sort, and the clearing of `seen`, by one CTA: the items stay in
-// shared memory between the passes.
+// Rows [lo, hi) of the result, zeroed a warp to a row; with `seen`, only those
+// of absent tokens.
+struct ZeroRows {
+    uint8_t *rows;
+    size_t stride, bytes;  // of a row
+    uint32_t piece;        // bytes to a store
+    const uint8_t *seen;
+    uint32_t lo, hi;
+    template <class P>
+    __device__ __forceinline__ void row(uint8_t *p) const
+    {
+        for (size_t i = threadIdx.x & 31; i < bytes / sizeof(P); i += 32) reinterpret_cast<P *>(p)[i] = P{};
+    }
+    __device__ __forceinline__ void run(uint32_t cta, uint32_t ctas) const
+    {
+        const uint32_t warps = blockDim.x * blockDim.y / 32, warp = (threadIdx.y * blockDim.x + threadIdx.x) / 32;
+        const uint64_t first = lo + uint64_t(cta) * warps + warp;
+        for (uint64_t v = first; v < hi; v += uint64_t(ctas) * warps) {
+            if (seen != nullptr && seen[v]) continue;
+            uint8_t *p = rows + v * stride;
+            if (piece == 16) row<uint4>(p);
+            else if (piece == 8) row<uint2>(p);
+            else if (piece == 4) row<uint32_t>(p);
+            else row<uint16_t>(p);
+        }
+    }
+};
+
+// A short sort by the first CTA, whose items stay in shared memory between
+// the passes; the others zero the result.
 struct TokenSortSmem {
     BinSmem bins;
     uint2 items[2][kBinSingle];
@@ -104,18 +141,17 @@ struct TokenSortSmem {
 
 __global__ void __launch_bounds__(kBinThreads)
 token_sort_kernel(const void *ids, bool wide, uint32_t n, uint32_t vocab, uint32_t digit, int passes, uint2 *sorted,
-                  uint8_t *seen)
+                  uint32_t *header, ZeroRows zero)
 {
     extern __shared__ __align__(16) uint8_t token_smem[];
     TokenSortSmem &sm = *reinterpret_cast<TokenSortSmem *>(token_smem);
-    if (seen != nullptr)
-        for (uint32_t i = threadIdx.x; i < (vocab + 15u) / 16u; i += kBinThreads)  // `seen` has room for whole words
-            reinterpret_cast<uint4 *>(seen)[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (blockIdx.x > 0) {
+        zero.run(blockIdx.x - 1, gridDim.x - 1);
+        return;
+    }
+    if (threadIdx.x < kHeaderBytes / 4) header[threadIdx.x] = 0u;
     for (uint32_t i = threadIdx.x; i < n; i += kBinThreads) sm.items[0][i] = make_uint2(load_id(ids, wide, i, vocab), i);
     __syncthreads();
-    if (seen != nullptr)
-        for (uint32_t i = threadIdx.x; i < n; i += kBinThreads)
-            if (sm.items[0][i].x < vocab) seen[sm.items[0][i].x] = 1;
     for (int p = 0; p < passes; ++p) {
         const TokenPass src{nullptr, sm.items[p & 1], nullptr, false, wide, vocab, uint32_t(p) * digit,
                             (1u << digit) - 1u};
@@ -125,54 +161,35 @@ token_sort_kernel(const void *ids, bool wide, uint32_t n, uint32_t vocab, uint32
     }
 }
 
-template <class O, int N>
-__device__ __forceinline__ void put_sum(O *dst, const float (&sum)[N], float scale, bool accumulate)
-{
-    Piece<O, N> o;
-    if (accumulate) o = load_piece<O, N>(dst);
-#pragma unroll
-    for (int k = 0; k < N; ++k) {
-        const float r = scale * sum[k];
-        o.v[k] = row_from_float<O>(accumulate ? r + row_to_float(o.v[k]) : r);
-    }
-    store_piece<O, N>(dst, o);
-}
-
 struct GradOut {
     void *rows;
     size_t stride;
     float scale;
     bool accumulate;
-    const uint8_t *seen;
     uint32_t vocab;
 };
 
 // CTAs below `sums`: blocks of kBlock sorted positions, one to a row of
 // threads, summed run by run.  edges: two rows per block, the sum of its
 // first run where that began before the block, and of its last where that
-// began in the block and goes on.  The other CTAs zero rows of absent tokens.
+// began in the block and goes on.  The other CTAs zero rows.
 // The rows of the next kAhead positions, and what they are added to, are
 // loaded while the ones before are summed.
 template <class T, class O, int N, bool ADD>
 __global__ void __launch_bounds__(kRowThreads, GC_SUMS_CTAS)
 token_sums_kernel(const uint2 *__restrict__ sorted, uint32_t n, const T *__restrict__ g, size_t g_stride,
-                  uint32_t width, float *__restrict__ edges, GradOut out, uint32_t sums, uint32_t zero_rows)
+                  uint32_t width, float *__restrict__ edges, GradOut out, uint32_t parts, uint32_t sums, ZeroRows zero)
 {
     O *rows = static_cast<O *>(out.rows);
     const uint32_t columns = blockDim.x * N;
     if (blockIdx.x >= sums) {
-        const uint32_t first = (blockIdx.x - sums) * zero_rows, last = min(out.vocab, first + zero_rows);
-        for (uint32_t v = first + threadIdx.y; v < last; v += blockDim.y) {
-            if (out.seen[v]) continue;
-            for (uint32_t c = threadIdx.x * N; c < width; c += columns)
-                store_piece<O, N>(rows + size_t(v) * out.stride + c, zero_piece<O, N>());
-        }
+        zero.run(blockIdx.x - sums, gridDim.x - sums);
         return;
     }
     // Keys of the block's positions between those of its neighbours, and the
     // positions; none: the end of the tokens in range.
     __shared__ uint32_t s_key[kRowThreads / 32][kBlock + 2], s_at[kRowThreads / 32][kBlock];
-    const uint32_t parts = (width + columns - 1) / columns;  // of a row, neighbours in the grid
+    // `parts` CTAs, neighbours in the grid, share a row
     const uint32_t block = blockIdx.x / parts * blockDim.y + threadIdx.y, first = block * kBlock;
     const uint32_t none = out.vocab;
     uint32_t *key = s_key[threadIdx.y], *at = s_at[threadIdx.y];
@@ -235,49 +252,159 @@ token_sums_kernel(const uint2 *__restrict__ sorted, uint32_t n, const T *__restr
     }
 }
 
+// The same where rows can be copied in bulk (16-byte aligned): the block's
+// rows are copied into shared memory by the TMA unit, all at once, so that
+// the whole block is in flight without registers; and the rows to be added to
+// are fetched to L2.  blockDim.x threads, N elements each, to a slice.
+template <class T, class O, int N, bool ADD>
+__global__ void __launch_bounds__(kRowThreads)
+token_bulk_sums_kernel(const uint2 *__restrict__ sorted, uint32_t n, const T *__restrict__ g, size_t g_stride,
+                       uint32_t width, float *__restrict__ edges, GradOut out, uint32_t parts, uint8_t *ws,
+                       uint64_t timeout_ns, uint32_t sums, ZeroRows zero)
+{
+    if (blockIdx.x >= sums) {
+        zero.run(blockIdx.x - sums, gridDim.x - sums);
+        return;
+    }
+    extern __shared__ __align__(16) uint8_t slice_smem[];
+    __shared__ uint32_t s_key[kRowThreads / 32][kBlock + 2], s_at[kRowThreads / 32][kBlock];
+    __shared__ uint64_t s_bar[kRowThreads / 32];
+    O *rows = static_cast<O *>(out.rows);
+    const uint32_t columns = blockDim.x * N, lane = threadIdx.x & 31;
+    const uint32_t block = blockIdx.x / parts * blockDim.y + threadIdx.y, first = block * kBlock;
+    const uint32_t none = out.vocab;
+    uint32_t *key = s_key[threadIdx.y], *at = s_at[threadIdx.y];
+    const uint32_t c0 = (blockIdx.x % parts) * columns, here = min(columns, width - c0);
+    T *slice = reinterpret_cast<T *>(slice_smem) + size_t(threadIdx.y) * kBlock * columns;
+    for (uint32_t j = threadIdx.x; j < kBlock + 2; j += blockDim.x) {
+        const uint32_t i = first + j - 1;  // wraps before the first
+        const uint2 item = i < n ? sorted[i] : make_uint2(none, 0u);
+        key[j] = item.x;
+        if (j >= 1 && j <= kBlock) at[j - 1] = item.y;
+    }
+    if (threadIdx.x == 0) {
+        mbar_init(&s_bar[threadIdx.y], 1u);
+        fence_barrier_init();
+    }
+    __syncthreads();
+    if (key[1] == none) return;
+    if (threadIdx.x < 32) {
+        // Lane j copies row j; the tokens in range come first.
+        const uint32_t k = key[lane + 1];
+        const uint32_t rows_in = uint32_t(__popc(__ballot_sync(kFullMask, k != none)));
+        if (lane == 0) mbar_arrive_expect_tx(&s_bar[threadIdx.y], rows_in * here * uint32_t(sizeof(T)));
+        __syncwarp();
+        if (k != none) {
+            bulk_load(slice + size_t(lane) * columns, g + size_t(at[lane]) * g_stride + c0, here * uint32_t(sizeof(T)),
+                      &s_bar[threadIdx.y]);
+            if (ADD && key[lane + 2] != k) {
+                const O *old = rows + size_t(k) * out.stride + c0;
+                for (uint32_t e = 0; e < here; e += 128 / sizeof(O)) asm volatile("prefetch.global.L2 [%0];" ::"l"(old + e));
+            }
+        }
+    }
+    mbar_wait(&s_bar[threadIdx.y], 0u, ws, timeout_ns);
+    const uint32_t c = threadIdx.x * N;
+    if (c >= here) return;
+    Piece<float, N> sum{};
+    bool began = key[0] != key[1];
+    constexpr int kAhead = 4;
+    for (uint32_t base = 0; base < kBlock; base += kAhead) {
+        Piece<O, N> old[ADD ? kAhead : 1];
+        if (ADD)
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j)
+                if (key[base + j + 1] != none && key[base + j + 2] != key[base + j + 1])
+                    old[ADD ? j : 0] = load_piece<O, N>(rows + size_t(key[base + j + 1]) * out.stride + c0 + c);
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            const uint32_t k = key[base + j + 1];
+            if (k == none) return;
+            const Piece<T, N> x = load_piece<T, N>(slice + size_t(base + j) * columns + c);
+#pragma unroll
+            for (int e = 0; e < N; ++e) sum.v[e] += row_to_float(x.v[e]);
+            const bool ends = key[base + j + 2] != k;
+            if (ends && began) {
+                Piece<O, N> o;
+#pragma unroll
+                for (int e = 0; e < N; ++e) {
+                    const float r = out.scale * sum.v[e];
+                    o.v[e] = row_from_float<O>(ADD ? r + row_to_float(old[ADD ? j : 0].v[e]) : r);
+                }
+                store_piece<O, N>(rows + size_t(k) * out.stride + c0 + c, o);
+            } else if (ends || base + j + 1 == kBlock) {
+                store_piece<float, N>(edges + (size_t(block) * 2 + (began ? 1 : 0)) * width + c0 + c, sum);
+            }
+            if (ends) {
+                sum = Piece<float, N>{};
+                began = true;
+            }
+        }
+    }
+}
+
 // Tokens whose run crosses blocks: the block in which it began adds up its
-// parts.
+// parts.  kJoiners rows of threads take a share of the blocks each, and the
+// shares are added in order.
+constexpr int kJoiners = 8;
+
 template <class O, int N>
 __global__ void __launch_bounds__(kRowThreads)
 token_join_kernel(const uint2 *__restrict__ sorted, uint32_t n, uint32_t width, const float *__restrict__ edges,
-                  GradOut out)
+                  GradOut out, uint32_t parts)
 {
-    const uint32_t columns = blockDim.x * N, parts = (width + columns - 1) / columns;
-    const uint32_t block = blockIdx.x / parts * blockDim.y + threadIdx.y;
-    const uint32_t c = (blockIdx.x % parts) * columns + threadIdx.x * N;
+    constexpr int kAhead = 8;
+    __shared__ Piece<float, N> s_sum[kJoiners][32];
+    const uint32_t block = blockIdx.x / parts, lane = threadIdx.x, share = threadIdx.y;
+    const uint32_t c = (blockIdx.x % parts) * 32 * N + lane * N;
     const uint32_t blocks = (n + kBlock - 1) / kBlock;
-    if (block + 1 >= blocks) return;  // as does its whole warp
     const uint32_t first = block * kBlock, next = first + kBlock;
-    const uint32_t key = sorted[next - 1].x;
-    if (key >= out.vocab || sorted[next].x != key || (first > 0 && sorted[first - 1].x == key)) return;
+    const uint32_t key = sorted[next - 1].x, after = sorted[next].x, before = first > 0 ? sorted[first - 1].x : ~0u;
+    if (key >= out.vocab || after != key || before == key) return;
     // The blocks whose first key is it: the run reaches them.
     uint32_t more = 1;
-    for (bool on = true; on; ) {
-        const uint32_t b = block + more + 1 + (threadIdx.x & 31);
-        const uint32_t same = __ballot_sync(kFull, b < blocks && sorted[size_t(min(b, blocks - 1)) * kBlock].x == key);
-        more += uint32_t(__ffs(~same) == 0 ? 32 : __ffs(~same) - 1);
-        on = same == kFull;
+    for (bool on = true; on;) {
+        const uint32_t b = block + more + 1 + lane;
+        const uint32_t same = __ballot_sync(kFullMask, b < blocks && sorted[size_t(min(b, blocks - 1)) * kBlock].x == key);
+        more += same == kFullMask ? 32u : uint32_t(__ffs(~same) - 1);
+        on = same == kFullMask;
     }
-    if (c >= width) return;
-    const uint32_t lo = block + more;
-    constexpr int kAhead = 8;
-    const float *e = edges + (size_t(block) * 2 + 1) * width + c;
-    Piece<float, N> sum = load_piece<float, N>(e);
-    e += width;
-    for (uint32_t b = block + 1; b <= lo; b += kAhead) {
-        Piece<float, N> x[kAhead];
+    const uint32_t per = (more + kJoiners - 1) / kJoiners;
+    const uint32_t lo = min(more, share * per), hi = min(more, lo + per);
+    Piece<float, N> sum{};
+    if (c < width) {
+        const float *e = edges + size_t(block) * 2 * width + c;
+        if (share == 0) sum = load_piece<float, N>(e + width);
+        e += size_t(lo + 1) * 2 * width;
+        for (uint32_t b = lo; b < hi; b += kAhead) {
+            Piece<float, N> x[kAhead];
 #pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
-            x[j] = Piece<float, N>{};
-            if (b + j <= lo) x[j] = load_piece<float, N>(e + size_t(j) * 2 * width);
+            for (int j = 0; j < kAhead; ++j) {
+                x[j] = Piece<float, N>{};
+                if (b + j < hi) x[j] = load_piece<float, N>(e + size_t(j) * 2 * width);
+            }
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j)
+#pragma unroll
+                for (int k = 0; k < N; ++k) sum.v[k] += x[j].v[k];
+            e += size_t(kAhead) * 2 * width;
         }
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j)
-#pragma unroll
-            for (int k = 0; k < N; ++k) sum.v[k] += x[j].v[k];
-        e += size_t(kAhead) * 2 * width;
     }
-    put_sum<O, N>(static_cast<O *>(out.rows) + size_t(key) * out.stride + c, sum.v, out.scale, out.accumulate);
+    s_sum[share][lane] = sum;
+    __syncthreads();
+    if (share > 0 || c >= width) return;
+    for (int j = 1; j < kJoiners; ++j)
+#pragma unroll
+        for (int k = 0; k < N; ++k) sum.v[k] += s_sum[j][lane].v[k];
+    O *dst = static_cast<O *>(out.rows) + size_t(key) * out.stride + c;
+    Piece<O, N> o;
+    if (out.accumulate) o = load_piece<O, N>(dst);
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        const float r = out.scale * sum.v[k];
+        o.v[k] = row_from_float<O>(out.accumulate ? r + row_to_float(o.v[k]) : r);
+    }
+    store_piece<O, N>(dst, o);
 }
 
 int key_bits(size_t vocab)
@@ -287,61 +414,86 @@ int key_bits(size_t vocab)
     return bits;
 }
 
+// The workspace starts with the library's header, of which only the error
+// word is used; `seen` follows, so that one clear serves both.
 struct GradLayout {
-    size_t items_a, items_b, table, seen, edges, total;
+    size_t seen, items_a, items_b, table, edges, total;
 };
 
 GradLayout grad_layout(size_t n, size_t vocab, size_t width)
 {
     GradLayout l{};
     const size_t items = gch::align_up(8 * n, 256);
-    l.items_a = 0;
-    l.items_b = items;
-    l.table = 2 * items;
-    l.seen = l.table + gch::align_up(bin_table_bytes(n, 512), 256);
-    l.edges = l.seen + gch::align_up(vocab, 256);
+    l.seen = kHeaderBytes;
+    l.items_a = l.seen + gch::align_up(vocab, 256);
+    l.items_b = l.items_a + items;
+    l.table = l.items_b + items;
+    l.edges = l.table + gch::align_up(bin_table_bytes(n, 512), 256);
     l.total = l.edges + gch::align_up(gch::ceil_div(n, size_t(kBlock)) * 2 * width * 4, 256) + 256;
     return l;
 }
 
+// CTAs for the rest of the rows to zero.
+uint32_t zero_ctas(const ZeroRows &z)
+{
+    const size_t rows = z.hi - z.lo, per = kZeroBytes / z.bytes < 8 ? 8 : kZeroBytes / z.bytes;
+    return uint32_t(gch::ceil_div(rows, per));
+}
+
 template <class T, class O, int N>
 cudaError_t run_grad_rows(const uint2 *sorted, uint32_t n, const void *g, size_t g_stride, size_t width,
-                          float *edges, const GradOut &out, cudaStream_t s)
+                          float *edges, const GradOut &out, const ZeroRows &zero, uint8_t *ws, cudaStream_t s)
 {
-    const dim3 threads = row_block(width / N);
-    const uint32_t blocks = uint32_t(gch::ceil_div(n, kBlock));
+    const uint32_t blocks = uint32_t(gch::ceil_div(n, kBlock)), zeros = zero_ctas(zero);
+    // Bulk copies need 16-byte aligned rows; a slice narrower than a warp's
+    // pieces is not worth one.
+    const bool bulk = ((uintptr_t(g) | g_stride * sizeof(T) | width * sizeof(T)) & 15u) == 0 && width / N >= 32;
+    dim3 threads = row_block(width / N);
+    if (bulk) {
+        const uint32_t most = kSliceBytes / (N * sizeof(T));
+        if (threads.x > most) threads.x = most;
+        threads.y = std::min(kRowThreads / threads.x, kSliceBytes / uint32_t(threads.x * N * sizeof(T)));
+    }
     const size_t parts = gch::ceil_div(width / N, threads.x);
     const size_t sums = gch::ceil_div(blocks, threads.y) * parts;
-    const size_t zero_rows = gch::align_up(gch::ceil_div(kZeroBytes, width * sizeof(O)), threads.y);
-    const size_t zeros = out.accumulate ? 0 : gch::ceil_div(out.vocab, zero_rows);
-    if (sums + zeros > 0x7fffffffu) return cudaErrorInvalidConfiguration;
-    auto kernel = out.accumulate ? token_sums_kernel<T, O, N, true> : token_sums_kernel<T, O, N, false>;
-    if (sums + zeros > 0)
+    const size_t joins = blocks > 1 ? (blocks - 1) * gch::ceil_div(width / N, 32) : 0;
+    if (sums + zeros > 0x7fffffffu || joins > 0x7fffffffu) return cudaErrorInvalidConfiguration;
+    if (sums + zeros > 0 && bulk) {
+        auto kernel = out.accumulate ? token_bulk_sums_kernel<T, O, N, true> : token_bulk_sums_kernel<T, O, N, false>;
+        const size_t smem = size_t(threads.x) * N * sizeof(T) * kBlock * threads.y;
+        // Raises the kernel's shared-memory limit, once per device.
+        if (gch::persistent_grid(reinterpret_cast<const void *>(kernel), kRowThreads, size_t(kSliceBytes) * kBlock, 1) <= 0)
+            return cudaErrorInvalidConfiguration;
+        kernel<<<uint32_t(sums + zeros), threads, smem, s>>>(sorted, n, static_cast<const T *>(g), g_stride,
+                                                             uint32_t(width), edges, out, uint32_t(parts), ws,
+                                                             gch::LaunchOpts{}.timeout_ns, uint32_t(sums), zero);
+    } else if (sums + zeros > 0) {
+        auto kernel = out.accumulate ? token_sums_kernel<T, O, N, true> : token_sums_kernel<T, O, N, false>;
         kernel<<<uint32_t(sums + zeros), threads, 0, s>>>(sorted, n, static_cast<const T *>(g), g_stride,
-                                                          uint32_t(width), edges, out, uint32_t(sums),
-                                                          uint32_t(zero_rows));
-    if (blocks > 1)
-        token_join_kernel<O, N><<<uint32_t(sums), threads, 0, s>>>(sorted, n, uint32_t(width), edges, out);
+                                                          uint32_t(width), edges, out, uint32_t(parts),
+                                                          uint32_t(sums), zero);
+    }
+    if (joins > 0)
+        token_join_kernel<O, N><<<uint32_t(joins), dim3(32, kJoiners), 0, s>>>(
+            sorted, n, uint32_t(width), edges, out, uint32_t(gch::ceil_div(width / N, 32)));
     return cudaGetLastError();
 }
 
 // Pieces of N elements, N a power of two that both rows allow and that fills
 // 16 bytes of the result at most.
-#define GC_GRAD_BY_PIECE(T, O, n)                                                   \
-    switch (n) {                                                                    \
-    case 1: return run_grad_rows<T, O, 1>(sorted, n_, g, g_stride, width, edges, out, s); \
-    case 2: return run_grad_rows<T, O, 2>(sorted, n_, g, g_stride, width, edges, out, s); \
-    case 4: return run_grad_rows<T, O, 4>(sorted, n_, g, g_stride, width, edges, out, s); \
-    default: return run_grad_rows<T, O, 16 / int(sizeof(O))>(sorted, n_, g, g_stride, width, edges, out, s); \
-    }
-
+#define GC_GRAD_CALL(T, O, N) return run_grad_rows<T, O, N>(sorted, n_, g, g_stride, width, edges, out, zero, ws, s)
 template <class T, class O>
 cudaError_t grad_rows(const uint2 *sorted, uint32_t n_, const void *g, size_t g_stride, size_t width, float *edges,
-                      const GradOut &out, cudaStream_t s)
+                      const GradOut &out, const ZeroRows &zero, uint8_t *ws, cudaStream_t s)
 {
     const int in = gch::piece_elems(uint64_t(uintptr_t(g)) | sizeof(T) * (g_stride | width), sizeof(T));
     const int to = gch::piece_elems(uint64_t(uintptr_t(out.rows)) | sizeof(O) * (out.stride | width), sizeof(O));
-    GC_GRAD_BY_PIECE(T, O, (in < to ? in : to))
+    switch (in < to ? in : to) {
+    case 1: GC_GRAD_CALL(T, O, 1);
+    case 2: GC_GRAD_CALL(T, O, 2);
+    case 4: GC_GRAD_CALL(T, O, 4);
+    default: GC_GRAD_CALL(T, O, 16 / int(sizeof(O)));
+    }
 }
 
 #define GC_BY_PIECE(T, n, CALL)                                     \
@@ -389,32 +541,54 @@ cudaError_t launch_embedding_grad(const void *g, size_t g_stride, gc_row_dtype g
     uint8_t *seen = accumulate ? nullptr : ws + l.seen;
     float *edges = reinterpret_cast<float *>(ws + l.edges);
     const int bits = key_bits(vocab), passes = int(ceil_div(bits, 9)), digit = int(ceil_div(bits, passes));
+    const size_t elem = odt == GC_ROW_F32 ? 4 : 2;
+    const int to = piece_elems(uint64_t(uintptr_t(dtable)) | elem * (dtable_stride | width), int(elem));
+    ZeroRows zero{static_cast<uint8_t *>(dtable), dtable_stride * elem, width * elem, uint32_t(to * elem), seen, 0u,
+                  accumulate ? 0u : vocab};
+    // A kernel's part of the rows to zero, about `bytes`; the rest stays.
+    auto part = [&](size_t bytes) {
+        ZeroRows z = zero;
+        const size_t rows = bytes / zero.bytes;
+        z.hi = uint32_t(std::min(size_t(zero.hi), zero.lo + rows));
+        zero.lo = z.hi;
+        return z;
+    };
     cudaError_t e = cudaSuccess;
     if (n > 0 && gcd::bin_chunks(n) == 1) {
+        // Everything is zeroed here, before any row is written.
         if (persistent_grid(reinterpret_cast<const void *>(token_sort_kernel), gcd::kBinThreads, sizeof(TokenSortSmem),
                             1) <= 0)
             return cudaErrorInvalidConfiguration;
-        token_sort_kernel<<<1, gcd::kBinThreads, sizeof(TokenSortSmem), s>>>(
-            ids, wide, n, vocab, uint32_t(digit), passes, items[passes & 1], seen);
+        zero.seen = nullptr;
+        const uint32_t others = std::min(zero_ctas(zero), kZeroCtas);
+        token_sort_kernel<<<1 + others, gcd::kBinThreads, sizeof(TokenSortSmem), s>>>(
+            ids, wide, n, vocab, uint32_t(digit), passes, items[passes & 1], reinterpret_cast<uint32_t *>(ws), zero);
+        zero.lo = zero.hi;
         e = cudaGetLastError();
     } else {
-        if (seen) e = cudaMemsetAsync(seen, 0, vocab, s);
+        e = cudaMemsetAsync(ws, 0, accumulate ? size_t(kHeaderBytes) : l.seen + vocab, s);
         for (int p = 0; n > 0 && p < passes && e == cudaSuccess; ++p) {
             const TokenPass src{ids, items[p & 1], seen, p == 0, wide, vocab, uint32_t(p * digit), (1u << digit) - 1u};
             const TokenSink sink{src, items[(p & 1) ^ 1]};
-            e = gcd::launch_bin_count(src, n, 1u << digit, table, s);
-            if (e == cudaSuccess) e = gcd::launch_bin_place(src, sink, n, 1u << digit, 1u, table, s);
+            // The first count finds out which tokens are absent.
+            const ZeroRows beside = part(p == 0 ? 0 : kCountZeros);
+            e = gcd::launch_bin_count(src, n, 1u << digit, table, s, beside, beside.lo < beside.hi ? kZeroCtas : 0u);
+            if (e != cudaSuccess) break;
+            const ZeroRows beside_place = part(kPlaceZeros);
+            e = gcd::launch_bin_place(src, sink, n, 1u << digit, 1u, table, s, beside_place,
+                                      beside_place.lo < beside_place.hi ? kZeroCtas : 0u);
         }
     }
     if (e != cudaSuccess) return e;
     const uint2 *sorted = items[passes & 1];
-    const GradOut out{dtable, dtable_stride, scale, accumulate, seen, vocab};
-    if (gdt == GC_ROW_F32) return grad_rows<float, float>(sorted, n, g, g_stride, width, edges, out, s);
+    const GradOut out{dtable, dtable_stride, scale, accumulate, vocab};
+    if (gdt == GC_ROW_F32) return grad_rows<float, float>(sorted, n, g, g_stride, width, edges, out, zero, ws, s);
     if (gdt == GC_ROW_BF16)
-        return odt == GC_ROW_F32 ? grad_rows<__nv_bfloat16, float>(sorted, n, g, g_stride, width, edges, out, s)
-                                 : grad_rows<__nv_bfloat16, __nv_bfloat16>(sorted, n, g, g_stride, width, edges, out, s);
-    return odt == GC_ROW_F32 ? grad_rows<__half, float>(sorted, n, g, g_stride, width, edges, out, s)
-                             : grad_rows<__half, __half>(sorted, n, g, g_stride, width, edges, out, s);
+        return odt == GC_ROW_F32
+                   ? grad_rows<__nv_bfloat16, float>(sorted, n, g, g_stride, width, edges, out, zero, ws, s)
+                   : grad_rows<__nv_bfloat16, __nv_bfloat16>(sorted, n, g, g_stride, width, edges, out, zero, ws, s);
+    return odt == GC_ROW_F32 ? grad_rows<__half, float>(sorted, n, g, g_stride, width, edges, out, zero, ws, s)
+                             : grad_rows<__half, __half>(sorted, n, g, g_stride, width, edges, out, zero, ws, s);
 }
 
 }  // namespace gch

@@ -59,14 +59,24 @@ __device__ __forceinline__ uint32_t bin_block_scan(uint32_t v, uint32_t *s_warp,
     return before + incl - v;
 }
 
+// Work for CTAs beyond the chunks, while those wait for memory.
+struct NoExtra {
+    __device__ __forceinline__ void run(uint32_t, uint32_t) const {}
+};
+
 // Source: bin(i) in [0, bins], where `bins` marks an item that goes nowhere.
 // Counts are written bin-major, counts[b * bin_count_stride(chunks) + c], with
 // zeros up to the stride.
-template <class Source>
+template <class Source, class Extra>
 __global__ void __launch_bounds__(kBinThreads)
-bin_count_kernel(Source src, uint32_t n, uint32_t chunk, uint32_t bins, uint32_t *__restrict__ counts)
+bin_count_kernel(Source src, uint32_t n, uint32_t chunk, uint32_t chunks, uint32_t bins,
+                 uint32_t *__restrict__ counts, Extra extra)
 {
     __shared__ uint32_t s_hist[kMaxBins];
+    if (blockIdx.x >= chunks) {
+        extra.run(blockIdx.x - chunks, gridDim.x - chunks);
+        return;
+    }
     for (uint32_t b = threadIdx.x; b < bins; b += kBinThreads) s_hist[b] = 0u;
     __syncthreads();
     const uint32_t first = blockIdx.x * chunk, last = min(n - first, chunk) + first;
@@ -76,11 +86,11 @@ bin_count_kernel(Source src, uint32_t n, uint32_t chunk, uint32_t bins, uint32_t
         if (b < bins) atomicAdd(&s_hist[b], 1u);
     }
     __syncthreads();
-    const uint32_t stride = bin_count_stride(gridDim.x);
+    const uint32_t stride = bin_count_stride(chunks);
     for (uint32_t b = threadIdx.x; b < bins; b += kBinThreads) {
         counts[size_t(b) * stride + blockIdx.x] = s_hist[b];
         if (blockIdx.x == 0)
-            for (uint32_t c = gridDim.x; c < stride; ++c) counts[size_t(b) * stride + c] = 0u;
+            for (uint32_t c = chunks; c < stride; ++c) counts[size_t(b) * stride + c] = 0u;
     }
 }
 
@@ -200,21 +210,25 @@ __device__ __forceinline__ void bin_place_chunk(const Source &src, const Sink &s
 // Sink: place(i, destination), drop(i); start(b, start, count) once per bin
 // and end(total) once, by CTA 0.  Dynamic shared memory: kBinWarps * bins
 // words.
-template <class Source, class Sink>
+template <class Source, class Sink, class Extra>
 __global__ void __launch_bounds__(kBinThreads)
-bin_place_kernel(Source src, Sink sink, uint32_t n, uint32_t chunk, uint32_t bins, uint32_t align,
-                 const uint32_t *__restrict__ counts)
+bin_place_kernel(Source src, Sink sink, uint32_t n, uint32_t chunk, uint32_t chunks, uint32_t bins, uint32_t align,
+                 const uint32_t *__restrict__ counts, Extra extra)
 {
     extern __shared__ uint32_t s_cnt[];
     __shared__ BinSmem sm;
-    bin_place_chunk(src, sink, n, chunk, gridDim.x, blockIdx.x, bins, align, counts, s_cnt, sm);
+    if (blockIdx.x < chunks) bin_place_chunk(src, sink, n, chunk, chunks, blockIdx.x, bins, align, counts, s_cnt, sm);
+    else extra.run(blockIdx.x - chunks, gridDim.x - chunks);
 }
 
-template <class Source>
-cudaError_t launch_bin_count(const Source &src, uint32_t n, uint32_t bins, uint32_t *counts, cudaStream_t s)
+// `others`: CTAs for `extra`.
+template <class Source, class Extra = NoExtra>
+cudaError_t launch_bin_count(const Source &src, uint32_t n, uint32_t bins, uint32_t *counts, cudaStream_t s,
+                             const Extra &extra = Extra{}, uint32_t others = 0)
 {
     if (bin_chunks(n) == 1) return cudaSuccess;
-    bin_count_kernel<Source><<<bin_chunks(n), kBinThreads, 0, s>>>(src, n, bin_chunk_elems(n), bins, counts);
+    bin_count_kernel<Source, Extra><<<bin_chunks(n) + others, kBinThreads, 0, s>>>(
+        src, n, bin_chunk_elems(n), bin_chunks(n), bins, counts, extra);
     return cudaGetLastError();
 }
 
@@ -224,14 +238,15 @@ inline bool bin_place_smem(const void *kernel)
     return gch::persistent_grid(kernel, kBinThreads, size_t(kBinWarps) * kMaxBins * sizeof(uint32_t), 1) > 0;
 }
 
-template <class Source, class Sink>
+template <class Source, class Sink, class Extra = NoExtra>
 cudaError_t launch_bin_place(const Source &src, const Sink &sink, uint32_t n, uint32_t bins,
-                             uint32_t align, const uint32_t *counts, cudaStream_t s)
+                             uint32_t align, const uint32_t *counts, cudaStream_t s, const Extra &extra = Extra{},
+                             uint32_t others = 0)
 {
-    auto kernel = bin_place_kernel<Source, Sink>;
+    auto kernel = bin_place_kernel<Source, Sink, Extra>;
     if (!bin_place_smem(reinterpret_cast<const void *>(kernel))) return cudaErrorInvalidConfiguration;
-    kernel<<<bin_chunks(n), kBinThreads, size_t(kBinWarps) * bins * sizeof(uint32_t), s>>>(
-        src, sink, n, bin_chunk_elems(n), bins, align, counts);
+    kernel<<<bin_chunks(n) + others, kBinThreads, size_t(kBinWarps) * bins * sizeof(uint32_t), s>>>(
+        src, sink, n, bin_chunk_elems(n), bin_chunks(n), bins, align, counts, extra);
     return cudaGetLastError();
 }
 
