@@ -205,40 +205,30 @@ token_sums_kernel(const uint2 *__restrict__ sorted, uint32_t n, const T *__restr
     constexpr int kAhead = ADD ? 4 : 8;
     Piece<T, N> x[kAhead];
     Piece<O, N> old[ADD ? kAhead : 1];
-    auto load = [&](uint32_t base) {
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
-            const uint32_t k = base + j < kBlock ? key[base + j + 1] : none;
-            if (k == none) continue;
-            x[j] = load_piece<T, N>(g + size_t(at[base + j]) * g_stride + c);
-            if (ADD && key[base + j + 2] != k) old[ADD ? j : 0] = load_piece<O, N>(rows + size_t(k) * out.stride + c);
-        }
+    auto load = [&](uint32_t at_j, int j) {
+        const uint32_t k = at_j < kBlock ? key[at_j + 1] : none;
+        if (k == none) return;
+        x[j] = load_piece<T, N>(g + size_t(at[at_j]) * g_stride + c);
+        if (ADD && key[at_j + 2] != k) old[ADD ? j : 0] = load_piece<O, N>(rows + size_t(k) * out.stride + c);
     };
     Piece<float, N> sum{};
     bool began = key[0] != key[1];
-    load(0);
-    for (uint32_t base = 0; base < kBlock; base += kAhead) {
-        Piece<T, N> now[kAhead];
-        Piece<O, N> add[ADD ? kAhead : 1];
 #pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
-            now[j] = x[j];
-            if (ADD) add[j] = old[j];
-        }
-        load(base + kAhead);
+    for (int j = 0; j < kAhead; ++j) load(j, j);
+    for (uint32_t base = 0; base < kBlock; base += kAhead) {
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
             const uint32_t k = key[base + j + 1];
             if (k == none) return;
 #pragma unroll
-            for (int e = 0; e < N; ++e) sum.v[e] += row_to_float(now[j].v[e]);
+            for (int e = 0; e < N; ++e) sum.v[e] += row_to_float(x[j].v[e]);
             const bool ends = key[base + j + 2] != k;
             if (ends && began) {
                 Piece<O, N> o;
 #pragma unroll
                 for (int e = 0; e < N; ++e) {
                     const float r = out.scale * sum.v[e];
-                    o.v[e] = row_from_float<O>(ADD ? r + row_to_float(add[ADD ? j : 0].v[e]) : r);
+                    o.v[e] = row_from_float<O>(ADD ? r + row_to_float(old[ADD ? j : 0].v[e]) : r);
                 }
                 store_piece<O, N>(rows + size_t(k) * out.stride + c, o);
             } else if (ends || base + j + 1 == kBlock) {
@@ -248,6 +238,7 @@ token_sums_kernel(const uint2 *__restrict__ sorted, uint32_t n, const T *__restr
                 sum = Piece<float, N>{};
                 began = true;
             }
+            load(base + kAhead + j, j);
         }
     }
 }

@@ -19,6 +19,8 @@
 //     those above, and a sort of the collected; a last pass sums and draws.
 //     Where the collected do not fit or do not hold the cut, the leader finds
 //     it by radix selection over the whole row (select_cut).
+#include <type_traits>
+
 #include <cooperative_groups.h>
 
 #include "gc_internal.h"
@@ -29,15 +31,26 @@ namespace {
 using namespace gcd;
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 512;
+#ifndef GC_SAMPLE_THREADS
+#define GC_SAMPLE_THREADS 512
+#endif
+#ifndef GC_SAMPLE_CTAS
+#define GC_SAMPLE_CTAS 2
+#endif
+constexpr int kThreads = GC_SAMPLE_THREADS;
 constexpr int kWarps = kThreads / 32;
+constexpr int kResident = GC_SAMPLE_CTAS;                // CTAs per SM
 constexpr uint32_t kMaxTeam = 8;
-constexpr uint32_t kList = 8192;            // candidates that the leader can hold
-constexpr int kBins = 2048;                 // histogram of z, 64 bins to a unit
-constexpr float kBinsPerUnit = 64.0f;
+constexpr uint32_t kList = 4096;            // candidates that a CTA can hold
+// Histogram of the distance below the maximum in powers of two, 64 bins to a
+// power; from bin kBinsUsed on weights round to 0 of 2^-40.
+constexpr int kBins = 4096;
+constexpr uint32_t kBinsUsed = 42 * 64;
+constexpr float kBinsPerPower = 64.0f;
 constexpr int kSubBins = 1024;              // histogram of the list
 constexpr uint32_t kFew = 1024;             // of the list's tokens near a cut
 constexpr int kLoads = 4;                   // pieces of 16 bytes that a thread loads at a time
+constexpr int kSample = 8;                  // pieces per thread that bound the k-th largest value
 constexpr float kFixed = 1099511627776.0f;  // 2^40
 constexpr float kUniformLo = 0x1p-25f, kUniformHi = 1.0f - 0x1p-24f;
 // -log u lies in [2^-24, 17.4] and the largest token weighs 1, so a token
@@ -77,15 +90,41 @@ struct Cut {
     __device__ __forceinline__ bool keeps(float x, uint32_t i) const { return x > value || (x == value && i <= index); }
 };
 
-// z = (x - m) / t and w = exp(z) of a row; the quotient as a product with
-// 1 / t, one rounding more, and no division per token.
+// z = (x - m) / t and w = exp(z) of a row.  The quotient is a product with
+// 1 / t, one rounding more and no division per token, and w a power of two,
+// whose argument takes the same products.
 struct Scale {
-    float m, inv;
-    __device__ __forceinline__ Scale(float m_, float t) : m(m_), inv(fminf(fmaxf(1.0f / t, 1.17549435e-38f), 3.402823466e38f)) {}
+    float m, inv, power;  // power: log2(e) / t
+    __device__ __forceinline__ Scale(float m_, float t) : m(m_)
+    {
+        inv = fminf(fmaxf(1.0f / t, 1.17549435e-38f), 3.402823466e38f);
+        power = fminf(inv * 1.44269504f, 3.402823466e38f);
+    }
     __device__ __forceinline__ float z(float x) const { return (x - m) * inv; }
-    __device__ __forceinline__ float w(float x) const { return expf(z(x)); }
+    __device__ __forceinline__ float log_w(float x) const { return (x - m) * power; }  // to base 2
+    __device__ __forceinline__ float w(float x) const { return exp2f(log_w(x)); }
     __device__ __forceinline__ uint64_t fixed(float x) const { return __float2ull_rn(w(x) * kFixed); }
 };
+
+// The largest value of a piece; NaN counts for nothing.
+template <class T, int N>
+__device__ __forceinline__ float piece_max(const Piece<T, N> &p)
+{
+    if constexpr (sizeof(T) == 4) {
+        float r = p.v[0];
+#pragma unroll
+        for (int e = 1; e < N; ++e) r = fmaxf(r, p.v[e]);
+        return r;
+    } else {
+        // two at a time
+        using Pair = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
+        const Pair *q = reinterpret_cast<const Pair *>(p.v);
+        Pair r = q[0];
+#pragma unroll
+        for (int e = 1; e < N / 2; ++e) r = __hmax2(r, q[e]);
+        return fmaxf(row_to_float(T(r.x)), row_to_float(T(r.y)));
+    }
+}
 
 // A key to find the largest of and a weight to add up, reduced together.
 struct KeySum {
@@ -94,7 +133,7 @@ struct KeySum {
 };
 
 struct Smem {
-    uint64_t list[kList];
+    uint64_t list[kList];        // candidates; the leader's, then all of them
     alignas(16) uint32_t hist[kBins];
     union {
         uint64_t sub[kSubBins];
@@ -104,7 +143,7 @@ struct Smem {
     KeySum slot[2][kMaxTeam];
     uint64_t scan[kWarps];
     uint64_t cut, above;
-    uint32_t count;              // candidates appended (may pass kList)
+    uint32_t count;              // candidates appended to this list (may pass kList)
     uint32_t bin, state;
     bool found;
 };
@@ -146,33 +185,30 @@ struct Row {
             for (uint32_t e = 0; e < kVec; ++e) p.v[e] = row_from_float<T>(-INFINITY);
         }
     }
-    // f(values, index of the first) for this thread's pieces and, as a piece
-    // of one value, its single element; -inf where there is no token.  All
-    // threads of a warp call f together.  N pieces are loaded while the N
-    // before them are in work.
+    // f(piece, index of its first) for this thread's pieces and, as a piece of
+    // one value, its single element; -inf where there is no token.  All
+    // threads of a warp call f together.  A piece's registers are loaded anew
+    // as soon as f has its copy, so N - 1 loads are under way throughout.
     template <int N, class F>
     __device__ __forceinline__ void each(const F &f) const
     {
-        float v[kVec];
-        {
-            const uint32_t s = single();
+        const uint32_t s = single();
+        if (__any_sync(kFull, s < vocab)) {
+            Piece<T, kVec> one;
 #pragma unroll
-            for (uint32_t e = 1; e < kVec; ++e) v[e] = -INFINITY;
-            v[0] = s < vocab ? row_to_float(x[s]) : -INFINITY;
-            if (__any_sync(kFull, s < vocab)) f(v, s);
+            for (uint32_t e = 1; e < kVec; ++e) one.v[e] = row_from_float<T>(-INFINITY);
+            one.v[0] = s < vocab ? x[s] : row_from_float<T>(-INFINITY);
+            f(one, s);
         }
-        Piece<T, kVec> now[N], next[N];
+        Piece<T, kVec> p[N];
 #pragma unroll
-        for (int q = 0; q < N; ++q) load(q * team + me, now[q]);
+        for (int q = 0; q < N; ++q) load(q * team + me, p[q]);
         for (uint32_t base = 0; base < pieces; base += N * team) {
 #pragma unroll
-            for (int q = 0; q < N; ++q) load(base + (N + q) * team + me, next[q]);
-#pragma unroll
             for (int q = 0; q < N; ++q) {
-#pragma unroll
-                for (uint32_t e = 0; e < kVec; ++e) v[e] = row_to_float(now[q].v[e]);
-                f(v, head + (base + q * team + me) * kVec);
-                now[q] = next[q];
+                const Piece<T, kVec> now = p[q];
+                load(base + (N + q) * team + me, p[q]);
+                f(now, head + (base + q * team + me) * kVec);
             }
         }
     }
@@ -250,16 +286,48 @@ struct Team {
     }
     __device__ __forceinline__ uint64_t largest(uint64_t key) { return reduce(KeySum{key, 0.0f}).key; }
     __device__ __forceinline__ float sum(float v) { return reduce(KeySum{0u, v}).sum; }
-    // Adds this warp's keys to the leader's list; every lane calls it.
-    __device__ __forceinline__ void append(bool mine, uint64_t key) const
+    // Adds the tokens of a piece with a bit in `which` to this CTA's list; all
+    // lanes of the warp together.
+    template <class T, int N>
+    __device__ __forceinline__ void append(uint32_t which, const Piece<T, N> &x, uint32_t i) const
     {
-        const uint32_t who = __ballot_sync(kFull, mine);
-        if (who == 0u) return;
+        const uint32_t lane = threadIdx.x & 31;
+        uint32_t c = __popc(which), incl = c;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t y = __shfl_up_sync(kFull, incl, o);
+            if (lane >= uint32_t(o)) incl += y;
+        }
         uint32_t at = 0u;
-        const int first = __ffs(who) - 1, lane = threadIdx.x & 31;
-        if (lane == first) at = atomicAdd(&lead->count, uint32_t(__popc(who)));
-        at = __shfl_sync(kFull, at, first) + __popc(who & ((1u << lane) - 1u));
-        if (mine && at < kList) lead->list[at] = key;
+        if (lane == 31) at = atomicAdd(&sm.count, incl);
+        at = __shfl_sync(kFull, at, 31) + incl - c;
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+            if ((which >> e) & 1u) {
+                if (at < kList) sm.list[at] = order_key(sample_value(row_to_float(x.v[e])), i + e);
+                ++at;
+            }
+    }
+    // After a sync that follows every append: the tokens in all lists, to
+    // every thread.  If they fit, the leader's list becomes all of them.
+    __device__ __forceinline__ uint32_t gather_lists() const
+    {
+        uint32_t n = sm.count;
+        if (size > 1) {
+            n = 0u;
+            for (uint32_t c = 0; c < size; ++c) n += peer(c)->count;
+            if (rank == 0 && n <= kList) {
+                uint32_t at = sm.count;
+                for (uint32_t c = 1; c < size; ++c) {
+                    const Smem *p = peer(c);
+                    const uint32_t m = p->count;
+                    for (uint32_t j = threadIdx.x; j < m; j += kThreads) sm.list[at + j] = p->list[j];
+                    at += m;
+                }
+            }
+            __syncthreads();
+        }
+        return n;
     }
 };
 
@@ -292,17 +360,18 @@ struct Draw {
             slope = -1.00001f / b;
         }
     }
-    // Offers the tokens of a piece with kept[e]; all lanes together.
+    // Offers the tokens of a piece with a bit in `kept`; all lanes together.
     template <uint32_t N>
-    __device__ __forceinline__ void offer(const float (&w)[N], const bool (&kept)[N], const float (&u)[N], uint32_t i)
+    __device__ __forceinline__ void offer(const float (&w)[N], uint32_t kept, const float (&u)[N], uint32_t i)
     {
-        bool any = false;
+        uint32_t any = 0u;
 #pragma unroll
-        for (uint32_t e = 0; e < N; ++e) any |= kept[e] && w[e] >= kLightest && open(w[e], fmaxf(u[e], kUniformLo));
-        if (!__any_sync(kFull, any)) return;
+        for (uint32_t e = 0; e < N; ++e) any |= open(w[e], fmaxf(u[e], kUniformLo)) ? 1u << e : 0u;
+        any &= kept;
+        if (!__any_sync(kFull, any != 0u)) return;
 #pragma unroll
         for (uint32_t e = 0; e < N; ++e)
-            if (kept[e] && w[e] >= kLightest && open(w[e], fmaxf(u[e], kUniformLo))) take(w[e], u[e], i + e);
+            if ((any >> e) & 1u) take(w[e], u[e], i + e);
         share();
     }
     __device__ __forceinline__ uint64_t key() const { return best > 0.0f ? order_key(best, index) : 0u; }
@@ -521,14 +590,17 @@ __device__ __noinline__ uint64_t select_cut(uint64_t target, Smem &sm, const Eac
 // low bits; a conversion instruction takes eight times its issue slots.
 __device__ __forceinline__ uint32_t round_small(float x) { return __float_as_uint(x + 8388608.0f) & 0x7fffffu; }
 
-// Bin of a token: its distance below the maximum in steps of 1/64, rounded;
-// kBins for tokens 32 or more below, whose weights round to 0 of 2^-40.
-__device__ __forceinline__ uint32_t z_bin(float z) { return round_small(fminf(-z * kBinsPerUnit, float(kBins))); }
+// Bin of a token from the base-2 logarithm of its weight, rounded; kBinsUsed
+// and more: no weight, or NaN.
+__device__ __forceinline__ uint32_t weight_bin(float log_w)
+{
+    return round_small(fminf(log_w * -kBinsPerPower, float(kBins - 1)));
+}
 
-// A bin's weights, all below 2^(1 - e) for e = bin_power, are counted in units
+// A bin's weights, all below 2^(1 - e) for e = its power, are counted in units
 // of 2^-(e + bits), 2^bits times the vocabulary at most 2^31, so that a bin of
 // all tokens fits 32 bits.
-__device__ __forceinline__ int bin_power(uint32_t bin) { return int((bin * 1477u) >> 16); }  // 1477 / 2^16 < log2(e) / 64
+__device__ __forceinline__ int bin_power(uint32_t bin) { return int(bin >> 6); }
 
 __device__ __forceinline__ uint64_t share_of(float p, double fixed_sum)
 {
@@ -547,29 +619,29 @@ struct Kept {
 
 // The cut at `target` (select_cut's) found by the team.  MASS: amounts are
 // weights and the target is a share p of their sum; else each token counts 1
-// and the target is k.  Only the tokens of `floor` count.  With `kept`, the
-// tokens above the cut's bins are added to it on the way and the leader adds
-// the rest; returns whether it did.
-template <bool MASS, class T>
-__device__ __noinline__ bool find_cut(Team &team, const Row<T> &row, const Scale &scale, uint64_t floor_key, uint32_t k,
-                                      float p, float q, Kept *kept, uint64_t &cut_key)
+// and the target is k.  FLOOR: only the tokens of `floor` count.  With `kept`,
+// the tokens above the cut's bins are added to it on the way and the leader
+// adds the rest; returns whether it did.
+template <bool MASS, bool FLOOR, class T>
+__device__ __noinline__ bool find_cut(Team &team, const Row<T> &row, const Scale &row_scale, uint64_t floor_key,
+                                      uint32_t k, float p, float q, Kept *kept, uint64_t &cut_key)
 {
     constexpr uint32_t kVec = Row<T>::kVec;
     Smem &sm = team.sm;
+    const Scale scale = row_scale;
     const Cut floor(floor_key);
     const int bits = min(14, __clz(int(row.vocab)) - 1);
     for (int b = threadIdx.x; b < kBins; b += kThreads) sm.hist[b] = 0u;
-    if (threadIdx.x == 0) sm.count = 0u;
     team.sync();
     float mass = 0.0f;
-    row.template each<2>([&](const float (&x)[kVec], uint32_t i) {
+    row.template each<4>([&](const Piece<T, kVec> &x, uint32_t i) {
 #pragma unroll
         for (uint32_t e = 0; e < kVec; ++e) {
-            const float v = sample_value(x[e]), z = scale.z(v);
-            const uint32_t b = z_bin(z);
-            if (b >= uint32_t(kBins) || !floor.keeps(v, i + e)) continue;
+            const float v = sample_value(row_to_float(x.v[e])), l = scale.log_w(v);
+            const uint32_t b = weight_bin(l);
+            if (b >= kBinsUsed || (FLOOR && !floor.keeps(v, i + e))) continue;
             if (MASS) {
-                const float w = expf(z);
+                const float w = exp2f(l);
                 mass += w;
                 atomicAdd(&sm.hist[b], round_small(w * __int_as_float((127 + bits + bin_power(b)) << 23)));
             } else {
@@ -583,7 +655,7 @@ __device__ __noinline__ bool find_cut(Team &team, const Row<T> &row, const Scale
     if (MASS) {
         target = share_of(p, double(mass) * double(kFixed));
     } else if (mass < float(k)) {
-        cut_key = floor_key;  // the cut lies 32 below the maximum or more, where no weight is left
+        cut_key = floor_key;  // the cut lies where no weight is left
         return false;
     }
     // The rounded amounts may miss the cut's bin where the bins about it hold
@@ -594,14 +666,18 @@ __device__ __noinline__ bool find_cut(Team &team, const Row<T> &row, const Scale
     for (int tries = 0; state == kAgain && tries < 4; ++tries) {
         uint64_t rough = 0u;
         if (team.rank == 0) {
-            // Thread j owns bins 4 j to 4 j + 3.
+            // A thread owns kPer neighbouring bins.
             constexpr int kPer = kBins / kThreads;
             uint64_t part[kPer], sum = 0u, all;
 #pragma unroll
             for (int j = 0; j < kPer; ++j) part[j] = 0u;
             for (uint32_t c = 0; c < team.size; ++c) {
-                const uint4 h = reinterpret_cast<const uint4 *>(team.peer(c)->hist)[threadIdx.x];
-                part[0] += h.x, part[1] += h.y, part[2] += h.z, part[3] += h.w;
+                const uint4 *h = reinterpret_cast<const uint4 *>(team.peer(c)->hist) + threadIdx.x * (kPer / 4);
+#pragma unroll
+                for (int j = 0; j < kPer; j += 4) {
+                    const uint4 v = h[j / 4];
+                    part[j] += v.x, part[j + 1] += v.y, part[j + 2] += v.z, part[j + 3] += v.w;
+                }
             }
 #pragma unroll
             for (int j = 0; j < kPer; ++j) {
@@ -619,7 +695,6 @@ __device__ __noinline__ bool find_cut(Team &team, const Row<T> &row, const Scale
                 if (at < aim && at + part[j] >= aim) sm.bin = threadIdx.x * kPer + j;
                 at += part[j];
             }
-            if (threadIdx.x == 0) sm.count = 0u;
             __syncthreads();
             const uint32_t lo = sm.bin > 0 ? sm.bin - 1 : 0;
             if (lo / kPer == threadIdx.x) {
@@ -632,49 +707,43 @@ __device__ __noinline__ bool find_cut(Team &team, const Row<T> &row, const Scale
             __syncthreads();
             rough = sm.above;
         }
+        if (threadIdx.x == 0) sm.count = 0u;
         team.sync();
-        // Tokens of the cut's bin and its neighbours to the list, those above added up.
-        const uint32_t bin = team.lead->bin, lo = bin > 0 ? bin - 1 : 0, hi = min(bin + 1, uint32_t(kBins - 1));
+        // Tokens of the cut's bin and its neighbours, as an interval of
+        // values, to the list; those above it added up.
+        const uint32_t bin = team.lead->bin, lo = bin > 0 ? bin - 1 : 0;
+        const float unit = 1.0f / (kBinsPerPower * scale.power);
+        const float top = bin > 1 ? scale.m - (float(lo) - 0.5f) * unit : 3.402823466e38f;
+        const float low = fmaxf(scale.m - (float(bin) + 1.5f) * unit, -3.402823466e38f);
         mass = 0.0f;
         mine = Kept();
-        row.template each<2>([&](const float (&x)[kVec], uint32_t i) {
-            float most = -INFINITY;
-#pragma unroll
-            for (uint32_t e = 0; e < kVec; ++e) most = fmaxf(most, sample_value(x[e]));
-            if (!__any_sync(kFull, z_bin(scale.z(most)) <= hi)) return;
+        row.template each<4>([&](const Piece<T, kVec> &x, uint32_t i) {
+            if (!__any_sync(kFull, piece_max(x) >= low)) return;
             float w[kVec];
-            bool sure[kVec];
-            bool some = false;
-            uint32_t list = 0u;
+            uint32_t list = 0u, sure = 0u;
 #pragma unroll
             for (uint32_t e = 0; e < kVec; ++e) {
-                const float v = sample_value(x[e]), z = scale.z(v);
-                const uint32_t b = z_bin(z);
-                const bool in = b <= hi && floor.keeps(v, i + e);
-                w[e] = expf(z);
-                if (in && b >= lo) list |= 1u << e;
-                sure[e] = in && b < lo;
-                mass += sure[e] ? (MASS ? w[e] : 1.0f) : 0.0f;
-                sure[e] = sure[e] && w[e] >= q;
-                mine.sum += sure[e] ? w[e] : 0.0f;
-                some |= sure[e];
+                const float v = sample_value(row_to_float(x.v[e]));
+                const bool in = v >= low && (!FLOOR || floor.keeps(v, i + e)), above = in && v > top;
+                w[e] = scale.w(v);
+                if (in && !above) list |= 1u << e;
+                mass += above ? (MASS ? w[e] : 1.0f) : 0.0f;
+                const bool keep = above && w[e] >= q;
+                mine.sum += keep ? w[e] : 0.0f;
+                if (keep) sure |= 1u << e;
             }
-            if (__any_sync(kFull, list != 0u)) {
-#pragma unroll
-                for (uint32_t e = 0; e < kVec; ++e)
-                    team.append((list >> e) & 1u, order_key(sample_value(x[e]), i + e));
-            }
-            if (kept && __any_sync(kFull, some)) {
+            if (__any_sync(kFull, list != 0u)) team.append(list, x, i);
+            if (kept && __any_sync(kFull, sure != 0u)) {
                 float u[kVec];
                 row.uniforms(i, u);
                 mine.draw.offer(w, sure, u, i);
             }
         });
-        mass = team.sum(mass);
+        mass = team.sum(mass);  // past which every list is complete
+        const uint32_t n = team.gather_lists();
         if (team.rank == 0) {
             // The cut is in the list if the tokens above it stay below the
             // target and the list reaches it.  A histogram leaves few to sort.
-            const uint32_t n = sm.count;
             const uint64_t above = MASS ? uint64_t(double(mass) * double(kFixed) + 0.5) : uint64_t(mass);
             error = int64_t(above) - int64_t(rough);
             auto amount = [&](uint64_t key) { return MASS ? scale.fixed(key_value(key)) : uint64_t(1); };
@@ -686,8 +755,8 @@ __device__ __noinline__ bool find_cut(Team &team, const Row<T> &row, const Scale
             };
             SubBin sub{0.0f, 0.0f, uint32_t(kSubBins), 0u};
             if (n <= kList && above < target) {
-                const float step = 1.0f / (kBinsPerUnit * scale.inv);
-                sub = sub_bin(sm, n, scale.m - (float(lo) - 0.5f) * step, 3.0f * step, above, target, amount);
+                const float first = fminf(top, scale.m);
+                sub = sub_bin(sm, n, first, first - low, above, target, amount);
             }
             if (threadIdx.x == 0) sm.state = n <= kList ? kAgain : kMissed;
             if (sub.at < uint32_t(kSubBins)) {
@@ -723,11 +792,11 @@ __device__ __noinline__ bool find_cut(Team &team, const Row<T> &row, const Scale
         if (team.rank == 0) {
             const Row<T> whole(row.x, row.u, row.vocab, 0, 1);
             const uint64_t cut = select_cut(target, sm, [&](auto add) {
-                whole.template each<1>([&](const float (&x)[kVec], uint32_t i) {
+                whole.template each<1>([&](const Piece<T, kVec> &x, uint32_t i) {
 #pragma unroll
                     for (uint32_t e = 0; e < kVec; ++e) {
-                        const float v = sample_value(x[e]);
-                        if (v > -INFINITY && floor.keeps(v, i + e))
+                        const float v = sample_value(row_to_float(x.v[e]));
+                        if (v > -INFINITY && (!FLOOR || floor.keeps(v, i + e)))
                             add(order_key(v, i + e), MASS ? scale.fixed(v) : uint64_t(1));
                     }
                 });
@@ -742,12 +811,11 @@ __device__ __noinline__ bool find_cut(Team &team, const Row<T> &row, const Scale
     return state == kFound && kept != nullptr;
 }
 
-// The rest of a row whose candidates, all tokens not below `threshold`, are in
-// the leader's list, by the leader's CTA: top-k, sort, top-p, min-p, draw.
-__device__ __noinline__ void finish_list(Smem &sm, uint32_t k, float t, float p, float q, float threshold,
+// The rest of a row whose n candidates, all tokens not below `threshold`, are
+// in the leader's list, by the leader's CTA: top-k, sort, top-p, min-p, draw.
+__device__ __noinline__ void finish_list(Smem &sm, uint32_t n, uint32_t k, float t, float p, float q, float threshold,
                                          const float *__restrict__ u, int32_t *token, float *logprob)
 {
-    uint32_t n = sm.count;
     uint64_t *list = sm.list;
     Team alone(sm, 1);
     if (n > 64) {
@@ -797,7 +865,7 @@ __device__ __noinline__ void finish_list(Smem &sm, uint32_t k, float t, float p,
 }
 
 template <class T>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, kResident)
 sample_kernel(const T *__restrict__ logits, size_t logits_stride, uint32_t vocab,
               const float *__restrict__ uniform, size_t uniform_stride, const float *__restrict__ temperature,
               const int32_t *__restrict__ top_k, const float *__restrict__ top_p, const float *__restrict__ min_p,
@@ -819,46 +887,45 @@ sample_kernel(const T *__restrict__ logits, size_t logits_stride, uint32_t vocab
     float *logprob = logprobs ? logprobs + r : nullptr;
 
     // Top-k by one pass that collects candidates: all tokens of a short row;
-    // else the k-th largest of the threads' maxima over each CTA's first batch, rounded
-    // down to 16 bits, bounds the k-th largest value from below, and about k
-    // in kBatch tokens get in.
-    constexpr uint32_t kBatch = kLoads * kThreads * kVec;
+    // else the k-th largest of the threads' maxima over each CTA's first
+    // kBatch tokens, rounded down to 16 bits, bounds the k-th largest value
+    // from below, and about k in kBatch tokens get in.
+    constexpr uint32_t kBatch = kSample * kThreads * kVec;
     const bool brief = vocab <= kList / 2;
     if (!greedy && k < vocab &&
-        (brief || (k <= uint32_t(kThreads) && uint64_t(k) * vocab <= uint64_t(kBatch) * (kList / 2)))) {
+        (brief || (k <= uint32_t(kThreads * 3 / 4) && uint64_t(k) * vocab <= uint64_t(kBatch) * (kList / 2)))) {
         if (threadIdx.x == 0) sm.count = 0u;
         float threshold = -INFINITY;
         team.sync();
         if (!brief) {
             float best = -INFINITY;
 #pragma unroll
-            for (int j = 0; j < kLoads; ++j) {
-                Piece<T, kVec> pc;
-                row.load(j * row.team + row.me, pc);
+            for (int b = 0; b < kSample; b += kLoads) {
+                Piece<T, kVec> pc[kLoads];
 #pragma unroll
-                for (uint32_t e = 0; e < kVec; ++e) best = fmaxf(best, row_to_float(pc.v[e]));
+                for (int j = 0; j < kLoads; ++j) row.load((b + j) * row.team + row.me, pc[j]);
+#pragma unroll
+                for (int j = 0; j < kLoads; ++j) best = fmaxf(best, piece_max(pc[j]));
             }
             const uint32_t least = kth_largest(best > -INFINITY ? order_bits(sample_value(best)) : 0u, k);
             if (least) threshold = order_value(least);
         }
-        row.template each<kLoads>([&](const float (&x)[kVec], uint32_t i) {
-            float best = -INFINITY;
+        threshold = fmaxf(threshold, -3.402823466e38f);  // -inf is no candidate
+        row.template each<kLoads>([&](const Piece<T, kVec> &x, uint32_t i) {
+            if (!__any_sync(kFull, piece_max(x) >= threshold)) return;
+            uint32_t which = 0u;
 #pragma unroll
-            for (uint32_t e = 0; e < kVec; ++e) best = fmaxf(best, x[e]);
-            if (!__any_sync(kFull, best > -INFINITY && best >= threshold)) return;
-#pragma unroll
-            for (uint32_t e = 0; e < kVec; ++e) {
-                const float v = sample_value(x[e]);
-                team.append(v > -INFINITY && v >= threshold, order_key(v, i + e));
-            }
+            for (uint32_t e = 0; e < kVec; ++e)
+                if (row_to_float(x.v[e]) >= threshold) which |= 1u << e;
+            team.append(which, x, i);
         });
         team.sync();
-        const uint32_t n = team.lead->count;
-        team.sync();  // finish_list counts anew
+        const uint32_t n = team.gather_lists();
+        team.sync();  // the leader has read every list, and counts anew
         if (n <= kList) {
             if (team.rank == 0) {
                 if (n > 0) {
-                    finish_list(sm, k, t, p, q, threshold, row.u, token, logprob);
+                    finish_list(sm, n, k, t, p, q, threshold, row.u, token, logprob);
                 } else if (threadIdx.x == 0) {
                     *token = -1;
                     if (logprob) *logprob = -INFINITY;
@@ -871,15 +938,13 @@ sample_kernel(const T *__restrict__ logits, size_t logits_stride, uint32_t vocab
     // The first of the order.
     float best = -INFINITY;
     uint32_t at = ~0u;
-    row.template each<kLoads>([&](const float (&x)[kVec], uint32_t i) {
-        float top = -INFINITY;
-#pragma unroll
-        for (uint32_t e = 0; e < kVec; ++e) top = fmaxf(top, sample_value(x[e]));
+    row.template each<kLoads>([&](const Piece<T, kVec> &x, uint32_t i) {
+        const float top = sample_value(piece_max(x));
         if (top > best || (top == best && i < at)) {
             best = top;
 #pragma unroll
             for (int e = int(kVec) - 1; e >= 0; --e)
-                if (sample_value(x[e]) == top) at = i + e;
+                if (sample_value(row_to_float(x.v[e])) == top) at = i + e;
         }
     });
     const uint64_t first = team.largest(best > -INFINITY ? order_key(best, at) : 0u);
@@ -895,25 +960,30 @@ sample_kernel(const T *__restrict__ logits, size_t logits_stride, uint32_t vocab
     Kept kept;
     uint64_t cut_key = 0u;
     bool done = false;
-    if (k < vocab) done = find_cut<false>(team, row, scale, 0u, k, 1.0f, q, p < 1.0f ? nullptr : &kept, cut_key);
-    if (p < 1.0f) done = find_cut<true>(team, row, scale, cut_key, 0u, p, q, &kept, cut_key);
+    if (k < vocab) done = find_cut<false, false>(team, row, scale, 0u, k, 1.0f, q, p < 1.0f ? nullptr : &kept, cut_key);
+    if (p < 1.0f)
+        done = cut_key ? find_cut<true, true>(team, row, scale, cut_key, 0u, p, q, &kept, cut_key)
+                       : find_cut<true, false>(team, row, scale, 0u, 0u, p, q, &kept, cut_key);
     if (!done) {
         kept = Kept();
         const Cut cut(cut_key);
-        row.template each<2>([&](const float (&x)[kVec], uint32_t i) {
+        const bool all = cut_key == 0u;
+        row.template each<2>([&](const Piece<T, kVec> &x, uint32_t i) {
             float w[kVec];
-            bool in[kVec];
-            bool some = false;
+            uint32_t in = 0u;
 #pragma unroll
             for (uint32_t e = 0; e < kVec; ++e) {
-                const float v = sample_value(x[e]);
+                const float v = sample_value(row_to_float(x.v[e]));
                 w[e] = scale.w(v);
-                in[e] = cut.keeps(v, i + e) && w[e] >= q;
-                kept.sum += in[e] ? w[e] : 0.0f;
-                in[e] = in[e] && w[e] >= kLightest;
-                some |= in[e];
+                if (w[e] >= q && w[e] > 0.0f) in |= 1u << e;
             }
-            if (!__any_sync(kFull, some)) return;
+            if (!all)
+#pragma unroll
+                for (uint32_t e = 0; e < kVec; ++e)
+                    if (!cut.keeps(sample_value(row_to_float(x.v[e])), i + e)) in &= ~(1u << e);
+            if (!__any_sync(kFull, in != 0u)) return;
+#pragma unroll
+            for (uint32_t e = 0; e < kVec; ++e) kept.sum += (in >> e) & 1u ? w[e] : 0.0f;
             float u[kVec];
             row.uniforms(i, u);
             kept.draw.offer(w, in, u, i);
@@ -931,8 +1001,8 @@ sample_kernel(const T *__restrict__ logits, size_t logits_stride, uint32_t vocab
 template <class T, class... A>
 cudaError_t run_sample(const void *logits, uint32_t rows, uint32_t vocab, cudaStream_t s, size_t stride, A... args)
 {
-    // Few rows are spread over more SMs, down to one batch of a row per CTA.
-    const uint64_t slots = 2u * uint64_t(gch::sm_count());
+    // Few rows are spread over more CTAs, down to four pieces per thread.
+    const uint64_t slots = uint64_t(kResident) * uint64_t(gch::sm_count());
     uint32_t team = 1;
     while (team < kMaxTeam && uint64_t(rows) * (2 * team) <= slots &&
            vocab >= 2 * team * (kThreads * kLoads * uint32_t(16 / sizeof(T))))

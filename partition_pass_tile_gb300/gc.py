@@ -14,6 +14,7 @@ partition_pass_tile_gb300.build``) the first call raises.
 from __future__ import annotations
 
 import ctypes
+from functools import lru_cache
 from pathlib import Path
 from typing import NamedTuple
 
@@ -521,9 +522,21 @@ def _rows(t: torch.Tensor) -> tuple[int, int]:
     """(pointer, row stride) of a 2-D tensor whose rows are contiguous."""
     if not t.is_cuda:
         raise ValueError("libgc takes CUDA tensors (device pointers)")
-    if t.dim() != 2 or (t.size(1) > 1 and t.stride(1) != 1):
+    stride, shape = t.stride(), t.shape
+    if len(shape) != 2 or (stride[1] != 1 and shape[1] > 1):
         raise ValueError("libgc takes 2-D row arrays whose rows are contiguous")
-    return t.data_ptr(), t.stride(0) if t.size(0) > 1 else t.size(1)
+    return t.data_ptr(), stride[0] if shape[0] > 1 else shape[1]
+
+
+# The current stream's handle without the stream object that
+# torch.cuda.current_stream() makes (0.1 against 2.8 us a call).
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _handle(stream, device: torch.device) -> int:
+    if stream is None and _current_raw_stream is not None:
+        return _current_raw_stream(device.index)
+    return _stream(stream)
 
 
 def _ids(t: torch.Tensor) -> int:
@@ -547,13 +560,13 @@ def _typed(t: torch.Tensor | None, dtype: torch.dtype, n: int, what: str) -> int
 
 def _new(shape, dtype: torch.dtype, device, stream, value=None) -> torch.Tensor:
     """A tensor whose memory belongs to the stream that the call runs on."""
-    if stream is not None:
-        s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))
-        with torch.cuda.stream(s):
-            return _new(shape, dtype, device, None, value)
-    if value is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    return torch.full(shape, value, dtype=dtype, device=device)
+    if stream is None:
+        if value is None:
+            return torch.empty(shape, dtype=dtype, device=device)
+        return torch.full(shape, value, dtype=dtype, device=device)
+    s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))
+    with torch.cuda.stream(s):
+        return _new(shape, dtype, device, None, value)
 
 
 def _like(t: torch.Tensor | None, shape, dtype: torch.dtype, device, stream, what: str) -> torch.Tensor:
@@ -569,11 +582,13 @@ def _scratch(ws: torch.Tensor | None, nbytes: int, device, stream) -> torch.Tens
     return ws if ws is not None else _new(max(nbytes, 256), torch.uint8, device, stream)
 
 
+@lru_cache(maxsize=1024)
 def expert_rows(tokens: int, topk: int, experts: int, align: int = 1) -> int:
     """gc_expert_rows: rows that hold any routing (0 for arguments out of range)."""
     return int(load().gc_expert_rows(tokens, topk, experts, align))
 
 
+@lru_cache(maxsize=1024)
 def expert_workspace_bytes(tokens: int, topk: int, experts: int) -> int:
     return int(load().gc_expert_workspace_bytes(tokens, topk, experts))
 
@@ -588,31 +603,36 @@ def expert_dispatch(x: torch.Tensor | None, ids: torch.Tensor, experts: int, ali
     block starting at a multiple of `align`; rows without a pair are zeros.
     x None makes the plan alone (rows None).
     """
-    if ids.dim() != 2:
+    shape = ids.shape
+    if len(shape) != 2:
         raise ValueError("ids is [tokens, topk]")
-    tokens, topk = ids.shape
-    lib = load()
-    rows = plan.pairs.numel() if plan is not None else lib.gc_expert_rows(tokens, topk, experts, align)
+    tokens, topk = shape
     dev = ids.device
     if plan is None:
-        plan = ExpertPlan(*(_new(shape, torch.int32, dev, stream)
-                            for shape in ((experts + 1,), (experts,), (tokens, topk), (rows,))))
+        rows = expert_rows(tokens, topk, experts, align)
+        plan = ExpertPlan(_new(experts + 1, torch.int32, dev, stream), _new(experts, torch.int32, dev, stream),
+                          _new(shape, torch.int32, dev, stream), _new(rows, torch.int32, dev, stream))
+        where = [t.data_ptr() for t in plan]
+    else:
+        rows = plan.pairs.numel()
+        where = [_typed(plan.offsets, torch.int32, experts + 1, "plan.offsets"),
+                 _typed(plan.counts, torch.int32, experts, "plan.counts"),
+                 _typed(plan.slots, torch.int32, tokens * topk, "plan.slots"),
+                 _typed(plan.pairs, torch.int32, rows, "plan.pairs")]
     xp, xs, op, os, width, dt = None, 0, None, 0, 0, ROW_F32
     if x is not None:
         xp, xs = _rows(x)
-        if x.size(0) != tokens:
-            raise ValueError(f"x has {x.size(0)} rows, ids has {tokens} tokens")
-        width, dt = x.size(1), row_dtype_code(x.dtype)
+        n, width = x.shape
+        if n != tokens:
+            raise ValueError(f"x has {n} rows, ids has {tokens} tokens")
+        dt = row_dtype_code(x.dtype)
         out = _like(out, (rows, width), x.dtype, dev, stream, "out")
         op, os = _rows(out)
-    ws = _scratch(ws, lib.gc_expert_workspace_bytes(tokens, topk, experts), dev, stream)
-    _check(lib.gc_expert_dispatch(
-        _ptr(ids), _ids(ids), tokens, topk, experts, align, xp, xs, width, dt, op, os, rows,
-        _typed(plan.offsets, torch.int32, experts + 1, "plan.offsets"),
-        _typed(plan.counts, torch.int32, experts, "plan.counts"),
-        _typed(plan.slots, torch.int32, tokens * topk, "plan.slots"),
-        _typed(plan.pairs, torch.int32, rows, "plan.pairs"), _ptr(ws), ws.numel(), _stream(stream)),
-        "gc_expert_dispatch")
+    if ws is None:
+        ws = _scratch(None, expert_workspace_bytes(tokens, topk, experts), dev, stream)
+    _check(load().gc_expert_dispatch(
+        _ptr(ids), _ids(ids), tokens, topk, experts, align, xp, xs, width, dt, op, os, rows, *where, _ptr(ws),
+        ws.numel(), _handle(stream, dev)), "gc_expert_dispatch")
     return out, plan
 
 
@@ -629,7 +649,7 @@ def expert_combine(y: torch.Tensor, slots: torch.Tensor, weights: torch.Tensor |
     _check(load().gc_expert_combine(
         yp, ys, rows, _typed(slots, torch.int32, tokens * topk, "slots"),
         _typed(weights, torch.float32, tokens * topk, "weights"), tokens, topk, width,
-        row_dtype_code(y.dtype), op, os, _stream(stream)), "gc_expert_combine")
+        row_dtype_code(y.dtype), op, os, _handle(stream, y.device)), "gc_expert_combine")
     return out
 
 
@@ -667,7 +687,7 @@ def expert_combine_grad(g: torch.Tensor, y: torch.Tensor | None, slots: torch.Te
     _check(load().gc_expert_combine_grad(
         gp, gs, yp, ys, rows, _typed(slots, torch.int32, tokens * topk, "slots"),
         _typed(pairs, torch.int32, rows, "pairs"), _typed(weights, torch.float32, tokens * topk, "weights"),
-        tokens, topk, width, row_dtype_code(g.dtype), dp, ds, wp, _stream(stream)), "gc_expert_combine_grad")
+        tokens, topk, width, row_dtype_code(g.dtype), dp, ds, wp, _handle(stream, g.device)), "gc_expert_combine_grad")
     return dy, dweights if y is not None else None
 
 
@@ -680,7 +700,7 @@ def embedding(table: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, out: t
     out = _like(out, (*ids.shape, width), table.dtype, table.device, stream, "out")
     op, os = _rows(out if out.dim() == 2 else out.view(n, width))
     _check(load().gc_embedding(tp, ts, vocab, width, row_dtype_code(table.dtype), _ptr(ids), _ids(ids), n,
-                               scale, op, os, _stream(stream)), "gc_embedding")
+                               scale, op, os, _handle(stream, table.device)), "gc_embedding")
     return out
 
 
@@ -710,7 +730,7 @@ def embedding_grad(g: torch.Tensor, ids: torch.Tensor, vocab: int, scale: float 
     ws = _scratch(ws, lib.gc_embedding_grad_workspace_bytes(n, vocab, width), g.device, stream)
     _check(lib.gc_embedding_grad(gp, gs, row_dtype_code(g.dtype), _ptr(ids), _ids(ids), n, vocab, width, scale,
                                  op, os, row_dtype_code(dt), int(accumulate), _ptr(ws), ws.numel(),
-                                 _stream(stream)), "gc_embedding_grad")
+                                 _handle(stream, g.device)), "gc_embedding_grad")
     return out
 
 
@@ -745,5 +765,5 @@ def sample(logits: torch.Tensor, uniform: torch.Tensor | None = None, temperatur
                             _typed(top_k, torch.int32, rows, "top_k"),
                             _typed(top_p, torch.float32, rows, "top_p"),
                             _typed(min_p, torch.float32, rows, "min_p"), _ptr(tokens), _ptr(logprobs),
-                            _stream(stream)), "gc_sample")
+                            _handle(stream, dev)), "gc_sample")
     return tokens, logprobs

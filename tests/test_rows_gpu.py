@@ -316,12 +316,18 @@ def logits_of(rng, rows, vocab, dtype, kind, pad, shift):
         x[rng.random(x.shape) < 0.9] = torch.finfo(DTYPES[dtype]).min
     elif kind == "far":
         x *= 40
+    elif kind == "broken":
+        # NaN and -inf among the logits, and in every third row some infinities
+        x[rng.random(x.shape) < 0.2] = np.nan
+        x[rng.random(x.shape) < 0.1] = -np.inf
+        for r in range(0, rows, 3):
+            x[r, rng.integers(0, x.shape[1], 3)] = np.inf
     wide = torch.from_numpy(x).to(DTYPES[dtype])
     return wide.cuda()[:, shift:shift + vocab], wide[:, shift:shift + vocab].double().numpy()
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
-@pytest.mark.parametrize("kind", ["bulk", "peaked", "flat", "steps", "masked", "lowest", "far"])
+@pytest.mark.parametrize("kind", ["bulk", "peaked", "flat", "steps", "masked", "lowest", "far", "broken"])
 @pytest.mark.parametrize("vocab,pad,shift", [(1, 0, 0), (2, 3, 1), (33, 0, 0), (1000, 1, 1), (4096, 0, 8),
                                              (5003, 5, 2), (40001, 0, 0)])
 def test_sample(vocab, pad, shift, kind, dtype):
