@@ -49,7 +49,10 @@ constexpr uint32_t kBinsUsed = 42 * 64;
 constexpr float kBinsPerPower = 64.0f;
 constexpr int kSubBins = 1024;              // histogram of the list
 constexpr uint32_t kFew = 1024;             // of the list's tokens near a cut
-constexpr int kLoads = 4;                   // pieces of 16 bytes that a thread loads at a time
+#ifndef GC_SAMPLE_RING
+#define GC_SAMPLE_RING 3
+#endif
+constexpr int kRing = GC_SAMPLE_RING;       // pieces of 16 bytes that a thread has under way
 constexpr int kSample = 8;                  // pieces per thread that bound the k-th largest value
 constexpr float kFixed = 1099511627776.0f;  // 2^40
 constexpr float kUniformLo = 0x1p-25f, kUniformHi = 1.0f - 0x1p-24f;
@@ -133,6 +136,7 @@ struct KeySum {
 };
 
 struct Smem {
+    uint4 ring[kRing][kThreads];
     uint64_t list[kList];        // candidates; the leader's, then all of them
     alignas(16) uint32_t hist[kBins];
     union {
@@ -185,49 +189,68 @@ struct Row {
             for (uint32_t e = 0; e < kVec; ++e) p.v[e] = row_from_float<T>(-INFINITY);
         }
     }
-    // f(piece, index of its first) for this thread's pieces and, as a piece of
-    // one value, its single element; -inf where there is no token.  All
-    // threads of a warp call f together.  A piece's registers are loaded anew
-    // as soon as f has its copy, so N - 1 loads are under way throughout.
-    template <int N, class F>
-    __device__ __forceinline__ void each(const F &f) const
+    // f(piece, its copy in shared memory, index of its first) for this thread's
+    // pieces and, as a piece of one value, its single element; -inf where there
+    // is no token.  All threads of a warp call f together.  The pieces come
+    // through a ring of asynchronous copies, each thread's its own: kRing - 1 of
+    // them are under way at any time, and f's code is there once, which matters
+    // more than unrolling it (an unrolled f of the sizes below waits for
+    // instructions).
+    template <class F>
+    __device__ __forceinline__ void each(Smem &sm, const F &f) const
     {
+        uint4 *ring = &sm.ring[0][threadIdx.x];
+        Piece<T, kVec> none;
+#pragma unroll
+        for (uint32_t e = 0; e < kVec; ++e) none.v[e] = row_from_float<T>(-INFINITY);
+        auto copy = [&](uint32_t j, int slot) {
+            if (j < pieces)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(uint32_t(
+                                 __cvta_generic_to_shared(ring + slot * kThreads))),
+                             "l"(x + head + size_t(j) * kVec)
+                             : "memory");
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
         const uint32_t s = single();
-        if (__any_sync(kFull, s < vocab)) {
-            Piece<T, kVec> one;
+        bool lone = __any_sync(kFull, s < vocab);
+        if (!lone)
 #pragma unroll
-            for (uint32_t e = 1; e < kVec; ++e) one.v[e] = row_from_float<T>(-INFINITY);
-            one.v[0] = s < vocab ? x[s] : row_from_float<T>(-INFINITY);
-            f(one, s);
-        }
-        Piece<T, kVec> p[N];
+            for (int q = 0; q < kRing; ++q) copy(q * team + me, q);
+        int slot = 0;
+        for (uint32_t base = 0; lone || base < pieces;) {
+            Piece<T, kVec> now = none;
+            T *at = reinterpret_cast<T *>(ring + slot * kThreads);
+            uint32_t i = s;
+            if (lone) {
+                if (s < vocab) now.v[0] = x[s];
+                store_piece<T, kVec>(at, now);
+            } else {
+                asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
+                if (base + me < pieces) now = load_piece<T, kVec>(at);
+                i = head + (base + me) * kVec;
+            }
+            f(now, static_cast<const T *>(at), i);
+            if (lone) {
+                lone = false;
 #pragma unroll
-        for (int q = 0; q < N; ++q) load(q * team + me, p[q]);
-        for (uint32_t base = 0; base < pieces; base += N * team) {
-#pragma unroll
-            for (int q = 0; q < N; ++q) {
-                const Piece<T, kVec> now = p[q];
-                load(base + (N + q) * team + me, p[q]);
-                f(now, head + (base + q * team + me) * kVec);
+                for (int q = 0; q < kRing; ++q) copy(q * team + me, q);
+            } else {
+                copy(base + kRing * team + me, slot);  // f is done with the slot
+                slot = slot + 1 < kRing ? slot + 1 : 0;
+                base += team;
             }
         }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
     }
-    // u of the tokens of a piece, 0 past the end.  Rows of u that are aligned
-    // otherwise than the pieces are read as the 16-byte words around them.
+    // u of the tokens of a piece, 0 past the end.
     __device__ __forceinline__ void uniforms(uint32_t i, float (&r)[kVec]) const
     {
-        if (i >= 4u && i + kVec + 4u <= vocab && i >= head) {
-            const float4 *p = reinterpret_cast<const float4 *>(u + i - shift);
-            float w[kVec + 4];
+        if (shift == 0 && i >= head && i + kVec <= vocab) {
 #pragma unroll
-            for (uint32_t e = 0; e < kVec; e += 4) *reinterpret_cast<float4 *>(&w[e]) = __ldcs(p + e / 4);
-            if (shift) {
-                const float4 a = __ldcs(p + kVec / 4);
-                w[kVec] = a.x, w[kVec + 1] = a.y, w[kVec + 2] = a.z;
+            for (uint32_t e = 0; e < kVec; e += 4) {
+                const float4 w = __ldcs(reinterpret_cast<const float4 *>(u + i + e));
+                r[e] = w.x, r[e + 1] = w.y, r[e + 2] = w.z, r[e + 3] = w.w;
             }
-#pragma unroll
-            for (uint32_t e = 0; e < kVec; ++e)
-                r[e] = shift == 0 ? w[e] : shift == 1 ? w[e + 1] : shift == 2 ? w[e + 2] : w[e + 3];
         } else {
 #pragma unroll
             for (uint32_t e = 0; e < kVec; ++e) r[e] = i + e < vocab ? u[i + e] : 0.0f;
@@ -286,27 +309,17 @@ struct Team {
     }
     __device__ __forceinline__ uint64_t largest(uint64_t key) { return reduce(KeySum{key, 0.0f}).key; }
     __device__ __forceinline__ float sum(float v) { return reduce(KeySum{0u, v}).sum; }
-    // Adds the tokens of a piece with a bit in `which` to this CTA's list; all
-    // lanes of the warp together.
-    template <class T, int N>
-    __device__ __forceinline__ void append(uint32_t which, const Piece<T, N> &x, uint32_t i) const
+    // Adds the tokens of a piece (in shared memory) with a bit in `which` to
+    // this CTA's list.
+    template <class T>
+    __device__ __forceinline__ void append(uint32_t which, const T *x, uint32_t i) const
     {
-        const uint32_t lane = threadIdx.x & 31;
-        uint32_t c = __popc(which), incl = c;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t y = __shfl_up_sync(kFull, incl, o);
-            if (lane >= uint32_t(o)) incl += y;
+        if (which == 0u) return;
+        uint32_t at = atomicAdd(&sm.count, uint32_t(__popc(which)));
+        for (; which; which &= which - 1, ++at) {
+            const uint32_t e = __ffs(which) - 1;
+            if (at < kList) sm.list[at] = order_key(sample_value(row_to_float(x[e])), i + e);
         }
-        uint32_t at = 0u;
-        if (lane == 31) at = atomicAdd(&sm.count, incl);
-        at = __shfl_sync(kFull, at, 31) + incl - c;
-#pragma unroll
-        for (int e = 0; e < N; ++e)
-            if ((which >> e) & 1u) {
-                if (at < kList) sm.list[at] = order_key(sample_value(row_to_float(x.v[e])), i + e);
-                ++at;
-            }
     }
     // After a sync that follows every append: the tokens in all lists, to
     // every thread.  If they fit, the leader's list becomes all of them.
@@ -361,17 +374,22 @@ struct Draw {
         }
     }
     // Offers the tokens of a piece with a bit in `kept`; all lanes together.
-    template <uint32_t N>
-    __device__ __forceinline__ void offer(const float (&w)[N], uint32_t kept, const float (&u)[N], uint32_t i)
+    template <uint32_t N, class T>
+    __device__ __forceinline__ void offer(const float (&w)[N], uint32_t kept, const Row<T> &row, const Scale &scale,
+                                          const T *x, uint32_t i)
     {
+        float u[N];
+        row.uniforms(i, u);
         uint32_t any = 0u;
 #pragma unroll
         for (uint32_t e = 0; e < N; ++e) any |= open(w[e], fmaxf(u[e], kUniformLo)) ? 1u << e : 0u;
         any &= kept;
         if (!__any_sync(kFull, any != 0u)) return;
-#pragma unroll
-        for (uint32_t e = 0; e < N; ++e)
-            if ((any >> e) & 1u) take(w[e], u[e], i + e);
+        for (; any; any &= any - 1) {
+            const uint32_t e = __ffs(any) - 1;
+            take(scale.w(sample_value(row_to_float(x[e]))), row.u[i + e], i + e);
+        }
+        __syncwarp();
         share();
     }
     __device__ __forceinline__ uint64_t key() const { return best > 0.0f ? order_key(best, index) : 0u; }
@@ -634,7 +652,7 @@ __device__ __noinline__ bool find_cut(Team &team, const Row<T> &row, const Scale
     for (int b = threadIdx.x; b < kBins; b += kThreads) sm.hist[b] = 0u;
     team.sync();
     float mass = 0.0f;
-    row.template each<4>([&](const Piece<T, kVec> &x, uint32_t i) {
+    row.each(sm, [&](const Piece<T, kVec> &x, const T *, uint32_t i) {
 #pragma unroll
         for (uint32_t e = 0; e < kVec; ++e) {
             const float v = sample_value(row_to_float(x.v[e])), l = scale.log_w(v);
@@ -717,7 +735,7 @@ __device__ __noinline__ bool find_cut(Team &team, const Row<T> &row, const Scale
         const float low = fmaxf(scale.m - (float(bin) + 1.5f) * unit, -3.402823466e38f);
         mass = 0.0f;
         mine = Kept();
-        row.template each<4>([&](const Piece<T, kVec> &x, uint32_t i) {
+        row.each(sm, [&](const Piece<T, kVec> &x, const T *at, uint32_t i) {
             if (!__any_sync(kFull, piece_max(x) >= low)) return;
             float w[kVec];
             uint32_t list = 0u, sure = 0u;
@@ -732,12 +750,8 @@ __device__ __noinline__ bool find_cut(Team &team, const Row<T> &row, const Scale
                 mine.sum += keep ? w[e] : 0.0f;
                 if (keep) sure |= 1u << e;
             }
-            if (__any_sync(kFull, list != 0u)) team.append(list, x, i);
-            if (kept && __any_sync(kFull, sure != 0u)) {
-                float u[kVec];
-                row.uniforms(i, u);
-                mine.draw.offer(w, sure, u, i);
-            }
+            team.append(list, at, i);
+            if (kept && __any_sync(kFull, sure != 0u)) mine.draw.offer(w, sure, row, scale, at, i);
         });
         mass = team.sum(mass);  // past which every list is complete
         const uint32_t n = team.gather_lists();
@@ -792,7 +806,7 @@ __device__ __noinline__ bool find_cut(Team &team, const Row<T> &row, const Scale
         if (team.rank == 0) {
             const Row<T> whole(row.x, row.u, row.vocab, 0, 1);
             const uint64_t cut = select_cut(target, sm, [&](auto add) {
-                whole.template each<1>([&](const Piece<T, kVec> &x, uint32_t i) {
+                whole.each(sm, [&](const Piece<T, kVec> &x, const T *, uint32_t i) {
 #pragma unroll
                     for (uint32_t e = 0; e < kVec; ++e) {
                         const float v = sample_value(row_to_float(x.v[e]));
@@ -900,24 +914,24 @@ sample_kernel(const T *__restrict__ logits, size_t logits_stride, uint32_t vocab
         if (!brief) {
             float best = -INFINITY;
 #pragma unroll
-            for (int b = 0; b < kSample; b += kLoads) {
-                Piece<T, kVec> pc[kLoads];
+            for (int b = 0; b < kSample; b += kSample / 2) {
+                Piece<T, kVec> pc[kSample / 2];
 #pragma unroll
-                for (int j = 0; j < kLoads; ++j) row.load((b + j) * row.team + row.me, pc[j]);
+                for (int j = 0; j < kSample / 2; ++j) row.load((b + j) * row.team + row.me, pc[j]);
 #pragma unroll
-                for (int j = 0; j < kLoads; ++j) best = fmaxf(best, piece_max(pc[j]));
+                for (int j = 0; j < kSample / 2; ++j) best = fmaxf(best, piece_max(pc[j]));
             }
             const uint32_t least = kth_largest(best > -INFINITY ? order_bits(sample_value(best)) : 0u, k);
             if (least) threshold = order_value(least);
         }
         threshold = fmaxf(threshold, -3.402823466e38f);  // -inf is no candidate
-        row.template each<kLoads>([&](const Piece<T, kVec> &x, uint32_t i) {
+        row.each(sm, [&](const Piece<T, kVec> &x, const T *at, uint32_t i) {
             if (!__any_sync(kFull, piece_max(x) >= threshold)) return;
             uint32_t which = 0u;
 #pragma unroll
             for (uint32_t e = 0; e < kVec; ++e)
                 if (row_to_float(x.v[e]) >= threshold) which |= 1u << e;
-            team.append(which, x, i);
+            team.append(which, at, i);
         });
         team.sync();
         const uint32_t n = team.gather_lists();
@@ -938,13 +952,12 @@ sample_kernel(const T *__restrict__ logits, size_t logits_stride, uint32_t vocab
     // The first of the order.
     float best = -INFINITY;
     uint32_t at = ~0u;
-    row.template each<kLoads>([&](const Piece<T, kVec> &x, uint32_t i) {
+    row.each(sm, [&](const Piece<T, kVec> &x, const T *p, uint32_t i) {
         const float top = sample_value(piece_max(x));
         if (top > best || (top == best && i < at)) {
             best = top;
-#pragma unroll
             for (int e = int(kVec) - 1; e >= 0; --e)
-                if (sample_value(row_to_float(x.v[e])) == top) at = i + e;
+                if (sample_value(row_to_float(p[e])) == top) at = i + e;
         }
     });
     const uint64_t first = team.largest(best > -INFINITY ? order_key(best, at) : 0u);
@@ -965,10 +978,10 @@ sample_kernel(const T *__restrict__ logits, size_t logits_stride, uint32_t vocab
         done = cut_key ? find_cut<true, true>(team, row, scale, cut_key, 0u, p, q, &kept, cut_key)
                        : find_cut<true, false>(team, row, scale, 0u, 0u, p, q, &kept, cut_key);
     if (!done) {
-        kept = Kept();
+        Kept last;  // one whose address nobody takes
         const Cut cut(cut_key);
         const bool all = cut_key == 0u;
-        row.template each<2>([&](const Piece<T, kVec> &x, uint32_t i) {
+        row.each(sm, [&](const Piece<T, kVec> &x, const T *at, uint32_t i) {
             float w[kVec];
             uint32_t in = 0u;
 #pragma unroll
@@ -983,11 +996,10 @@ sample_kernel(const T *__restrict__ logits, size_t logits_stride, uint32_t vocab
                     if (!cut.keeps(sample_value(row_to_float(x.v[e])), i + e)) in &= ~(1u << e);
             if (!__any_sync(kFull, in != 0u)) return;
 #pragma unroll
-            for (uint32_t e = 0; e < kVec; ++e) kept.sum += (in >> e) & 1u ? w[e] : 0.0f;
-            float u[kVec];
-            row.uniforms(i, u);
-            kept.draw.offer(w, in, u, i);
+            for (uint32_t e = 0; e < kVec; ++e) last.sum += (in >> e) & 1u ? w[e] : 0.0f;
+            last.draw.offer(w, in, row, scale, at, i);
         });
+        kept = last;
     }
     const KeySum end = team.reduce(KeySum{kept.draw.key(), kept.sum});
     if (team.rank == 0 && threadIdx.x == 0) {
@@ -1005,7 +1017,7 @@ cudaError_t run_sample(const void *logits, uint32_t rows, uint32_t vocab, cudaSt
     const uint64_t slots = uint64_t(kResident) * uint64_t(gch::sm_count());
     uint32_t team = 1;
     while (team < kMaxTeam && uint64_t(rows) * (2 * team) <= slots &&
-           vocab >= 2 * team * (kThreads * kLoads * uint32_t(16 / sizeof(T))))
+           vocab >= 2 * team * (kThreads * 4 * uint32_t(16 / sizeof(T))))
         team *= 2;
     // Raises the kernel's shared-memory limit, once per device.
     auto kernel = sample_kernel<T>;
