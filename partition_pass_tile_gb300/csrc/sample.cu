@@ -9,8 +9,8 @@
 // not depend on its order.
 //
 // A team of 1 to 8 CTAs (a cluster) owns a row; the first CTA is its leader.
-//   - no cut (neither top-k nor top-p): one pass for the maximum, one for the
-//     sum and the draw;
+//   - no filter: one pass for the sum and the draw; min-p alone: one before it
+//     for the maximum;
 //   - a small top-k, or a short row: one pass collects the candidates, the
 //     tokens not below a lower bound of the top_k-th largest value, in the
 //     leader's shared memory, which sorts them and does the rest there;
@@ -878,6 +878,38 @@ __device__ __noinline__ void finish_list(Smem &sm, uint32_t n, uint32_t k, float
         }
 }
 
+// The tokens from the cut on that weigh at least q: the sum of their weights
+// and the draw, this thread's share.
+template <class T>
+__device__ __noinline__ Kept draw_row(const Team &team, const Row<T> &row, const Scale &row_scale, uint64_t cut_key,
+                                      float q)
+{
+    constexpr uint32_t kVec = Row<T>::kVec;
+    Kept kept;
+    const Scale scale = row_scale;
+    const Cut cut(cut_key);
+    const bool all = cut_key == 0u;
+    row.each(team.sm, [&](const Piece<T, kVec> &x, const T *at, uint32_t i) {
+        float w[kVec];
+        uint32_t in = 0u;
+#pragma unroll
+        for (uint32_t e = 0; e < kVec; ++e) {
+            const float v = sample_value(row_to_float(x.v[e]));
+            w[e] = scale.w(v);
+            if (w[e] >= q && w[e] > 0.0f) in |= 1u << e;
+        }
+        if (!all)
+#pragma unroll
+            for (uint32_t e = 0; e < kVec; ++e)
+                if (!cut.keeps(sample_value(row_to_float(x.v[e])), i + e)) in &= ~(1u << e);
+        if (!__any_sync(kFull, in != 0u)) return;
+#pragma unroll
+        for (uint32_t e = 0; e < kVec; ++e) kept.sum += (in >> e) & 1u ? w[e] : 0.0f;
+        kept.draw.offer(w, in, row, scale, at, i);
+    });
+    return kept;
+}
+
 template <class T>
 __global__ void __launch_bounds__(kThreads, kResident)
 sample_kernel(const T *__restrict__ logits, size_t logits_stride, uint32_t vocab,
@@ -949,6 +981,29 @@ sample_kernel(const T *__restrict__ logits, size_t logits_stride, uint32_t vocab
         }
     }
 
+    // Without a filter nothing needs the maximum: any token near it serves as
+    // the weights' unit, and one pass is enough unless they come out too large.
+    if (!greedy && k == vocab && p >= 1.0f && q == 0.0f) {
+        Piece<T, kVec> pc;
+        row.load(row.me, pc);
+        const float near = sample_value(piece_max(pc));
+        const uint64_t unit = team.largest(near > -INFINITY ? order_key(near, 0u) : 0u);
+        if (unit != 0u) {
+            const Scale scale(key_value(unit), t);
+            const Kept kept = draw_row(team, row, scale, 0u, 0.0f);
+            const KeySum end = team.reduce(KeySum{kept.draw.key(), kept.sum});
+            if (end.sum < 1e30f) {
+                if (team.rank == 0 && threadIdx.x == 0) {
+                    const uint32_t i = key_index(end.key);
+                    *token = int32_t(i);
+                    if (logprob) *logprob = scale.z(row.value(i)) - logf(end.sum);
+                }
+                team.sync();  // no CTA leaves while another may write to its slots
+                return;
+            }
+        }
+    }
+
     // The first of the order.
     float best = -INFINITY;
     uint32_t at = ~0u;
@@ -977,30 +1032,7 @@ sample_kernel(const T *__restrict__ logits, size_t logits_stride, uint32_t vocab
     if (p < 1.0f)
         done = cut_key ? find_cut<true, true>(team, row, scale, cut_key, 0u, p, q, &kept, cut_key)
                        : find_cut<true, false>(team, row, scale, 0u, 0u, p, q, &kept, cut_key);
-    if (!done) {
-        Kept last;  // one whose address nobody takes
-        const Cut cut(cut_key);
-        const bool all = cut_key == 0u;
-        row.each(sm, [&](const Piece<T, kVec> &x, const T *at, uint32_t i) {
-            float w[kVec];
-            uint32_t in = 0u;
-#pragma unroll
-            for (uint32_t e = 0; e < kVec; ++e) {
-                const float v = sample_value(row_to_float(x.v[e]));
-                w[e] = scale.w(v);
-                if (w[e] >= q && w[e] > 0.0f) in |= 1u << e;
-            }
-            if (!all)
-#pragma unroll
-                for (uint32_t e = 0; e < kVec; ++e)
-                    if (!cut.keeps(sample_value(row_to_float(x.v[e])), i + e)) in &= ~(1u << e);
-            if (!__any_sync(kFull, in != 0u)) return;
-#pragma unroll
-            for (uint32_t e = 0; e < kVec; ++e) last.sum += (in >> e) & 1u ? w[e] : 0.0f;
-            last.draw.offer(w, in, row, scale, at, i);
-        });
-        kept = last;
-    }
+    if (!done) kept = draw_row(team, row, scale, cut_key, q);
     const KeySum end = team.reduce(KeySum{kept.draw.key(), kept.sum});
     if (team.rank == 0 && threadIdx.x == 0) {
         const uint32_t i = key_index(end.key);
@@ -1013,11 +1045,11 @@ sample_kernel(const T *__restrict__ logits, size_t logits_stride, uint32_t vocab
 template <class T, class... A>
 cudaError_t run_sample(const void *logits, uint32_t rows, uint32_t vocab, cudaStream_t s, size_t stride, A... args)
 {
-    // Few rows are spread over more CTAs, down to four pieces per thread.
+    // Few rows are spread over more CTAs, down to two pieces per thread.
     const uint64_t slots = uint64_t(kResident) * uint64_t(gch::sm_count());
     uint32_t team = 1;
     while (team < kMaxTeam && uint64_t(rows) * (2 * team) <= slots &&
-           vocab >= 2 * team * (kThreads * 4 * uint32_t(16 / sizeof(T))))
+           vocab >= 2 * team * (kThreads * 2 * uint32_t(16 / sizeof(T))))
         team *= 2;
     // Raises the kernel's shared-memory limit, once per device.
     auto kernel = sample_kernel<T>;
