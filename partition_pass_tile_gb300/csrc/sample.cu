@@ -322,24 +322,33 @@ struct Team {
         }
     }
     // After a sync that follows every append: the tokens in all lists, to
-    // every thread.  If they fit, the leader's list becomes all of them.
+    // every thread.  If they fit, the leader's list becomes all of them; its
+    // threads read the others' lists as one.
     __device__ __forceinline__ uint32_t gather_lists() const
     {
-        uint32_t n = sm.count;
-        if (size > 1) {
-            n = 0u;
-            for (uint32_t c = 0; c < size; ++c) n += peer(c)->count;
-            if (rank == 0 && n <= kList) {
-                uint32_t at = sm.count;
-                for (uint32_t c = 1; c < size; ++c) {
-                    const Smem *p = peer(c);
-                    const uint32_t m = p->count;
-                    for (uint32_t j = threadIdx.x; j < m; j += kThreads) sm.list[at + j] = p->list[j];
-                    at += m;
-                }
-            }
-            __syncthreads();
+        if (size == 1) return sm.count;
+        const uint32_t lane = threadIdx.x & 31;
+        uint32_t upto = lane < size ? peer(lane)->count : 0u;
+#pragma unroll
+        for (uint32_t o = 1; o < kMaxTeam; o <<= 1) {
+            const uint32_t y = __shfl_up_sync(kFull, upto, o);
+            if (lane >= o) upto += y;
         }
+        const uint32_t n = __shfl_sync(kFull, upto, size - 1), mine = __shfl_sync(kFull, upto, 0);
+        if (rank == 0 && n <= kList)
+            for (uint32_t base = mine; base < n; base += kThreads) {
+                const uint32_t j = base + threadIdx.x;
+                uint32_t c = 0u, start = 0u;
+                for (uint32_t q = 0; q + 1 < size; ++q) {
+                    const uint32_t end = __shfl_sync(kFull, upto, q);
+                    if (j >= end) {
+                        c = q + 1;
+                        start = end;
+                    }
+                }
+                if (j < n) sm.list[j] = peer(c)->list[j - start];
+            }
+        __syncthreads();
         return n;
     }
 };
@@ -689,7 +698,9 @@ __device__ __noinline__ bool find_cut(Team &team, const Row<T> &row, const Scale
             uint64_t part[kPer], sum = 0u, all;
 #pragma unroll
             for (int j = 0; j < kPer; ++j) part[j] = 0u;
-            for (uint32_t c = 0; c < team.size; ++c) {
+#pragma unroll
+            for (uint32_t c = 0; c < kMaxTeam; ++c) {
+                if (c >= team.size) break;
                 const uint4 *h = reinterpret_cast<const uint4 *>(team.peer(c)->hist) + threadIdx.x * (kPer / 4);
 #pragma unroll
                 for (int j = 0; j < kPer; j += 4) {
