@@ -25,7 +25,10 @@ constexpr uint32_t kBlock = 32;     // sorted positions per block
 #ifndef GC_SUMS_CTAS
 #define GC_SUMS_CTAS 4
 #endif
-constexpr int kLookups = 4;         // rows per thread of a lookup
+#ifndef GC_LOOKUPS
+#define GC_LOOKUPS 4
+#endif
+constexpr int kLookups = GC_LOOKUPS;         // rows per thread of a lookup
 constexpr size_t kZeroBytes = 32768;  // zeroed per CTA of the sums, about
 // A bulk sum's CTA holds kBlock rows of up to this many bytes per row of
 // threads, 64 KiB in all: three CTAs to an SM.
@@ -108,25 +111,15 @@ struct TokenSink {
 struct ZeroRows {
     uint8_t *rows;
     size_t stride, bytes;  // of a row
-    uint32_t piece;        // bytes to a store
     const uint8_t *seen;
     uint32_t lo, hi;
-    template <class P>
-    __device__ __forceinline__ void row(uint8_t *p) const
-    {
-        for (size_t i = threadIdx.x & 31; i < bytes / sizeof(P); i += 32) reinterpret_cast<P *>(p)[i] = P{};
-    }
     __device__ __forceinline__ void run(uint32_t cta, uint32_t ctas) const
     {
         const uint32_t warps = blockDim.x * blockDim.y / 32, warp = (threadIdx.y * blockDim.x + threadIdx.x) / 32;
         const uint64_t first = lo + uint64_t(cta) * warps + warp;
         for (uint64_t v = first; v < hi; v += uint64_t(ctas) * warps) {
             if (seen != nullptr && seen[v]) continue;
-            uint8_t *p = rows + v * stride;
-            if (piece == 16) row<uint4>(p);
-            else if (piece == 8) row<uint2>(p);
-            else if (piece == 4) row<uint32_t>(p);
-            else row<uint16_t>(p);
+            zero_row(rows + v * stride, bytes);
         }
     }
 };
@@ -145,6 +138,7 @@ token_sort_kernel(const void *ids, bool wide, uint32_t n, uint32_t vocab, uint32
 {
     extern __shared__ __align__(16) uint8_t token_smem[];
     TokenSortSmem &sm = *reinterpret_cast<TokenSortSmem *>(token_smem);
+    chain_start();
     if (blockIdx.x > 0) {
         zero.run(blockIdx.x - 1, gridDim.x - 1);
         return;
@@ -182,6 +176,8 @@ token_sums_kernel(const uint2 *__restrict__ sorted, uint32_t n, const T *__restr
 {
     O *rows = static_cast<O *>(out.rows);
     const uint32_t columns = blockDim.x * N;
+    chain_start();
+    chain_wait();
     if (blockIdx.x >= sums) {
         zero.run(blockIdx.x - sums, gridDim.x - sums);
         return;
@@ -253,6 +249,8 @@ token_bulk_sums_kernel(const uint2 *__restrict__ sorted, uint32_t n, const T *__
                        uint32_t width, float *__restrict__ edges, GradOut out, uint32_t parts, uint8_t *ws,
                        uint64_t timeout_ns, uint32_t sums, ZeroRows zero)
 {
+    chain_start();
+    chain_wait();
     if (blockIdx.x >= sums) {
         zero.run(blockIdx.x - sums, gridDim.x - sums);
         return;
@@ -346,6 +344,7 @@ token_join_kernel(const uint2 *__restrict__ sorted, uint32_t n, uint32_t width, 
 {
     constexpr int kAhead = 8;
     __shared__ Piece<float, N> s_sum[kJoiners][32];
+    chain_wait();
     const uint32_t block = blockIdx.x / parts, lane = threadIdx.x, share = threadIdx.y;
     const uint32_t c = (blockIdx.x % parts) * 32 * N + lane * N;
     const uint32_t blocks = (n + kBlock - 1) / kBlock;
@@ -449,25 +448,36 @@ cudaError_t run_grad_rows(const uint2 *sorted, uint32_t n, const void *g, size_t
     const size_t sums = gch::ceil_div(blocks, threads.y) * parts;
     const size_t joins = blocks > 1 ? (blocks - 1) * gch::ceil_div(width / N, 32) : 0;
     if (sums + zeros > 0x7fffffffu || joins > 0x7fffffffu) return cudaErrorInvalidConfiguration;
-    if (sums + zeros > 0 && bulk) {
+    if (n == 0) {
+        // Only zeros, after the clear, which is no kernel to chain to.
+        if (zeros > 0)
+            token_sums_kernel<T, O, N, false><<<zeros, threads, 0, s>>>(sorted, n, static_cast<const T *>(g), g_stride,
+                                                                       uint32_t(width), edges, out, uint32_t(parts), 0u,
+                                                                       zero);
+        return cudaGetLastError();
+    }
+    if (bulk) {
         auto kernel = out.accumulate ? token_bulk_sums_kernel<T, O, N, true> : token_bulk_sums_kernel<T, O, N, false>;
         const size_t smem = size_t(threads.x) * N * sizeof(T) * kBlock * threads.y;
         // Raises the kernel's shared-memory limit, once per device.
         if (gch::persistent_grid(reinterpret_cast<const void *>(kernel), kRowThreads, size_t(kSliceBytes) * kBlock, 1) <= 0)
             return cudaErrorInvalidConfiguration;
-        kernel<<<uint32_t(sums + zeros), threads, smem, s>>>(sorted, n, static_cast<const T *>(g), g_stride,
-                                                             uint32_t(width), edges, out, uint32_t(parts), ws,
-                                                             gch::LaunchOpts{}.timeout_ns, uint32_t(sums), zero);
-    } else if (sums + zeros > 0) {
+        const cudaError_t e = gch::launch_next(kernel, dim3(uint32_t(sums + zeros)), threads, smem, s, sorted, n,
+                                               static_cast<const T *>(g), g_stride, uint32_t(width), edges, out,
+                                               uint32_t(parts), ws, gch::LaunchOpts{}.timeout_ns, uint32_t(sums), zero);
+        if (e != cudaSuccess) return e;
+    } else {
         auto kernel = out.accumulate ? token_sums_kernel<T, O, N, true> : token_sums_kernel<T, O, N, false>;
-        kernel<<<uint32_t(sums + zeros), threads, 0, s>>>(sorted, n, static_cast<const T *>(g), g_stride,
-                                                          uint32_t(width), edges, out, uint32_t(parts),
-                                                          uint32_t(sums), zero);
+        const cudaError_t e = gch::launch_next(kernel, dim3(uint32_t(sums + zeros)), threads, 0, s, sorted, n,
+                                               static_cast<const T *>(g), g_stride, uint32_t(width), edges, out,
+                                               uint32_t(parts), uint32_t(sums), zero);
+        if (e != cudaSuccess) return e;
     }
     if (joins > 0)
-        token_join_kernel<O, N><<<uint32_t(joins), dim3(32, kJoiners), 0, s>>>(
-            sorted, n, uint32_t(width), edges, out, uint32_t(gch::ceil_div(width / N, 32)));
-    return cudaGetLastError();
+        return gch::launch_next(token_join_kernel<O, N>, dim3(uint32_t(joins)), dim3(32, kJoiners), 0, s, sorted, n,
+                                uint32_t(width), static_cast<const float *>(edges), out,
+                                uint32_t(gch::ceil_div(width / N, 32)));
+    return cudaSuccess;
 }
 
 // Pieces of N elements, N a power of two that both rows allow and that fills
@@ -533,9 +543,7 @@ cudaError_t launch_embedding_grad(const void *g, size_t g_stride, gc_row_dtype g
     float *edges = reinterpret_cast<float *>(ws + l.edges);
     const int bits = key_bits(vocab), passes = int(ceil_div(bits, 9)), digit = int(ceil_div(bits, passes));
     const size_t elem = odt == GC_ROW_F32 ? 4 : 2;
-    const int to = piece_elems(uint64_t(uintptr_t(dtable)) | elem * (dtable_stride | width), int(elem));
-    ZeroRows zero{static_cast<uint8_t *>(dtable), dtable_stride * elem, width * elem, uint32_t(to * elem), seen, 0u,
-                  accumulate ? 0u : vocab};
+    ZeroRows zero{static_cast<uint8_t *>(dtable), dtable_stride * elem, width * elem, seen, 0u, accumulate ? 0u : vocab};
     // A kernel's part of the rows to zero, about `bytes`; the rest stays.
     auto part = [&](size_t bytes) {
         ZeroRows z = zero;
@@ -563,7 +571,8 @@ cudaError_t launch_embedding_grad(const void *g, size_t g_stride, gc_row_dtype g
             const TokenSink sink{src, items[(p & 1) ^ 1]};
             // The first count finds out which tokens are absent.
             const ZeroRows beside = part(p == 0 ? 0 : kCountZeros);
-            e = gcd::launch_bin_count(src, n, 1u << digit, table, s, beside, beside.lo < beside.hi ? kZeroCtas : 0u);
+            e = gcd::launch_bin_count(src, n, 1u << digit, table, s, beside, beside.lo < beside.hi ? kZeroCtas : 0u,
+                                      p > 0);
             if (e != cudaSuccess) break;
             const ZeroRows beside_place = part(kPlaceZeros);
             e = gcd::launch_bin_place(src, sink, n, 1u << digit, 1u, table, s, beside_place,

@@ -48,17 +48,18 @@ dim3 row_block(size_t pieces)
     return dim3(tx, kRowThreads / tx);
 }
 
-// Rows without a pair: -1 in pairs and zeros.  One warp takes 32 rows, each
-// lane looks one up in the experts' blocks.
-template <class E, int N>
+// Rows without a pair: -1 in pairs and zeros.  One warp takes kPadRows rows,
+// each lane looks one up in the experts' blocks.
+constexpr uint32_t kPadRows = 8;
+
 __device__ __forceinline__ void expert_pad_rows(uint32_t first, uint32_t rows, uint32_t experts,
                                                 const int32_t *__restrict__ offsets,
                                                 const int32_t *__restrict__ counts, int32_t *__restrict__ pairs,
-                                                E *__restrict__ out, size_t out_stride, uint32_t pieces)
+                                                uint8_t *__restrict__ out, size_t stride_bytes, size_t row_bytes)
 {
     const uint32_t lane = threadIdx.x & 31, r = first + lane;
     bool pad = false;
-    if (r < rows) {
+    if (lane < kPadRows && r < rows) {
         pad = r >= uint32_t(offsets[experts]);
         if (!pad) {
             // the last block that starts at or before r, which is not an empty one
@@ -74,27 +75,39 @@ __device__ __forceinline__ void expert_pad_rows(uint32_t first, uint32_t rows, u
     }
     uint32_t left = __ballot_sync(0xffffffffu, pad);
     if (out == nullptr) return;
-    for (; left; left &= left - 1) {
-        E *dst = out + size_t(first + __ffs(left) - 1) * out_stride;
-        for (uint32_t c = lane; c < pieces; c += 32) store_piece<E, N>(dst + size_t(c) * N, Piece<E, N>{});
-    }
+    for (; left; left &= left - 1) zero_row(out + size_t(first + __ffs(left) - 1) * stride_bytes, row_bytes);
 }
 
-// One token's row to its slots: read once, written up to topk times.
+// One token's row to its slots: read once, kSpread pieces per thread at a
+// time, and written up to topk times.
+constexpr int kSpread = 4;
+
 template <class E, int N>
 __device__ __forceinline__ void expert_spread_row(const E *__restrict__ src, const uint32_t *slots, uint32_t topk,
                                                   uint32_t rows, E *__restrict__ out, size_t out_stride,
                                                   uint32_t pieces)
 {
-    for (uint32_t c = threadIdx.x; c < pieces; c += blockDim.x) {
-        const Piece<E, N> v = load_piece<E, N>(src + size_t(c) * N);
-        for (uint32_t j = 0; j < topk; ++j)
-            if (slots[j] < rows) store_piece<E, N>(out + size_t(slots[j]) * out_stride + size_t(c) * N, v);
+    for (uint32_t base = threadIdx.x; base < pieces; base += kSpread * blockDim.x) {
+        Piece<E, N> v[kSpread];
+#pragma unroll
+        for (int q = 0; q < kSpread; ++q) {
+            const uint32_t c = base + q * blockDim.x;
+            if (c < pieces) v[q] = load_piece<E, N>(src + size_t(c) * N);
+        }
+        for (uint32_t j = 0; j < topk; ++j) {
+            if (slots[j] >= rows) continue;
+            E *dst = out + size_t(slots[j]) * out_stride;
+#pragma unroll
+            for (int q = 0; q < kSpread; ++q) {
+                const uint32_t c = base + q * blockDim.x;
+                if (c < pieces) store_piece<E, N>(dst + size_t(c) * N, v[q]);
+            }
+        }
     }
 }
 
 // E: an integer of the element's size.  CTAs below `spread` move tokens, one
-// to a row of threads; the others take 32 rows per warp.
+// to a row of threads; the others look for rows without a pair.
 template <class E, int N>
 __global__ void __launch_bounds__(kRowThreads)
 expert_rows_kernel(const E *__restrict__ x, size_t x_stride, uint32_t tokens, uint32_t topk, uint32_t experts,
@@ -102,11 +115,13 @@ expert_rows_kernel(const E *__restrict__ x, size_t x_stride, uint32_t tokens, ui
                    const int32_t *__restrict__ slots, int32_t *__restrict__ pairs, uint32_t rows,
                    E *__restrict__ out, size_t out_stride, uint32_t pieces, uint32_t spread)
 {
+    chain_wait();
     if (blockIdx.x >= spread) {
         const uint32_t warp = (threadIdx.y * blockDim.x + threadIdx.x) >> 5;
-        const uint64_t first = (uint64_t(blockIdx.x - spread) * (kRowThreads / 32) + warp) * 32u;
+        const uint64_t first = (uint64_t(blockIdx.x - spread) * (kRowThreads / 32) + warp) * kPadRows;
         if (first < rows)
-            expert_pad_rows<E, N>(uint32_t(first), rows, experts, offsets, counts, pairs, out, out_stride, pieces);
+            expert_pad_rows(uint32_t(first), rows, experts, offsets, counts, pairs, reinterpret_cast<uint8_t *>(out),
+                            out_stride * sizeof(E), size_t(pieces) * N * sizeof(E));
         return;
     }
     __shared__ uint32_t s_slots[kRowThreads / 32][GC_MAX_TOPK];
@@ -124,7 +139,7 @@ expert_rows_kernel(const E *__restrict__ x, size_t x_stride, uint32_t tokens, ui
 
 // The whole dispatch of up to kSmallPairs pairs in one launch: every CTA counts
 // all pairs itself, which takes less than a second launch.  CTAs below tokens
-// move one token each, the others 32 rows per warp.
+// move one token each, the others look for rows without a pair.
 constexpr uint32_t kSmallPairs = 1024;
 
 template <class E, int N>
@@ -162,9 +177,10 @@ expert_small_kernel(ExpertSource src, ExpertSink sink, uint32_t npairs, uint32_t
     __syncthreads();
     const uint32_t t = blockIdx.x, tokens = npairs / topk;
     if (t >= tokens) {
-        const uint32_t first = ((t - tokens) * (kRowThreads / 32) + warp) * 32u;
+        const uint32_t first = ((t - tokens) * (kRowThreads / 32) + warp) * kPadRows;
         if (first < rows)
-            expert_pad_rows<E, N>(first, rows, experts, s_offsets, s_counts, sink.pairs, out, out_stride, pieces);
+            expert_pad_rows(first, rows, experts, s_offsets, s_counts, sink.pairs, reinterpret_cast<uint8_t *>(out),
+                            out_stride * sizeof(E), size_t(pieces) * N * sizeof(E));
         return;
     }
     // A warp per choice: the earlier pairs of the same expert.
@@ -186,16 +202,10 @@ expert_small_kernel(ExpertSource src, ExpertSink sink, uint32_t npairs, uint32_t
 }
 
 // The rows of kAhead choices are loaded together.
-#ifndef GC_COMBINE_AHEAD
-#define GC_COMBINE_AHEAD 4
-#endif
-#ifndef GC_COMBINE_CTAS
-#define GC_COMBINE_CTAS 4
-#endif
-constexpr int kAhead = GC_COMBINE_AHEAD;
+constexpr int kAhead = 4;
 
 template <class T, int N>
-__global__ void __launch_bounds__(kRowThreads, GC_COMBINE_CTAS)
+__global__ void __launch_bounds__(kRowThreads, 4)
 expert_combine_kernel(const T *__restrict__ y, size_t y_stride, uint32_t rows, const int32_t *__restrict__ slots,
                       const float *__restrict__ weights, uint32_t tokens, uint32_t topk, uint32_t pieces,
                       T *__restrict__ out, size_t out_stride)
@@ -300,7 +310,7 @@ template <class E, int N>
 void run_rows(const void *x, size_t x_stride, size_t width, uint32_t tokens, uint32_t topk, const ExpertSource &src,
               const ExpertSink &sink, uint32_t align, uint32_t rows, void *out, size_t out_stride, cudaStream_t s)
 {
-    const uint32_t pieces = uint32_t(width / N), pads = uint32_t(gch::ceil_div(rows, kRowThreads));
+    const uint32_t pieces = uint32_t(width / N), pads = uint32_t(gch::ceil_div(rows, kPadRows * (kRowThreads / 32)));
     const E *from = static_cast<const E *>(x);
     E *to = static_cast<E *>(out);
     if (tokens * topk <= kSmallPairs) {
@@ -310,9 +320,9 @@ void run_rows(const void *x, size_t x_stride, size_t width, uint32_t tokens, uin
     }
     const dim3 block = row_block(pieces);
     const uint32_t spread = out ? uint32_t(gch::ceil_div(tokens, block.y)) : 0;
-    expert_rows_kernel<E, N><<<spread + pads, block, 0, s>>>(from, x_stride, tokens, topk, src.experts, sink.offsets,
-                                                             sink.counts, sink.slots, sink.pairs, rows, to, out_stride,
-                                                             pieces, spread);
+    gch::launch_next(expert_rows_kernel<E, N>, dim3(spread + pads), block, 0, s, from, x_stride, tokens, topk,
+                     src.experts, static_cast<const int32_t *>(sink.offsets), static_cast<const int32_t *>(sink.counts),
+                     static_cast<const int32_t *>(sink.slots), sink.pairs, rows, to, out_stride, pieces, spread);
 }
 
 // Row kernels by piece size: 16 bytes down to one element.

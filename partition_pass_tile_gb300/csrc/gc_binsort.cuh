@@ -73,6 +73,8 @@ bin_count_kernel(Source src, uint32_t n, uint32_t chunk, uint32_t chunks, uint32
                  uint32_t *__restrict__ counts, Extra extra)
 {
     __shared__ uint32_t s_hist[kMaxBins];
+    chain_start();
+    chain_wait();
     if (blockIdx.x >= chunks) {
         extra.run(blockIdx.x - chunks, gridDim.x - chunks);
         return;
@@ -217,18 +219,25 @@ bin_place_kernel(Source src, Sink sink, uint32_t n, uint32_t chunk, uint32_t chu
 {
     extern __shared__ uint32_t s_cnt[];
     __shared__ BinSmem sm;
+    chain_start();
+    chain_wait();
     if (blockIdx.x < chunks) bin_place_chunk(src, sink, n, chunk, chunks, blockIdx.x, bins, align, counts, s_cnt, sm);
     else extra.run(blockIdx.x - chunks, gridDim.x - chunks);
 }
 
-// `others`: CTAs for `extra`.
+// `others`: CTAs for `extra`.  Both are kernels of a chain (launch_next), the
+// count kernel its first unless `chained`.
 template <class Source, class Extra = NoExtra>
 cudaError_t launch_bin_count(const Source &src, uint32_t n, uint32_t bins, uint32_t *counts, cudaStream_t s,
-                             const Extra &extra = Extra{}, uint32_t others = 0)
+                             const Extra &extra = Extra{}, uint32_t others = 0, bool chained = false)
 {
     if (bin_chunks(n) == 1) return cudaSuccess;
-    bin_count_kernel<Source, Extra><<<bin_chunks(n) + others, kBinThreads, 0, s>>>(
-        src, n, bin_chunk_elems(n), bin_chunks(n), bins, counts, extra);
+    auto kernel = bin_count_kernel<Source, Extra>;
+    const dim3 grid(bin_chunks(n) + others);
+    if (chained)
+        return gch::launch_next(kernel, grid, dim3(kBinThreads), 0, s, src, n, bin_chunk_elems(n), bin_chunks(n), bins,
+                                counts, extra);
+    kernel<<<grid, kBinThreads, 0, s>>>(src, n, bin_chunk_elems(n), bin_chunks(n), bins, counts, extra);
     return cudaGetLastError();
 }
 
@@ -245,8 +254,12 @@ cudaError_t launch_bin_place(const Source &src, const Sink &sink, uint32_t n, ui
 {
     auto kernel = bin_place_kernel<Source, Sink, Extra>;
     if (!bin_place_smem(reinterpret_cast<const void *>(kernel))) return cudaErrorInvalidConfiguration;
-    kernel<<<bin_chunks(n) + others, kBinThreads, size_t(kBinWarps) * bins * sizeof(uint32_t), s>>>(
-        src, sink, n, bin_chunk_elems(n), bin_chunks(n), bins, align, counts, extra);
+    const dim3 grid(bin_chunks(n) + others);
+    const size_t smem = size_t(kBinWarps) * bins * sizeof(uint32_t);
+    if (bin_chunks(n) > 1)
+        return gch::launch_next(kernel, grid, dim3(kBinThreads), smem, s, src, sink, n, bin_chunk_elems(n),
+                                bin_chunks(n), bins, align, counts, extra);
+    kernel<<<grid, kBinThreads, smem, s>>>(src, sink, n, bin_chunk_elems(n), bin_chunks(n), bins, align, counts, extra);
     return cudaGetLastError();
 }
 

@@ -7,6 +7,7 @@
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <cuda_runtime.h>
 
 namespace gcd {
 
@@ -61,9 +62,50 @@ __device__ __forceinline__ uint32_t load_id(const void *ids, bool wide, uint64_t
     return v >= 0 && v < int64_t(limit) ? uint32_t(v) : limit;
 }
 
+// Zeros over `bytes` of a row by one warp, whatever its alignment: 16 bytes at
+// a time between the boundaries, two outside them.
+__device__ __forceinline__ void zero_row(void *row, size_t bytes)
+{
+    uint8_t *p = static_cast<uint8_t *>(row);
+    const uint32_t lane = threadIdx.x & 31;
+    const size_t lead = size_t(-reinterpret_cast<intptr_t>(p)) & 15u, head = lead < bytes ? lead : bytes;
+    const size_t body = (bytes - head) / 16, tail = head + body * 16;
+    if (lane < head / 2) reinterpret_cast<uint16_t *>(p)[lane] = 0;
+    for (size_t i = lane; i < body; i += 32) reinterpret_cast<uint4 *>(p + head)[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (lane < (bytes - tail) / 2) reinterpret_cast<uint16_t *>(p + tail)[lane] = 0;
+}
+
+// Programmatic launches: a kernel launched by launch_next may start while the
+// one before it in the stream still runs.  Each kernel of such a chain lets
+// its successor start at once and touches nothing that its predecessor writes
+// (or reads, if it writes it) before chain_wait, which returns when the
+// predecessor has finished.
+__device__ __forceinline__ void chain_start()
+{
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+__device__ __forceinline__ void chain_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 }  // namespace gcd
 
 namespace gch {
+
+template <class... P, class... A>
+cudaError_t launch_next(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, A... args)
+{
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
 
 // Elements per access for rows of `elem`-byte elements: the largest piece of
 // at most 16 bytes that divides every address and length in `bits` (the
