@@ -25,10 +25,7 @@ constexpr uint32_t kBlock = 32;     // sorted positions per block
 #ifndef GC_SUMS_CTAS
 #define GC_SUMS_CTAS 4
 #endif
-#ifndef GC_LOOKUPS
-#define GC_LOOKUPS 4
-#endif
-constexpr int kLookups = GC_LOOKUPS;         // rows per thread of a lookup
+constexpr int kLookups = 2;         // rows per thread of a lookup
 constexpr size_t kZeroBytes = 32768;  // zeroed per CTA of the sums, about
 // A bulk sum's CTA holds kBlock rows of up to this many bytes per row of
 // threads, 64 KiB in all: three CTAs to an SM.
@@ -70,7 +67,7 @@ embedding_kernel(const T *__restrict__ table, size_t table_stride, uint32_t voca
             if (id[r] < vocab)  // zeros stay zeros whatever the scale
 #pragma unroll
                 for (int k = 0; k < N; ++k) v[r].v[k] = row_from_float<T>(scale * row_to_float(v[r].v[k]));
-            if (first + r < n) store_piece<T, N>(out + size_t(first + r) * out_stride + size_t(c) * N, v[r]);
+            if (first + r < n) stream_piece<T, N>(out + size_t(first + r) * out_stride + size_t(c) * N, v[r]);
         }
     }
 }

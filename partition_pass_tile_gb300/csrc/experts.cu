@@ -100,7 +100,7 @@ __device__ __forceinline__ void expert_spread_row(const E *__restrict__ src, con
 #pragma unroll
             for (int q = 0; q < kSpread; ++q) {
                 const uint32_t c = base + q * blockDim.x;
-                if (c < pieces) store_piece<E, N>(dst + size_t(c) * N, v[q]);
+                if (c < pieces) stream_piece<E, N>(dst + size_t(c) * N, v[q]);
             }
         }
     }
@@ -263,7 +263,7 @@ expert_combine_grad_kernel(const T *__restrict__ g, size_t g_stride, const T *__
                 Piece<T, N> o;
 #pragma unroll
                 for (int i = 0; i < N; ++i) o.v[i] = row_from_float<T>(w * row_to_float(a.v[i]));
-                store_piece<T, N>(dy + size_t(slot) * dy_stride + size_t(c) * N, o);
+                stream_piece<T, N>(dy + size_t(slot) * dy_stride + size_t(c) * N, o);
                 if (dweights) {
                     const Piece<T, N> b = load_piece<T, N>(y + size_t(slot) * y_stride + size_t(c) * N);
 #pragma unroll

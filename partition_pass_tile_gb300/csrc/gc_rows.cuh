@@ -44,6 +44,14 @@ __device__ __forceinline__ void store_piece(T *p, const Piece<T, N> &x)
     *reinterpret_cast<Piece<T, N> *>(p) = x;
 }
 
+// A store of a row that is not read again soon: the lines leave L2 first.
+template <class T, int N>
+__device__ __forceinline__ void stream_piece(T *p, const Piece<T, N> &x)
+{
+    if constexpr (sizeof(Piece<T, N>) == 16) __stcs(reinterpret_cast<uint4 *>(p), *reinterpret_cast<const uint4 *>(&x));
+    else store_piece<T, N>(p, x);
+}
+
 template <class T, int N>
 __device__ __forceinline__ Piece<T, N> zero_piece()
 {

@@ -31,15 +31,9 @@ namespace {
 using namespace gcd;
 namespace cg = cooperative_groups;
 
-#ifndef GC_SAMPLE_THREADS
-#define GC_SAMPLE_THREADS 512
-#endif
-#ifndef GC_SAMPLE_CTAS
-#define GC_SAMPLE_CTAS 2
-#endif
-constexpr int kThreads = GC_SAMPLE_THREADS;
+constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kResident = GC_SAMPLE_CTAS;                // CTAs per SM
+constexpr int kResident = 2;                // CTAs per SM
 constexpr uint32_t kMaxTeam = 8;
 constexpr uint32_t kList = 4096;            // candidates that a CTA can hold
 // Histogram of the distance below the maximum in powers of two, 64 bins to a
@@ -49,10 +43,7 @@ constexpr uint32_t kBinsUsed = 42 * 64;
 constexpr float kBinsPerPower = 64.0f;
 constexpr int kSubBins = 1024;              // histogram of the list
 constexpr uint32_t kFew = 1024;             // of the list's tokens near a cut
-#ifndef GC_SAMPLE_RING
-#define GC_SAMPLE_RING 3
-#endif
-constexpr int kRing = GC_SAMPLE_RING;       // pieces of 16 bytes that a thread has under way
+constexpr int kRing = 3;       // pieces of 16 bytes that a thread has under way
 constexpr int kSample = 8;                  // pieces per thread that bound the k-th largest value
 constexpr float kFixed = 1099511627776.0f;  // 2^40
 constexpr float kUniformLo = 0x1p-25f, kUniformHi = 1.0f - 0x1p-24f;
@@ -195,11 +186,16 @@ struct Row {
     // through a ring of asynchronous copies, each thread's its own: kRing - 1 of
     // them are under way at any time, and f's code is there once, which matters
     // more than unrolling it (an unrolled f of the sizes below waits for
-    // instructions).
-    template <class F>
+    // instructions).  With U the tokens' u come along, through a ring laid over
+    // the list and the histogram, and f takes this thread's slot of it too: the
+    // floats of a piece, four to a row of threads.
+    template <bool U = false, class F>
     __device__ __forceinline__ void each(Smem &sm, const F &f) const
     {
+        constexpr int kWords = kVec / 4;
+        static_assert(sizeof(float4) * kRing * 2 * kThreads <= sizeof(sm.list) + sizeof(sm.hist), "ring of u");
         uint4 *ring = &sm.ring[0][threadIdx.x];
+        float4 *uring = reinterpret_cast<float4 *>(sm.list) + threadIdx.x;
         Piece<T, kVec> none;
 #pragma unroll
         for (uint32_t e = 0; e < kVec; ++e) none.v[e] = row_from_float<T>(-INFINITY);
@@ -209,6 +205,22 @@ struct Row {
                                  __cvta_generic_to_shared(ring + slot * kThreads))),
                              "l"(x + head + size_t(j) * kVec)
                              : "memory");
+            if (U && j < pieces) {
+                const float *from = u + head + size_t(j) * kVec;
+#pragma unroll
+                for (int q = 0; q < kWords; ++q) {
+                    const uint32_t to = uint32_t(__cvta_generic_to_shared(uring + (slot * kWords + q) * kThreads));
+                    if (shift == 0) {
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from + 4 * q) : "memory");
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to + 4u * e),
+                                         "l"(from + 4 * q + e)
+                                         : "memory");
+                    }
+                }
+            }
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
         const uint32_t s = single();
@@ -224,12 +236,14 @@ struct Row {
             if (lone) {
                 if (s < vocab) now.v[0] = x[s];
                 store_piece<T, kVec>(at, now);
+                if (U) uring[0].x = s < vocab ? u[s] : 0.0f;
             } else {
                 asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
                 if (base + me < pieces) now = load_piece<T, kVec>(at);
                 i = head + (base + me) * kVec;
             }
-            f(now, static_cast<const T *>(at), i);
+            if constexpr (U) f(now, static_cast<const T *>(at), i, static_cast<const float4 *>(uring + slot * kWords * kThreads));
+            else f(now, static_cast<const T *>(at), i);
             if (lone) {
                 lone = false;
 #pragma unroll
@@ -384,11 +398,9 @@ struct Draw {
     }
     // Offers the tokens of a piece with a bit in `kept`; all lanes together.
     template <uint32_t N, class T>
-    __device__ __forceinline__ void offer(const float (&w)[N], uint32_t kept, const Row<T> &row, const Scale &scale,
-                                          const T *x, uint32_t i)
+    __device__ __forceinline__ void offer(const float (&w)[N], uint32_t kept, const float (&u)[N], const Row<T> &row,
+                                          const Scale &scale, const T *x, uint32_t i)
     {
-        float u[N];
-        row.uniforms(i, u);
         uint32_t any = 0u;
 #pragma unroll
         for (uint32_t e = 0; e < N; ++e) any |= open(w[e], fmaxf(u[e], kUniformLo)) ? 1u << e : 0u;
@@ -762,7 +774,11 @@ __device__ __noinline__ bool find_cut(Team &team, const Row<T> &row, const Scale
                 if (keep) sure |= 1u << e;
             }
             team.append(list, at, i);
-            if (kept && __any_sync(kFull, sure != 0u)) mine.draw.offer(w, sure, row, scale, at, i);
+            if (kept && __any_sync(kFull, sure != 0u)) {
+                float u[kVec];
+                row.uniforms(i, u);
+                mine.draw.offer(w, sure, u, row, scale, at, i);
+            }
         });
         mass = team.sum(mass);  // past which every list is complete
         const uint32_t n = team.gather_lists();
@@ -899,24 +915,46 @@ __device__ __noinline__ Kept draw_row(const Team &team, const Row<T> &row, const
     Kept kept;
     const Scale scale = row_scale;
     const Cut cut(cut_key);
-    const bool all = cut_key == 0u;
     row.each(team.sm, [&](const Piece<T, kVec> &x, const T *at, uint32_t i) {
-        float w[kVec];
+        float w[kVec], u[kVec];
         uint32_t in = 0u;
 #pragma unroll
         for (uint32_t e = 0; e < kVec; ++e) {
             const float v = sample_value(row_to_float(x.v[e]));
             w[e] = scale.w(v);
-            if (w[e] >= q && w[e] > 0.0f) in |= 1u << e;
+            if (w[e] >= q && w[e] > 0.0f && cut.keeps(v, i + e)) in |= 1u << e;
         }
-        if (!all)
-#pragma unroll
-            for (uint32_t e = 0; e < kVec; ++e)
-                if (!cut.keeps(sample_value(row_to_float(x.v[e])), i + e)) in &= ~(1u << e);
         if (!__any_sync(kFull, in != 0u)) return;
 #pragma unroll
         for (uint32_t e = 0; e < kVec; ++e) kept.sum += (in >> e) & 1u ? w[e] : 0.0f;
-        kept.draw.offer(w, in, row, scale, at, i);
+        row.uniforms(i, u);
+        kept.draw.offer(w, in, u, row, scale, at, i);
+    });
+    return kept;
+}
+
+// The same of all tokens, whose u are all needed and come with the logits.
+template <class T>
+__device__ __noinline__ Kept draw_all(const Team &team, const Row<T> &row, const Scale &row_scale)
+{
+    constexpr uint32_t kVec = Row<T>::kVec;
+    Kept kept;
+    const Scale scale = row_scale;
+    row.template each<true>(team.sm, [&](const Piece<T, kVec> &x, const T *at, uint32_t i, const float4 *us) {
+        float w[kVec], u[kVec];
+        uint32_t in = 0u;
+#pragma unroll
+        for (uint32_t e = 0; e < kVec; e += 4) {
+            const float4 r = us[e / 4 * kThreads];
+            u[e] = r.x, u[e + 1] = r.y, u[e + 2] = r.z, u[e + 3] = r.w;
+        }
+#pragma unroll
+        for (uint32_t e = 0; e < kVec; ++e) {
+            w[e] = scale.w(sample_value(row_to_float(x.v[e])));
+            kept.sum += w[e];
+            if (w[e] > 0.0f) in |= 1u << e;
+        }
+        kept.draw.offer(w, in, u, row, scale, at, i);
     });
     return kept;
 }
@@ -1001,7 +1039,7 @@ sample_kernel(const T *__restrict__ logits, size_t logits_stride, uint32_t vocab
         const uint64_t unit = team.largest(near > -INFINITY ? order_key(near, 0u) : 0u);
         if (unit != 0u) {
             const Scale scale(key_value(unit), t);
-            const Kept kept = draw_row(team, row, scale, 0u, 0.0f);
+            const Kept kept = draw_all(team, row, scale);
             const KeySum end = team.reduce(KeySum{kept.draw.key(), kept.sum});
             if (end.sum < 1e30f) {
                 if (team.rank == 0 && threadIdx.x == 0) {
