@@ -30,10 +30,11 @@ constexpr size_t kZeroBytes = 32768;  // zeroed per CTA of the sums, about
 // A bulk sum's CTA holds kBlock rows of up to this many bytes per row of
 // threads, 64 KiB in all: three CTAs to an SM.
 constexpr uint32_t kSliceBytes = 2048;
-// Zeroed beside a count and a place kernel, whose CTAs wait for memory most
-// of the time: about what an idle GPU writes meanwhile.
-constexpr size_t kCountZeros = size_t(20) << 20, kPlaceZeros = size_t(44) << 20;
-constexpr uint32_t kZeroCtas = 300;
+// Positions that one CTA sorts alone, the other CTAs zeroing the result
+// meanwhile: 23 us for the gradient of 4096 tokens of 512 in a table of 32768,
+// 31 us with the sort of more tokens, which takes over where both take as long.
+constexpr uint32_t kSortAlone = 4096;
+constexpr uint32_t kZeroCtas = 300;   // of them, two to an SM
 
 // tx threads across a row's pieces, kRowThreads / tx rows.
 dim3 row_block(size_t pieces)
@@ -125,7 +126,7 @@ struct ZeroRows {
 // the passes; the others zero the result.
 struct TokenSortSmem {
     BinSmem bins;
-    uint2 items[2][kBinSingle];
+    uint2 items[2][kSortAlone];
     uint32_t cnt[kBinWarps << 9];
 };
 
@@ -330,68 +331,95 @@ token_bulk_sums_kernel(const uint2 *__restrict__ sorted, uint32_t n, const T *__
 }
 
 // Tokens whose run crosses blocks: the block in which it began adds up its
-// parts.  kJoiners rows of threads take a share of the blocks each, and the
-// shares are added in order.
+// parts.  A CTA takes kJoiners blocks and 32 pieces of a row, a warp to a
+// block; a run that reaches more than kAhead further blocks is left to all
+// warps, which take a share of them each and add the shares in order.
 constexpr int kJoiners = 8;
 
 template <class O, int N>
-__global__ void __launch_bounds__(kRowThreads)
+__global__ void __launch_bounds__(32 * kJoiners)
 token_join_kernel(const uint2 *__restrict__ sorted, uint32_t n, uint32_t width, const float *__restrict__ edges,
                   GradOut out, uint32_t parts)
 {
-    constexpr int kAhead = 8;
+    constexpr uint32_t kAhead = 8;
     __shared__ Piece<float, N> s_sum[kJoiners][32];
+    __shared__ uint32_t s_more[kJoiners], s_key[kJoiners];
     chain_wait();
-    const uint32_t block = blockIdx.x / parts, lane = threadIdx.x, share = threadIdx.y;
+    const uint32_t lane = threadIdx.x, warp = threadIdx.y;
+    const uint32_t group = blockIdx.x / parts * kJoiners, block = group + warp;
     const uint32_t c = (blockIdx.x % parts) * 32 * N + lane * N;
     const uint32_t blocks = (n + kBlock - 1) / kBlock;
-    const uint32_t first = block * kBlock, next = first + kBlock;
-    const uint32_t key = sorted[next - 1].x, after = sorted[next].x, before = first > 0 ? sorted[first - 1].x : ~0u;
-    if (key >= out.vocab || after != key || before == key) return;
-    // The blocks whose first key is it: the run reaches them.
-    uint32_t more = 1;
-    for (bool on = true; on;) {
-        const uint32_t b = block + more + 1 + lane;
-        const uint32_t same = __ballot_sync(kFullMask, b < blocks && sorted[size_t(min(b, blocks - 1)) * kBlock].x == key);
-        more += same == kFullMask ? 32u : uint32_t(__ffs(~same) - 1);
-        on = same == kFullMask;
-    }
-    const uint32_t per = (more + kJoiners - 1) / kJoiners;
-    const uint32_t lo = min(more, share * per), hi = min(more, lo + per);
-    Piece<float, N> sum{};
-    if (c < width) {
-        const float *e = edges + size_t(block) * 2 * width + c;
-        if (share == 0) sum = load_piece<float, N>(e + width);
-        e += size_t(lo + 1) * 2 * width;
-        for (uint32_t b = lo; b < hi; b += kAhead) {
+    // Blocks b + lo + 1 to b + hi of the run that began in block b.
+    auto add = [&](Piece<float, N> &sum, uint32_t b, uint32_t lo, uint32_t hi) {
+        const float *e = edges + (size_t(b) + lo + 1) * 2 * width + c;
+        for (uint32_t i = lo; i < hi; i += kAhead) {
             Piece<float, N> x[kAhead];
 #pragma unroll
-            for (int j = 0; j < kAhead; ++j) {
+            for (uint32_t j = 0; j < kAhead; ++j) {
                 x[j] = Piece<float, N>{};
-                if (b + j < hi) x[j] = load_piece<float, N>(e + size_t(j) * 2 * width);
+                if (i + j < hi) x[j] = load_piece<float, N>(e + size_t(j) * 2 * width);
             }
 #pragma unroll
-            for (int j = 0; j < kAhead; ++j)
+            for (uint32_t j = 0; j < kAhead; ++j)
 #pragma unroll
                 for (int k = 0; k < N; ++k) sum.v[k] += x[j].v[k];
             e += size_t(kAhead) * 2 * width;
         }
+    };
+    auto put = [&](uint32_t key, const Piece<float, N> &sum) {
+        O *dst = static_cast<O *>(out.rows) + size_t(key) * out.stride + c;
+        Piece<O, N> o;
+        if (out.accumulate) o = load_piece<O, N>(dst);
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const float r = out.scale * sum.v[k];
+            o.v[k] = row_from_float<O>(out.accumulate ? r + row_to_float(o.v[k]) : r);
+        }
+        store_piece<O, N>(dst, o);
+    };
+    uint32_t more = 0u;
+    if (block + 1 < blocks) {
+        const uint32_t first = block * kBlock, next = first + kBlock;
+        const uint32_t key = sorted[next - 1].x, after = sorted[next].x, before = first > 0 ? sorted[first - 1].x : ~0u;
+        if (key < out.vocab && after == key && before != key) {
+            // The blocks whose first key is it: the run reaches them.
+            more = 1;
+            for (bool on = true; on;) {
+                const uint32_t b = block + more + 1 + lane;
+                const uint32_t same =
+                    __ballot_sync(kFullMask, b < blocks && sorted[size_t(min(b, blocks - 1)) * kBlock].x == key);
+                more += same == kFullMask ? 32u : uint32_t(__ffs(~same) - 1);
+                on = same == kFullMask;
+            }
+            if (more <= kAhead && c < width) {
+                Piece<float, N> sum = load_piece<float, N>(edges + (size_t(block) * 2 + 1) * width + c);
+                add(sum, block, 0, more);
+                put(key, sum);
+            }
+            if (lane == 0) s_key[warp] = key;
+        }
     }
-    s_sum[share][lane] = sum;
+    if (lane == 0) s_more[warp] = more > kAhead ? more : 0u;
     __syncthreads();
-    if (share > 0 || c >= width) return;
-    for (int j = 1; j < kJoiners; ++j)
+    for (uint32_t w = 0; w < kJoiners; ++w) {
+        const uint32_t far = s_more[w];
+        if (far == 0u) continue;  // the same for all
+        const uint32_t b = group + w, per = (far + kJoiners - 1) / kJoiners;
+        Piece<float, N> sum{};
+        if (c < width) {
+            if (warp == 0) sum = load_piece<float, N>(edges + (size_t(b) * 2 + 1) * width + c);
+            add(sum, b, min(far, warp * per), min(far, (warp + 1) * per));
+        }
+        s_sum[warp][lane] = sum;
+        __syncthreads();
+        if (warp == 0 && c < width) {
+            for (int j = 1; j < kJoiners; ++j)
 #pragma unroll
-        for (int k = 0; k < N; ++k) sum.v[k] += s_sum[j][lane].v[k];
-    O *dst = static_cast<O *>(out.rows) + size_t(key) * out.stride + c;
-    Piece<O, N> o;
-    if (out.accumulate) o = load_piece<O, N>(dst);
-#pragma unroll
-    for (int k = 0; k < N; ++k) {
-        const float r = out.scale * sum.v[k];
-        o.v[k] = row_from_float<O>(out.accumulate ? r + row_to_float(o.v[k]) : r);
+                for (int k = 0; k < N; ++k) sum.v[k] += s_sum[j][lane].v[k];
+            put(s_key[w], sum);
+        }
+        __syncthreads();
     }
-    store_piece<O, N>(dst, o);
 }
 
 int key_bits(size_t vocab)
@@ -443,7 +471,7 @@ cudaError_t run_grad_rows(const uint2 *sorted, uint32_t n, const void *g, size_t
     }
     const size_t parts = gch::ceil_div(width / N, threads.x);
     const size_t sums = gch::ceil_div(blocks, threads.y) * parts;
-    const size_t joins = blocks > 1 ? (blocks - 1) * gch::ceil_div(width / N, 32) : 0;
+    const size_t joins = blocks > 1 ? gch::ceil_div(blocks - 1, kJoiners) * gch::ceil_div(width / N, 32) : 0;
     if (sums + zeros > 0x7fffffffu || joins > 0x7fffffffu) return cudaErrorInvalidConfiguration;
     if (n == 0) {
         // Only zeros, after the clear, which is no kernel to chain to.
@@ -541,16 +569,8 @@ cudaError_t launch_embedding_grad(const void *g, size_t g_stride, gc_row_dtype g
     const int bits = key_bits(vocab), passes = int(ceil_div(bits, 9)), digit = int(ceil_div(bits, passes));
     const size_t elem = odt == GC_ROW_F32 ? 4 : 2;
     ZeroRows zero{static_cast<uint8_t *>(dtable), dtable_stride * elem, width * elem, seen, 0u, accumulate ? 0u : vocab};
-    // A kernel's part of the rows to zero, about `bytes`; the rest stays.
-    auto part = [&](size_t bytes) {
-        ZeroRows z = zero;
-        const size_t rows = bytes / zero.bytes;
-        z.hi = uint32_t(std::min(size_t(zero.hi), zero.lo + rows));
-        zero.lo = z.hi;
-        return z;
-    };
     cudaError_t e = cudaSuccess;
-    if (n > 0 && gcd::bin_chunks(n) == 1) {
+    if (n > 0 && n <= kSortAlone) {
         // Everything is zeroed here, before any row is written.
         if (persistent_grid(reinterpret_cast<const void *>(token_sort_kernel), gcd::kBinThreads, sizeof(TokenSortSmem),
                             1) <= 0)
@@ -566,14 +586,8 @@ cudaError_t launch_embedding_grad(const void *g, size_t g_stride, gc_row_dtype g
         for (int p = 0; n > 0 && p < passes && e == cudaSuccess; ++p) {
             const TokenPass src{ids, items[p & 1], seen, p == 0, wide, vocab, uint32_t(p * digit), (1u << digit) - 1u};
             const TokenSink sink{src, items[(p & 1) ^ 1]};
-            // The first count finds out which tokens are absent.
-            const ZeroRows beside = part(p == 0 ? 0 : kCountZeros);
-            e = gcd::launch_bin_count(src, n, 1u << digit, table, s, beside, beside.lo < beside.hi ? kZeroCtas : 0u,
-                                      p > 0);
-            if (e != cudaSuccess) break;
-            const ZeroRows beside_place = part(kPlaceZeros);
-            e = gcd::launch_bin_place(src, sink, n, 1u << digit, 1u, table, s, beside_place,
-                                      beside_place.lo < beside_place.hi ? kZeroCtas : 0u);
+            e = gcd::launch_bin_count(src, n, 1u << digit, table, s, p > 0);
+            if (e == cudaSuccess) e = gcd::launch_bin_place(src, sink, n, 1u << digit, 1u, table, s);
         }
     }
     if (e != cudaSuccess) return e;

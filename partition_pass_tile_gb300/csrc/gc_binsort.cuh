@@ -6,10 +6,10 @@
 // bin; bin_place_kernel adds the counts of the chunks before its own and of
 // the smaller bins (each bin's total rounded up to `align`) to get where its
 // first item of each bin goes, ranks its own items, and hands every item's
-// destination to a sink.  A single chunk (up to kBinSingle items) needs no
-// count kernel.  Within a chunk a warp owns a contiguous segment and takes 32
-// items at a time, so the rank is: earlier warps' counts of the bin + this
-// warp's count so far + the earlier lanes with the same bin.
+// destination to a sink.  Within a chunk a warp owns a contiguous segment and
+// takes 32 items at a time, so the rank is: earlier warps' counts of the bin +
+// this warp's count so far + the earlier lanes with the same bin.  A single
+// chunk needs no count kernel (bin_place_chunk with chunks == 1).
 #pragma once
 
 #include "gc_internal.h"
@@ -22,11 +22,9 @@ constexpr int kBinWarps = kBinThreads / 32;
 constexpr uint32_t kMaxBins = 2048;
 constexpr uint32_t kBinChunks = 128;   // most chunks: every CTA reads all chunks' counts
 constexpr uint32_t kBinMinChunk = 1024;
-constexpr uint32_t kBinSingle = 4096;  // items that one CTA places alone
 
 inline uint32_t bin_chunk_elems(size_t n)
 {
-    if (n <= kBinSingle) return kBinSingle;
     const size_t even = gch::align_up(gch::ceil_div(n, size_t(kBinChunks)), size_t(kBinThreads));
     return uint32_t(even > kBinMinChunk ? even : kBinMinChunk);
 }
@@ -59,26 +57,17 @@ __device__ __forceinline__ uint32_t bin_block_scan(uint32_t v, uint32_t *s_warp,
     return before + incl - v;
 }
 
-// Work for CTAs beyond the chunks, while those wait for memory.
-struct NoExtra {
-    __device__ __forceinline__ void run(uint32_t, uint32_t) const {}
-};
-
 // Source: bin(i) in [0, bins], where `bins` marks an item that goes nowhere.
 // Counts are written bin-major, counts[b * bin_count_stride(chunks) + c], with
 // zeros up to the stride.
-template <class Source, class Extra>
+template <class Source>
 __global__ void __launch_bounds__(kBinThreads)
-bin_count_kernel(Source src, uint32_t n, uint32_t chunk, uint32_t chunks, uint32_t bins,
-                 uint32_t *__restrict__ counts, Extra extra)
+bin_count_kernel(Source src, uint32_t n, uint32_t chunk, uint32_t bins,
+                 uint32_t *__restrict__ counts)
 {
     __shared__ uint32_t s_hist[kMaxBins];
     chain_start();
     chain_wait();
-    if (blockIdx.x >= chunks) {
-        extra.run(blockIdx.x - chunks, gridDim.x - chunks);
-        return;
-    }
     for (uint32_t b = threadIdx.x; b < bins; b += kBinThreads) s_hist[b] = 0u;
     __syncthreads();
     const uint32_t first = blockIdx.x * chunk, last = min(n - first, chunk) + first;
@@ -88,7 +77,7 @@ bin_count_kernel(Source src, uint32_t n, uint32_t chunk, uint32_t chunks, uint32
         if (b < bins) atomicAdd(&s_hist[b], 1u);
     }
     __syncthreads();
-    const uint32_t stride = bin_count_stride(chunks);
+    const uint32_t chunks = gridDim.x, stride = bin_count_stride(chunks);
     for (uint32_t b = threadIdx.x; b < bins; b += kBinThreads) {
         counts[size_t(b) * stride + blockIdx.x] = s_hist[b];
         if (blockIdx.x == 0)
@@ -212,32 +201,29 @@ __device__ __forceinline__ void bin_place_chunk(const Source &src, const Sink &s
 // Sink: place(i, destination), drop(i); start(b, start, count) once per bin
 // and end(total) once, by CTA 0.  Dynamic shared memory: kBinWarps * bins
 // words.
-template <class Source, class Sink, class Extra>
+template <class Source, class Sink>
 __global__ void __launch_bounds__(kBinThreads)
-bin_place_kernel(Source src, Sink sink, uint32_t n, uint32_t chunk, uint32_t chunks, uint32_t bins, uint32_t align,
-                 const uint32_t *__restrict__ counts, Extra extra)
+bin_place_kernel(Source src, Sink sink, uint32_t n, uint32_t chunk, uint32_t bins, uint32_t align,
+                 const uint32_t *__restrict__ counts)
 {
     extern __shared__ uint32_t s_cnt[];
     __shared__ BinSmem sm;
     chain_start();
     chain_wait();
-    if (blockIdx.x < chunks) bin_place_chunk(src, sink, n, chunk, chunks, blockIdx.x, bins, align, counts, s_cnt, sm);
-    else extra.run(blockIdx.x - chunks, gridDim.x - chunks);
+    bin_place_chunk(src, sink, n, chunk, gridDim.x, blockIdx.x, bins, align, counts, s_cnt, sm);
 }
 
-// `others`: CTAs for `extra`.  Both are kernels of a chain (launch_next), the
-// count kernel its first unless `chained`.
-template <class Source, class Extra = NoExtra>
+// Both are kernels of a chain (launch_next), the count kernel its first
+// unless `chained`.
+template <class Source>
 cudaError_t launch_bin_count(const Source &src, uint32_t n, uint32_t bins, uint32_t *counts, cudaStream_t s,
-                             const Extra &extra = Extra{}, uint32_t others = 0, bool chained = false)
+                             bool chained = false)
 {
-    if (bin_chunks(n) == 1) return cudaSuccess;
-    auto kernel = bin_count_kernel<Source, Extra>;
-    const dim3 grid(bin_chunks(n) + others);
+    auto kernel = bin_count_kernel<Source>;
     if (chained)
-        return gch::launch_next(kernel, grid, dim3(kBinThreads), 0, s, src, n, bin_chunk_elems(n), bin_chunks(n), bins,
-                                counts, extra);
-    kernel<<<grid, kBinThreads, 0, s>>>(src, n, bin_chunk_elems(n), bin_chunks(n), bins, counts, extra);
+        return gch::launch_next(kernel, dim3(bin_chunks(n)), dim3(kBinThreads), 0, s, src, n, bin_chunk_elems(n), bins,
+                                counts);
+    kernel<<<bin_chunks(n), kBinThreads, 0, s>>>(src, n, bin_chunk_elems(n), bins, counts);
     return cudaGetLastError();
 }
 
@@ -247,20 +233,15 @@ inline bool bin_place_smem(const void *kernel)
     return gch::persistent_grid(kernel, kBinThreads, size_t(kBinWarps) * kMaxBins * sizeof(uint32_t), 1) > 0;
 }
 
-template <class Source, class Sink, class Extra = NoExtra>
-cudaError_t launch_bin_place(const Source &src, const Sink &sink, uint32_t n, uint32_t bins,
-                             uint32_t align, const uint32_t *counts, cudaStream_t s, const Extra &extra = Extra{},
-                             uint32_t others = 0)
+template <class Source, class Sink>
+cudaError_t launch_bin_place(const Source &src, const Sink &sink, uint32_t n, uint32_t bins, uint32_t align,
+                             const uint32_t *counts, cudaStream_t s)
 {
-    auto kernel = bin_place_kernel<Source, Sink, Extra>;
+    auto kernel = bin_place_kernel<Source, Sink>;
     if (!bin_place_smem(reinterpret_cast<const void *>(kernel))) return cudaErrorInvalidConfiguration;
-    const dim3 grid(bin_chunks(n) + others);
-    const size_t smem = size_t(kBinWarps) * bins * sizeof(uint32_t);
-    if (bin_chunks(n) > 1)
-        return gch::launch_next(kernel, grid, dim3(kBinThreads), smem, s, src, sink, n, bin_chunk_elems(n),
-                                bin_chunks(n), bins, align, counts, extra);
-    kernel<<<grid, kBinThreads, smem, s>>>(src, sink, n, bin_chunk_elems(n), bin_chunks(n), bins, align, counts, extra);
-    return cudaGetLastError();
+    return gch::launch_next(kernel, dim3(bin_chunks(n)), dim3(kBinThreads),
+                            size_t(kBinWarps) * bins * sizeof(uint32_t), s, src, sink, n, bin_chunk_elems(n), bins,
+                            align, counts);
 }
 
 }  // namespace gcd
