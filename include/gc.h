@@ -453,7 +453,7 @@ gc_status gc_partition_at(const void *d_in, void *d_out, size_t out_capacity,
  * this library follows; each declaration states its formula.
  *
  *   - A row array holds rows of `width` elements of a gc_row_dtype; element
- *     (r, c) is at r * stride + c, stride in elements, stride >= width,
+ *     (r, c) is at r * stride + c, stride in elements, width <= stride < 2^31,
  *     1 <= width <= GC_MAX_ROW_WIDTH, at most GC_MAX_ELEMENTS rows.  Row
  *     pointers need only the element's own alignment; arrays whose pointer
  *     and strides are multiples of 16 bytes move in 16-byte pieces.
@@ -466,6 +466,8 @@ gc_status gc_partition_at(const void *d_in, void *d_out, size_t out_capacity,
  *   - Calls are asynchronous on `stream`, allocate nothing and can be
  *     captured in a CUDA graph.  A workspace (256-byte aligned, contents
  *     immaterial, no initialisation needed) is scratch of that one call.
+ *     gc_query_device_status on gc_embedding_grad's reports a staged copy
+ *     that did not arrive in time (GC_ERR_TIMEOUT).
  *   - Inputs must not overlap outputs, nor outputs one another, except where
  *     stated (GC_ERR_INVALID_VALUE).
  */

@@ -47,7 +47,7 @@ gc_status check_spans(std::initializer_list<Span> spans)
     return GC_OK;
 }
 
-// Strides stay below 2^40 elements, so no offset of a row overflows 64 bits.
+// Rows and strides below 2^31, so no offset of an element overflows 64 bits.
 bool valid_rows(size_t rows, size_t stride, size_t width)
 {
     return rows <= GC_MAX_ELEMENTS && width >= 1 && width <= GC_MAX_ROW_WIDTH && stride >= width &&

@@ -425,3 +425,62 @@ def test_row_operators_on_another_stream_and_in_a_graph():
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(held, step()))
+
+
+def test_offsets_beyond_32_bits():
+    # Rows whose element offsets pass 2^32: the last of a large table, its
+    # gradient, and logits whose rows lie 2^31 - 16 elements apart.
+    vocab, width = 1_100_000, 4096
+    table = torch.empty(vocab, width, dtype=torch.bfloat16, device="cuda")
+    ids = torch.tensor([vocab - 1, 0, vocab - 2, vocab, vocab - 1], device="cuda")
+    table[ids[:3]] = torch.arange(3, device="cuda", dtype=torch.bfloat16).unsqueeze(1) + 1
+    out = gc.embedding(table, ids)
+    assert out[:, 0].tolist() == [1.0, 2.0, 3.0, 0.0, 1.0] and bool((out == out[:, :1]).all())
+    g = torch.ones(5, width, dtype=torch.bfloat16, device="cuda")
+    table.fill_(7.0)
+    gc.embedding_grad(g, ids, vocab, out=table)
+    assert table[ids[:3], 5].tolist() == [2.0, 1.0, 1.0] and not table[1:vocab - 2].any()
+    del table
+    stride, vocab = 2 ** 31 - 16, 5001
+    wide = torch.full((2 * stride + vocab,), -9.0, dtype=torch.bfloat16, device="cuda")
+    x = wide.as_strided((3, vocab), (stride, 1))
+    x[2, 4321] = 30.0
+    u = torch.rand(3, vocab, device="cuda")
+    assert gc.sample(x)[0].tolist() == [0, 0, 4321]
+    assert gc.sample(x, u, top_p=0.9)[0][2].item() == 4321
+    y = wide.as_strided((3, 64), (stride, 1))
+    slots = torch.tensor([[2, 0]], dtype=torch.int32, device="cuda")
+    assert bool((gc.expert_combine(y, slots)[0] == -18.0).all())
+
+
+def test_example_learns():
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples",
+                        "language_model_step.py")
+    spec = importlib.util.spec_from_file_location("language_model_step", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    model = example.Model(vocab=300, width=64, experts=5, topk=2, align=8)
+    g = torch.Generator(device="cuda").manual_seed(2)
+    ids = torch.randint(300, (90,), generator=g, device="cuda")
+    targets = (ids * 7 + 3) % 300
+    # the gradient along itself against a central difference: the loss is
+    # smooth but for the choice of experts, which a step of 1e-3 leaves alone;
+    # float32 sums of the loss leave about 1e-6 / 1e-3 of noise
+    loss, d_logits, saved = model.loss(ids, targets)
+    grads = model.backward(d_logits, saved)
+    for name, grad in grads.items():
+        d = grad / grad.norm()
+        ends = []
+        for h in (1e-3, -1e-3):
+            model.params[name] += h * d
+            ends.append(model.loss(ids, targets)[0].double().item())
+            model.params[name] -= h * d
+        assert abs((ends[0] - ends[1]) / 2e-3 - grad.norm().item()) <= 0.02 * grad.norm().item() + 2e-3, name
+    first = loss.item()
+    for _ in range(60):
+        last = model.train_step(ids, targets).item()
+    assert last < 0.5 * first
+    tokens, logprobs = model.sample(ids, g)
+    assert tokens.shape == (90,) and bool((logprobs <= 0).all())
