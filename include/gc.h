@@ -488,7 +488,10 @@ typedef enum { GC_ID_I32 = 0, GC_ID_I64 = 1 } gc_id_type;
  */
 size_t gc_expert_rows(size_t tokens, size_t topk, uint32_t experts, uint32_t align);
 
-/* Workspace bytes of gc_expert_dispatch; 0 for arguments out of range. */
+/*
+ * Workspace bytes of gc_expert_dispatch; 0 for arguments out of range.  256:
+ * the call checks its workspace and does not touch it.
+ */
 size_t gc_expert_workspace_bytes(size_t tokens, size_t topk, uint32_t experts);
 
 /*

@@ -346,7 +346,7 @@ namespace gch {
 
 size_t expert_workspace_bytes(size_t npairs, uint32_t experts)
 {
-    return npairs > kSmallPairs ? align_up(gcd::bin_table_bytes(npairs, experts), 256) : 256;
+    return npairs > kSmallPairs ? align_up(gcd::bin_table_bytes(npairs, experts), 256) + 256 : 256;
 }
 
 cudaError_t launch_expert_dispatch(const void *ids, bool wide, uint32_t npairs, uint32_t topk, uint32_t experts,

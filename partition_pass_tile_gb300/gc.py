@@ -582,6 +582,16 @@ def _scratch(ws: torch.Tensor | None, nbytes: int, device, stream) -> torch.Tens
     return ws if ws is not None else _new(max(nbytes, 256), torch.uint8, device, stream)
 
 
+# gc_expert_workspace_bytes of a dispatch whose workspace is checked and not touched.
+EXPERT_WORKSPACE_UNUSED = 256
+
+
+@lru_cache(maxsize=None)
+def _untouched(device: torch.device) -> torch.Tensor:
+    """What such calls on a device pass as their workspace."""
+    return torch.empty(EXPERT_WORKSPACE_UNUSED, dtype=torch.uint8, device=device)
+
+
 @lru_cache(maxsize=1024)
 def expert_rows(tokens: int, topk: int, experts: int, align: int = 1) -> int:
     """gc_expert_rows: rows that hold any routing (0 for arguments out of range)."""
@@ -608,17 +618,23 @@ def expert_dispatch(x: torch.Tensor | None, ids: torch.Tensor, experts: int, ali
         raise ValueError("ids is [tokens, topk]")
     tokens, topk = shape
     dev = ids.device
+    need = expert_workspace_bytes(tokens, topk, experts)
     if plan is None:
         rows = expert_rows(tokens, topk, experts, align)
+        if need == 0 or (rows == 0 and tokens > 0):
+            raise GcError(1, "gc_expert_dispatch")  # arguments out of range
+        # four tensors: each costs the host less than a view of a common one
         plan = ExpertPlan(_new(experts + 1, torch.int32, dev, stream), _new(experts, torch.int32, dev, stream),
                           _new(shape, torch.int32, dev, stream), _new(rows, torch.int32, dev, stream))
-        where = [t.data_ptr() for t in plan]
+        where = (plan.offsets.data_ptr(), plan.counts.data_ptr(), plan.slots.data_ptr(), plan.pairs.data_ptr())
     else:
         rows = plan.pairs.numel()
-        where = [_typed(plan.offsets, torch.int32, experts + 1, "plan.offsets"),
+        where = (_typed(plan.offsets, torch.int32, experts + 1, "plan.offsets"),
                  _typed(plan.counts, torch.int32, experts, "plan.counts"),
                  _typed(plan.slots, torch.int32, tokens * topk, "plan.slots"),
-                 _typed(plan.pairs, torch.int32, rows, "plan.pairs")]
+                 _typed(plan.pairs, torch.int32, rows, "plan.pairs"))
+    if ws is None:
+        ws = _untouched(dev) if need == EXPERT_WORKSPACE_UNUSED else _scratch(None, need, dev, stream)
     xp, xs, op, os, width, dt = None, 0, None, 0, 0, ROW_F32
     if x is not None:
         xp, xs = _rows(x)
@@ -628,8 +644,6 @@ def expert_dispatch(x: torch.Tensor | None, ids: torch.Tensor, experts: int, ali
         dt = row_dtype_code(x.dtype)
         out = _like(out, (rows, width), x.dtype, dev, stream, "out")
         op, os = _rows(out)
-    if ws is None:
-        ws = _scratch(None, expert_workspace_bytes(tokens, topk, experts), dev, stream)
     _check(load().gc_expert_dispatch(
         _ptr(ids), _ids(ids), tokens, topk, experts, align, xp, xs, width, dt, op, os, rows, *where, _ptr(ws),
         ws.numel(), _handle(stream, dev)), "gc_expert_dispatch")

@@ -151,6 +151,9 @@ def test_binding_refusals(lib):
         gc.expert_dispatch(x, ids[0], 4)
     with pytest.raises(ValueError):
         gc.embedding_grad(x, ids[:, 0], 5, accumulate=True)
+    for experts, align in ((0, 1), (2049, 1), (-3, 1), (4, 0), (4, 1 << 17)):
+        with pytest.raises(gc.GcError):
+            gc.expert_dispatch(x, ids, experts, align=align)
 
 
 def test_reference_gradients_against_differences():
