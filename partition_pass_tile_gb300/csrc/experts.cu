@@ -4,7 +4,10 @@
 // The plan is a stable partition of the tokens * topk pairs into one bin per
 // expert (gc_binsort.cuh); the rest moves rows: one row per pair out, a
 // weighted sum of topk rows per token back, and for the gradient one scaled
-// row and one dot product per pair.  All of it is bound by HBM traffic.
+// row and one dot product per pair.  Plans wait for memory (11 us for 131072
+// pairs, three kernels); the row kernels are bound by HBM traffic, and each
+// works token by token, so that a token's row is read once and the k rows of
+// its experts are the only ones touched at random, whole rows at a time.
 #include "gc_binsort.cuh"
 #include "gc_internal.h"
 #include "gc_rows.cuh"
@@ -79,7 +82,11 @@ __device__ __forceinline__ void expert_pad_rows(uint32_t first, uint32_t rows, u
 }
 
 // One token's row to its slots: read once, kSpread pieces per thread at a
-// time, and written up to topk times.
+// time, and written up to topk times.  Against gathering by destination row,
+// which reads every token's row topk times (from L2 at best): 16384 x 8 pairs
+// of 2048 bf16, 205 -> 126 us with the plan, 100 us of it the bytes at the copy
+// rate.  Rows of odd width move element by element, and are latency-bound: 1531
+// x 3 of 1001 float16 37 us with one element per thread at a time, 20 with four.
 constexpr int kSpread = 4;
 
 template <class E, int N>
@@ -203,7 +210,10 @@ expert_small_kernel(ExpertSource src, ExpertSink sink, uint32_t npairs, uint32_t
         expert_spread_row<E, N>(x + size_t(t) * x_stride, s_slots, topk, rows, out, out_stride, pieces);
 }
 
-// The rows of kAhead choices are loaded together.
+// The rows of kAhead choices are loaded together; sums in float32 in the order
+// of the choices.  16384 x 8 pairs of 2048 bf16: 109 us, 83% of the copy rate
+// (604 MB); with 8 choices at a time 160 us and with 2 at six CTAs per SM 190,
+// for want of registers.
 constexpr int kAhead = 4;
 
 template <class T, int N>
@@ -243,7 +253,9 @@ expert_combine_kernel(const T *__restrict__ y, size_t y_stride, uint32_t rows, c
 }
 
 // One warp per pair: the scaled gradient row and the dot product; then one
-// warp per row without a pair: zeros.
+// warp per row without a pair: zeros.  A token's pairs are neighbouring warps,
+// so its gradient row comes from HBM once.  8192 x 8 pairs of 4096 bf16: 182 us,
+// 93% of the copy rate.
 template <class T, int N>
 __global__ void __launch_bounds__(kRowThreads)
 expert_combine_grad_kernel(const T *__restrict__ g, size_t g_stride, const T *__restrict__ y, size_t y_stride,
