@@ -22,9 +22,6 @@ using namespace gcd;
 
 constexpr int kRowThreads = 256;
 constexpr uint32_t kBlock = 32;     // sorted positions per block
-#ifndef GC_SUMS_CTAS
-#define GC_SUMS_CTAS 4
-#endif
 constexpr int kLookups = 2;         // rows per thread of a lookup
 constexpr size_t kZeroBytes = 32768;  // zeroed per CTA of the sums, about
 // A bulk sum's CTA holds kBlock rows of up to this many bytes per row of
@@ -58,19 +55,30 @@ embedding_kernel(const T *__restrict__ table, size_t table_stride, uint32_t voca
     uint32_t id[kLookups];
 #pragma unroll
     for (int r = 0; r < kLookups; ++r) id[r] = first + r < n ? load_id(ids, wide, first + r, vocab) : vocab;
-    for (uint32_t c = threadIdx.x; c < pieces; c += blockDim.x) {
-        Piece<T, N> v[kLookups];
+    constexpr int kCols = kNarrow<T, N>;
+    for (uint32_t base = threadIdx.x; base < pieces; base += kCols * blockDim.x) {
+        Piece<T, N> v[kLookups][kCols];
+#pragma unroll
+        for (int r = 0; r < kLookups; ++r)
+#pragma unroll
+            for (int q = 0; q < kCols; ++q) {
+                const uint32_t c = base + q * blockDim.x;
+                v[r][q] = zero_piece<T, N>();
+                if (id[r] < vocab && c < pieces)
+                    v[r][q] = load_piece<T, N>(table + size_t(id[r]) * table_stride + size_t(c) * N);
+            }
 #pragma unroll
         for (int r = 0; r < kLookups; ++r) {
-            v[r] = zero_piece<T, N>();
-            if (id[r] < vocab) v[r] = load_piece<T, N>(table + size_t(id[r]) * table_stride + size_t(c) * N);
-        }
+            if (first + r >= n) break;
 #pragma unroll
-        for (int r = 0; r < kLookups; ++r) {
-            if (id[r] < vocab)  // zeros stay zeros whatever the scale
+            for (int q = 0; q < kCols; ++q) {
+                const uint32_t c = base + q * blockDim.x;
+                if (c >= pieces) break;
+                if (id[r] < vocab)  // zeros stay zeros whatever the scale
 #pragma unroll
-                for (int k = 0; k < N; ++k) v[r].v[k] = row_from_float<T>(scale * row_to_float(v[r].v[k]));
-            if (first + r < n) stream_piece<T, N>(out + size_t(first + r) * out_stride + size_t(c) * N, v[r]);
+                    for (int k = 0; k < N; ++k) v[r][q].v[k] = row_from_float<T>(scale * row_to_float(v[r][q].v[k]));
+                stream_piece<T, N>(out + size_t(first + r) * out_stride + size_t(c) * N, v[r][q]);
+            }
         }
     }
 }
@@ -170,7 +178,7 @@ struct GradOut {
 // The rows of the next kAhead positions, and what they are added to, are
 // loaded while the ones before are summed.
 template <class T, class O, int N, bool ADD>
-__global__ void __launch_bounds__(kRowThreads, GC_SUMS_CTAS)
+__global__ void __launch_bounds__(kRowThreads, 4)
 token_sums_kernel(const uint2 *__restrict__ sorted, uint32_t n, const T *__restrict__ g, size_t g_stride,
                   uint32_t width, float *__restrict__ edges, GradOut out, uint32_t parts, uint32_t sums, ZeroRows zero)
 {
@@ -198,7 +206,7 @@ token_sums_kernel(const uint2 *__restrict__ sorted, uint32_t n, const T *__restr
     __syncthreads();
     const uint32_t c = (blockIdx.x % parts) * columns + threadIdx.x * N;
     if (key[1] == none || c >= width) return;
-    constexpr int kAhead = ADD ? 4 : 8;
+    constexpr int kAhead = (ADD ? 4 : 8) * (sizeof(T) * N <= 4 ? 2 : 1);
     Piece<T, N> x[kAhead];
     Piece<O, N> old[ADD ? kAhead : 1];
     auto load = [&](uint32_t at_j, int j) {

@@ -222,14 +222,15 @@ expert_combine_kernel(const T *__restrict__ y, size_t y_stride, uint32_t rows, c
                       const float *__restrict__ weights, uint32_t tokens, uint32_t topk, uint32_t pieces,
                       T *__restrict__ out, size_t out_stride)
 {
+    constexpr int kCols = sizeof(T) * N >= 8 ? 1 : kNarrow<T, N>;  // at 8 bytes two cost more registers than they give
     const uint32_t t = blockIdx.x * blockDim.y + threadIdx.y;
     if (t >= tokens) return;
-    for (uint32_t c = threadIdx.x; c < pieces; c += blockDim.x) {
-        float acc[N] = {};
+    for (uint32_t first = threadIdx.x; first < pieces; first += kCols * blockDim.x) {
+        float acc[kCols][N] = {};
         for (uint32_t base = 0; base < topk; base += kAhead) {
             uint32_t slot[kAhead];
             float w[kAhead];
-            Piece<T, N> v[kAhead];
+            Piece<T, N> v[kAhead][kCols];
 #pragma unroll
             for (int j = 0; j < kAhead; ++j) {
                 const uint64_t p = uint64_t(t) * topk + base + j;
@@ -238,17 +239,29 @@ expert_combine_kernel(const T *__restrict__ y, size_t y_stride, uint32_t rows, c
             }
 #pragma unroll
             for (int j = 0; j < kAhead; ++j)
-                if (slot[j] < rows) v[j] = load_piece<T, N>(y + size_t(slot[j]) * y_stride + size_t(c) * N);
+                if (slot[j] < rows)
+#pragma unroll
+                    for (int q = 0; q < kCols; ++q) {
+                        const uint32_t c = first + q * blockDim.x;
+                        if (c < pieces) v[j][q] = load_piece<T, N>(y + size_t(slot[j]) * y_stride + size_t(c) * N);
+                    }
 #pragma unroll
             for (int j = 0; j < kAhead; ++j)
                 if (slot[j] < rows)
 #pragma unroll
-                    for (int i = 0; i < N; ++i) acc[i] = fmaf(w[j], row_to_float(v[j].v[i]), acc[i]);
-        }
-        Piece<T, N> o;
+                    for (int q = 0; q < kCols; ++q)
 #pragma unroll
-        for (int i = 0; i < N; ++i) o.v[i] = row_from_float<T>(acc[i]);
-        store_piece<T, N>(out + size_t(t) * out_stride + size_t(c) * N, o);
+                        for (int i = 0; i < N; ++i) acc[q][i] = fmaf(w[j], row_to_float(v[j][q].v[i]), acc[q][i]);
+        }
+#pragma unroll
+        for (int q = 0; q < kCols; ++q) {
+            const uint32_t c = first + q * blockDim.x;
+            if (c >= pieces) break;
+            Piece<T, N> o;
+#pragma unroll
+            for (int i = 0; i < N; ++i) o.v[i] = row_from_float<T>(acc[q][i]);
+            store_piece<T, N>(out + size_t(t) * out_stride + size_t(c) * N, o);
+        }
     }
 }
 
@@ -272,16 +285,32 @@ expert_combine_grad_kernel(const T *__restrict__ g, size_t g_stride, const T *__
         if (slot < rows) {
             const float w = weights ? weights[p] : 1.0f;
             const T *gr = g + size_t(p / topk) * g_stride;
-            for (uint32_t c = lane; c < pieces; c += 32) {
-                const Piece<T, N> a = load_piece<T, N>(gr + size_t(c) * N);
-                Piece<T, N> o;
+            constexpr int kCols = kNarrow<T, N>;
+            for (uint32_t first = lane; first < pieces; first += 32 * kCols) {
+                // Narrow pieces of both rows are loaded together; 16-byte ones
+                // of y after the store, which is the faster order for them (98
+                // against 106 us for 8192 x 8 pairs of 2048 bf16).
+                Piece<T, N> a[kCols], b[kCols];
 #pragma unroll
-                for (int i = 0; i < N; ++i) o.v[i] = row_from_float<T>(w * row_to_float(a.v[i]));
-                stream_piece<T, N>(dy + size_t(slot) * dy_stride + size_t(c) * N, o);
-                if (dweights) {
-                    const Piece<T, N> b = load_piece<T, N>(y + size_t(slot) * y_stride + size_t(c) * N);
+                for (int q = 0; q < kCols; ++q) {
+                    const uint32_t c = first + 32 * q;
+                    if (c >= pieces) break;
+                    a[q] = load_piece<T, N>(gr + size_t(c) * N);
+                    if (kCols > 1 && dweights) b[q] = load_piece<T, N>(y + size_t(slot) * y_stride + size_t(c) * N);
+                }
 #pragma unroll
-                    for (int i = 0; i < N; ++i) dot = fmaf(row_to_float(a.v[i]), row_to_float(b.v[i]), dot);
+                for (int q = 0; q < kCols; ++q) {
+                    const uint32_t c = first + 32 * q;
+                    if (c >= pieces) break;
+                    Piece<T, N> o;
+#pragma unroll
+                    for (int i = 0; i < N; ++i) o.v[i] = row_from_float<T>(w * row_to_float(a[q].v[i]));
+                    stream_piece<T, N>(dy + size_t(slot) * dy_stride + size_t(c) * N, o);
+                    if (dweights) {
+                        if (kCols == 1) b[q] = load_piece<T, N>(y + size_t(slot) * y_stride + size_t(c) * N);
+#pragma unroll
+                        for (int i = 0; i < N; ++i) dot = fmaf(row_to_float(a[q].v[i]), row_to_float(b[q].v[i]), dot);
+                    }
                 }
             }
         }

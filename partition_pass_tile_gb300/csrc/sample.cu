@@ -582,25 +582,40 @@ __device__ __forceinline__ uint32_t kth_largest(uint32_t o, uint32_t k)
     return at;
 }
 
-// The largest key K such that the amounts of all keys >= K sum to at least
-// target (>= 1); 0 if they all together do not.  By radix selection, 8 bits a
-// round, over the whole row by one CTA; its histogram is laid over the list.
-// `each` calls its argument with every token's key and amount.
+// The largest key K such that `above` and the amounts of all keys >= K sum to
+// at least target (> above); 0 if they all together do not.  By radix
+// selection, 8 bits a round, over the whole row by one CTA; its histogram is
+// laid over the list.  `each` calls its argument with the tokens' keys and
+// amounts.
 template <class Each>
-__device__ __noinline__ uint64_t select_cut(uint64_t target, Smem &sm, const Each &each)
+__device__ __noinline__ uint64_t select_cut(uint64_t target, uint64_t above, Smem &sm, const Each &each)
 {
     uint64_t *hist = sm.list;
-    uint64_t prefix = 0u, above = 0u;
+    uint64_t prefix = 0u;
     for (int shift = 56; shift >= 0; shift -= 8) {
         __syncthreads();
         for (int b = threadIdx.x; b < 256; b += kThreads) hist[b] = 0u;
         if (threadIdx.x == 0) sm.found = false;
         __syncthreads();
+        // Equal values, of which there are many where this is needed, fall in
+        // one bin: a thread adds up what follows in the same bin.
+        uint32_t bin = 0u;
+        uint64_t sum = 0u;
+        auto flush = [&]() {
+            if (sum)
+                atomicAdd(reinterpret_cast<unsigned long long *>(&hist[bin]), static_cast<unsigned long long>(sum));
+        };
         each([&](uint64_t key, uint64_t amount) {
-            if (shift == 56 || (key >> (shift + 8)) == (prefix >> (shift + 8)))
-                atomicAdd(reinterpret_cast<unsigned long long *>(&hist[(key >> shift) & 255u]),
-                          static_cast<unsigned long long>(amount));
+            if (shift != 56 && (key >> (shift + 8)) != (prefix >> (shift + 8))) return;
+            const uint32_t b = uint32_t(key >> shift) & 255u;
+            if (b != bin) {
+                flush();
+                bin = b;
+                sum = 0u;
+            }
+            sum += amount;
         });
+        flush();
         __syncthreads();
         if (threadIdx.x < 32) {
             // Lane l owns bins 255 - 8 l down to 248 - 8 l.
@@ -710,6 +725,8 @@ __device__ __noinline__ bool find_cut(Team &team, const Row<T> &row, const Scale
     int64_t error = 0;
     Kept mine;
     uint32_t state = kAgain;
+    float top = 0.0f, low = 0.0f;  // the interval of the collected, and what lies above it
+    uint64_t above = 0u;
     for (int tries = 0; state == kAgain && tries < 4; ++tries) {
         uint64_t rough = 0u;
         if (team.rank == 0) {
@@ -762,8 +779,8 @@ __device__ __noinline__ bool find_cut(Team &team, const Row<T> &row, const Scale
         // values, to the list; those above it added up.
         const uint32_t bin = team.lead->bin, lo = bin > 0 ? bin - 1 : 0;
         const float unit = 1.0f / (kBinsPerPower * scale.power);
-        const float top = bin > 1 ? scale.m - (float(lo) - 0.5f) * unit : 3.402823466e38f;
-        const float low = fmaxf(scale.m - (float(bin) + 1.5f) * unit, -3.402823466e38f);
+        top = bin > 1 ? scale.m - (float(lo) - 0.5f) * unit : 3.402823466e38f;
+        low = fmaxf(scale.m - (float(bin) + 1.5f) * unit, -3.402823466e38f);
         mass = 0.0f;
         mine = Kept();
         row.each(sm, [&](const Piece<T, kVec> &x, const T *at, uint32_t i) {
@@ -773,11 +790,11 @@ __device__ __noinline__ bool find_cut(Team &team, const Row<T> &row, const Scale
 #pragma unroll
             for (uint32_t e = 0; e < kVec; ++e) {
                 const float v = sample_value(row_to_float(x.v[e]));
-                const bool in = v >= low && (!FLOOR || floor.keeps(v, i + e)), above = in && v > top;
+                const bool in = v >= low && (!FLOOR || floor.keeps(v, i + e)), over = in && v > top;
                 w[e] = scale.w(v);
-                if (in && !above) list |= 1u << e;
-                mass += above ? (MASS ? w[e] : 1.0f) : 0.0f;
-                const bool keep = above && w[e] >= q;
+                if (in && !over) list |= 1u << e;
+                mass += over ? (MASS ? w[e] : 1.0f) : 0.0f;
+                const bool keep = over && w[e] >= q;
                 mine.sum += keep ? w[e] : 0.0f;
                 if (keep) sure |= 1u << e;
             }
@@ -785,6 +802,9 @@ __device__ __noinline__ bool find_cut(Team &team, const Row<T> &row, const Scale
             if (kept && __any_sync(kFull, sure != 0u)) {
                 float u[kVec];
                 row.uniforms(i, u);
+                // where one piece is kept the next is likely to be
+                const uint32_t next = i + row.team * kVec;
+                if (next < row.vocab) asm volatile("prefetch.global.L2 [%0];" ::"l"(row.u + next));
                 mine.draw.offer(w, sure, u, row, scale, at, i);
             }
         });
@@ -793,7 +813,7 @@ __device__ __noinline__ bool find_cut(Team &team, const Row<T> &row, const Scale
         if (team.rank == 0) {
             // The cut is in the list if the tokens above it stay below the
             // target and the list reaches it.  A histogram leaves few to sort.
-            const uint64_t above = MASS ? uint64_t(double(mass) * double(kFixed) + 0.5) : uint64_t(mass);
+            above = MASS ? uint64_t(double(mass) * double(kFixed) + 0.5) : uint64_t(mass);
             error = int64_t(above) - int64_t(rough);
             auto amount = [&](uint64_t key) { return MASS ? scale.fixed(key_value(key)) : uint64_t(1); };
             auto keep = [&](uint64_t key) {
@@ -839,17 +859,32 @@ __device__ __noinline__ bool find_cut(Team &team, const Row<T> &row, const Scale
     if (kept) *kept = mine;
     if (state != kFound) {
         if (team.rank == 0) {
+            // Among the interval's tokens where those were only too many (equal
+            // values), else among all.
             const Row<T> whole(row.x, row.u, row.vocab, 0, 1);
-            const uint64_t cut = select_cut(target, sm, [&](auto add) {
-                whole.each(sm, [&](const Piece<T, kVec> &x, const T *, uint32_t i) {
+            if (state != kMissed || above >= target) {
+                top = 3.402823466e38f;
+                low = -top;
+                above = 0u;
+            }
+            uint64_t cut = 0u;
+            for (bool on = true; on;) {
+                cut = select_cut(target, above, sm, [&](auto add) {
+                    whole.each(sm, [&](const Piece<T, kVec> &x, const T *, uint32_t i) {
+                        if (!__any_sync(kFull, piece_max(x) >= low)) return;
 #pragma unroll
-                    for (uint32_t e = 0; e < kVec; ++e) {
-                        const float v = sample_value(row_to_float(x.v[e]));
-                        if (v > -INFINITY && (!FLOOR || floor.keeps(v, i + e)))
-                            add(order_key(v, i + e), MASS ? scale.fixed(v) : uint64_t(1));
-                    }
+                        for (uint32_t e = 0; e < kVec; ++e) {
+                            const float v = sample_value(row_to_float(x.v[e]));
+                            if (v >= low && v <= top && (!FLOOR || floor.keeps(v, i + e)))
+                                add(order_key(v, i + e), MASS ? scale.fixed(v) : uint64_t(1));
+                        }
+                    });
                 });
-            });
+                on = cut == 0u && above != 0u;  // rounding: once more, among all
+                top = 3.402823466e38f;
+                low = -top;
+                above = 0u;
+            }
             __syncthreads();
             if (threadIdx.x == 0) sm.cut = cut;
         }
