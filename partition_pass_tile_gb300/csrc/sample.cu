@@ -12,9 +12,9 @@
 // A team of 1 to 8 CTAs (a cluster) owns a row; the first CTA is its leader.
 //   - no filter: one pass for the sum and the draw; min-p alone: one before it
 //     for the maximum;
-//   - a small top-k, or top-k of a short row: one pass collects the candidates,
-//     the tokens not below a lower bound of the top_k-th largest value, and the
-//     leader sorts a few of them and does the rest;
+//   - a small top-k, or a short row: one pass collects the candidates, all
+//     tokens or those not below a lower bound of the top_k-th largest value, and
+//     the leader sorts a few of them and does the rest;
 //   - else each cut is found by a histogram of the tokens over their weight, a
 //     pass that collects the tokens about the cut's bin and adds up those
 //     above, and a sort of few of the collected; the last cut's pass draws on
@@ -504,7 +504,10 @@ __device__ __noinline__ void sort_list(uint64_t *list, uint32_t n)
 
 // Where of the list a cut falls, by one CTA: the bin of a histogram over
 // (top - x) * rate, and the amounts of the bins before it and of the tokens
-// `before` the list; kSubBins where the list does not reach the target.
+// `before` the list; kSubBins where the list does not reach the target.  With
+// `open` the last bin is not counted: it is where thousands of tokens without
+// weight may lie, whose atomics would follow one another (400 rows of 4000, top-k
+// with top-p: 123 us so, 18 without).
 struct SubBin {
     float top, rate;
     uint32_t at;
@@ -516,17 +519,20 @@ struct SubBin {
 };
 
 template <class Amount>
-__device__ __forceinline__ SubBin sub_bin(Smem &sm, uint32_t n, float top, float span, uint64_t before, uint64_t target,
-                                          const Amount &amount)
+__device__ __forceinline__ SubBin sub_bin(Smem &sm, uint32_t n, float top, float span, bool open, uint64_t before,
+                                          uint64_t target, const Amount &amount)
 {
     SubBin r{top, float(kSubBins) / fmaxf(span, 1e-30f), kSubBins, 0u};
     __syncthreads();
     for (int b = threadIdx.x; b < kSubBins; b += kThreads) sm.sub[b] = 0u;
     if (threadIdx.x == 0) sm.bin = kSubBins;
     __syncthreads();
-    for (uint32_t j = threadIdx.x; j < n; j += kThreads)
-        atomicAdd(reinterpret_cast<unsigned long long *>(&sm.sub[r.of(sm.list[j])]),
-                  static_cast<unsigned long long>(amount(sm.list[j])));
+    for (uint32_t j = threadIdx.x; j < n; j += kThreads) {
+        const uint32_t b = r.of(sm.list[j]);
+        if (!open || b + 1 < uint32_t(kSubBins))
+            atomicAdd(reinterpret_cast<unsigned long long *>(&sm.sub[b]),
+                      static_cast<unsigned long long>(amount(sm.list[j])));
+    }
     __syncthreads();
     constexpr int kPer = kSubBins / kThreads;
     uint64_t part[kPer], sum = 0u, all;
@@ -827,7 +833,7 @@ __device__ __noinline__ bool find_cut(Team &team, const Row<T> &row, const Scale
             SubBin sub{0.0f, 0.0f, uint32_t(kSubBins), 0u};
             if (n <= kList && above < target) {
                 const float first = fminf(top, scale.m);
-                sub = sub_bin(sm, n, first, first - low, above, target, amount);
+                sub = sub_bin(sm, n, first, first - low, false, above, target, amount);
             }
             if (threadIdx.x == 0) sm.state = n <= kList ? kAgain : kMissed;
             if (sub.at < uint32_t(kSubBins)) {
@@ -898,56 +904,80 @@ __device__ __noinline__ bool find_cut(Team &team, const Row<T> &row, const Scale
 }
 
 // The rest of a row whose n candidates, all tokens not below `threshold`, are
-// in the leader's list, by the leader's CTA: top-k, sort, top-p, min-p, draw.
+// in the leader's list, by the leader's CTA: top-k, top-p, min-p, draw.  A
+// histogram of the list finds the first cut's bin, and few tokens are left to
+// sort: with top-k those down to the bin, else the bin of the top-p cut alone,
+// the tokens above it being kept as they are.
 __device__ __noinline__ void finish_list(Smem &sm, uint32_t n, uint32_t k, float t, float p, float q, float threshold,
                                          const float *__restrict__ u, int32_t *token, float *logprob)
 {
     uint64_t *list = sm.list;
     Team alone(sm, 1);
-    if (n > 64) {
-        // A histogram of the values leaves k and a few to sort.
-        uint64_t most = 0u;
-        for (uint32_t j = threadIdx.x; j < n; j += kThreads) most = sm.list[j] > most ? sm.list[j] : most;
-        const float m = key_value(alone.largest(most));
-        const SubBin sub = sub_bin(sm, n, m, m - fmaxf(threshold, m - 32.0f * t), 0u, min(k, n),
-                                   [](uint64_t) { return uint64_t(1); });
-        // The last bin of a span of 32 t holds tokens without weight, which may go.
-        const uint32_t last = m - 32.0f * t > threshold ? min(sub.at, uint32_t(kSubBins - 2)) : sub.at;
+    uint64_t most = 0u;
+    for (uint32_t j = threadIdx.x; j < n; j += kThreads) most = list[j] > most ? list[j] : most;
+    const Scale scale(key_value(alone.largest(most)), t);
+    // Down to the threshold, or 32 t below the maximum, where no weight is left.
+    const bool open = scale.m - 32.0f * t > threshold;
+    const float span = scale.m - fmaxf(threshold, scale.m - 32.0f * t);
+    Kept kept;
+    float x = 0.0f;  // of the token that this thread would draw
+    auto keep = [&](uint64_t key) {
+        const uint32_t i = key_index(key);
+        const float w = scale.w(key_value(key));
+        if (w < q) return;
+        kept.sum += w;
+        if (w < kLightest) return;
+        kept.draw.take(w, u[i], i);
+        if (kept.draw.index == i) x = key_value(key);
+    };
+    uint64_t before = 0u, target = ~uint64_t(0), sum = 0u, all;
+    bool cut = false;  // top-p's target is known
+    if (n > 64 && k < n) {
+        const SubBin sub = sub_bin(sm, n, scale.m, span, open, 0u, k, [](uint64_t) { return uint64_t(1); });
+        const uint32_t last = open ? min(sub.at, uint32_t(kSubBins - 2)) : sub.at;
         const uint32_t few = pick_few(sm, n, [&](uint64_t key) { return sub.of(key) <= last; });
         if (few <= kFew) {
             list = sm.few;
             n = few;
+        }
+    } else if (n > 64 && p < 1.0f) {
+        for (uint32_t j = threadIdx.x; j < n; j += kThreads) sum += scale.fixed(key_value(list[j]));
+        block_scan(sum, sm, all);
+        const uint64_t aim = share_of(p, double(all));
+        const SubBin sub = sub_bin(sm, n, scale.m, span, open, 0u, aim,
+                                   [&](uint64_t key) { return scale.fixed(key_value(key)); });
+        const uint32_t few = pick_few(sm, n, [&](uint64_t key) { return sub.of(key) == sub.at; });
+        if (sub.at < uint32_t(kSubBins) && few <= kFew) {
+            for (uint32_t j = threadIdx.x; j < n; j += kThreads)
+                if (sub.of(list[j]) < sub.at) keep(list[j]);
+            list = sm.few;
+            n = few;
+            cut = true;
+            target = aim;
+            before = sub.before;
         }
     }
     for (uint32_t j = threadIdx.x; j < n; j += kThreads)  // on their way while the list is sorted
         asm volatile("prefetch.global.L2 [%0];" ::"l"(u + key_index(list[j])));
     sort_list(list, n);
     n = min(k, n);
-    const Scale scale(key_value(list[0]), t);
     const uint32_t per = (n + kThreads - 1) / kThreads;
     const uint32_t first = min(n, threadIdx.x * per), last = min(n, first + per);
-    uint64_t before = 0u, target = ~uint64_t(0);
     if (p < 1.0f) {
-        uint64_t sum = 0u, all;
+        sum = 0u;
         for (uint32_t j = first; j < last; ++j) sum += scale.fixed(key_value(list[j]));
-        before = block_scan(sum, sm, all);
-        target = share_of(p, double(all));
+        before += block_scan(sum, sm, all);
+        if (!cut) target = share_of(p, double(all));
     }
-    Kept kept;
     for (uint32_t j = first; j < last && before < target; ++j) {
-        const uint32_t i = key_index(list[j]);
-        const float w = scale.w(key_value(list[j]));
+        keep(list[j]);
         if (p < 1.0f) before += scale.fixed(key_value(list[j]));
-        if (w < q) continue;
-        kept.sum += w;
-        if (w >= kLightest) kept.draw.take(w, u[i], i);
     }
     const KeySum end = alone.reduce(KeySum{kept.draw.key(), kept.sum});
-    for (uint32_t j = first; j < last; ++j)
-        if (key_index(list[j]) == key_index(end.key)) {
-            *token = int32_t(key_index(end.key));
-            if (logprob) *logprob = scale.z(key_value(list[j])) - logf(end.sum);
-        }
+    if (kept.draw.key() == end.key) {
+        *token = int32_t(key_index(end.key));
+        if (logprob) *logprob = scale.z(x) - logf(end.sum);
+    }
 }
 
 // The tokens from the cut on that weigh at least q: the sum of their weights
@@ -1026,19 +1056,20 @@ sample_kernel(const T *__restrict__ logits, size_t logits_stride, uint32_t vocab
     int32_t *token = tokens + r;
     float *logprob = logprobs ? logprobs + r : nullptr;
 
-    // Top-k by one pass that collects candidates: all tokens of a short row;
-    // else the k-th largest of the threads' maxima over each CTA's first
-    // kBatch tokens, rounded down to 16 bits, bounds the k-th largest value
-    // from below, and about k in kBatch tokens get in; at k = kThreads / 2,
-    // -512 ln(1 - 1/2) = 355 a batch, which a list has room for.
+    // By one pass that collects candidates: all tokens of a short row (one of
+    // 4000 with top-p 0.9: 18 us); with a small top-k those not below a bound,
+    // the k-th largest of the threads' maxima over each CTA's first kBatch
+    // tokens, rounded down to 16 bits (7 us; 12 where all are listed). About k in
+    // kBatch tokens get in; at k = kThreads / 2, -512 ln(1 - 1/2) = 355 a batch,
+    // which a list has room for.
     constexpr uint32_t kBatch = kSample * kThreads * kVec;
-    const bool brief = vocab <= kList / 2;
-    if (!greedy && k < vocab &&
+    const bool brief = vocab <= kList && (k == vocab || k <= kFew / 2);
+    if (!greedy && (k < vocab || p < 1.0f) &&
         (brief || (k <= uint32_t(kThreads / 2) && uint64_t(k) * vocab <= uint64_t(kBatch) * (kList / 2)))) {
         if (threadIdx.x == 0) sm.count = 0u;
         float threshold = -INFINITY;
         team.sync();
-        if (!brief) {
+        if (!brief || (k <= uint32_t(kThreads / 2) && vocab > uint32_t(kFew))) {
             float best = -INFINITY;
 #pragma unroll
             for (int b = 0; b < kSample; b += kSample / 2) {
@@ -1091,7 +1122,9 @@ sample_kernel(const T *__restrict__ logits, size_t logits_stride, uint32_t vocab
                 if (team.rank == 0 && threadIdx.x == 0) {
                     const uint32_t i = key_index(end.key);
                     *token = int32_t(i);
-                    if (logprob) *logprob = scale.z(row.value(i)) - logf(end.sum);
+                    // z and log(sum) are far from 0 where the unit is far from the
+                    // maximum; the quotient does not lose what they share
+                    if (logprob) *logprob = fminf(logf(scale.w(row.value(i)) / end.sum), 0.0f);
                 }
                 team.sync();  // no CTA leaves while another may write to its slots
                 return;
