@@ -337,6 +337,18 @@ def test_sample(vocab, pad, shift, kind, dtype):
     check_sample(x, x64, u[:, :vocab], PARAMS, vocab)
 
 
+@pytest.mark.parametrize("kind", ["bulk", "flat", "lowest", "far", "broken"])
+@pytest.mark.parametrize("vocab,dtype", [(64, "f32"), (65, "bf16"), (1024, "f16"), (1025, "f32"), (4095, "f32"),
+                                         (4097, "bf16")])
+def test_sample_many_short_rows(vocab, dtype, kind):
+    rng = np.random.default_rng(vocab + len(kind))
+    params = [(t, k, p, q) for t in (0.02, 1.0, 5.0) for k in (0, 64, 257, 513) for p in (1.0, 0.9, 0.4)
+              for q in (0.0, 0.02)] * 3
+    x, x64 = logits_of(rng, len(params), vocab, dtype, kind, 3, 0)
+    u = torch.from_numpy(rng.random((len(params), vocab)).astype(np.float32)).clamp_(max=1 - 2.0 ** -24).cuda()
+    check_sample(x, x64, u, params, vocab)
+
+
 @pytest.mark.parametrize("dtype,vocab", [("bf16", 262147), ("f32", 131072), ("f16", 200001)])
 def test_sample_large_vocabulary(dtype, vocab):
     rng = np.random.default_rng(vocab)
