@@ -23,9 +23,9 @@
 //     rows of 128000 equal bf16 logits take 0.6 ms, 100 us is usual.
 // Measured, kernel alone, after a flush that leaves L2 dirty (a plain maximum
 // of every row of 512 x 128000 float32 takes 64 us so): that batch with top-k 50
-// 78 us against 295 by histograms; unfiltered 129 us in one pass against 199 in
-// two; top-p 0.95 397 us, three passes whose second and third read 262 MB again,
-// more than L2.  One row of 128000 bf16: 16 us unfiltered or top-k, 53 us top-p.
+// 80 us against 295 by histograms; unfiltered 127 us in one pass against 199 in
+// two; top-p 0.95 at T = 1.2 453 us, three passes whose second and third read
+// 262 MB again, more than L2, at T = 0.5 143 us, one pass.  One row of 128000 bf16: 16 us unfiltered or top-k, 53 us top-p.
 // 512 threads at two CTAs per SM and rings of three pieces: more rows or pieces
 // under way are slower (256 threads at four CTAs 109 us for top-k 50, rings of
 // six 80, clusters of two 102), because HBM serves fewer, longer streams better.
@@ -907,9 +907,11 @@ __device__ __noinline__ bool find_cut(Team &team, const Row<T> &row, const Scale
 // in the leader's list, by the leader's CTA: top-k, top-p, min-p, draw.  A
 // histogram of the list finds the first cut's bin, and few tokens are left to
 // sort: with top-k those down to the bin, else the bin of the top-p cut alone,
-// the tokens above it being kept as they are.
-__device__ __noinline__ void finish_list(Smem &sm, uint32_t n, uint32_t k, float t, float p, float q, float threshold,
-                                         const float *__restrict__ u, int32_t *token, float *logprob)
+// the tokens above it being kept as they are.  `total` is the sum of all
+// tokens' weights where the list may not hold every one that has some; returns
+// false, with nothing written, where the list then ends before the top-p cut.
+__device__ __noinline__ bool finish_list(Smem &sm, uint32_t n, uint32_t k, float t, float p, float q, float threshold,
+                                         float total, const float *__restrict__ u, int32_t *token, float *logprob)
 {
     uint64_t *list = sm.list;
     Team alone(sm, 1);
@@ -943,7 +945,8 @@ __device__ __noinline__ void finish_list(Smem &sm, uint32_t n, uint32_t k, float
     } else if (n > 64 && p < 1.0f) {
         for (uint32_t j = threadIdx.x; j < n; j += kThreads) sum += scale.fixed(key_value(list[j]));
         block_scan(sum, sm, all);
-        const uint64_t aim = share_of(p, double(all));
+        const uint64_t aim = share_of(p, total > 0.0f ? double(total) * double(kFixed) : double(all));
+        if (all < aim) return false;
         const SubBin sub = sub_bin(sm, n, scale.m, span, open, 0u, aim,
                                    [&](uint64_t key) { return scale.fixed(key_value(key)); });
         const uint32_t few = pick_few(sm, n, [&](uint64_t key) { return sub.of(key) == sub.at; });
@@ -967,7 +970,8 @@ __device__ __noinline__ void finish_list(Smem &sm, uint32_t n, uint32_t k, float
         sum = 0u;
         for (uint32_t j = first; j < last; ++j) sum += scale.fixed(key_value(list[j]));
         before += block_scan(sum, sm, all);
-        if (!cut) target = share_of(p, double(all));
+        if (!cut) target = share_of(p, total > 0.0f ? double(total) * double(kFixed) : double(all));
+        if (!cut && all < target) return false;
     }
     for (uint32_t j = first; j < last && before < target; ++j) {
         keep(list[j]);
@@ -978,6 +982,27 @@ __device__ __noinline__ void finish_list(Smem &sm, uint32_t n, uint32_t k, float
         *token = int32_t(key_index(end.key));
         if (logprob) *logprob = scale.z(x) - logf(end.sum);
     }
+    return true;
+}
+
+// A value that about k in kBatch of the row's tokens are not below: the k-th
+// largest of the threads' maxima over the CTA's first kBatch tokens, rounded
+// down to 16 bits.
+template <class T>
+__device__ __forceinline__ float sample_bound(const Row<T> &row, uint32_t k)
+{
+    constexpr uint32_t kVec = Row<T>::kVec;
+    float best = -INFINITY;
+#pragma unroll
+    for (int b = 0; b < kSample; b += kSample / 2) {
+        Piece<T, kVec> pc[kSample / 2];
+#pragma unroll
+        for (int j = 0; j < kSample / 2; ++j) row.load((b + j) * row.team + row.me, pc[j]);
+#pragma unroll
+        for (int j = 0; j < kSample / 2; ++j) best = fmaxf(best, piece_max(pc[j]));
+    }
+    const uint32_t least = kth_largest(best > -INFINITY ? order_bits(sample_value(best)) : 0u, k);
+    return least ? order_value(least) : -INFINITY;
 }
 
 // The tokens from the cut on that weigh at least q: the sum of their weights
@@ -1069,19 +1094,7 @@ sample_kernel(const T *__restrict__ logits, size_t logits_stride, uint32_t vocab
         if (threadIdx.x == 0) sm.count = 0u;
         float threshold = -INFINITY;
         team.sync();
-        if (!brief || (k <= uint32_t(kThreads / 2) && vocab > uint32_t(kFew))) {
-            float best = -INFINITY;
-#pragma unroll
-            for (int b = 0; b < kSample; b += kSample / 2) {
-                Piece<T, kVec> pc[kSample / 2];
-#pragma unroll
-                for (int j = 0; j < kSample / 2; ++j) row.load((b + j) * row.team + row.me, pc[j]);
-#pragma unroll
-                for (int j = 0; j < kSample / 2; ++j) best = fmaxf(best, piece_max(pc[j]));
-            }
-            const uint32_t least = kth_largest(best > -INFINITY ? order_bits(sample_value(best)) : 0u, k);
-            if (least) threshold = order_value(least);
-        }
+        if (!brief || (k <= uint32_t(kThreads / 2) && vocab > uint32_t(kFew))) threshold = sample_bound(row, k);
         threshold = fmaxf(threshold, -3.402823466e38f);  // -inf is no candidate
         row.each(sm, [&](const Piece<T, kVec> &x, const T *at, uint32_t i) {
             if (!__any_sync(kFull, piece_max(x) >= threshold)) return;
@@ -1097,7 +1110,7 @@ sample_kernel(const T *__restrict__ logits, size_t logits_stride, uint32_t vocab
         if (n <= kList) {
             if (team.rank == 0) {
                 if (n > 0) {
-                    finish_list(sm, n, k, t, p, q, threshold, row.u, token, logprob);
+                    finish_list(sm, n, k, t, p, q, threshold, 0.0f, row.u, token, logprob);
                 } else if (threadIdx.x == 0) {
                     *token = -1;
                     if (logprob) *logprob = -INFINITY;
@@ -1132,11 +1145,43 @@ sample_kernel(const T *__restrict__ logits, size_t logits_stride, uint32_t vocab
         }
     }
 
-    // The first of the order.
+    // The first of the order.  Where top-p stands alone and a CTA has a row, the
+    // same pass lists the largest tokens and adds up all weights, in units of the
+    // thread's maximum so far: the cut of a row with a few likely tokens is in
+    // the list, and the row is done.  512 x 128000 float32, normal logits with 40
+    // raised by up to 12, against the passes below alone: T = 0.5, p = 0.95 143 us
+    // for 270; T = 0.7, p = 0.9 244 for 299; where no list holds the cut, T = 1.2,
+    // p = 0.95, 455 for 395.  Not for rows of a few samples (200 x 20000: 33 us for
+    // 49, but 70 for 55), nor for few rows, whose time is that of the barriers.
+    const uint32_t wish = min(uint32_t(kThreads / 2), uint32_t(uint64_t(kBatch) * (kList / 2) / vocab));
+    const bool likely =
+        !greedy && k == vocab && p < 1.0f && team.size == 1 && vocab >= 3u * kBatch && wish >= 32u;
+    float threshold = INFINITY, unit = -3.402823466e38f, total = 0.0f;
+    const float power = Scale(0.0f, t).power;
+    if (likely) {
+        if (threadIdx.x == 0) sm.count = 0u;
+        threshold = fmaxf(sample_bound(row, wish), -3.402823466e38f);
+        __syncthreads();
+    }
     float best = -INFINITY;
     uint32_t at = ~0u;
     row.each(sm, [&](const Piece<T, kVec> &x, const T *p, uint32_t i) {
         const float top = sample_value(piece_max(x));
+        if (likely) {
+            if (top > unit) {
+                total *= exp2f((unit - top) * power);
+                unit = top;
+            }
+#pragma unroll
+            for (uint32_t e = 0; e < kVec; ++e) total += exp2f((sample_value(row_to_float(x.v[e])) - unit) * power);
+            if (__any_sync(kFull, top >= threshold)) {
+                uint32_t which = 0u;
+#pragma unroll
+                for (uint32_t e = 0; e < kVec; ++e)
+                    if (row_to_float(x.v[e]) >= threshold) which |= 1u << e;
+                team.append(which, p, i);
+            }
+        }
         if (top > best || (top == best && i < at)) {
             best = top;
             for (int e = int(kVec) - 1; e >= 0; --e)
@@ -1153,6 +1198,13 @@ sample_kernel(const T *__restrict__ logits, size_t logits_stride, uint32_t vocab
         return;
     }
     const Scale scale(key_value(first), t);
+    if (likely) {
+        total = team.sum(total * scale.w(unit));
+        const uint32_t n = sm.count;
+        __syncthreads();
+        if (n <= kList && finish_list(sm, n, k, t, p, q, threshold, total, row.u, token, logprob)) return;
+        __syncthreads();
+    }
     Kept kept;
     uint64_t cut_key = 0u;
     bool done = false;
