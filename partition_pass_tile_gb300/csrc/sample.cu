@@ -25,7 +25,8 @@
 // of every row of 512 x 128000 float32 takes 64 us so): that batch with top-k 50
 // 80 us against 295 by histograms; unfiltered 127 us in one pass against 199 in
 // two; top-p 0.95 at T = 1.2 453 us, three passes whose second and third read
-// 262 MB again, more than L2, at T = 0.5 143 us, one pass.  One row of 128000 bf16: 16 us unfiltered or top-k, 53 us top-p.
+// 262 MB again, more than L2, at T = 0.5 143 us, one pass.  One row of 128000
+// bf16: 16 us unfiltered or top-k, 53 us top-p.
 // 512 threads at two CTAs per SM and rings of three pieces: more rows or pieces
 // under way are slower (256 threads at four CTAs 109 us for top-k 50, rings of
 // six 80, clusters of two 102), because HBM serves fewer, longer streams better.
