@@ -306,6 +306,19 @@ struct Team {
         if (size == 1) __syncthreads();
         else cg::this_cluster().sync();
     }
+    // A CTA's shared memory may be touched by others only once it runs, which
+    // no launch promises of a cluster's CTAs by itself: each announces itself
+    // by started(), and nobody looks into another before all_started().  Both
+    // together are a sync.
+    __device__ __forceinline__ void started() const
+    {
+        if (size > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    }
+    __device__ __forceinline__ void all_started() const
+    {
+        if (size == 1) __syncthreads();
+        else asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    }
     // The same value to every thread of the team: the largest key and the sum,
     // added in a fixed order.  Buffers alternate: one is written again two
     // reductions later, past a barrier that follows every read of it.
@@ -1071,6 +1084,8 @@ sample_kernel(const T *__restrict__ logits, size_t logits_stride, uint32_t vocab
     Smem &sm = *reinterpret_cast<Smem *>(sample_smem);
     constexpr uint32_t kVec = Row<T>::kVec;
     Team team(sm, cg::this_cluster().num_blocks());
+    if (threadIdx.x == 0) sm.count = 0u;
+    team.started();
     const uint32_t r = blockIdx.x / team.size;
     const Row<T> row(logits + size_t(r) * logits_stride, uniform + size_t(r) * uniform_stride, vocab, team.rank,
                      team.size);
@@ -1081,6 +1096,7 @@ sample_kernel(const T *__restrict__ logits, size_t logits_stride, uint32_t vocab
     const uint32_t k = top_k && top_k[r] > 0 ? min(uint32_t(top_k[r]), vocab) : vocab;
     int32_t *token = tokens + r;
     float *logprob = logprobs ? logprobs + r : nullptr;
+    team.all_started();
 
     // By one pass that collects candidates: all tokens of a short row (one of
     // 4000 with top-p 0.9: 18 us); with a small top-k those not below a bound,
@@ -1092,9 +1108,7 @@ sample_kernel(const T *__restrict__ logits, size_t logits_stride, uint32_t vocab
     const bool brief = vocab <= kList && (k == vocab || k <= kFew / 2);
     if (!greedy && (k < vocab || p < 1.0f) &&
         (brief || (k <= uint32_t(kThreads / 2) && uint64_t(k) * vocab <= uint64_t(kBatch) * (kList / 2)))) {
-        if (threadIdx.x == 0) sm.count = 0u;
         float threshold = -INFINITY;
-        team.sync();
         if (!brief || (k <= uint32_t(kThreads / 2) && vocab > uint32_t(kFew))) threshold = sample_bound(row, k);
         threshold = fmaxf(threshold, -3.402823466e38f);  // -inf is no candidate
         row.each(sm, [&](const Piece<T, kVec> &x, const T *at, uint32_t i) {
