@@ -882,15 +882,16 @@ __device__ __noinline__ bool find_cut(Team &team, const Row<T> &row, const Scale
     if (state != kFound) {
         if (team.rank == 0) {
             // Among the interval's tokens where those were only too many (equal
-            // values), else among all.
+            // values), else among all; and among all where the interval ends
+            // before the cut, which the rounded amounts allow.
             const Row<T> whole(row.x, row.u, row.vocab, 0, 1);
-            if (state != kMissed || above >= target) {
-                top = 3.402823466e38f;
-                low = -top;
-                above = 0u;
-            }
             uint64_t cut = 0u;
-            for (bool on = true; on;) {
+            for (bool part = state == kMissed && above < target, on = true; on; part = false) {
+                if (!part) {
+                    top = 3.402823466e38f;
+                    low = -top;
+                    above = 0u;
+                }
                 cut = select_cut(target, above, sm, [&](auto add) {
                     whole.each(sm, [&](const Piece<T, kVec> &x, const T *, uint32_t i) {
                         if (!__any_sync(kFull, piece_max(x) >= low)) return;
@@ -902,10 +903,7 @@ __device__ __noinline__ bool find_cut(Team &team, const Row<T> &row, const Scale
                         }
                     });
                 });
-                on = cut == 0u && above != 0u;  // rounding: once more, among all
-                top = 3.402823466e38f;
-                low = -top;
-                above = 0u;
+                on = cut == 0u && part;
             }
             __syncthreads();
             if (threadIdx.x == 0) sm.cut = cut;
