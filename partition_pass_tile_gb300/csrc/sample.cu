@@ -5,9 +5,9 @@
 // index, which is the descending order of the 64-bit key
 //     (order-preserving bits of x) << 32 | ~index,
 // so a filter is a cut of that key.  Sums of weights are float32 trees whose
-// order the row's length and the team's size decide, and, where atomics add,
-// whole multiples of 2^-40 of the largest weight: the same call always finds
-// the same cut.
+// order the row's length and the team's size decide, and, where atomics add or
+// have decided the order (of a list), whole multiples of 2^-40 of the largest
+// weight: the same call always finds the same cut, and gives the same bits.
 //
 // A team of 1 to 8 CTAs (a cluster) owns a row; the first CTA is its leader.
 //   - no filter: one pass for the sum and the draw; min-p alone: one before it
@@ -110,6 +110,9 @@ struct Scale {
     __device__ __forceinline__ float w(float x) const { return exp2f(log_w(x)); }
     __device__ __forceinline__ uint64_t fixed(float x) const { return __float2ull_rn(w(x) * kFixed); }
 };
+
+// A sum of weights in units of 2^-40.
+__device__ __forceinline__ float from_fixed(uint64_t units) { return __ull2float_rn(units) * (1.0f / kFixed); }
 
 // The largest value of a piece; NaN counts for nothing.
 template <class T, int N>
@@ -838,10 +841,11 @@ __device__ __noinline__ bool find_cut(Team &team, const Row<T> &row, const Scale
             above = MASS ? uint64_t(double(mass) * double(kFixed) + 0.5) : uint64_t(mass);
             error = int64_t(above) - int64_t(rough);
             auto amount = [&](uint64_t key) { return MASS ? scale.fixed(key_value(key)) : uint64_t(1); };
+            uint64_t listed = 0u;  // kept weights of the list
             auto keep = [&](uint64_t key) {
                 const float w = scale.w(key_value(key));
                 if (!kept || w < q) return;
-                mine.sum += w;
+                listed += scale.fixed(key_value(key));
                 if (w >= kLightest) mine.draw.take(w, row.u[key_index(key)], key_index(key));
             };
             SubBin sub{0.0f, 0.0f, uint32_t(kSubBins), 0u};
@@ -871,6 +875,11 @@ __device__ __noinline__ bool find_cut(Team &team, const Row<T> &row, const Scale
                         sm.cut = list[j];
                         sm.state = kFound;
                     }
+                }
+                if (kept) {
+                    __syncthreads();
+                    block_scan(listed, sm, all);
+                    if (threadIdx.x == 0) mine.sum += from_fixed(all);
                 }
             }
         }
@@ -935,14 +944,15 @@ __device__ __noinline__ bool finish_list(Smem &sm, uint32_t n, uint32_t k, float
     const float span = scale.m - fmaxf(threshold, scale.m - 32.0f * t);
     Kept kept;
     float x = 0.0f;  // of the token that this thread would draw
-    auto keep = [&](uint64_t key) {
+    auto keep = [&](uint64_t key) {  // whether it is
         const uint32_t i = key_index(key);
         const float w = scale.w(key_value(key));
-        if (w < q) return;
+        if (w < q) return false;
         kept.sum += w;
-        if (w < kLightest) return;
+        if (w < kLightest) return true;
         kept.draw.take(w, u[i], i);
         if (kept.draw.index == i) x = key_value(key);
+        return true;
     };
     uint64_t before = 0u, target = ~uint64_t(0), sum = 0u, all;
     bool cut = false;  // top-p's target is known
@@ -963,8 +973,12 @@ __device__ __noinline__ bool finish_list(Smem &sm, uint32_t n, uint32_t k, float
                                    [&](uint64_t key) { return scale.fixed(key_value(key)); });
         const uint32_t few = pick_few(sm, n, [&](uint64_t key) { return sub.of(key) == sub.at; });
         if (sub.at < uint32_t(kSubBins) && few <= kFew) {
+            // added up in units, since the list's order is not the same every time
+            uint64_t listed = 0u;
             for (uint32_t j = threadIdx.x; j < n; j += kThreads)
-                if (sub.of(list[j]) < sub.at) keep(list[j]);
+                if (sub.of(list[j]) < sub.at && keep(list[j])) listed += scale.fixed(key_value(list[j]));
+            block_scan(listed, sm, all);
+            kept.sum = threadIdx.x == 0 ? from_fixed(all) : 0.0f;
             list = sm.few;
             n = few;
             cut = true;
