@@ -165,10 +165,12 @@ def read_peaks() -> tuple[float, str]:
         return FALLBACK_HBM_GBS, "fallback"
 
 
-# Sources that build the kernels profiles/dram_traffic.json records (the
-# persistent scan, select and partition kernels and their launchers); the
-# digit sort and the workspace-free entry point build none of them.
-TRAFFIC_SOURCES_EXCLUDED = {"radix.cu", "noalloc.cu"}
+# The sources of the kernels that profiles/dram_traffic.json records (the
+# persistent scan, select and partition kernels and their launchers) are all
+# but these: the digit sort, the workspace-free entry point and the row
+# operators build none of them.
+TRAFFIC_SOURCES_EXCLUDED = {"radix.cu", "noalloc.cu", "api_rows.cu", "embedding.cu", "experts.cu", "sample.cu",
+                            "gc_binsort.cuh", "gc_rows.cuh", "gc_rows_internal.h"}
 
 
 def kernel_source_hash() -> str:

@@ -4,7 +4,7 @@
 #include <initializer_list>
 
 #include "../../include/gc.h"
-#include "gc_internal.h"
+#include "gc_rows_internal.h"
 
 namespace {
 

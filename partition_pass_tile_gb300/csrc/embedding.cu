@@ -12,9 +12,9 @@
 #include <algorithm>
 
 #include "gc_binsort.cuh"
-#include "gc_internal.h"
 #include "gc_pipe.cuh"
 #include "gc_rows.cuh"
+#include "gc_rows_internal.h"
 
 namespace {
 

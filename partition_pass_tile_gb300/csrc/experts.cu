@@ -9,8 +9,8 @@
 // works token by token, so that a token's row is read once and the k rows of
 // its experts are the only ones touched at random, whole rows at a time.
 #include "gc_binsort.cuh"
-#include "gc_internal.h"
 #include "gc_rows.cuh"
+#include "gc_rows_internal.h"
 
 namespace {
 

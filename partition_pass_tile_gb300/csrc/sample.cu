@@ -34,8 +34,8 @@
 
 #include <cooperative_groups.h>
 
-#include "gc_internal.h"
 #include "gc_rows.cuh"
+#include "gc_rows_internal.h"
 
 namespace {
 
