@@ -467,7 +467,8 @@ gc_status gc_partition_at(const void *d_in, void *d_out, size_t out_capacity,
  *     captured in a CUDA graph.  A workspace (256-byte aligned, contents
  *     immaterial, no initialisation needed) is scratch of that one call.
  *     gc_query_device_status on gc_embedding_grad's reports a staged copy
- *     that did not arrive in time (GC_ERR_TIMEOUT).
+ *     that did not arrive in time (GC_ERR_TIMEOUT); the rows of the result
+ *     that it should have added to are then NaN.
  *   - Inputs must not overlap outputs, nor outputs one another, except where
  *     stated (GC_ERR_INVALID_VALUE).
  */

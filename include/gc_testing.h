@@ -62,6 +62,21 @@ gc_status gc_testing_select_if_noalloc_stalled_barrier(const void *d_in, void *d
                                                        cudaStream_t stream);
 
 /*
+ * gc_embedding_grad whose bulk copies never seem to arrive: each block of
+ * sorted positions waits for 16 bytes more than are copied, records
+ * GC_ERR_TIMEOUT after timeout_ns nanoseconds of device time, gives up after
+ * twice that, and its sums are NaN.  Only calls whose rows are copied in bulk
+ * wait (d_g, its stride and its width multiples of 16 bytes, 32 pieces or
+ * more to a row); others are as usual.  gc_query_device_status then returns
+ * GC_ERR_TIMEOUT, and the workspace is fit for the next call.
+ */
+gc_status gc_testing_embedding_grad_stalled(const void *d_g, size_t g_stride, gc_row_dtype g_dtype,
+                                            const void *d_ids, gc_id_type id_type, size_t n, size_t vocab,
+                                            size_t width, float scale, void *d_dtable, size_t dtable_stride,
+                                            gc_row_dtype out_dtype, int accumulate, void *d_ws,
+                                            size_t ws_bytes, uint64_t timeout_ns, cudaStream_t stream);
+
+/*
  * Process-wide switch: while on is non-zero, every scan, select-if and
  * partition (the one-bit split included) runs its one-tile-per-CTA kernels
  * (dynamic tile ids, a warp look-back, a memset of the tile counter and

@@ -4,6 +4,7 @@
 #include <initializer_list>
 
 #include "../../include/gc.h"
+#include "../../include/gc_testing.h"
 #include "gc_rows_internal.h"
 
 namespace {
@@ -57,6 +58,31 @@ bool valid_rows(size_t rows, size_t stride, size_t width)
 bool valid_routing(size_t tokens, size_t topk)
 {
     return topk >= 1 && topk <= GC_MAX_TOPK && tokens <= GC_MAX_ELEMENTS && tokens * topk <= GC_MAX_ELEMENTS;
+}
+
+// gc_embedding_grad, with its wait.
+gc_status embedding_grad(const void *d_g, size_t g_stride, gc_row_dtype g_dtype, const void *d_ids, gc_id_type id_type,
+                         size_t n, size_t vocab, size_t width, float scale, void *d_dtable, size_t dtable_stride,
+                         gc_row_dtype out_dtype, int accumulate, void *d_ws, size_t ws_bytes, cudaStream_t stream,
+                         const StagedWait &wait = {})
+{
+    if (!valid_row_dtype(g_dtype) || !valid_id_type(id_type) || !valid_rows(n, g_stride, width) ||
+        !valid_rows(vocab, dtable_stride, width) || vocab >= GC_MAX_ELEMENTS)
+        return GC_ERR_INVALID_VALUE;
+    if (!valid_row_dtype(out_dtype)) return GC_ERR_INVALID_VALUE;
+    if (out_dtype != g_dtype && out_dtype != GC_ROW_F32) return GC_ERR_UNSUPPORTED;
+    if (d_ws == nullptr || (n > 0 && (d_ids == nullptr || d_g == nullptr)) || (vocab > 0 && d_dtable == nullptr))
+        return GC_ERR_INVALID_VALUE;
+    if ((reinterpret_cast<uintptr_t>(d_ws) & 255u) != 0) return GC_ERR_MISALIGNED;
+    if (ws_bytes < embedding_grad_workspace_bytes(n, vocab, width)) return GC_ERR_WORKSPACE_TOO_SMALL;
+    const gc_status st = check_spans({row_span(d_g, n, g_stride, width, g_dtype, false),
+                                      flat(d_ids, n, id_type == GC_ID_I64 ? 8 : 4, false),
+                                      row_span(d_dtable, vocab, dtable_stride, width, out_dtype, true),
+                                      Span{d_ws, ws_bytes, 256, true}});
+    if (st != GC_OK || vocab == 0) return st;
+    return from_cuda(launch_embedding_grad(d_g, g_stride, g_dtype, d_ids, id_type == GC_ID_I64, uint32_t(n),
+                                           uint32_t(vocab), width, scale, d_dtable, dtable_stride, out_dtype,
+                                           accumulate != 0, static_cast<uint8_t *>(d_ws), stream, wait));
 }
 
 }  // namespace
@@ -182,23 +208,21 @@ gc_status gc_embedding_grad(const void *d_g, size_t g_stride, gc_row_dtype g_dty
                             size_t dtable_stride, gc_row_dtype out_dtype, int accumulate, void *d_ws,
                             size_t ws_bytes, cudaStream_t stream)
 {
-    if (!valid_row_dtype(g_dtype) || !valid_id_type(id_type) || !valid_rows(n, g_stride, width) ||
-        !valid_rows(vocab, dtable_stride, width) || vocab >= GC_MAX_ELEMENTS)
-        return GC_ERR_INVALID_VALUE;
-    if (!valid_row_dtype(out_dtype)) return GC_ERR_INVALID_VALUE;
-    if (out_dtype != g_dtype && out_dtype != GC_ROW_F32) return GC_ERR_UNSUPPORTED;
-    if (d_ws == nullptr || (n > 0 && (d_ids == nullptr || d_g == nullptr)) || (vocab > 0 && d_dtable == nullptr))
-        return GC_ERR_INVALID_VALUE;
-    if ((reinterpret_cast<uintptr_t>(d_ws) & 255u) != 0) return GC_ERR_MISALIGNED;
-    if (ws_bytes < embedding_grad_workspace_bytes(n, vocab, width)) return GC_ERR_WORKSPACE_TOO_SMALL;
-    const gc_status st = check_spans({row_span(d_g, n, g_stride, width, g_dtype, false),
-                                      flat(d_ids, n, id_type == GC_ID_I64 ? 8 : 4, false),
-                                      row_span(d_dtable, vocab, dtable_stride, width, out_dtype, true),
-                                      Span{d_ws, ws_bytes, 256, true}});
-    if (st != GC_OK || vocab == 0) return st;
-    return from_cuda(launch_embedding_grad(d_g, g_stride, g_dtype, d_ids, id_type == GC_ID_I64, uint32_t(n),
-                                           uint32_t(vocab), width, scale, d_dtable, dtable_stride, out_dtype,
-                                           accumulate != 0, static_cast<uint8_t *>(d_ws), stream));
+    return embedding_grad(d_g, g_stride, g_dtype, d_ids, id_type, n, vocab, width, scale, d_dtable, dtable_stride,
+                          out_dtype, accumulate, d_ws, ws_bytes, stream);
+}
+
+gc_status gc_testing_embedding_grad_stalled(const void *d_g, size_t g_stride, gc_row_dtype g_dtype, const void *d_ids,
+                                            gc_id_type id_type, size_t n, size_t vocab, size_t width, float scale,
+                                            void *d_dtable, size_t dtable_stride, gc_row_dtype out_dtype,
+                                            int accumulate, void *d_ws, size_t ws_bytes, uint64_t timeout_ns,
+                                            cudaStream_t stream)
+{
+    StagedWait wait;
+    wait.timeout_ns = timeout_ns;
+    wait.missing = 16;
+    return embedding_grad(d_g, g_stride, g_dtype, d_ids, id_type, n, vocab, width, scale, d_dtable, dtable_stride,
+                          out_dtype, accumulate, d_ws, ws_bytes, stream, wait);
 }
 
 gc_status gc_sample(const void *d_logits, size_t logits_stride, size_t rows, size_t vocab, gc_row_dtype dtype,

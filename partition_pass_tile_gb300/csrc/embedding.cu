@@ -11,6 +11,8 @@
 // sums.  Every sum's order depends on the ids alone.
 #include <algorithm>
 
+#include <math_constants.h>
+
 #include "gc_binsort.cuh"
 #include "gc_pipe.cuh"
 #include "gc_rows.cuh"
@@ -248,18 +250,37 @@ token_sums_kernel(const uint2 *__restrict__ sorted, uint32_t n, const T *__restr
     }
 }
 
+// Until a block's copies have arrived.  Past timeout_ns the wait is recorded
+// as GC_ERR_TIMEOUT, and past twice that it is given up: false.
+__device__ __forceinline__ bool staged_wait(uint64_t *bar, uint8_t *ws, uint64_t timeout_ns)
+{
+    if (mbar_try_wait(bar, 0u)) return true;
+    const uint64_t t0 = global_timer_ns();
+    for (bool late = false; !mbar_try_wait(bar, 0u);) {
+        const uint64_t waited = global_timer_ns() - t0;
+        if (late && waited > 2 * timeout_ns) return false;
+        if (!late && waited > timeout_ns) {
+            record_error(ws, kTimeoutCode, 0xffffffffu);
+            late = true;
+        }
+    }
+    return true;
+}
+
 // The same where rows can be copied in bulk (16-byte aligned): the block's
 // rows are copied into shared memory by the TMA unit, all at once, so that
 // the whole block is in flight without registers; and the rows to be added to
 // are fetched to L2.  blockDim.x threads, N elements each, to a slice.  The
 // gradient of 32768 tokens of 128000 x 2048 bf16 takes 203 us by these kernels
 // and 231 by the one above (193 since the join takes eight blocks a CTA), of
-// 4096 x 512 23 and 29; 1.05 GB of it is the table, written at 6.9 TB/s.
+// 4096 x 512 23 and 29; 1.05 GB of it is the table, written at 6.9 TB/s.  Where
+// the copies do not arrive the block's sums are NaN.  `missing`: bytes waited
+// for that nobody copies (0 but in a test).
 template <class T, class O, int N, bool ADD>
 __global__ void __launch_bounds__(kRowThreads)
 token_bulk_sums_kernel(const uint2 *__restrict__ sorted, uint32_t n, const T *__restrict__ g, size_t g_stride,
                        uint32_t width, float *__restrict__ edges, GradOut out, uint32_t parts, uint8_t *ws,
-                       uint64_t timeout_ns, uint32_t sums, ZeroRows zero)
+                       uint64_t timeout_ns, uint32_t missing, uint32_t sums, ZeroRows zero)
 {
     chain_start();
     chain_wait();
@@ -293,7 +314,7 @@ token_bulk_sums_kernel(const uint2 *__restrict__ sorted, uint32_t n, const T *__
         // Lane j copies row j; the tokens in range come first.
         const uint32_t k = key[lane + 1];
         const uint32_t rows_in = uint32_t(__popc(__ballot_sync(kFullMask, k != none)));
-        if (lane == 0) mbar_arrive_expect_tx(&s_bar[threadIdx.y], rows_in * here * uint32_t(sizeof(T)));
+        if (lane == 0) mbar_arrive_expect_tx(&s_bar[threadIdx.y], rows_in * here * uint32_t(sizeof(T)) + missing);
         __syncwarp();
         if (k != none) {
             bulk_load(slice + size_t(lane) * columns, g + size_t(at[lane]) * g_stride + c0, here * uint32_t(sizeof(T)),
@@ -304,9 +325,15 @@ token_bulk_sums_kernel(const uint2 *__restrict__ sorted, uint32_t n, const T *__
             }
         }
     }
-    mbar_wait(&s_bar[threadIdx.y], 0u, ws, timeout_ns);
+    const bool arrived = staged_wait(&s_bar[threadIdx.y], ws, timeout_ns);
     const uint32_t c = threadIdx.x * N;
     if (c >= here) return;
+    if (!arrived) {
+        Piece<T, N> nan;
+#pragma unroll
+        for (int e = 0; e < N; ++e) nan.v[e] = row_from_float<T>(CUDART_NAN_F);
+        for (uint32_t j = 0; j < kBlock; ++j) store_piece<T, N>(slice + size_t(j) * columns + c, nan);
+    }
     Piece<float, N> sum{};
     bool began = key[0] != key[1];
     constexpr int kAhead = 4;
@@ -470,8 +497,9 @@ uint32_t zero_ctas(const ZeroRows &z)
 }
 
 template <class T, class O, int N>
-cudaError_t run_grad_rows(const uint2 *sorted, uint32_t n, const void *g, size_t g_stride, size_t width,
-                          float *edges, const GradOut &out, const ZeroRows &zero, uint8_t *ws, cudaStream_t s)
+cudaError_t run_grad_rows(const uint2 *sorted, uint32_t n, const void *g, size_t g_stride, size_t width, float *edges,
+                          const GradOut &out, const ZeroRows &zero, uint8_t *ws, const gch::StagedWait &wait,
+                          cudaStream_t s)
 {
     const uint32_t blocks = uint32_t(gch::ceil_div(n, kBlock)), zeros = zero_ctas(zero);
     // Bulk copies need 16-byte aligned rows; a slice narrower than a warp's
@@ -503,7 +531,7 @@ cudaError_t run_grad_rows(const uint2 *sorted, uint32_t n, const void *g, size_t
             return cudaErrorInvalidConfiguration;
         const cudaError_t e = gch::launch_next(kernel, dim3(uint32_t(sums + zeros)), threads, smem, s, sorted, n,
                                                static_cast<const T *>(g), g_stride, uint32_t(width), edges, out,
-                                               uint32_t(parts), ws, gch::LaunchOpts{}.timeout_ns, uint32_t(sums), zero);
+                                               uint32_t(parts), ws, wait.timeout_ns, wait.missing, uint32_t(sums), zero);
         if (e != cudaSuccess) return e;
     } else {
         auto kernel = out.accumulate ? token_sums_kernel<T, O, N, true> : token_sums_kernel<T, O, N, false>;
@@ -521,10 +549,10 @@ cudaError_t run_grad_rows(const uint2 *sorted, uint32_t n, const void *g, size_t
 
 // Pieces of N elements, N a power of two that both rows allow and that fills
 // 16 bytes of the result at most.
-#define GC_GRAD_CALL(T, O, N) return run_grad_rows<T, O, N>(sorted, n_, g, g_stride, width, edges, out, zero, ws, s)
+#define GC_GRAD_CALL(T, O, N) return run_grad_rows<T, O, N>(sorted, n_, g, g_stride, width, edges, out, zero, ws, wait, s)
 template <class T, class O>
 cudaError_t grad_rows(const uint2 *sorted, uint32_t n_, const void *g, size_t g_stride, size_t width, float *edges,
-                      const GradOut &out, const ZeroRows &zero, uint8_t *ws, cudaStream_t s)
+                      const GradOut &out, const ZeroRows &zero, uint8_t *ws, const gch::StagedWait &wait, cudaStream_t s)
 {
     const int in = gch::piece_elems(uint64_t(uintptr_t(g)) | sizeof(T) * (g_stride | width), sizeof(T));
     const int to = gch::piece_elems(uint64_t(uintptr_t(out.rows)) | sizeof(O) * (out.stride | width), sizeof(O));
@@ -573,7 +601,8 @@ cudaError_t launch_embedding(const void *table, size_t table_stride, uint32_t vo
 
 cudaError_t launch_embedding_grad(const void *g, size_t g_stride, gc_row_dtype gdt, const void *ids, bool wide,
                                   uint32_t n, uint32_t vocab, size_t width, float scale, void *dtable,
-                                  size_t dtable_stride, gc_row_dtype odt, bool accumulate, uint8_t *ws, cudaStream_t s)
+                                  size_t dtable_stride, gc_row_dtype odt, bool accumulate, uint8_t *ws, cudaStream_t s,
+                                  const StagedWait &wait)
 {
     const GradLayout l = grad_layout(n, vocab, width);
     uint2 *items[2] = {reinterpret_cast<uint2 *>(ws + l.items_a), reinterpret_cast<uint2 *>(ws + l.items_b)};
@@ -607,13 +636,13 @@ cudaError_t launch_embedding_grad(const void *g, size_t g_stride, gc_row_dtype g
     if (e != cudaSuccess) return e;
     const uint2 *sorted = items[passes & 1];
     const GradOut out{dtable, dtable_stride, scale, accumulate, vocab};
-    if (gdt == GC_ROW_F32) return grad_rows<float, float>(sorted, n, g, g_stride, width, edges, out, zero, ws, s);
+    if (gdt == GC_ROW_F32) return grad_rows<float, float>(sorted, n, g, g_stride, width, edges, out, zero, ws, wait, s);
     if (gdt == GC_ROW_BF16)
         return odt == GC_ROW_F32
-                   ? grad_rows<__nv_bfloat16, float>(sorted, n, g, g_stride, width, edges, out, zero, ws, s)
-                   : grad_rows<__nv_bfloat16, __nv_bfloat16>(sorted, n, g, g_stride, width, edges, out, zero, ws, s);
-    return odt == GC_ROW_F32 ? grad_rows<__half, float>(sorted, n, g, g_stride, width, edges, out, zero, ws, s)
-                             : grad_rows<__half, __half>(sorted, n, g, g_stride, width, edges, out, zero, ws, s);
+                   ? grad_rows<__nv_bfloat16, float>(sorted, n, g, g_stride, width, edges, out, zero, ws, wait, s)
+                   : grad_rows<__nv_bfloat16, __nv_bfloat16>(sorted, n, g, g_stride, width, edges, out, zero, ws, wait, s);
+    return odt == GC_ROW_F32 ? grad_rows<__half, float>(sorted, n, g, g_stride, width, edges, out, zero, ws, wait, s)
+                             : grad_rows<__half, __half>(sorted, n, g, g_stride, width, edges, out, zero, ws, wait, s);
 }
 
 }  // namespace gch

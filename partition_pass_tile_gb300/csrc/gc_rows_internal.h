@@ -22,10 +22,17 @@ cudaError_t launch_expert_combine_grad(const void *g, size_t g_stride, const voi
 cudaError_t launch_embedding(const void *table, size_t table_stride, uint32_t vocab, size_t width, gc_row_dtype dt,
                              const void *ids, bool wide, uint32_t n, float scale, void *out, size_t out_stride,
                              cudaStream_t s);
+// The gradient's wait for its bulk copies; `missing`: bytes waited for that
+// nobody copies, which makes it run out.
+struct StagedWait {
+    uint64_t timeout_ns = LaunchOpts{}.timeout_ns;
+    uint32_t missing = 0;
+};
 size_t embedding_grad_workspace_bytes(size_t n, size_t vocab, size_t width);
 cudaError_t launch_embedding_grad(const void *g, size_t g_stride, gc_row_dtype gdt, const void *ids, bool wide,
                                   uint32_t n, uint32_t vocab, size_t width, float scale, void *out,
-                                  size_t out_stride, gc_row_dtype odt, bool accumulate, uint8_t *ws, cudaStream_t s);
+                                  size_t out_stride, gc_row_dtype odt, bool accumulate, uint8_t *ws, cudaStream_t s,
+                                  const StagedWait &wait = {});
 cudaError_t launch_sample(const void *logits, size_t logits_stride, uint32_t rows, uint32_t vocab, gc_row_dtype dt,
                           const float *uniform, size_t uniform_stride, const float *temperature,
                           const int32_t *top_k, const float *top_p, const float *min_p, int32_t *tokens,

@@ -99,6 +99,7 @@ def load(path: str | Path | None = None) -> ctypes.CDLL:
         "gc_embedding": ([V, Z, Z, Z, I, V, I, Z, F, V, Z, V], S),
         "gc_embedding_grad_workspace_bytes": ([Z, Z, Z], Z),
         "gc_embedding_grad": ([V, Z, I, V, I, Z, Z, Z, F, V, Z, I, I, V, Z, V], S),
+        "gc_testing_embedding_grad_stalled": ([V, Z, I, V, I, Z, Z, Z, F, V, Z, I, I, V, Z, U64, V], S),
         "gc_sample": ([V, Z, Z, Z, I, V, Z, V, V, V, V, V, V, V], S),
     }
     for name, (args, res) in sig.items():
@@ -729,7 +730,8 @@ def embedding_grad(g: torch.Tensor, ids: torch.Tensor, vocab: int, scale: float 
 
     g: the gradient of embedding's output, ids.shape + (width,).  out_dtype:
     g's type (the default) or float32.  accumulate adds to `out`, leaving the
-    rows of absent tokens alone.
+    rows of absent tokens alone.  Rows whose staged copies did not arrive in
+    time are NaN; query_device_status of the caller's `ws` says so too.
     """
     n, width = ids.numel(), g.size(-1)
     if accumulate and out is None:
@@ -746,6 +748,16 @@ def embedding_grad(g: torch.Tensor, ids: torch.Tensor, vocab: int, scale: float 
                                  op, os, row_dtype_code(dt), int(accumulate), _ptr(ws), ws.numel(),
                                  _handle(stream, g.device)), "gc_embedding_grad")
     return out
+
+
+def testing_embedding_grad_stalled(g: torch.Tensor, ids: torch.Tensor, out: torch.Tensor, ws: torch.Tensor,
+                                   timeout_ns: int, accumulate: bool = False, stream=None) -> int:
+    """Test hook (include/gc_testing.h): returns the launch status."""
+    gp, gs = _rows(g)
+    op, os = _rows(out)
+    return int(load().gc_testing_embedding_grad_stalled(
+        gp, gs, row_dtype_code(g.dtype), _ptr(ids), _ids(ids), ids.numel(), out.size(0), out.size(1), 1.0, op, os,
+        row_dtype_code(out.dtype), int(accumulate), _ptr(ws), ws.numel(), timeout_ns, _handle(stream, g.device)))
 
 
 def _per_row(v, dtype: torch.dtype, rows: int, device, stream) -> torch.Tensor | None:
