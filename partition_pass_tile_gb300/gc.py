@@ -130,11 +130,22 @@ def pred_code(pred) -> int:
     return PRED_NAMES[pred] if isinstance(pred, str) else int(pred)
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _on_device(t: torch.Tensor) -> None:
+    """libgc launches on the current device, so every tensor has to be there."""
+    at = t.get_device()
+    if at < 0:
+        raise ValueError("libgc takes CUDA tensors (device pointers)")
+    if at != _current_device():
+        raise ValueError(f"libgc runs on the current device, cuda:{_current_device()}, and a tensor is on cuda:{at}")
+
+
 def _ptr(t: torch.Tensor | None) -> int | None:
     if t is None:
         return None
-    if not t.is_cuda:
-        raise ValueError("libgc takes CUDA tensors (device pointers)")
+    _on_device(t)
     if not t.is_contiguous():
         raise ValueError("libgc takes contiguous tensors")
     return t.data_ptr()
@@ -521,8 +532,7 @@ def row_dtype_code(dtype: torch.dtype) -> int:
 
 def _rows(t: torch.Tensor) -> tuple[int, int]:
     """(pointer, row stride) of a 2-D tensor whose rows are contiguous."""
-    if not t.is_cuda:
-        raise ValueError("libgc takes CUDA tensors (device pointers)")
+    _on_device(t)
     stride, shape = t.stride(), t.shape
     if len(shape) != 2 or (stride[1] != 1 and shape[1] > 1):
         raise ValueError("libgc takes 2-D row arrays whose rows are contiguous")
