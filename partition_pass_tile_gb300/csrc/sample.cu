@@ -152,6 +152,7 @@ struct Smem {
     KeySum slot[2][kMaxTeam];
     uint64_t scan[kWarps];
     uint64_t cut, above;
+    uint64_t units;              // kept weights of a list's tokens, in units of 2^-40 of the largest
     uint32_t count;              // candidates appended to this list (may pass kList)
     uint32_t bin, state;
     bool found;
@@ -465,6 +466,16 @@ __device__ __noinline__ uint64_t block_scan(uint64_t v, Smem &sm, uint64_t &tota
     total = __shfl_sync(kFull, c, kWarps - 1);
     const uint64_t before = __shfl_sync(kFull, c, warp > 0 ? warp - 1 : 0);
     return (warp > 0 ? before : 0u) + incl - v;
+}
+
+// Adds v to *sum (in shared memory), by all lanes of the warp together; a
+// barrier lies between the last and who reads it.
+__device__ __forceinline__ void add_units(uint64_t v, uint64_t *sum)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+    if ((threadIdx.x & 31) == 0 && v != 0u)
+        atomicAdd(reinterpret_cast<unsigned long long *>(sum), static_cast<unsigned long long>(v));
 }
 
 // Sorts up to 64 keys descending, two to a lane of one warp.
@@ -798,7 +809,10 @@ __device__ __noinline__ bool find_cut(Team &team, const Row<T> &row, const Scale
             __syncthreads();
             rough = sm.above;
         }
-        if (threadIdx.x == 0) sm.count = 0u;
+        if (threadIdx.x == 0) {
+            sm.count = 0u;
+            sm.units = 0u;
+        }
         team.sync();
         // Tokens of the cut's bin and its neighbours, as an interval of
         // values, to the list; those above it added up.
@@ -841,12 +855,11 @@ __device__ __noinline__ bool find_cut(Team &team, const Row<T> &row, const Scale
             above = MASS ? uint64_t(double(mass) * double(kFixed) + 0.5) : uint64_t(mass);
             error = int64_t(above) - int64_t(rough);
             auto amount = [&](uint64_t key) { return MASS ? scale.fixed(key_value(key)) : uint64_t(1); };
-            uint64_t listed = 0u;  // kept weights of the list
-            auto keep = [&](uint64_t key) {
+            auto keep = [&](uint64_t key) {  // its weight if it is kept
                 const float w = scale.w(key_value(key));
-                if (!kept || w < q) return;
-                listed += scale.fixed(key_value(key));
+                if (!kept || w < q) return 0.0f;
                 if (w >= kLightest) mine.draw.take(w, row.u[key_index(key)], key_index(key));
+                return w;
             };
             SubBin sub{0.0f, 0.0f, uint32_t(kSubBins), 0u};
             if (n <= kList && above < target) {
@@ -857,9 +870,19 @@ __device__ __noinline__ bool find_cut(Team &team, const Row<T> &row, const Scale
             if (sub.at < uint32_t(kSubBins)) {
                 uint32_t few = pick_few(sm, n, [&](uint64_t key) { return sub.of(key) == sub.at; });
                 const bool fits = few <= kFew;
-                if (fits)
+                if (fits) {
+                    // The list's order is not the same every time: added up in
+                    // units, as the histogram has done if none is lighter than q.
+                    const bool known = MASS && !(q > 0.0f);
+                    uint64_t units = 0u;
                     for (uint32_t j = threadIdx.x; j < n; j += kThreads)
-                        if (sub.of(sm.list[j]) < sub.at) keep(sm.list[j]);
+                        if (sub.of(sm.list[j]) < sub.at) {
+                            const float w = keep(sm.list[j]);
+                            if (!known) units += __float2ull_rn(w * kFixed);
+                        }
+                    if (!known) add_units(units, &sm.units);
+                    else if (threadIdx.x == 0) sm.units = sub.before - above;
+                }
                 uint64_t *list = fits ? sm.few : sm.list;
                 few = fits ? few : n;
                 sort_list(list, few);
@@ -869,17 +892,12 @@ __device__ __noinline__ bool find_cut(Team &team, const Row<T> &row, const Scale
                 for (uint32_t j = first; j < last; ++j) sum += amount(list[j]);
                 uint64_t before = (fits ? sub.before : above) + block_scan(sum, sm, all);
                 for (uint32_t j = first; j < last && before < target; ++j) {
-                    keep(list[j]);
+                    mine.sum += keep(list[j]);
                     before += amount(list[j]);
                     if (before >= target) {
                         sm.cut = list[j];
                         sm.state = kFound;
                     }
-                }
-                if (kept) {
-                    __syncthreads();
-                    block_scan(listed, sm, all);
-                    if (threadIdx.x == 0) mine.sum += from_fixed(all);
                 }
             }
         }
@@ -887,7 +905,10 @@ __device__ __noinline__ bool find_cut(Team &team, const Row<T> &row, const Scale
         state = team.lead->state;
         team.sync();  // everyone has read it, and the list may be filled anew
     }
-    if (kept) *kept = mine;
+    if (kept) {
+        *kept = mine;
+        if (team.rank == 0 && threadIdx.x == 0) kept->sum += from_fixed(sm.units);
+    }
     if (state != kFound) {
         if (team.rank == 0) {
             // Among the interval's tokens where those were only too many (equal
@@ -936,6 +957,7 @@ __device__ __noinline__ bool finish_list(Smem &sm, uint32_t n, uint32_t k, float
 {
     uint64_t *list = sm.list;
     Team alone(sm, 1);
+    if (threadIdx.x == 0) sm.units = 0u;
     uint64_t most = 0u;
     for (uint32_t j = threadIdx.x; j < n; j += kThreads) most = list[j] > most ? list[j] : most;
     const Scale scale(key_value(alone.largest(most)), t);
@@ -944,15 +966,14 @@ __device__ __noinline__ bool finish_list(Smem &sm, uint32_t n, uint32_t k, float
     const float span = scale.m - fmaxf(threshold, scale.m - 32.0f * t);
     Kept kept;
     float x = 0.0f;  // of the token that this thread would draw
-    auto keep = [&](uint64_t key) {  // whether it is
+    auto keep = [&](uint64_t key) {  // its weight if it is kept
         const uint32_t i = key_index(key);
         const float w = scale.w(key_value(key));
-        if (w < q) return false;
-        kept.sum += w;
-        if (w < kLightest) return true;
+        if (w < q) return 0.0f;
+        if (w < kLightest) return w;
         kept.draw.take(w, u[i], i);
         if (kept.draw.index == i) x = key_value(key);
-        return true;
+        return w;
     };
     uint64_t before = 0u, target = ~uint64_t(0), sum = 0u, all;
     bool cut = false;  // top-p's target is known
@@ -973,12 +994,15 @@ __device__ __noinline__ bool finish_list(Smem &sm, uint32_t n, uint32_t k, float
                                    [&](uint64_t key) { return scale.fixed(key_value(key)); });
         const uint32_t few = pick_few(sm, n, [&](uint64_t key) { return sub.of(key) == sub.at; });
         if (sub.at < uint32_t(kSubBins) && few <= kFew) {
-            // added up in units, since the list's order is not the same every time
-            uint64_t listed = 0u;
+            // added up in units, as in find_cut
+            uint64_t units = 0u;
             for (uint32_t j = threadIdx.x; j < n; j += kThreads)
-                if (sub.of(list[j]) < sub.at && keep(list[j])) listed += scale.fixed(key_value(list[j]));
-            block_scan(listed, sm, all);
-            kept.sum = threadIdx.x == 0 ? from_fixed(all) : 0.0f;
+                if (sub.of(list[j]) < sub.at) {
+                    const float w = keep(list[j]);
+                    if (q > 0.0f) units += __float2ull_rn(w * kFixed);
+                }
+            if (q > 0.0f) add_units(units, &sm.units);
+            else if (threadIdx.x == 0) sm.units = sub.before;
             list = sm.few;
             n = few;
             cut = true;
@@ -1000,9 +1024,10 @@ __device__ __noinline__ bool finish_list(Smem &sm, uint32_t n, uint32_t k, float
         if (!cut && all < target) return false;
     }
     for (uint32_t j = first; j < last && before < target; ++j) {
-        keep(list[j]);
+        kept.sum += keep(list[j]);
         if (p < 1.0f) before += scale.fixed(key_value(list[j]));
     }
+    if (threadIdx.x == 0) kept.sum += from_fixed(sm.units);  // past sort_list's barriers
     const KeySum end = alone.reduce(KeySum{kept.draw.key(), kept.sum});
     if (kept.draw.key() == end.key) {
         *token = int32_t(key_index(end.key));
