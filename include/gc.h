@@ -469,8 +469,9 @@ gc_status gc_partition_at(const void *d_in, void *d_out, size_t out_capacity,
  *     gc_query_device_status on gc_embedding_grad's reports a staged copy
  *     that did not arrive in time (GC_ERR_TIMEOUT); the rows of the result
  *     that it should have added to are then NaN.
- *   - Inputs must not overlap outputs, nor outputs one another, except where
- *     stated (GC_ERR_INVALID_VALUE).
+ *   - Inputs must not overlap outputs, nor outputs one another
+ *     (GC_ERR_INVALID_VALUE).  An array reaches from its first element to its
+ *     last: column slices of one array overlap in this sense.
  */
 typedef enum { GC_ROW_F32 = 0, GC_ROW_BF16 = 1, GC_ROW_F16 = 2 } gc_row_dtype;
 typedef enum { GC_ID_I32 = 0, GC_ID_I64 = 1 } gc_id_type;
@@ -594,7 +595,17 @@ gc_status gc_embedding_grad(const void *d_g, size_t g_stride, gc_row_dtype g_dty
  * T <= 0 or NaN: the first of the order, logprob 0; u is not read.  Every
  * token forbidden: token -1, logprob -inf.
  * z - log(-log u) of a token 20 below the maximum cannot be the largest, so
- * such tokens' u are not read; tokens whose w underflows to 0 are never kept.
+ * such tokens' u do not influence the result; but the whole row's u may be
+ * read unless T <= 0 or NaN.  Tokens whose w underflows to 0 are never kept.
+ *
+ * Roundings: w is exp2 of (x - m) * (log2(e) / T) in float32, off by at most
+ * (1 + 5/4 |z|) * 2^-22 of itself.  Without a filter any of the row's logits
+ * down to 69 T below m may stand for it, and |z| counts from there.  Sums of w
+ * are float32, one thread's terms in a row, off by at most (vocab / 512 + 16) *
+ * 2^-24, or exact sums of w rounded to 2^-40.  top-p compares two such sums;
+ * where a sum of predecessors comes that near to top_p times all, its last
+ * token may be kept or not.  min-p compares the rounded w; the order, its ties
+ * and top-k are exact.
  *
  * d_logits: rows x vocab of dtype, vocab <= GC_MAX_SAMPLE_VOCAB.  d_uniform:
  * float32, same shape, its own stride; NULL draws every row with T = 0.

@@ -21,12 +21,13 @@
 //     the way.  Where the collected do not fit (thousands of equal values) or do
 //     not hold the cut, the leader finds it by radix selection (select_cut): 64
 //     rows of 128000 equal bf16 logits take 0.6 ms, 100 us is usual.
-// Measured, kernel alone, after a flush that leaves L2 dirty (a plain maximum
-// of every row of 512 x 128000 float32 takes 64 us so): that batch with top-k 50
-// 80 us against 295 by histograms; unfiltered 127 us in one pass against 199 in
-// two; top-p 0.95 at T = 1.2 453 us, three passes whose second and third read
-// 262 MB again, more than L2, at T = 0.5 143 us, one pass.  One row of 128000
-// bf16: 16 us unfiltered or top-k, 53 us top-p.
+// Measured, kernel alone, 512 x 128000 float32 (262 MB, 39 us at the copy rate)
+// with nothing of it in L2: greedy 57 us; top-k 50 74 us against 295 by
+// histograms; unfiltered 119 us (524 MB) in one pass against 199 in two; min-p
+// 133 us, two passes; top-p 0.95 at T = 1.2 453 us, three reads of the logits,
+// more than L2 holds, and most of the random numbers (1.10 GB); at T = 0.5 143
+// us, one pass.  After a flush that leaves L2 dirty 4 to 10 us more.  One row of
+// 128000 bf16: 13 us unfiltered or top-k, 44 us top-p.
 // 512 threads at two CTAs per SM and rings of three pieces: more rows or pieces
 // under way are slower (256 threads at four CTAs 109 us for top-k 50, rings of
 // six 80, clusters of two 102), because HBM serves fewer, longer streams better.
@@ -1202,9 +1203,11 @@ sample_kernel(const T *__restrict__ logits, size_t logits_stride, uint32_t vocab
     // thread's maximum so far: the cut of a row with a few likely tokens is in
     // the list, and the row is done.  512 x 128000 float32, normal logits with 40
     // raised by up to 12, against the passes below alone: T = 0.5, p = 0.95 143 us
-    // for 270; T = 0.7, p = 0.9 244 for 299; where no list holds the cut, T = 1.2,
-    // p = 0.95, 455 for 395.  Not for rows of a few samples (200 x 20000: 33 us for
-    // 49, but 70 for 55), nor for few rows, whose time is that of the barriers.
+    // for 266; T = 0.7, p = 0.9 244 for 295; where no list holds the cut, T = 1,
+    // p = 0.95 444 for 385 and T = 1.2 453 for 391 (304 x 128000 bf16: 68 for 129,
+    // 147 for 154, 203 for 174 and 203 for 172).  Which it will be shows in the row
+    // alone.  Not for rows of a few samples (200 x 20000: 33 us for 49, but 70 for
+    // 55), nor for few rows, whose time is that of the barriers.
     const uint32_t wish = min(uint32_t(kThreads / 2), uint32_t(uint64_t(kBatch) * (kList / 2) / vocab));
     const bool likely =
         !greedy && k == vocab && p < 1.0f && team.size == 1 && vocab >= 3u * kBatch && wish >= 32u;

@@ -511,6 +511,9 @@ def partition_at(x: torch.Tensor, pred, out: torch.Tensor, offsets: torch.Tensor
 
 
 # ---------------------------------------------------------------- rows
+#
+# Autograd does not see these calls: their results have no grad_fn, whatever
+# requires a gradient among the arguments.  Each gradient is a call of its own.
 
 ROW_DTYPES = {torch.float32: ROW_F32, torch.bfloat16: ROW_BF16, torch.float16: ROW_F16}
 
@@ -622,7 +625,8 @@ def expert_dispatch(x: torch.Tensor | None, ids: torch.Tensor, experts: int, ali
     x: [tokens, width] rows; ids: [tokens, topk] int32 or int64, ids outside
     [0, experts) are dropped.  rows: [expert_rows(...), width], each expert's
     block starting at a multiple of `align`; rows without a pair are zeros.
-    x None makes the plan alone (rows None).
+    x None makes the plan alone (rows None).  The gradient with respect to x is
+    expert_dispatch_grad; autograd does not see the call.
     """
     shape = ids.shape
     if len(shape) != 2:
@@ -663,7 +667,10 @@ def expert_dispatch(x: torch.Tensor | None, ids: torch.Tensor, experts: int, ali
 
 def expert_combine(y: torch.Tensor, slots: torch.Tensor, weights: torch.Tensor | None = None,
                    out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
-    """out[t] = sum_j weights[t, j] * y[slots[t, j]] (weights None: all 1; slot -1: nothing)."""
+    """out[t] = sum_j weights[t, j] * y[slots[t, j]] (weights None: all 1; slot -1: nothing).
+
+    The gradients are expert_combine_grad's; autograd does not see the call.
+    """
     if slots.dim() != 2:
         raise ValueError("slots is [tokens, topk]")
     tokens, topk = slots.shape
@@ -718,7 +725,10 @@ def expert_combine_grad(g: torch.Tensor, y: torch.Tensor | None, slots: torch.Te
 
 def embedding(table: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, out: torch.Tensor | None = None,
               stream=None) -> torch.Tensor:
-    """scale * table[ids], zeros for ids outside the table -> ids.shape + (width,)."""
+    """scale * table[ids], zeros for ids outside the table -> ids.shape + (width,).
+
+    The gradient is embedding_grad; autograd does not see the call.
+    """
     n = ids.numel()
     tp, ts = _rows(table)
     vocab, width = table.shape
