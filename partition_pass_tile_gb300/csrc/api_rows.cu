@@ -79,7 +79,7 @@ gc_status embedding_grad(const void *d_g, size_t g_stride, gc_row_dtype g_dtype,
                                       flat(d_ids, n, id_type == GC_ID_I64 ? 8 : 4, false),
                                       row_span(d_dtable, vocab, dtable_stride, width, out_dtype, true),
                                       Span{d_ws, ws_bytes, 256, true}});
-    if (st != GC_OK || vocab == 0) return st;
+    if (st != GC_OK) return st;
     return from_cuda(launch_embedding_grad(d_g, g_stride, g_dtype, d_ids, id_type == GC_ID_I64, uint32_t(n),
                                            uint32_t(vocab), width, scale, d_dtable, dtable_stride, out_dtype,
                                            accumulate != 0, static_cast<uint8_t *>(d_ws), stream, wait));

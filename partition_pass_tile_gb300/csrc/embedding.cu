@@ -613,6 +613,7 @@ cudaError_t launch_embedding_grad(const void *g, size_t g_stride, gc_row_dtype g
     const size_t elem = odt == GC_ROW_F32 ? 4 : 2;
     ZeroRows zero{static_cast<uint8_t *>(dtable), dtable_stride * elem, width * elem, seen, 0u, accumulate ? 0u : vocab};
     cudaError_t e = cudaSuccess;
+    if (vocab == 0) return cudaMemsetAsync(ws, 0, kHeaderBytes, s);  // no row, and no error
     if (n > 0 && n <= kSortAlone) {
         // Everything is zeroed here, before any row is written.
         if (persistent_grid(reinterpret_cast<const void *>(token_sort_kernel), gcd::kBinThreads, sizeof(TokenSortSmem),

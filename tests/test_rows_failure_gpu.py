@@ -53,3 +53,16 @@ def test_rows_that_are_not_copied_in_bulk_do_not_wait():
     assert gc.query_device_status(ws) == 0
     want, size, count = ref.embedding_grad(g64, host, 50, 1.0)
     assert off(out, want, size, count[:, None], "f32") <= 1
+
+
+@pytest.mark.parametrize("n,vocab", [(5, 0), (0, 0), (0, 7), (5, 7), (5000, 7)])
+def test_the_status_of_a_call_on_an_uninitialised_workspace(n, vocab):
+    # a workspace needs no initialisation, whatever the call has to do
+    ws = torch.full((gc.embedding_grad_workspace_bytes(n, vocab, 64),), 255, dtype=torch.uint8, device="cuda")
+    ids = torch.zeros(n, dtype=torch.int64, device="cuda")
+    for accumulate in (False, True):
+        ws.fill_(255)
+        out = torch.zeros(vocab, 64, device="cuda")
+        gc.embedding_grad(torch.ones(n, 64, device="cuda"), ids, vocab, out=out, accumulate=accumulate, ws=ws)
+        assert gc.query_device_status(ws) == 0
+        assert not out[1:].any() and (vocab == 0 or bool((out[0] == n).all()))
