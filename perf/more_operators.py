@@ -101,6 +101,7 @@ def draw(rng):
         heads, group = _spread(rng, 1, 16), rng.choice([1, 2, 4, 5, 8])
         length = _spread(rng, 16, 65536)
         queries = rng.choice([1, 1, _spread(rng, 2, 256)])
+        heads = min(heads, max(1, 250_000_000 // (group * queries * length * SIZE[dtype])))
         most = max(1, 250_000_000 // (heads * group * queries * length * SIZE[dtype]))
         return {"op": op, "batch": _spread(rng, 1, min(64, most)), "heads": heads, "group": group, "queries": queries,
                 "length": length, "ragged": rng.random() < 0.5, "decay": rng.choice([1.0, 1.0, 0.9]), "dtype": dtype}
@@ -108,8 +109,10 @@ def draw(rng):
     width = rng.choice([64, 80, 128, 128, 192, 256, _spread(rng, 32, 256)])
     value_width = rng.choice([width, width, 64, 33])
     budget = max(8, int(length * rng.choice([0.06, 0.25, 0.5, 0.9])))
+    # a cache that is rewritten whole costs no more than the largest case's bytes
     row = (width + value_width) * SIZE[dtype]
-    return {"op": "evict", "batch": _spread(rng, 1, min(32, max(1, 500_000_000 // (heads * length * row)))),
+    heads = min(heads, max(1, 400_000_000 // (budget * 2 * row + length * 4)))
+    return {"op": "evict", "batch": _spread(rng, 1, min(32, max(1, 400_000_000 // (heads * (budget * 2 * row + length * 4))))),
             "heads": heads, "length": length, "width": width, "value_width": value_width, "budget": budget,
             "sinks": rng.choice([0, 4]), "recent": rng.choice([0, 1, budget // 8, budget // 2]),
             "ragged": rng.random() < 0.4, "order": rng.choice(["head", "token"]), "dtype": dtype}
