@@ -481,6 +481,7 @@ typedef enum { GC_ID_I32 = 0, GC_ID_I64 = 1 } gc_id_type;
 #define GC_MAX_EXPERT_ALIGN 65536u
 #define GC_MAX_SAMPLE_VOCAB 4194304u
 #define GC_MAX_ROW_WIDTH 16777216u
+#define GC_MAX_DRAFTS 64u
 
 /*
  * Rows that hold any routing of tokens * topk pairs to `experts` experts,
@@ -547,6 +548,61 @@ gc_status gc_expert_combine_grad(const void *d_g, size_t g_stride, const void *d
                                  const int32_t *d_pairs, const float *d_weights, size_t tokens,
                                  size_t topk, size_t width, gc_row_dtype dtype, void *d_dy,
                                  size_t dy_stride, float *d_dweights, cudaStream_t stream);
+
+/* Workspace bytes of gc_expert_route; 0 for arguments out of range. */
+size_t gc_expert_route_workspace_bytes(size_t tokens, uint32_t experts);
+
+/*
+ * Every token's experts, with x its logits (float32 of them, +inf counts as
+ * the largest finite float32, NaN and -inf as an expert closed to the token)
+ * and p = softmax(x):
+ *
+ *   order       by x descending, equal values by index ascending
+ *   ids[t, j]   the j-th of the order, -1 where no open expert is left
+ *   weights[t, j] = p[ids[t, j]], with normalize != 0 divided by their sum
+ *               over the token's choices; 0 where ids is -1
+ *   counts[e]   pairs (t, j) with ids == e; counts[experts] = n, the tokens
+ *               with a choice
+ *   load[e]     = sum over t of p[t, e] / n, the experts' mean probability
+ *   loss        = experts * sum over e of counts[e] / (sum of counts) * load[e],
+ *               1 where load and counts are even, more where they are not
+ *
+ * A token t with mask[t] == 0 (padding) has no choice and counts for nothing;
+ * d_mask may be NULL.  n == 0: load and loss are 0.  ids and weights are what
+ * gc_expert_dispatch and gc_expert_combine take.
+ *
+ * d_logits: tokens rows of `experts` of dtype.  1 <= topk <= experts,
+ * topk <= GC_MAX_TOPK, experts <= GC_MAX_EXPERTS.  d_ids, d_weights: tokens *
+ * topk; d_counts: experts + 1; d_load: experts; d_loss: one.  d_counts, d_load
+ * and d_loss may be NULL; without d_counts nothing is added up, and the other
+ * two have to be NULL.
+ *
+ * Roundings: p by exp2 of (x - max) * log2(e), off by at most (4 + 3/2 |x -
+ * max|) * 2^-23 of itself; a token's sums are float32 trees.  load adds float32
+ * sums of the tokens of one thread, in their order, in double.
+ */
+gc_status gc_expert_route(const void *d_logits, size_t logits_stride, size_t tokens, uint32_t experts,
+                          gc_row_dtype dtype, size_t topk, int normalize, const uint8_t *d_mask,
+                          int32_t *d_ids, float *d_weights, int32_t *d_counts, float *d_load,
+                          float *d_loss, void *d_ws, size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * Gradient of gc_expert_route with respect to the logits, from that of its
+ * weights (float32, tokens * topk) and of its loss (one float32); either may
+ * be NULL and counts as 0.  With a[e] = dloss * experts / n * counts[e] / (sum
+ * of counts):
+ *   dx[t, e] = p[e] (a[e] - <p, a>) + the sum over the choices j of
+ *       normalize != 0:  [ids[t, j] == e] w_j (g_j - <w, g>)
+ *       normalize == 0:  [ids[t, j] == e] w_j g_j - p[e] w_j g_j
+ * w the weights, g their gradients.  The choices themselves and the counts are
+ * constants.  Rows of tokens without a choice (ids[t, 0] outside [0, experts))
+ * are zeros.  d_ids and d_counts are gc_expert_route's; d_counts may be NULL
+ * where d_dloss is.  d_dx: rows like the logits', of the same type.
+ */
+gc_status gc_expert_route_grad(const void *d_logits, size_t logits_stride, size_t tokens,
+                               uint32_t experts, gc_row_dtype dtype, size_t topk, int normalize,
+                               const int32_t *d_ids, const int32_t *d_counts, const float *d_dweights,
+                               const float *d_dloss, void *d_dx, size_t dx_stride, cudaStream_t stream);
 
 /*
  * Embedding lookup: out[i] = scale * table[ids[i]], zeros for an id outside
@@ -618,6 +674,118 @@ gc_status gc_sample(const void *d_logits, size_t logits_stride, size_t rows, siz
                     const float *d_temperature, const int32_t *d_top_k, const float *d_top_p,
                     const float *d_min_p, int32_t *d_tokens, float *d_logprobs,
                     cudaStream_t stream);
+
+/* Workspace bytes of gc_sample_verify; 0 for arguments out of range. */
+size_t gc_sample_verify_workspace_bytes(size_t sequences, size_t drafts, size_t vocab);
+
+/*
+ * Drafted tokens against the target's probabilities: the several-token form
+ * of an unfiltered gc_sample, whose result is distributed as if the target had
+ * drawn every token itself.  Per sequence b, with T its temperature, x the
+ * target's logits of position j (row b * (drafts + 1) + j, read as gc_sample
+ * reads them), p = softmax(x / T), q the same of the draft's logits (row b *
+ * drafts + j) and d its drafted token:
+ *
+ *   accepted   positions 0, 1, ... while d is in [0, vocab) and
+ *              accept[b, j] * q[d] < p[d]; their number is accepted[b] = a
+ *   drawn      at position a: the token with the largest r / -log v, equal
+ *              values the lowest index; v = uniform[b, .].  r = max(p - q, 0)
+ *              where position a was rejected, p where its drafted token is
+ *              outside [0, vocab) (the end of a short draft) or a == drafts
+ *   tokens[b, .]  the accepted ones, the drawn one, then -1
+ *   logprobs[b, .]  log p of each token at its position, -inf behind them
+ *
+ * T <= 0 or NaN: p is 1 for the first of the largest x and 0 elsewhere;
+ * positions are accepted while d is that token, the drawn token is that of
+ * position a, logprob 0, and neither the draft's logits nor random numbers are
+ * read.  No draft logits (d_draft_logits NULL): q is 1 for d, drafts that were
+ * not drawn.  Random numbers are clamped to [2^-25, 1 - 2^-24], NaN counts as
+ * 2^-25.  A position whose logits are all forbidden: token -1, logprob -inf.
+ * Where p - q rounds to nothing everywhere, p stands for it.
+ * Filters (top-k, top-p, min-p) are applied to the logits beforehand, by -inf
+ * in the target's and the draft's.
+ *
+ * Roundings: p and q are exp2 of (x - max) * (log2(e) / T) in float32, off by
+ * at most (4 + 5/4 |z|) * 2^-22 of themselves, |z| = (max - x) / T; sums are
+ * float32 trees over at most 2^-12 of the vocabulary per thread; the
+ * comparison is in double.  The result is that of these p and q: a position
+ * whose u q and p agree to that many bits may be decided either way.
+ *
+ * d_logits: sequences * (drafts + 1) rows of `vocab`, d_draft_logits:
+ * sequences * drafts rows of the same type; d_drafts: int32, sequences *
+ * drafts; d_accept: float32 like d_drafts; d_uniform: float32, sequences rows
+ * of vocab; both NULL draw every sequence with T = 0.  d_temperature: one per
+ * sequence or NULL (1).  d_tokens, d_logprobs (may be NULL): sequences *
+ * (drafts + 1); d_accepted: sequences.  0 <= drafts <= GC_MAX_DRAFTS, vocab <=
+ * GC_MAX_SAMPLE_VOCAB.
+ */
+gc_status gc_sample_verify(const void *d_logits, size_t logits_stride, const void *d_draft_logits,
+                           size_t draft_stride, size_t sequences, size_t drafts, size_t vocab,
+                           gc_row_dtype dtype, const int32_t *d_drafts, const float *d_accept,
+                           const float *d_uniform, size_t uniform_stride, const float *d_temperature,
+                           int32_t *d_tokens, int32_t *d_accepted, float *d_logprobs, void *d_ws,
+                           size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * Attention weights added to the scores of a cache's positions: for sequence
+ * b, head h of the cache and position l < lengths[b],
+ *   out[b, h, l] = decay * scores[b, h, l] + the sum over the heads
+ *       h * group ... h * group + group - 1 and the queries below
+ *       counted[b] of weights[b, head, query, l]
+ * and 0 for the positions from lengths[b] on, whose weights and scores are not
+ * read.  Weight (b, head, query, l) is at b * batch_stride + head *
+ * head_stride + query * query_stride + l, strides in elements (0 where a
+ * dimension has one entry).  d_scores: batch * heads rows of `length`, NULL
+ * counts as zeros; d_out: rows like them, and may be d_scores itself with the
+ * same stride.  d_lengths, d_counted: int32, one per sequence, clamped to [0,
+ * length] and [0, queries]; NULL: all.  Sums are float32, added in the order
+ * of the rows by up to eight threads and then over the threads.
+ */
+gc_status gc_cache_score(const void *d_weights, size_t batch_stride, size_t head_stride,
+                         size_t query_stride, gc_row_dtype dtype, size_t batch, size_t heads,
+                         size_t group, size_t queries, size_t length, const float *d_scores,
+                         size_t scores_stride, float decay, const int32_t *d_lengths,
+                         const int32_t *d_counted, float *d_out, size_t out_stride,
+                         cudaStream_t stream);
+
+/*
+ * The rows of a cache: row (b, h, l) of `width` elements is at b *
+ * batch_stride + h * head_stride + l * row_stride, strides in elements, below
+ * 2^31 for a row and 2^48 for the others.  Rows of outputs must not overlap
+ * one another.
+ */
+typedef struct {
+    void *d_rows;
+    size_t batch_stride, head_stride, row_stride, width;
+} gc_cache_rows;
+
+/* Workspace bytes of gc_cache_evict; 0 for arguments out of range. */
+size_t gc_cache_evict_workspace_bytes(size_t batch, size_t heads, size_t budget);
+
+/*
+ * The positions that a bounded cache keeps, with their rows: of the n =
+ * lengths[b] positions of head h of sequence b all if n <= budget, else
+ *   - the first `sinks`, and the last `recent`,
+ *   - of those between, the budget - sinks - recent with the highest scores,
+ *     equal scores (-0 and +0 are equal) the lower position, NaN below all.
+ * They keep their order: kept row i is that of the i-th of them.
+ *
+ * keys, values: the cache's rows, batch x heads x length of dtype; values may
+ * be NULL, with kept_values.  d_scores (float32) and d_positions (int32, NULL:
+ * the index): batch * heads rows of `length`.  d_lengths: one per sequence,
+ * clamped to [0, length]; NULL: length.  Outputs: kept_keys, kept_values:
+ * batch x heads x budget rows of the same widths; rows from the sequence's new
+ * length on are left as they were.  d_kept_scores, d_kept_positions: batch *
+ * heads * budget, from the new length on 0 and -1.  d_kept_lengths: min(n,
+ * budget) per sequence.  sinks + recent <= budget, budget >= 1.
+ */
+gc_status gc_cache_evict(const gc_cache_rows *keys, const gc_cache_rows *values, gc_row_dtype dtype,
+                         const float *d_scores, size_t scores_stride, const int32_t *d_positions,
+                         size_t positions_stride, const int32_t *d_lengths, size_t batch,
+                         size_t heads, size_t length, size_t budget, size_t sinks, size_t recent,
+                         const gc_cache_rows *kept_keys, const gc_cache_rows *kept_values,
+                         float *d_kept_scores, int32_t *d_kept_positions, int32_t *d_kept_lengths,
+                         void *d_ws, size_t ws_bytes, cudaStream_t stream);
 
 /*
  * SYNCHRONOUS.  Waits for `stream`, then reads and clears the device-side

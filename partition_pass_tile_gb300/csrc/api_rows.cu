@@ -85,6 +85,45 @@ gc_status embedding_grad(const void *d_g, size_t g_stride, gc_row_dtype g_dtype,
                                            accumulate != 0, static_cast<uint8_t *>(d_ws), stream, wait));
 }
 
+// Whether the last of n entries `stride` apart is at less than 2^60.
+bool valid_extent(size_t n, size_t stride) { return n <= 1 || stride < (size_t(1) << 60) / n; }
+
+// The rows of a cache: offsets that fit, and for an output no row on another.
+bool valid_cache(const gc_cache_rows &c, size_t batch, size_t heads, size_t rows, bool write)
+{
+    if (c.width < 1 || c.width > GC_MAX_ROW_WIDTH || c.row_stride >= (size_t(1) << 31) ||
+        c.head_stride >= (size_t(1) << 48) || c.batch_stride >= (size_t(1) << 48) ||
+        !valid_extent(batch, c.batch_stride) || !valid_extent(heads, c.head_stride))
+        return false;
+    if (!write || batch == 0 || heads == 0 || rows == 0) return true;
+    struct {
+        size_t n, stride;
+    } d[3] = {{rows, c.row_stride}, {heads, c.head_stride}, {batch, c.batch_stride}};
+    for (int i = 0; i < 2; ++i)
+        for (int j = 0; j < 2; ++j)
+            if (d[j].stride > d[j + 1].stride) {
+                const auto t = d[j];
+                d[j] = d[j + 1], d[j + 1] = t;
+            }
+    size_t reach = c.width;  // elements from a part's first to past its last
+    for (const auto &x : d) {
+        if (x.n <= 1) continue;
+        if (x.stride < reach) return false;
+        reach += (x.n - 1) * x.stride;
+    }
+    return true;
+}
+
+Span cache_span(const gc_cache_rows &c, size_t batch, size_t heads, size_t rows, gc_row_dtype dt, bool write)
+{
+    if (c.d_rows == nullptr || batch == 0 || heads == 0 || rows == 0) return Span{nullptr, 0, row_elem(dt), write};
+    const size_t last = (batch - 1) * c.batch_stride + (heads - 1) * c.head_stride + (rows - 1) * c.row_stride + c.width;
+    return Span{c.d_rows, last * row_elem(dt), row_elem(dt), write};
+}
+
+// CTAs of one launch.
+bool valid_grid(size_t a, size_t b) { return b == 0 || a <= GC_MAX_ELEMENTS / b; }
+
 }  // namespace
 
 extern "C" {
@@ -243,6 +282,183 @@ gc_status gc_sample(const void *d_logits, size_t logits_stride, size_t rows, siz
     return from_cuda(launch_sample(d_logits, logits_stride, uint32_t(rows), uint32_t(vocab), dtype, d_uniform,
                                    uniform_stride, d_temperature, d_top_k, d_top_p, d_min_p, d_tokens, d_logprobs,
                                    stream));
+}
+
+size_t gc_expert_route_workspace_bytes(size_t tokens, uint32_t experts)
+{
+    if (tokens > GC_MAX_ELEMENTS || experts < 1 || experts > GC_MAX_EXPERTS) return 0;
+    return expert_route_workspace_bytes(tokens, experts);
+}
+
+gc_status gc_expert_route(const void *d_logits, size_t logits_stride, size_t tokens, uint32_t experts,
+                          gc_row_dtype dtype, size_t topk, int normalize, const uint8_t *d_mask, int32_t *d_ids,
+                          float *d_weights, int32_t *d_counts, float *d_load, float *d_loss, void *d_ws,
+                          size_t ws_bytes, cudaStream_t stream)
+{
+    if (!valid_row_dtype(dtype) || !valid_routing(tokens, topk) || experts < 1 || experts > GC_MAX_EXPERTS ||
+        topk > experts || !valid_rows(tokens, logits_stride, experts))
+        return GC_ERR_INVALID_VALUE;
+    if ((tokens > 0 && (d_logits == nullptr || d_ids == nullptr || d_weights == nullptr)) ||
+        (d_counts == nullptr && (d_load || d_loss)) || d_ws == nullptr)
+        return GC_ERR_INVALID_VALUE;
+    if ((reinterpret_cast<uintptr_t>(d_ws) & 255u) != 0) return GC_ERR_MISALIGNED;
+    if (ws_bytes < expert_route_workspace_bytes(tokens, experts)) return GC_ERR_WORKSPACE_TOO_SMALL;
+    const gc_status st = check_spans({row_span(d_logits, tokens, logits_stride, experts, dtype, false),
+                                      flat(d_mask, tokens, 1, false), flat(d_ids, tokens * topk, 4, true),
+                                      flat(d_weights, tokens * topk, 4, true),
+                                      flat(d_counts, size_t(experts) + 1, 4, true), flat(d_load, experts, 4, true),
+                                      flat(d_loss, 1, 4, true), Span{d_ws, ws_bytes, 256, true}});
+    if (st != GC_OK || (tokens == 0 && d_counts == nullptr)) return st;
+    return from_cuda(launch_expert_route(d_logits, logits_stride, uint32_t(tokens), experts, dtype, uint32_t(topk),
+                                         normalize != 0, d_mask, d_ids, d_weights, d_counts, d_load, d_loss,
+                                         static_cast<uint8_t *>(d_ws), stream));
+}
+
+gc_status gc_expert_route_grad(const void *d_logits, size_t logits_stride, size_t tokens, uint32_t experts,
+                               gc_row_dtype dtype, size_t topk, int normalize, const int32_t *d_ids,
+                               const int32_t *d_counts, const float *d_dweights, const float *d_dloss, void *d_dx,
+                               size_t dx_stride, cudaStream_t stream)
+{
+    if (!valid_row_dtype(dtype) || !valid_routing(tokens, topk) || experts < 1 || experts > GC_MAX_EXPERTS ||
+        topk > experts || !valid_rows(tokens, logits_stride, experts) || !valid_rows(tokens, dx_stride, experts))
+        return GC_ERR_INVALID_VALUE;
+    if ((tokens > 0 && (d_logits == nullptr || d_ids == nullptr || d_dx == nullptr)) ||
+        (d_dloss != nullptr && d_counts == nullptr))
+        return GC_ERR_INVALID_VALUE;
+    const gc_status st = check_spans({row_span(d_logits, tokens, logits_stride, experts, dtype, false),
+                                      flat(d_ids, tokens * topk, 4, false),
+                                      flat(d_counts, size_t(experts) + 1, 4, false),
+                                      flat(d_dweights, tokens * topk, 4, false), flat(d_dloss, 1, 4, false),
+                                      row_span(d_dx, tokens, dx_stride, experts, dtype, true)});
+    if (st != GC_OK || tokens == 0) return st;
+    return from_cuda(launch_expert_route_grad(d_logits, logits_stride, uint32_t(tokens), experts, dtype,
+                                              uint32_t(topk), normalize != 0, d_ids, d_counts, d_dweights, d_dloss,
+                                              d_dx, dx_stride, stream));
+}
+
+size_t gc_sample_verify_workspace_bytes(size_t sequences, size_t drafts, size_t vocab)
+{
+    if (sequences > GC_MAX_ELEMENTS || drafts > GC_MAX_DRAFTS || vocab < 1 || vocab > GC_MAX_SAMPLE_VOCAB) return 0;
+    return sample_verify_workspace_bytes(sequences, drafts, vocab);
+}
+
+gc_status gc_sample_verify(const void *d_logits, size_t logits_stride, const void *d_draft_logits, size_t draft_stride,
+                           size_t sequences, size_t drafts, size_t vocab, gc_row_dtype dtype, const int32_t *d_drafts,
+                           const float *d_accept, const float *d_uniform, size_t uniform_stride,
+                           const float *d_temperature, int32_t *d_tokens, int32_t *d_accepted, float *d_logprobs,
+                           void *d_ws, size_t ws_bytes, cudaStream_t stream)
+{
+    const size_t need = gc_sample_verify_workspace_bytes(sequences, drafts, vocab);
+    const size_t rows = sequences * (drafts + 1), drafted = sequences * drafts;
+    if (!valid_row_dtype(dtype) || need == 0 || !valid_rows(rows, logits_stride, vocab) ||
+        (d_draft_logits && !valid_rows(drafted, draft_stride, vocab)) ||
+        (d_uniform && !valid_rows(sequences, uniform_stride, vocab)))
+        return GC_ERR_INVALID_VALUE;
+    if ((sequences > 0 && (d_logits == nullptr || d_tokens == nullptr || d_accepted == nullptr)) ||
+        (drafted > 0 && (d_drafts == nullptr || (d_uniform && d_accept == nullptr))) || d_ws == nullptr)
+        return GC_ERR_INVALID_VALUE;
+    if ((reinterpret_cast<uintptr_t>(d_ws) & 255u) != 0) return GC_ERR_MISALIGNED;
+    if (ws_bytes < need) return GC_ERR_WORKSPACE_TOO_SMALL;
+    const gc_status st = check_spans({row_span(d_logits, rows, logits_stride, vocab, dtype, false),
+                                      row_span(d_draft_logits, drafted, draft_stride, vocab, dtype, false),
+                                      flat(d_drafts, drafted, 4, false), flat(d_accept, drafted, 4, false),
+                                      row_span(d_uniform, sequences, uniform_stride, vocab, GC_ROW_F32, false),
+                                      flat(d_temperature, sequences, 4, false), flat(d_tokens, rows, 4, true),
+                                      flat(d_accepted, sequences, 4, true), flat(d_logprobs, rows, 4, true),
+                                      Span{d_ws, ws_bytes, 256, true}});
+    if (st != GC_OK || sequences == 0) return st;
+    return from_cuda(launch_sample_verify(d_logits, logits_stride, drafts ? d_draft_logits : nullptr, draft_stride,
+                                          uint32_t(sequences), uint32_t(drafts), uint32_t(vocab), dtype, d_drafts,
+                                          d_accept, d_uniform, uniform_stride, d_temperature, d_tokens, d_accepted,
+                                          d_logprobs, static_cast<uint8_t *>(d_ws), stream));
+}
+
+gc_status gc_cache_score(const void *d_weights, size_t batch_stride, size_t head_stride, size_t query_stride,
+                         gc_row_dtype dtype, size_t batch, size_t heads, size_t group, size_t queries, size_t length,
+                         const float *d_scores, size_t scores_stride, float decay, const int32_t *d_lengths,
+                         const int32_t *d_counted, float *d_out, size_t out_stride, cudaStream_t stream)
+{
+    if (!valid_row_dtype(dtype) || batch > GC_MAX_ELEMENTS || heads > GC_MAX_ELEMENTS || group < 1 ||
+        group > GC_MAX_ELEMENTS || queries > GC_MAX_ELEMENTS || length > GC_MAX_ROW_WIDTH ||
+        !valid_grid(batch, heads) || !valid_grid(heads, group) || !valid_grid(group, queries) ||
+        !valid_grid(batch * heads, length / 32 + 1) || !valid_extent(batch, batch_stride) ||
+        !valid_extent(heads * group, head_stride) || !valid_extent(queries, query_stride))
+        return GC_ERR_INVALID_VALUE;
+    const size_t rows = batch * heads;
+    if (rows == 0 || length == 0) return GC_OK;
+    if ((d_scores && !valid_rows(rows, scores_stride, length)) || !valid_rows(rows, out_stride, length) ||
+        d_out == nullptr || (queries > 0 && d_weights == nullptr))
+        return GC_ERR_INVALID_VALUE;
+    Span weights{nullptr, 0, row_elem(dtype), false};
+    if (queries > 0) {
+        const size_t last = (batch - 1) * batch_stride + (heads * group - 1) * head_stride +
+                            (queries - 1) * query_stride + length;
+        weights = Span{d_weights, last * row_elem(dtype), row_elem(dtype), false};
+    }
+    // the scores may be updated in place
+    const bool in_place = d_scores == d_out;
+    if (in_place && scores_stride != out_stride) return GC_ERR_INVALID_VALUE;
+    const gc_status st = check_spans({weights,
+                                      in_place ? Span{} : row_span(d_scores, rows, scores_stride, length, GC_ROW_F32, false),
+                                      flat(d_lengths, batch, 4, false), flat(d_counted, batch, 4, false),
+                                      row_span(d_out, rows, out_stride, length, GC_ROW_F32, true)});
+    if (st != GC_OK) return st;
+    return from_cuda(launch_cache_score(d_weights, batch_stride, head_stride, query_stride, dtype, uint32_t(batch),
+                                        uint32_t(heads), uint32_t(group), uint32_t(queries), uint32_t(length),
+                                        d_scores, scores_stride, decay, d_lengths, d_counted, d_out, out_stride,
+                                        stream));
+}
+
+size_t gc_cache_evict_workspace_bytes(size_t batch, size_t heads, size_t budget)
+{
+    if (batch > GC_MAX_ELEMENTS || heads > GC_MAX_ELEMENTS || !valid_grid(batch, heads) || budget < 1 ||
+        budget > GC_MAX_ROW_WIDTH || !valid_grid(batch * heads, budget))
+        return 0;
+    return cache_evict_workspace_bytes(batch * heads, budget);
+}
+
+gc_status gc_cache_evict(const gc_cache_rows *keys, const gc_cache_rows *values, gc_row_dtype dtype,
+                         const float *d_scores, size_t scores_stride, const int32_t *d_positions,
+                         size_t positions_stride, const int32_t *d_lengths, size_t batch, size_t heads, size_t length,
+                         size_t budget, size_t sinks, size_t recent, const gc_cache_rows *kept_keys,
+                         const gc_cache_rows *kept_values, float *d_kept_scores, int32_t *d_kept_positions,
+                         int32_t *d_kept_lengths, void *d_ws, size_t ws_bytes, cudaStream_t stream)
+{
+    const size_t need = gc_cache_evict_workspace_bytes(batch, heads, budget);
+    if (!valid_row_dtype(dtype) || need == 0 || length > GC_MAX_ROW_WIDTH || sinks > budget || recent > budget - sinks ||
+        keys == nullptr || kept_keys == nullptr || (values == nullptr) != (kept_values == nullptr))
+        return GC_ERR_INVALID_VALUE;
+    const size_t rows = batch * heads, there = rows * length;
+    if (!valid_grid(rows, 8) || !valid_cache(*keys, batch, heads, length, false) ||
+        !valid_cache(*kept_keys, batch, heads, budget, true) || keys->width != kept_keys->width ||
+        (values && (!valid_cache(*values, batch, heads, length, false) ||
+                    !valid_cache(*kept_values, batch, heads, budget, true) || values->width != kept_values->width)))
+        return GC_ERR_INVALID_VALUE;
+    if (length > 0 && (!valid_rows(rows, scores_stride, length) ||
+                       (d_positions && !valid_rows(rows, positions_stride, length))))
+        return GC_ERR_INVALID_VALUE;
+    if ((there > 0 && (keys->d_rows == nullptr || d_scores == nullptr || (values && values->d_rows == nullptr))) ||
+        (rows > 0 && (kept_keys->d_rows == nullptr || (values && kept_values->d_rows == nullptr) ||
+                      d_kept_scores == nullptr || d_kept_positions == nullptr || d_kept_lengths == nullptr)) ||
+        d_ws == nullptr)
+        return GC_ERR_INVALID_VALUE;
+    if ((reinterpret_cast<uintptr_t>(d_ws) & 255u) != 0) return GC_ERR_MISALIGNED;
+    if (ws_bytes < need) return GC_ERR_WORKSPACE_TOO_SMALL;
+    const gc_status st = check_spans(
+        {cache_span(*keys, batch, heads, length, dtype, false),
+         values ? cache_span(*values, batch, heads, length, dtype, false) : Span{},
+         length ? row_span(d_scores, rows, scores_stride, length, GC_ROW_F32, false) : Span{},
+         length ? row_span(d_positions, rows, positions_stride, length, GC_ROW_F32, false) : Span{},
+         flat(d_lengths, batch, 4, false), cache_span(*kept_keys, batch, heads, budget, dtype, true),
+         values ? cache_span(*kept_values, batch, heads, budget, dtype, true) : Span{},
+         flat(d_kept_scores, rows * budget, 4, true), flat(d_kept_positions, rows * budget, 4, true),
+         flat(d_kept_lengths, batch, 4, true), Span{d_ws, ws_bytes, 256, true}});
+    if (st != GC_OK || rows == 0) return st;
+    return from_cuda(launch_cache_evict(keys, values, dtype, d_scores, scores_stride, d_positions, positions_stride,
+                                        d_lengths, uint32_t(batch), uint32_t(heads), uint32_t(length),
+                                        uint32_t(budget), uint32_t(sinks), uint32_t(recent), kept_keys, kept_values,
+                                        d_kept_scores, d_kept_positions, d_kept_lengths,
+                                        static_cast<uint8_t *>(d_ws), stream));
 }
 
 }  // extern "C"

@@ -1,6 +1,7 @@
 // gc_rows.cuh -- device building blocks of the row operators (experts.cu,
-// embedding.cu, sample.cu): element types, pieces of 2 to 16 bytes of a row
-// with their float32 values, and ids of either width.
+// route.cu, embedding.cu, sample.cu, verify.cu, cache.cu): element types, pieces
+// of 2 to 16 bytes of a row with their float32 values, the order of logits, and
+// ids of either width.
 #pragma once
 
 #include <cstdint>
@@ -67,6 +68,31 @@ __device__ __forceinline__ Piece<T, N> zero_piece()
     return z;
 }
 
+// A logit as the operators read it: NaN is -inf (a forbidden token or expert),
+// +inf the largest finite value.
+__device__ __forceinline__ float sample_value(float x) { return fminf(fmaxf(x, -INFINITY), 3.402823466e38f); }
+
+// Ascends with x; -0 and +0 are one value.
+__device__ __forceinline__ uint32_t order_bits(float x)
+{
+    const uint32_t b = __float_as_uint(x + 0.0f);
+    return b ^ (uint32_t(int32_t(b) >> 31) | 0x80000000u);
+}
+
+__device__ __forceinline__ float order_value(uint32_t o)
+{
+    return __uint_as_float((o & 0x80000000u) ? o ^ 0x80000000u : ~o);
+}
+
+// 2^x by the hardware's approximation, off by at most 2^-22 of itself; results
+// below 2^-126 are 0.
+__device__ __forceinline__ float pow2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // Id i of an int32 or int64 array; any value outside [0, limit) becomes limit
 // (limit <= 2^31 - 1).
 __device__ __forceinline__ uint32_t load_id(const void *ids, bool wide, uint64_t i, uint32_t limit)
@@ -87,6 +113,59 @@ __device__ __forceinline__ void zero_row(void *row, size_t bytes)
     if (lane < head / 2) reinterpret_cast<uint16_t *>(p)[lane] = 0;
     for (size_t i = lane; i < body; i += 32) reinterpret_cast<uint4 *>(p + head)[i] = make_uint4(0u, 0u, 0u, 0u);
     if (lane < (bytes - tail) / 2) reinterpret_cast<uint16_t *>(p + tail)[lane] = 0;
+}
+
+// Thread-block clusters.  What a CTA writes to its shared memory before a
+// cluster_sync the others read behind it.
+__device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t cluster_size()
+{
+    uint32_t n;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(n));
+    return n;
+}
+
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// The address of a variable in shared memory as CTA `rank` of the cluster has it.
+__device__ __forceinline__ uint32_t peer_address(const void *mine, uint32_t rank)
+{
+    uint32_t at;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                 : "=r"(at)
+                 : "r"(uint32_t(__cvta_generic_to_shared(mine))), "r"(rank));
+    return at;
+}
+
+__device__ __forceinline__ uint32_t peer_load(uint32_t at)
+{
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ uint4 peer_load4(uint32_t at)
+{
+    uint4 v;
+    asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(at)
+                 : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void peer_store(uint32_t at, double v)
+{
+    asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(at), "d"(v) : "memory");
 }
 
 // Programmatic launches: a kernel launched by launch_next may start while the

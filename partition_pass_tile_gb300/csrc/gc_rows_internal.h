@@ -1,11 +1,15 @@
 // gc_rows_internal.h -- the launchers of the row operators (experts.cu,
-// embedding.cu, sample.cu) that api_rows.cu dispatches to.  Arguments were
+// route.cu, embedding.cu, sample.cu, verify.cu, cache.cu) that api_rows.cu dispatches to.  Arguments were
 // validated there; strides and widths in elements, `wide`: int64 ids.
 #pragma once
 
 #include "gc_internal.h"
 
 namespace gch {
+
+// SMs that grids, and with them the order of sums, are planned for: sums and
+// workspaces do not depend on the device that a call finds.
+constexpr size_t kSms = 152;
 
 size_t expert_workspace_bytes(size_t npairs, uint32_t experts);
 cudaError_t launch_expert_dispatch(const void *ids, bool wide, uint32_t npairs, uint32_t topk, uint32_t experts,
@@ -37,5 +41,31 @@ cudaError_t launch_sample(const void *logits, size_t logits_stride, uint32_t row
                           const float *uniform, size_t uniform_stride, const float *temperature,
                           const int32_t *top_k, const float *top_p, const float *min_p, int32_t *tokens,
                           float *logprobs, cudaStream_t s);
+size_t expert_route_workspace_bytes(size_t tokens, uint32_t experts);
+cudaError_t launch_expert_route(const void *logits, size_t stride, uint32_t tokens, uint32_t experts, gc_row_dtype dt,
+                                uint32_t topk, bool normalize, const uint8_t *mask, int32_t *ids, float *weights,
+                                int32_t *counts, float *load, float *loss, uint8_t *ws, cudaStream_t s);
+cudaError_t launch_expert_route_grad(const void *logits, size_t stride, uint32_t tokens, uint32_t experts,
+                                     gc_row_dtype dt, uint32_t topk, bool normalize, const int32_t *ids,
+                                     const int32_t *counts, const float *dweights, const float *dloss, void *dx,
+                                     size_t dx_stride, cudaStream_t s);
+size_t sample_verify_workspace_bytes(size_t sequences, size_t drafts, size_t vocab);  // 0: too many rows
+cudaError_t launch_sample_verify(const void *logits, size_t logits_stride, const void *draft_logits,
+                                 size_t draft_stride, uint32_t sequences, uint32_t drafts, uint32_t vocab,
+                                 gc_row_dtype dt, const int32_t *ids, const float *accept, const float *uniform,
+                                 size_t uniform_stride, const float *temperature, int32_t *tokens, int32_t *accepted,
+                                 float *logprobs, uint8_t *ws, cudaStream_t s);
+cudaError_t launch_cache_score(const void *weights, size_t batch_stride, size_t head_stride, size_t query_stride,
+                               gc_row_dtype dt, uint32_t batch, uint32_t heads, uint32_t group, uint32_t queries,
+                               uint32_t length, const float *scores, size_t scores_stride, float decay,
+                               const int32_t *lengths, const int32_t *counted, float *out, size_t out_stride,
+                               cudaStream_t s);
+size_t cache_evict_workspace_bytes(size_t rows, size_t budget);
+cudaError_t launch_cache_evict(const gc_cache_rows *keys, const gc_cache_rows *values, gc_row_dtype dt,
+                               const float *scores, size_t scores_stride, const int32_t *positions,
+                               size_t positions_stride, const int32_t *lengths, uint32_t batch, uint32_t heads,
+                               uint32_t length, uint32_t budget, uint32_t sinks, uint32_t recent,
+                               const gc_cache_rows *kept_keys, const gc_cache_rows *kept_values, float *kept_scores,
+                               int32_t *kept_positions, int32_t *kept_lengths, uint8_t *ws, cudaStream_t s);
 
 }  // namespace gch

@@ -64,24 +64,9 @@ constexpr float kUniformLo = 0x1p-25f, kUniformHi = 1.0f - 0x1p-24f;
 constexpr float kLightest = 2.0611536e-9f;
 constexpr uint32_t kFull = 0xffffffffu;
 
-// x as the operator reads it: NaN is -inf, +inf the largest finite value.
-__device__ __forceinline__ float sample_value(float x) { return fminf(fmaxf(x, -INFINITY), 3.402823466e38f); }
-
-// Ascends with x; -0 and +0 are one value.
-__device__ __forceinline__ uint32_t order_bits(float x)
-{
-    const uint32_t b = __float_as_uint(x + 0.0f);
-    return b ^ (uint32_t(int32_t(b) >> 31) | 0x80000000u);
-}
-
 __device__ __forceinline__ uint64_t order_key(float x, uint32_t i)
 {
     return (uint64_t(order_bits(x)) << 32) | uint32_t(~i);
-}
-
-__device__ __forceinline__ float order_value(uint32_t o)
-{
-    return __uint_as_float((o & 0x80000000u) ? o ^ 0x80000000u : ~o);
 }
 
 __device__ __forceinline__ float key_value(uint64_t key) { return order_value(uint32_t(key >> 32)); }

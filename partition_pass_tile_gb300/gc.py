@@ -40,6 +40,14 @@ CMP_NAMES = {"<": LT, "<=": LE, ">": GT, ">=": GE, "==": EQ, "!=": NE,
 class Predicate(ctypes.Structure):
     """gc_predicate: x OP operand in the dtype's order, or (bits & mask) OP operand."""
     _fields_ = [("cmp", ctypes.c_int), ("operand", ctypes.c_uint32), ("mask", ctypes.c_uint32)]
+
+
+class CacheRows(ctypes.Structure):
+    """gc_cache_rows: where the rows of a cache are; strides and width in elements."""
+    _fields_ = [("d_rows", ctypes.c_void_p), ("batch_stride", ctypes.c_size_t), ("head_stride", ctypes.c_size_t),
+                ("row_stride", ctypes.c_size_t), ("width", ctypes.c_size_t)]
+
+
 STATUS = {0: "GC_OK", 1: "GC_ERR_INVALID_VALUE", 2: "GC_ERR_UNSUPPORTED",
           3: "GC_ERR_WORKSPACE_TOO_SMALL", 4: "GC_ERR_MISALIGNED", 5: "GC_ERR_CUDA",
           6: "GC_ERR_TIMEOUT", 7: "GC_ERR_DEVICE_CHECK"}
@@ -66,6 +74,7 @@ def load(path: str | Path | None = None) -> ctypes.CDLL:
     lib = ctypes.CDLL(str(p))
     V, Z, I, U64 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int, ctypes.c_uint64
     S, U32T, F = ctypes.c_int, ctypes.c_uint32, ctypes.c_float
+    R = ctypes.POINTER(CacheRows)
     sig = {
         "gc_status_string": ([S], ctypes.c_char_p),
         "gc_version": ([], ctypes.c_char_p),
@@ -96,11 +105,19 @@ def load(path: str | Path | None = None) -> ctypes.CDLL:
         "gc_expert_dispatch": ([V, I, Z, Z, U32T, U32T, V, Z, Z, I, V, Z, Z, V, V, V, V, V, Z, V], S),
         "gc_expert_combine": ([V, Z, Z, V, V, Z, Z, Z, I, V, Z, V], S),
         "gc_expert_combine_grad": ([V, Z, V, Z, Z, V, V, V, Z, Z, Z, I, V, Z, V, V], S),
+        "gc_expert_route_workspace_bytes": ([Z, U32T], Z),
+        "gc_expert_route": ([V, Z, Z, U32T, I, Z, I, V, V, V, V, V, V, V, Z, V], S),
+        "gc_expert_route_grad": ([V, Z, Z, U32T, I, Z, I, V, V, V, V, V, Z, V], S),
         "gc_embedding": ([V, Z, Z, Z, I, V, I, Z, F, V, Z, V], S),
         "gc_embedding_grad_workspace_bytes": ([Z, Z, Z], Z),
         "gc_embedding_grad": ([V, Z, I, V, I, Z, Z, Z, F, V, Z, I, I, V, Z, V], S),
         "gc_testing_embedding_grad_stalled": ([V, Z, I, V, I, Z, Z, Z, F, V, Z, I, I, V, Z, U64, V], S),
         "gc_sample": ([V, Z, Z, Z, I, V, Z, V, V, V, V, V, V, V], S),
+        "gc_sample_verify_workspace_bytes": ([Z, Z, Z], Z),
+        "gc_sample_verify": ([V, Z, V, Z, Z, Z, Z, I, V, V, V, Z, V, V, V, V, V, Z, V], S),
+        "gc_cache_score": ([V, Z, Z, Z, I, Z, Z, Z, Z, Z, V, Z, F, V, V, V, Z, V], S),
+        "gc_cache_evict_workspace_bytes": ([Z, Z, Z], Z),
+        "gc_cache_evict": ([R, R, I, V, Z, V, Z, V, Z, Z, Z, Z, Z, Z, R, R, V, V, V, V, Z, V], S),
     }
     for name, (args, res) in sig.items():
         f = getattr(lib, name)
@@ -813,3 +830,251 @@ def sample(logits: torch.Tensor, uniform: torch.Tensor | None = None, temperatur
                             _typed(min_p, torch.float32, rows, "min_p"), _ptr(tokens), _ptr(logprobs),
                             _handle(stream, dev)), "gc_sample")
     return tokens, logprobs
+
+
+def _rows3(t: torch.Tensor, what: str) -> tuple[int, int]:
+    """(pointer, row stride) of a [n, m, width] tensor whose rows are one row array."""
+    _on_device(t)
+    shape, stride = t.shape, t.stride()
+    if len(shape) == 3 and t.numel() == 0:
+        return t.data_ptr(), shape[2]
+    if len(shape) != 3 or (stride[2] != 1 and shape[2] > 1) or \
+            (shape[0] > 1 and shape[1] > 1 and stride[0] != shape[1] * stride[1]):
+        raise ValueError(f"{what} is a 3-D tensor of contiguous rows, the same distance apart throughout")
+    return t.data_ptr(), stride[1] if shape[1] > 1 else stride[0] if shape[0] > 1 else shape[2]
+
+
+class Routing(NamedTuple):
+    """What gc_expert_route made of the logits."""
+    ids: torch.Tensor             # [tokens, topk] int32, -1 where no expert is left
+    weights: torch.Tensor         # [tokens, topk] float32
+    counts: torch.Tensor | None   # [experts + 1] int32: pairs of each expert; tokens with a choice
+    load: torch.Tensor | None     # [experts] float32, mean probabilities
+    loss: torch.Tensor | None     # [1] float32
+
+
+@lru_cache(maxsize=1024)
+def expert_route_workspace_bytes(tokens: int, experts: int) -> int:
+    return int(load().gc_expert_route_workspace_bytes(tokens, experts))
+
+
+def expert_route(logits: torch.Tensor, topk: int, normalize: bool = True, mask: torch.Tensor | None = None,
+                 balance: bool = True, out: Routing | None = None, ws: torch.Tensor | None = None,
+                 stream=None) -> Routing:
+    """Every token's top-k experts with their weights, and how evenly they are used.
+
+    logits: [tokens, experts].  normalize: the weights of a token's choices sum
+    to 1, else they are softmax's.  mask: bool [tokens], False for tokens that
+    have no choice (padding).  balance False leaves counts, load and loss out.
+    ids and weights are what expert_dispatch and expert_combine take; the
+    gradient is expert_route_grad, autograd does not see the call.
+    """
+    lp, ls = _rows(logits)
+    tokens, experts = logits.shape
+    dev = logits.device
+    if not 0 < topk <= experts:
+        raise ValueError(f"topk is a number of [1, {experts}]")
+    o = out if out is not None else Routing(None, None, None, None, None)
+    ids = _like(o.ids, (tokens, topk), torch.int32, dev, stream, "out.ids")
+    weights = _like(o.weights, (tokens, topk), torch.float32, dev, stream, "out.weights")
+    counts = means = loss = None
+    if balance:
+        counts = _like(o.counts, (experts + 1,), torch.int32, dev, stream, "out.counts")
+        means = _like(o.load, (experts,), torch.float32, dev, stream, "out.load")
+        loss = _like(o.loss, (1,), torch.float32, dev, stream, "out.loss")
+    ws = _scratch(ws, expert_route_workspace_bytes(tokens, experts), dev, stream)
+    _check(load().gc_expert_route(
+        lp, ls, tokens, experts, row_dtype_code(logits.dtype), topk, int(normalize),
+        _typed(mask, torch.bool, tokens, "mask"), _ptr(ids), _ptr(weights), _ptr(counts), _ptr(means), _ptr(loss),
+        _ptr(ws), ws.numel(), _handle(stream, dev)), "gc_expert_route")
+    return Routing(ids, weights, counts, means, loss)
+
+
+def expert_route_grad(logits: torch.Tensor, ids: torch.Tensor, counts: torch.Tensor | None = None,
+                      dweights: torch.Tensor | None = None, dloss: torch.Tensor | None = None, normalize: bool = True,
+                      out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Gradient of expert_route with respect to its logits -> [tokens, experts].
+
+    dweights: float32 [tokens, topk], the gradient of its weights; dloss:
+    float32 [1], that of its loss; None counts as 0.  ids and counts (for
+    dloss) are expert_route's, normalize is what it was called with.
+    """
+    lp, ls = _rows(logits)
+    tokens, experts = logits.shape
+    if ids.dim() != 2 or ids.size(0) != tokens:
+        raise ValueError(f"ids is a tensor of shape ({tokens}, topk)")
+    topk = ids.size(1)
+    dev = logits.device
+    out = _like(out, (tokens, experts), logits.dtype, dev, stream, "out")
+    op, os = _rows(out)
+    _check(load().gc_expert_route_grad(
+        lp, ls, tokens, experts, row_dtype_code(logits.dtype), topk, int(normalize),
+        _typed(ids, torch.int32, tokens * topk, "ids"), _typed(counts, torch.int32, experts + 1, "counts"),
+        _typed(dweights, torch.float32, tokens * topk, "dweights"), _typed(dloss, torch.float32, 1, "dloss"), op, os,
+        _handle(stream, dev)), "gc_expert_route_grad")
+    return out
+
+
+@lru_cache(maxsize=1024)
+def sample_verify_workspace_bytes(sequences: int, drafts: int, vocab: int) -> int:
+    return int(load().gc_sample_verify_workspace_bytes(sequences, drafts, vocab))
+
+
+def sample_verify(logits: torch.Tensor, drafts: torch.Tensor, accept: torch.Tensor | None = None,
+                  uniform: torch.Tensor | None = None, draft_logits: torch.Tensor | None = None, temperature=None,
+                  tokens: torch.Tensor | None = None, accepted: torch.Tensor | None = None,
+                  logprobs: torch.Tensor | None = None, ws: torch.Tensor | None = None, stream=None):
+    """Drafted tokens accepted or replaced -> (tokens, accepted, logprobs).
+
+    logits: [sequences, drafts + 1, vocab], the target's; drafts: int32
+    [sequences, drafts], tokens outside the vocabulary end a short draft;
+    draft_logits: [sequences, drafts, vocab], what they were drawn from, None
+    for drafts without probabilities.  accept (like drafts) and uniform
+    ([sequences, vocab]): float32 random numbers of [0, 1); both None decode
+    greedily.  temperature: a number or one value per sequence, for target and
+    draft.  tokens and logprobs: [sequences, drafts + 1], the accepted tokens,
+    the drawn one, then -1 and -inf; accepted: [sequences] int32.
+    """
+    lp, ls = _rows3(logits, "logits")
+    sequences, places, vocab = logits.shape
+    n = places - 1
+    dev = logits.device
+    if n < 0 or drafts.dim() != 2 or tuple(drafts.shape) != (sequences, n):
+        raise ValueError("logits is [sequences, drafts + 1, vocab] and drafts [sequences, drafts]")
+    dp, ds = None, 0
+    if draft_logits is not None:
+        if draft_logits.dtype != logits.dtype or tuple(draft_logits.shape) != (sequences, n, vocab):
+            raise ValueError(f"draft_logits is a {logits.dtype} tensor of shape {(sequences, n, vocab)}")
+        dp, ds = _rows3(draft_logits, "draft_logits")
+    up, us = None, 0
+    if (accept is None) != (uniform is None):
+        raise ValueError("accept and uniform come together")
+    if uniform is not None:
+        if uniform.dtype != torch.float32 or tuple(uniform.shape) != (sequences, vocab):
+            raise ValueError(f"uniform is a float32 tensor of shape {(sequences, vocab)}")
+        up, us = _rows(uniform)
+    temperature = _per_row(temperature, torch.float32, sequences, dev, stream)
+    tokens = _like(tokens, (sequences, places), torch.int32, dev, stream, "tokens")
+    accepted = _like(accepted, (sequences,), torch.int32, dev, stream, "accepted")
+    logprobs = _like(logprobs, (sequences, places), torch.float32, dev, stream, "logprobs")
+    ws = _scratch(ws, sample_verify_workspace_bytes(sequences, n, vocab), dev, stream)
+    _check(load().gc_sample_verify(
+        lp, ls, dp, ds, sequences, n, vocab, row_dtype_code(logits.dtype),
+        _typed(drafts, torch.int32, sequences * n, "drafts"), _typed(accept, torch.float32, sequences * n, "accept"),
+        up, us, _typed(temperature, torch.float32, sequences, "temperature"), _ptr(tokens), _ptr(accepted),
+        _ptr(logprobs), _ptr(ws), ws.numel(), _handle(stream, dev)), "gc_sample_verify")
+    return tokens, accepted, logprobs
+
+
+def cache_score(weights: torch.Tensor, scores: torch.Tensor | None, heads: int | None = None, decay: float = 1.0,
+                lengths: torch.Tensor | None = None, queries: torch.Tensor | None = None,
+                out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Attention weights added to the scores of a cache's positions -> [batch, heads, length] float32.
+
+    weights: [batch, query heads, queries, length]; the query heads of a
+    cache's head are neighbours.  scores: [batch, heads, length] float32, or
+    None (zeros; then `heads` says how many).  out may be scores itself.
+    lengths, queries: int32 [batch], how many positions and queries of each
+    sequence count; out is 0 from its length on.
+    """
+    if weights.dim() != 4 or (weights.stride(3) != 1 and weights.size(3) > 1 and weights.numel() > 0):
+        raise ValueError("weights is a 4-D tensor [batch, query heads, queries, length] of contiguous rows")
+    _on_device(weights)
+    batch, query_heads, count, length = weights.shape
+    if scores is not None:
+        if heads not in (None, scores.size(1)):
+            raise ValueError(f"scores has {scores.size(1)} heads, not {heads}")
+        heads = scores.size(1)
+        if scores.dtype != torch.float32 or tuple(scores.shape) != (batch, heads, length):
+            raise ValueError(f"scores is a float32 tensor of shape {(batch, heads, length)}")
+    if not heads or query_heads % heads or not query_heads:
+        raise ValueError(f"{query_heads} query heads share {heads} heads of a cache")
+    dev = weights.device
+    out = _like(out, (batch, heads, length), torch.float32, dev, stream, "out")
+    sp, ss = (None, 0) if scores is None else _rows3(scores, "scores")
+    op, os = _rows3(out, "out")
+    strides = [s if n > 1 else 0 for s, n in zip(weights.stride(), weights.shape)]
+    _check(load().gc_cache_score(
+        weights.data_ptr(), *strides[:3], row_dtype_code(weights.dtype), batch, heads, query_heads // heads, count,
+        length, sp, ss, decay, _typed(lengths, torch.int32, batch, "lengths"),
+        _typed(queries, torch.int32, batch, "queries"), op, os, _handle(stream, dev)), "gc_cache_score")
+    return out
+
+
+class KeptCache(NamedTuple):
+    """What gc_cache_evict kept."""
+    keys: torch.Tensor            # [batch, heads, budget, width]
+    values: torch.Tensor | None   # [batch, heads, budget, value width]
+    scores: torch.Tensor          # [batch, heads, budget] float32
+    positions: torch.Tensor       # [batch, heads, budget] int32
+    lengths: torch.Tensor         # [batch] int32
+
+
+@lru_cache(maxsize=1024)
+def cache_evict_workspace_bytes(batch: int, heads: int, budget: int) -> int:
+    return int(load().gc_cache_evict_workspace_bytes(batch, heads, budget))
+
+
+def _cache_rows(t: torch.Tensor) -> CacheRows:
+    """A [batch, heads, length, width] tensor whose rows are contiguous."""
+    _on_device(t)
+    shape, stride = t.shape, t.stride()
+    if len(shape) == 4 and t.numel() == 0:
+        return CacheRows(t.data_ptr(), 0, 0, shape[3], shape[3])
+    if len(shape) != 4 or (stride[3] != 1 and shape[3] > 1):
+        raise ValueError("libgc takes 4-D caches [batch, heads, length, width] whose rows are contiguous")
+    return CacheRows(t.data_ptr(), *(s if n > 1 else 0 for s, n in zip(stride[:2], shape)),
+                     stride[2] if shape[2] > 1 else shape[3], shape[3])
+
+
+def cache_evict(keys: torch.Tensor, values: torch.Tensor | None, scores: torch.Tensor, budget: int, sinks: int = 0,
+                recent: int = 0, positions: torch.Tensor | None = None, lengths: torch.Tensor | None = None,
+                out: KeptCache | None = None, ws: torch.Tensor | None = None, stream=None) -> KeptCache:
+    """The positions with the highest scores, in their order, with their rows -> KeptCache.
+
+    keys, values: [batch, heads, length, width] in any layout with contiguous
+    rows (values None: a cache of one array); scores: float32 [batch, heads,
+    length]; positions: int32 like scores (None: 0, 1, ...); lengths: int32
+    [batch].  The first `sinks` and the last `recent` positions of a sequence
+    stay.  Rows of out.keys and out.values behind a sequence's new length are
+    left as they were; new tensors hold zeros there.
+    """
+    shape = keys.shape
+    kr = _cache_rows(keys)
+    batch, heads, length, width = shape
+    dev = keys.device
+    if scores.dtype != torch.float32 or tuple(scores.shape) != (batch, heads, length):
+        raise ValueError(f"scores is a float32 tensor of shape {(batch, heads, length)}")
+    if budget < 1 or sinks < 0 or recent < 0 or sinks + recent > budget:
+        raise ValueError("budget is at least 1, and sinks and recent fit into it")
+    sp, ss = _rows3(scores, "scores")
+    pp, ps = None, 0
+    if positions is not None:
+        if positions.dtype != torch.int32 or tuple(positions.shape) != (batch, heads, length):
+            raise ValueError(f"positions is an int32 tensor of shape {(batch, heads, length)}")
+        pp, ps = _rows3(positions, "positions")
+    fill = 0 if lengths is not None or length < budget else None
+    o = out if out is not None else KeptCache(None, None, None, None, None)
+
+    def rows(mine, t, what):
+        if mine is None:
+            return _new((batch, heads, budget, t.size(3)), t.dtype, dev, stream, fill)
+        return _like(mine, (batch, heads, budget, t.size(3)), t.dtype, dev, stream, what)
+
+    kept_keys = rows(o.keys, keys, "out.keys")
+    vr = kvr = kept_values = None
+    if values is not None:
+        if values.dtype != keys.dtype or values.shape[:3] != shape[:3]:
+            raise ValueError(f"values is a {keys.dtype} tensor of shape {(batch, heads, length)} + (width,)")
+        vr = _cache_rows(values)
+        kept_values = rows(o.values, values, "out.values")
+        kvr = _cache_rows(kept_values)
+    kept_scores = _like(o.scores, (batch, heads, budget), torch.float32, dev, stream, "out.scores")
+    kept_positions = _like(o.positions, (batch, heads, budget), torch.int32, dev, stream, "out.positions")
+    kept_lengths = _like(o.lengths, (batch,), torch.int32, dev, stream, "out.lengths")
+    ws = _scratch(ws, cache_evict_workspace_bytes(batch, heads, budget), dev, stream)
+    _check(load().gc_cache_evict(
+        kr, vr, row_dtype_code(keys.dtype), sp, ss, pp, ps, _typed(lengths, torch.int32, batch, "lengths"), batch,
+        heads, length, budget, sinks, recent, _cache_rows(kept_keys), kvr, _ptr(kept_scores), _ptr(kept_positions),
+        _ptr(kept_lengths), _ptr(ws), ws.numel(), _handle(stream, dev)), "gc_cache_evict")
+    return KeptCache(kept_keys, kept_values, kept_scores, kept_positions, kept_lengths)
