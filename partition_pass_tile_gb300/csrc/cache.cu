@@ -17,8 +17,9 @@ constexpr uint32_t kFull = 0xffffffffu;
 
 // ---------------------------------------------------------------- scores
 
+constexpr int kScoreThreads = 256;
 constexpr int kScoreRows = 8;   // rows that a thread has under way
-constexpr int kScoreY = 8;      // threads over the rows of one piece, at most
+constexpr uint32_t kScoreY = 8; // threads over the rows of one piece, at most
 
 struct Weights {
     size_t batch_stride, head_stride, query_stride;
@@ -31,72 +32,99 @@ __device__ __forceinline__ uint32_t clamp_length(const int32_t *lengths, uint32_
     return lengths ? uint32_t(min(max(lengths[b], 0), int32_t(most))) : most;
 }
 
-// 32 pieces across, the rows (queries of the group's heads, head by head) down
-// the threads of a block, then joined in their order.
+// Pieces across, the rows (queries of the group's heads, head by head) down the
+// threads of a block, whose sums are then joined in their order.  `whole`: the
+// scores and the result move in 16 bytes too.
 template <class T, int N>
-__global__ void __launch_bounds__(32 * kScoreY)
+__global__ void __launch_bounds__(kScoreThreads, 4)
 cache_score_kernel(const T *__restrict__ weights, Weights a, const float *scores, size_t scores_stride, float decay,
-                   float *out, size_t out_stride, uint32_t across)
+                   float *out, size_t out_stride, uint32_t across, bool whole)
 {
-    __shared__ float s_acc[kScoreY][N][33];
+    __shared__ float s_acc[N][kScoreThreads];
     const uint32_t bh = blockIdx.x / across, b = bh / a.heads, h = bh % a.heads;
-    const uint32_t first = (blockIdx.x % across * 32 + threadIdx.x) * N;
+    const uint32_t first = (blockIdx.x % across * blockDim.x + threadIdx.x) * N;
     const uint32_t length = clamp_length(a.lengths, b, a.length), queries = clamp_length(a.counted, b, a.queries);
-    const T *base = weights + size_t(b) * a.batch_stride + size_t(h) * a.group * a.head_stride;
     float acc[N] = {};
     if (first < length && queries > 0) {
-        const bool whole = first + N <= a.length;
-        const uint32_t rows = a.group * queries;
-        uint32_t head = threadIdx.y / queries, query = threadIdx.y % queries;
-        for (uint32_t r = threadIdx.y; r < rows; r += kScoreRows * blockDim.y) {
-            Piece<T, N> v[kScoreRows];
-#pragma unroll
-            for (int i = 0; i < kScoreRows; ++i) {
-                v[i] = zero_piece<T, N>();
-                if (r + i * blockDim.y < rows) {
-                    const T *p = base + size_t(head) * a.head_stride + size_t(query) * a.query_stride + first;
-                    if (whole) {
-                        v[i] = load_piece<T, N>(p);
-                    } else {
-                        for (uint32_t e = 0; first + e < a.length; ++e) v[i].v[e] = p[e];
-                    }
-                }
-                query += blockDim.y;
-                while (query >= queries) query -= queries, ++head;
+        const uint32_t rows = a.group * queries, y = blockDim.y;
+        // from one of this thread's rows to the next: heads, and queries that may carry into one more
+        const uint32_t dq = y % queries;
+        const int64_t step = int64_t(y / queries) * int64_t(a.head_stride) + int64_t(dq) * int64_t(a.query_stride);
+        const int64_t carry = int64_t(a.head_stride) - int64_t(queries) * int64_t(a.query_stride);
+        uint32_t query = threadIdx.y % queries;
+        const T *p = weights + size_t(b) * a.batch_stride +
+                     (size_t(h) * a.group + threadIdx.y / queries) * a.head_stride + size_t(query) * a.query_stride +
+                     first;
+        auto next = [&] {
+            p += step;
+            query += dq;
+            if (query >= queries) {
+                query -= queries;
+                p += carry;
             }
+        };
+        if (first + N <= a.length) {
+            for (uint32_t r = threadIdx.y; r < rows; r += kScoreRows * y) {
+                Piece<T, N> v[kScoreRows];
 #pragma unroll
-            for (int i = 0; i < kScoreRows; ++i)
+                for (int i = 0; i < kScoreRows; ++i) {
+                    v[i] = r + i * y < rows ? load_piece<T, N>(p) : zero_piece<T, N>();
+                    next();
+                }
 #pragma unroll
-                for (int e = 0; e < N; ++e) acc[e] += row_to_float(v[i].v[e]);
+                for (int i = 0; i < kScoreRows; ++i)
+#pragma unroll
+                    for (int e = 0; e < N; ++e) acc[e] += row_to_float(v[i].v[e]);
+            }
+        } else {  // the end of the rows
+            for (uint32_t r = threadIdx.y; r < rows; r += y, next())
+#pragma unroll
+                for (int e = 0; e < N; ++e)
+                    if (first + e < a.length) acc[e] += row_to_float(p[e]);
         }
     }
     if (blockDim.y > 1) {
+        const uint32_t at = threadIdx.y * blockDim.x + threadIdx.x;
 #pragma unroll
-        for (int e = 0; e < N; ++e) s_acc[threadIdx.y][e][threadIdx.x] = acc[e];
+        for (int e = 0; e < N; ++e) s_acc[e][at] = acc[e];
         __syncthreads();
         if (threadIdx.y > 0) return;
         for (uint32_t y = 1; y < blockDim.y; ++y)
 #pragma unroll
-            for (int e = 0; e < N; ++e) acc[e] += s_acc[y][e][threadIdx.x];
+            for (int e = 0; e < N; ++e) acc[e] += s_acc[e][y * blockDim.x + threadIdx.x];
+    }
+    if (first >= a.length) return;
+    const float *from = scores + size_t(bh) * scores_stride + first;
+    float *to = out + size_t(bh) * out_stride + first;
+    if (N >= 4 && whole && first + N <= a.length) {
+#pragma unroll
+        for (int e = 0; e < N; e += 4) {
+            float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (scores && first + e < length) s = *reinterpret_cast<const float4 *>(from + e);
+            float r[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float sum = acc[(e + k) % N];
+                r[k] = first + e + k < length ? scores ? fmaf(decay, r[k], sum) : sum : 0.0f;
+            }
+            *reinterpret_cast<float4 *>(to + e) = make_float4(r[0], r[1], r[2], r[3]);
+        }
+        return;
     }
 #pragma unroll
     for (int e = 0; e < N; ++e) {
-        const uint32_t i = first + e;
-        if (i >= a.length) break;
-        float s = 0.0f;
-        if (i < length) s = scores ? fmaf(decay, scores[size_t(bh) * scores_stride + i], acc[e]) : acc[e];
-        out[size_t(bh) * out_stride + i] = s;
+        if (first + e >= a.length) break;
+        to[e] = first + e < length ? scores ? fmaf(decay, from[e], acc[e]) : acc[e] : 0.0f;
     }
 }
 
 // ---------------------------------------------------------------- eviction
 
-constexpr int kEvictThreads = 512;
+constexpr int kEvictThreads = 1024;
 constexpr int kEvictWarps = kEvictThreads / 32;
 constexpr uint32_t kMaxTeam = 8;
-constexpr int kBins = 2048;
-static_assert(kBins == 4 * kEvictThreads, "four bins to a thread");
-constexpr uint32_t kTile = kEvictThreads * 4;
+constexpr int kBins = 4096;
+static_assert(kBins == 4 * kEvictThreads && kEvictWarps == 32, "four bins to a thread, a lane to a warp");
 
 struct Evict {
     uint32_t batch, heads, length, budget, sinks, recent;
@@ -113,8 +141,8 @@ struct Evict {
 // Ascends with the score; NaN is the least.
 __device__ __forceinline__ uint32_t score_key(float x) { return order_bits(fmaxf(x, -INFINITY)); }
 
-// Exclusive sum over the threads of a CTA; the total to all.
-__device__ __forceinline__ uint32_t cta_scan(uint32_t v, uint32_t &total, uint32_t *s_warp)
+// Exclusive sum over the threads of a CTA.
+__device__ __forceinline__ uint32_t cta_scan(uint32_t v, uint32_t *s_warp)
 {
     const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     uint32_t upto = v;
@@ -126,34 +154,29 @@ __device__ __forceinline__ uint32_t cta_scan(uint32_t v, uint32_t &total, uint32
     __syncthreads();
     if (lane == 31) s_warp[warp] = upto;
     __syncthreads();
-    uint32_t w = lane < kEvictWarps ? s_warp[lane] : 0;
-#pragma unroll
-    for (int o = 1; o < kEvictWarps; o <<= 1) {
-        const uint32_t y = __shfl_up_sync(kFull, w, o);
-        if (lane >= uint32_t(o)) w += y;
-    }
-    total = __shfl_sync(kFull, w, kEvictWarps - 1);
-    const uint32_t before = __shfl_sync(kFull, w, warp ? warp - 1 : 0);
-    return upto - v + (warp ? before : 0);
+    return upto - v + __reduce_add_sync(kFull, lane < warp ? s_warp[lane] : 0u);
 }
 
 struct SelectSmem {
     alignas(16) uint32_t hist[kBins];
-    uint32_t warp[kEvictWarps];
+    uint32_t warp[kEvictWarps], equals[kEvictWarps];
     uint32_t bin, rest;
     uint32_t above, equal;  // this CTA's scores above the cut and at it
 };
 
-// The kept positions of one head of one sequence, by a cluster.  The cut is the
-// score of rank m between the sinks and the recent positions, found by three
-// histograms of the ordered scores' bits, 11, 11 and 10 of them; of the scores
-// at the cut the first are kept.
+// The kept positions of one head of one sequence, by a cluster whose CTAs have
+// a share of its positions each, and whose warps K * 32 neighbouring positions
+// at a time, K to a lane, as ordered bits in registers.  The cut is the score of
+// rank m between the sinks and the recent positions, found by three histograms
+// of those bits, 12, 10 and 10 of them; of the scores at the cut the first are
+// kept.  A share of at most K * 1024 positions is read once.
+template <int K>
 __global__ void __launch_bounds__(kEvictThreads)
 cache_select_kernel(Evict a)
 {
     __shared__ SelectSmem sm;
     const uint32_t team = cluster_size(), rank = cluster_rank();
-    const uint32_t bh = blockIdx.x / team, b = bh / a.heads;
+    const uint32_t bh = blockIdx.x / team, b = bh / a.heads, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t n = clamp_length(a.lengths, b, a.length), kept = min(n, a.budget);
     const float *scores = a.scores + size_t(bh) * a.scores_stride;
     const int32_t *positions = a.positions ? a.positions + size_t(bh) * a.positions_stride : nullptr;
@@ -161,10 +184,10 @@ cache_select_kernel(Evict a)
     float *to_scores = a.kept_scores + size_t(bh) * a.budget;
     int32_t *to_positions = a.kept_positions + size_t(bh) * a.budget;
     chain_start();
-    auto keep = [&](uint32_t slot, uint32_t i, float x) {
+    auto keep = [&](uint32_t slot, uint32_t i) {
         if (slot >= a.budget) return;  // only if the scores change meanwhile
         list[slot] = int32_t(i);
-        to_scores[slot] = x;
+        to_scores[slot] = scores[i];
         to_positions[slot] = positions ? positions[i] : int32_t(i);
     };
     const uint32_t me = rank * kEvictThreads + threadIdx.x, all = team * kEvictThreads;
@@ -174,43 +197,60 @@ cache_select_kernel(Evict a)
         to_positions[slot] = -1;
     }
     if (n <= a.budget) {
-        for (uint32_t i = me; i < n; i += all) keep(i, i, scores[i]);
+        for (uint32_t i = me; i < n; i += all) keep(i, i);
         return;
     }
-    for (uint32_t i = me; i < a.sinks; i += all) keep(i, i, scores[i]);
-    for (uint32_t i = me; i < a.recent; i += all)
-        keep(a.budget - a.recent + i, n - a.recent + i, scores[n - a.recent + i]);
     const uint32_t want = a.budget - a.sinks - a.recent;
-    if (want == 0) return;
 
     // this CTA's part of what lies between
     const uint32_t middle = n - a.recent - a.sinks;
     const uint32_t share = (middle + team - 1) / team;
     const uint32_t first = a.sinks + min(rank * share, middle), end = a.sinks + min((rank + 1) * share, middle);
+    constexpr uint32_t kChunk = K * kEvictThreads;
+    const bool once = end - first <= kChunk;
+    uint32_t key[K];  // 0: no position
+    auto load = [&](uint32_t at) {
+        const uint32_t from = at + warp * (32 * K) + lane;
+#pragma unroll
+        for (int k = 0; k < K; ++k) key[k] = from + 32 * k < end ? score_key(scores[from + 32 * k]) : 0u;
+    };
+    if (once && want > 0) load(first);
+    // while they come
+    for (uint32_t i = me; i < a.sinks; i += all) keep(i, i);
+    for (uint32_t i = me; i < a.recent; i += all) keep(a.budget - a.recent + i, n - a.recent + i);
+    if (want == 0) return;
+
     uint32_t cut = 0, rest = want;  // the cut's bits so far; the scores at or above the cut that are still to be found
     for (int pass = 0; pass < 3; ++pass) {
-        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-        const uint32_t mask = pass == 0 ? 0u : pass == 1 ? 0xffe00000u : 0xfffffc00u;
-        const uint32_t bits = pass == 2 ? 1023u : 2047u;
+        const int shift = pass == 0 ? 20 : pass == 1 ? 10 : 0;
+        const uint32_t mask = pass == 0 ? 0u : pass == 1 ? 0xfff00000u : 0xfffffc00u;
+        const uint32_t bits = pass == 0 ? 4095u : 1023u;
         reinterpret_cast<uint4 *>(sm.hist)[threadIdx.x] = make_uint4(0u, 0u, 0u, 0u);
         __syncthreads();
-        for (uint32_t i = first + threadIdx.x; i < end; i += kEvictThreads) {
-            const uint32_t key = score_key(scores[i]);
-            if ((key & mask) == cut) atomicAdd(&sm.hist[(key >> shift) & bits], 1u);
+        for (uint32_t at = first; at < end; at += kChunk) {
+            if (!once) load(at);
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+                if (key[k] && (key[k] & mask) == cut) atomicAdd(&sm.hist[(key[k] >> shift) & bits], 1u);
         }
         cluster_sync();
         // from the highest bin down: thread i has bins kBins - 1 - 4 i and the three below
-        uint32_t c[4] = {}, sum = 0;
+        uint4 c = make_uint4(0u, 0u, 0u, 0u);
         for (uint32_t q = 0; q < team; ++q) {
             const uint4 h = peer_load4(peer_address(sm.hist + kBins - 4 - 4 * threadIdx.x, q));
-            c[0] += h.w, c[1] += h.z, c[2] += h.y, c[3] += h.x;
+            c.x += h.w, c.y += h.z, c.z += h.y, c.w += h.x;
         }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) sum += c[k];
-        uint32_t total, before = cta_scan(sum, total, sm.warp);
+        const uint32_t sum = c.x + c.y + c.z + c.w;
+        uint32_t before = cta_scan(sum, sm.warp);
         if (before < rest && rest <= before + sum) {
-            int k = 0;
-            while (before + c[k] < rest) before += c[k++];
+            uint32_t k = 0;
+            if (before + c.x < rest) {
+                before += c.x, k = 1;
+                if (before + c.y < rest) {
+                    before += c.y, k = 2;
+                    if (before + c.z < rest) before += c.z, k = 3;
+                }
+            }
             sm.bin = kBins - 1 - (4 * threadIdx.x + k);
             sm.rest = rest - before;
         }
@@ -218,47 +258,58 @@ cache_select_kernel(Evict a)
         cut |= sm.bin << shift;
         rest = sm.rest;
     }
-    // `rest` of the scores at the cut are kept
-    uint32_t above = 0, equal = 0;
-    for (uint32_t i = first + threadIdx.x; i < end; i += kEvictThreads) {
-        const uint32_t key = score_key(scores[i]);
-        above += key > cut;
-        equal += key == cut;
-    }
-    uint32_t total_above, total_equal;
-    cta_scan(above, total_above, sm.warp);
-    cta_scan(equal, total_equal, sm.warp);
-    if (threadIdx.x == 0) sm.above = total_above, sm.equal = total_equal;
-    cluster_sync();
-    uint32_t above_before = 0, equal_before = 0;
-    for (uint32_t q = 0; q < rank; ++q) {
-        above_before += peer_load(peer_address(&sm.above, q));
-        equal_before += peer_load(peer_address(&sm.equal, q));
-    }
-    cluster_sync();
-    for (uint32_t base = first; base < end; base += kTile) {
-        float x[4];
-        uint32_t flags = 0, counts = 0;  // counts: above in the low half, equal in the high
+
+    // `rest` of the scores at the cut are kept: how many of either kind lie before this CTA's
+    uint32_t up = 0, eq = 0;
+    if (team > 1) {
+        uint32_t above = 0, equal = 0;
+        for (uint32_t at = first; at < end; at += kChunk) {
+            if (!once) load(at);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const uint32_t i = base + 4 * threadIdx.x + k;
-            if (i >= end) continue;
-            x[k] = scores[i];
-            const uint32_t key = score_key(x[k]);
-            if (key > cut) flags |= 1u << k, counts += 1u;
-            else if (key == cut) flags |= 16u << k, counts += 1u << 16;
+            for (int k = 0; k < K; ++k) above += key[k] > cut, equal += key[k] == cut;
         }
-        uint32_t total, before = cta_scan(counts, total, sm.warp);
-        uint32_t up = above_before + (before & 0xffffu), eq = equal_before + (before >> 16);
+        above = __reduce_add_sync(kFull, above);
+        equal = __reduce_add_sync(kFull, equal);
+        if (lane == 0) sm.warp[warp] = above, sm.equals[warp] = equal;
+        __syncthreads();
+        if (warp == 0) {
+            above = __reduce_add_sync(kFull, sm.warp[lane]);
+            equal = __reduce_add_sync(kFull, sm.equals[lane]);
+            if (lane == 0) sm.above = above, sm.equal = equal;
+        }
+        cluster_sync();
+        for (uint32_t q = 0; q < rank; ++q) {
+            up += peer_load(peer_address(&sm.above, q));
+            eq += peer_load(peer_address(&sm.equal, q));
+        }
+        cluster_sync();  // nobody looks into another CTA any more
+    }
+    const uint32_t below = (1u << lane) - 1u;
+    for (uint32_t at = first; at < end; at += kChunk) {
+        if (!once) load(at);
+        uint32_t above = 0, equal = 0;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const bool is_above = flags >> k & 1u, is_equal = flags >> k & 16u;
-            if (is_above || (is_equal && eq < rest)) keep(a.sinks + up + min(eq, rest), base + 4 * threadIdx.x + k, x[k]);
-            up += is_above;
-            eq += is_equal;
+        for (int k = 0; k < K; ++k) {
+            above += __popc(__ballot_sync(kFull, key[k] > cut));
+            equal += __popc(__ballot_sync(kFull, key[k] == cut));
         }
-        above_before += total & 0xffffu;
-        equal_before += total >> 16;
+        __syncthreads();
+        if (lane == 0) sm.warp[warp] = above, sm.equals[warp] = equal;
+        __syncthreads();
+        uint32_t my_up = up + __reduce_add_sync(kFull, lane < warp ? sm.warp[lane] : 0u);
+        uint32_t my_eq = eq + __reduce_add_sync(kFull, lane < warp ? sm.equals[lane] : 0u);
+        up += __reduce_add_sync(kFull, sm.warp[lane]);
+        eq += __reduce_add_sync(kFull, sm.equals[lane]);
+        const uint32_t from = at + warp * (32 * K) + lane;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const bool is_above = key[k] > cut, is_equal = key[k] == cut;
+            const uint32_t ma = __ballot_sync(kFull, is_above), me_ = __ballot_sync(kFull, is_equal);
+            const uint32_t e = my_eq + __popc(me_ & below);
+            if (is_above || (is_equal && e < rest)) keep(a.sinks + my_up + __popc(ma & below) + min(e, rest), from + 32 * k);
+            my_up += __popc(ma);
+            my_eq += __popc(me_);
+        }
     }
 }
 
@@ -270,23 +321,27 @@ struct RowArray {
 struct Move {
     RowArray from[2], to[2];    // keys, values
     uint32_t pieces[2];         // of sizeof(P) bytes
-    uint32_t heads, length, budget;
+    uint32_t rows, heads, length, budget, sinks, recent;
     const int32_t *lengths, *list;
 };
 
 constexpr int kMoveThreads = 256;
 constexpr int kMoveAhead = 4;   // rows that a thread has under way
 
-// The kept rows: a row of threads per slot, kMoveAhead slots at a time.
+// The kept rows: a row of threads per slot, kMoveAhead slots at a time.  The
+// last slots of all heads come first: they are the recent positions, which need
+// not wait for the selection.
 template <class P>
 __global__ void __launch_bounds__(kMoveThreads)
 cache_move_kernel(Move a, uint32_t down)
 {
-    chain_wait();
-    const uint32_t bh = blockIdx.x / down, b = bh / a.heads, h = bh % a.heads, w = blockIdx.y;
-    const uint32_t kept = min(clamp_length(a.lengths, b, a.length), a.budget);
-    const uint32_t first = blockIdx.x % down * blockDim.y * kMoveAhead + threadIdx.y;
-    if (first >= kept) return;
+    const uint32_t block = down - 1 - blockIdx.x / a.rows, bh = blockIdx.x % a.rows;
+    const uint32_t b = bh / a.heads, h = bh % a.heads, w = blockIdx.y;
+    const uint32_t n = clamp_length(a.lengths, b, a.length), kept = min(n, a.budget);
+    const uint32_t slots = blockDim.y * kMoveAhead, first = block * slots + threadIdx.y;
+    // slots whose positions are known beforehand: those of the recent ones, of the sinks, and all of a short sequence
+    const bool known = n <= a.budget || block * slots >= a.budget - a.recent || (block + 1) * slots <= a.sinks;
+    if (!known) chain_wait();
     const uint8_t *from = a.from[w].p + size_t(b) * a.from[w].batch + size_t(h) * a.from[w].head;
     uint8_t *to = a.to[w].p + size_t(b) * a.to[w].batch + size_t(h) * a.to[w].head;
     const int32_t *list = a.list + size_t(bh) * a.budget;
@@ -294,7 +349,9 @@ cache_move_kernel(Move a, uint32_t down)
 #pragma unroll
     for (int k = 0; k < kMoveAhead; ++k) {
         const uint32_t slot = first + k * blockDim.y;
-        at[k] = slot < kept ? uint32_t(list[slot]) : ~0u;
+        if (slot >= kept) at[k] = ~0u;
+        else if (!known) at[k] = uint32_t(list[slot]);
+        else at[k] = slot < a.sinks ? slot : slot + (n - kept);
     }
     for (uint32_t c = threadIdx.x; c < a.pieces[w]; c += blockDim.x) {
         P v[kMoveAhead];
@@ -306,6 +363,7 @@ cache_move_kernel(Move a, uint32_t down)
             if (at[k] < a.length)
                 reinterpret_cast<P *>(to + size_t(first + k * blockDim.y) * a.to[w].row)[c] = v[k];
     }
+    if (known) chain_wait();  // the launch is done when both kernels are
 }
 
 template <class P>
@@ -328,10 +386,12 @@ cudaError_t run_score(const void *weights, const Weights &a, uint32_t batch, con
                       float decay, float *out, size_t out_stride, cudaStream_t s)
 {
     uint32_t y = 1;
-    while (y < uint32_t(kScoreY) && size_t(y) * kScoreRows < size_t(a.group) * a.queries) y <<= 1;
-    const uint32_t across = uint32_t(gch::ceil_div(a.length, 32 * N));
-    cache_score_kernel<T, N><<<across * batch * a.heads, dim3(32, y), 0, s>>>(
-        static_cast<const T *>(weights), a, scores, scores_stride, decay, out, out_stride, across);
+    while (y < kScoreY && size_t(y) * kScoreRows < size_t(a.group) * a.queries) y <<= 1;
+    const dim3 block(kScoreThreads / y, y);
+    const uint32_t across = uint32_t(gch::ceil_div(a.length, size_t(block.x) * N));
+    const bool whole = ((uintptr_t(scores) | uintptr_t(out) | 4 * (scores_stride | out_stride)) & 15u) == 0;
+    cache_score_kernel<T, N><<<across * batch * a.heads, block, 0, s>>>(
+        static_cast<const T *>(weights), a, scores, scores_stride, decay, out, out_stride, across, whole);
     return cudaGetLastError();
 }
 
@@ -373,9 +433,11 @@ cudaError_t launch_cache_evict(const gc_cache_rows *keys, const gc_cache_rows *v
     const Evict a{batch, heads, length, budget, sinks, recent, scores, scores_stride, positions, positions_stride,
                   lengths, kept_scores, kept_positions, kept_lengths, reinterpret_cast<int32_t *>(ws)};
     const uint32_t rows = batch * heads;
-    // A cluster per head: more CTAs where heads are few and caches long.
+    // A cluster per head: as many CTAs as read its positions once, 32 to a
+    // thread, and more where all of them still run at a time.
     uint32_t team = 1;
-    while (team < kMaxTeam && size_t(rows) * team * 2 <= size_t(sm_count()) * 4 && length > team * kTile) team *= 2;
+    while (team < kMaxTeam && length > team * 32 * kEvictThreads) team *= 2;
+    while (team < kMaxTeam && size_t(rows) * team * 2 <= kSms && length > team * 4 * kEvictThreads) team *= 2;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(rows * team);
     cfg.blockDim = dim3(kEvictThreads);
@@ -386,7 +448,8 @@ cudaError_t launch_cache_evict(const gc_cache_rows *keys, const gc_cache_rows *v
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, cache_select_kernel, a);
+    cudaError_t e = length <= team * 4 * kEvictThreads ? cudaLaunchKernelEx(&cfg, cache_select_kernel<4>, a)
+                                                       : cudaLaunchKernelEx(&cfg, cache_select_kernel<32>, a);
     if (e != cudaSuccess) return e;
 
     Move m{};
@@ -405,7 +468,7 @@ cudaError_t launch_cache_evict(const gc_cache_rows *keys, const gc_cache_rows *v
         m.to[w] = put(*to[w]);
         m.pieces[w] = uint32_t(from[w]->width * elem);
     }
-    m.heads = heads, m.length = length, m.budget = budget;
+    m.rows = rows, m.heads = heads, m.length = length, m.budget = budget, m.sinks = sinks, m.recent = recent;
     m.lengths = lengths, m.list = a.list;
     switch (piece_elems(bits, 2) * 2) {
     case 2: return run_move<uint16_t>(m, rows, arrays, s);
