@@ -169,8 +169,9 @@ def read_peaks() -> tuple[float, str]:
 # persistent scan, select and partition kernels and their launchers) are all
 # but these: the digit sort, the workspace-free entry point and the row
 # operators build none of them.
-TRAFFIC_SOURCES_EXCLUDED = {"radix.cu", "noalloc.cu", "api_rows.cu", "embedding.cu", "experts.cu", "sample.cu", "route.cu", "verify.cu", "cache.cu",
-                            "gc_binsort.cuh", "gc_rows.cuh", "gc_rows_internal.h"}
+TRAFFIC_SOURCES_EXCLUDED = {"radix.cu", "noalloc.cu", "api_rows.cu", "embedding.cu", "experts.cu", "sample.cu",
+                            "route.cu", "route_grad.cu", "verify.cu", "cache.cu", "gc_binsort.cuh", "gc_route.cuh",
+                            "gc_rows.cuh", "gc_rows_internal.h"}
 
 
 def kernel_source_hash() -> str:

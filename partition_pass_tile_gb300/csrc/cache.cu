@@ -135,7 +135,9 @@ struct Evict {
     const int32_t *lengths;     // NULL: all `length`
     float *kept_scores;
     int32_t *kept_positions, *kept_lengths;
-    int32_t *list;              // workspace: [batch * heads][budget] kept indices
+    int32_t *list;              // workspace: [batch * heads][budget], the positions kept for their scores
+
+    __host__ __device__ __forceinline__ uint32_t rows() const { return batch * heads; }
 };
 
 // Ascends with the score; NaN is the least.
@@ -179,27 +181,10 @@ cache_select_kernel(Evict a)
     const uint32_t bh = blockIdx.x / team, b = bh / a.heads, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t n = clamp_length(a.lengths, b, a.length), kept = min(n, a.budget);
     const float *scores = a.scores + size_t(bh) * a.scores_stride;
-    const int32_t *positions = a.positions ? a.positions + size_t(bh) * a.positions_stride : nullptr;
     int32_t *list = a.list + size_t(bh) * a.budget;
-    float *to_scores = a.kept_scores + size_t(bh) * a.budget;
-    int32_t *to_positions = a.kept_positions + size_t(bh) * a.budget;
     chain_start();
-    auto keep = [&](uint32_t slot, uint32_t i) {
-        if (slot >= a.budget) return;  // only if the scores change meanwhile
-        list[slot] = int32_t(i);
-        to_scores[slot] = scores[i];
-        to_positions[slot] = positions ? positions[i] : int32_t(i);
-    };
-    const uint32_t me = rank * kEvictThreads + threadIdx.x, all = team * kEvictThreads;
-    if (bh % a.heads == 0 && me == 0) a.kept_lengths[b] = int32_t(kept);
-    for (uint32_t slot = kept + me; slot < a.budget; slot += all) {
-        to_scores[slot] = 0.0f;
-        to_positions[slot] = -1;
-    }
-    if (n <= a.budget) {
-        for (uint32_t i = me; i < n; i += all) keep(i, i);
-        return;
-    }
+    if (bh % a.heads == 0 && rank == 0 && threadIdx.x == 0) a.kept_lengths[b] = int32_t(kept);
+    if (n <= a.budget) return;
     const uint32_t want = a.budget - a.sinks - a.recent;
 
     // this CTA's part of what lies between
@@ -214,11 +199,8 @@ cache_select_kernel(Evict a)
 #pragma unroll
         for (int k = 0; k < K; ++k) key[k] = from + 32 * k < end ? score_key(scores[from + 32 * k]) : 0u;
     };
-    if (once && want > 0) load(first);
-    // while they come
-    for (uint32_t i = me; i < a.sinks; i += all) keep(i, i);
-    for (uint32_t i = me; i < a.recent; i += all) keep(a.budget - a.recent + i, n - a.recent + i);
     if (want == 0) return;
+    if (once) load(first);
 
     uint32_t cut = 0, rest = want;  // the cut's bits so far; the scores at or above the cut that are still to be found
     for (int pass = 0; pass < 3; ++pass) {
@@ -306,7 +288,10 @@ cache_select_kernel(Evict a)
             const bool is_above = key[k] > cut, is_equal = key[k] == cut;
             const uint32_t ma = __ballot_sync(kFull, is_above), me_ = __ballot_sync(kFull, is_equal);
             const uint32_t e = my_eq + __popc(me_ & below);
-            if (is_above || (is_equal && e < rest)) keep(a.sinks + my_up + __popc(ma & below) + min(e, rest), from + 32 * k);
+            if (is_above || (is_equal && e < rest)) {
+                const uint32_t slot = a.sinks + my_up + __popc(ma & below) + min(e, rest);
+                if (slot < a.budget) list[slot] = int32_t(from + 32 * k);  // beyond it only if the scores change meanwhile
+            }
             my_up += __popc(ma);
             my_eq += __popc(me_);
         }
@@ -321,8 +306,7 @@ struct RowArray {
 struct Move {
     RowArray from[2], to[2];    // keys, values
     uint32_t pieces[2];         // of sizeof(P) bytes
-    uint32_t rows, heads, length, budget, sinks, recent;
-    const int32_t *lengths, *list;
+    uint32_t arrays;
 };
 
 constexpr int kMoveThreads = 256;
@@ -333,52 +317,70 @@ constexpr int kMoveAhead = 4;   // rows that a thread has under way
 // not wait for the selection.
 template <class P>
 __global__ void __launch_bounds__(kMoveThreads)
-cache_move_kernel(Move a, uint32_t down)
+cache_move_kernel(Evict a, Move m, uint32_t down)
 {
-    const uint32_t block = down - 1 - blockIdx.x / a.rows, bh = blockIdx.x % a.rows;
+    const uint32_t block = down - 1 - blockIdx.x / a.rows(), bh = blockIdx.x % a.rows();
     const uint32_t b = bh / a.heads, h = bh % a.heads, w = blockIdx.y;
     const uint32_t n = clamp_length(a.lengths, b, a.length), kept = min(n, a.budget);
     const uint32_t slots = blockDim.y * kMoveAhead, first = block * slots + threadIdx.y;
     // slots whose positions are known beforehand: those of the recent ones, of the sinks, and all of a short sequence
     const bool known = n <= a.budget || block * slots >= a.budget - a.recent || (block + 1) * slots <= a.sinks;
     if (!known) chain_wait();
-    const uint8_t *from = a.from[w].p + size_t(b) * a.from[w].batch + size_t(h) * a.from[w].head;
-    uint8_t *to = a.to[w].p + size_t(b) * a.to[w].batch + size_t(h) * a.to[w].head;
     const int32_t *list = a.list + size_t(bh) * a.budget;
+    // the position of a slot, or a.length
+    auto position = [&](uint32_t slot) {
+        if (slot >= kept) return a.length;
+        if (slot < a.sinks || n <= a.budget) return slot;
+        if (slot >= a.budget - a.recent) return slot + (n - a.budget);
+        return min(uint32_t(list[slot]), a.length);
+    };
+    if (w == m.arrays) {  // scores and positions, a thread to a slot
+        const uint32_t me = threadIdx.y * blockDim.x + threadIdx.x, slot = block * slots + me;
+        if (me < slots && slot < a.budget) {
+            const uint32_t i = position(slot);
+            float score = 0.0f;
+            int32_t at = -1;
+            if (i < a.length) {
+                score = a.scores[size_t(bh) * a.scores_stride + i];
+                at = a.positions ? a.positions[size_t(bh) * a.positions_stride + i] : int32_t(i);
+            }
+            a.kept_scores[size_t(bh) * a.budget + slot] = score;
+            a.kept_positions[size_t(bh) * a.budget + slot] = at;
+        }
+        if (known) chain_wait();
+        return;
+    }
+    const uint8_t *from = m.from[w].p + size_t(b) * m.from[w].batch + size_t(h) * m.from[w].head;
+    uint8_t *to = m.to[w].p + size_t(b) * m.to[w].batch + size_t(h) * m.to[w].head;
     uint32_t at[kMoveAhead];
 #pragma unroll
-    for (int k = 0; k < kMoveAhead; ++k) {
-        const uint32_t slot = first + k * blockDim.y;
-        if (slot >= kept) at[k] = ~0u;
-        else if (!known) at[k] = uint32_t(list[slot]);
-        else at[k] = slot < a.sinks ? slot : slot + (n - kept);
-    }
-    for (uint32_t c = threadIdx.x; c < a.pieces[w]; c += blockDim.x) {
+    for (int k = 0; k < kMoveAhead; ++k) at[k] = position(first + k * blockDim.y);
+    for (uint32_t c = threadIdx.x; c < m.pieces[w]; c += blockDim.x) {
         P v[kMoveAhead];
 #pragma unroll
         for (int k = 0; k < kMoveAhead; ++k)
-            if (at[k] < a.length) v[k] = reinterpret_cast<const P *>(from + size_t(at[k]) * a.from[w].row)[c];
+            if (at[k] < a.length) v[k] = reinterpret_cast<const P *>(from + size_t(at[k]) * m.from[w].row)[c];
 #pragma unroll
         for (int k = 0; k < kMoveAhead; ++k)
             if (at[k] < a.length)
-                reinterpret_cast<P *>(to + size_t(first + k * blockDim.y) * a.to[w].row)[c] = v[k];
+                reinterpret_cast<P *>(to + size_t(first + k * blockDim.y) * m.to[w].row)[c] = v[k];
     }
     if (known) chain_wait();  // the launch is done when both kernels are
 }
 
 template <class P>
-cudaError_t run_move(Move a, uint32_t rows, uint32_t arrays, cudaStream_t s)
+cudaError_t run_move(const Evict &a, Move m, cudaStream_t s)
 {
     uint32_t most = 1;
-    for (uint32_t w = 0; w < arrays; ++w) {
-        a.pieces[w] /= sizeof(P);
-        most = a.pieces[w] > most ? a.pieces[w] : most;
+    for (uint32_t w = 0; w < m.arrays; ++w) {
+        m.pieces[w] /= sizeof(P);
+        most = m.pieces[w] > most ? m.pieces[w] : most;
     }
-    uint32_t tx = 1;
+    uint32_t tx = kMoveAhead;  // so that a block has a thread to a slot
     while (tx < kMoveThreads && tx < most) tx <<= 1;
     const dim3 block(tx, kMoveThreads / tx);
     const uint32_t down = uint32_t(gch::ceil_div(a.budget, block.y * kMoveAhead));
-    return gch::launch_next(cache_move_kernel<P>, dim3(down * rows, arrays), block, 0, s, a, down);
+    return gch::launch_next(cache_move_kernel<P>, dim3(down * a.batch * a.heads, m.arrays + 1), block, 0, s, a, m, down);
 }
 
 template <class T, int N>
@@ -454,7 +456,7 @@ cudaError_t launch_cache_evict(const gc_cache_rows *keys, const gc_cache_rows *v
 
     Move m{};
     const size_t elem = dt == GC_ROW_F32 ? 4 : 2;
-    const uint32_t arrays = values ? 2 : 1;
+    const uint32_t arrays = m.arrays = values ? 2 : 1;
     uint64_t bits = 0;
     const gc_cache_rows *from[2] = {keys, values}, *to[2] = {kept_keys, kept_values};
     for (uint32_t w = 0; w < arrays; ++w) {
@@ -468,13 +470,11 @@ cudaError_t launch_cache_evict(const gc_cache_rows *keys, const gc_cache_rows *v
         m.to[w] = put(*to[w]);
         m.pieces[w] = uint32_t(from[w]->width * elem);
     }
-    m.rows = rows, m.heads = heads, m.length = length, m.budget = budget, m.sinks = sinks, m.recent = recent;
-    m.lengths = lengths, m.list = a.list;
     switch (piece_elems(bits, 2) * 2) {
-    case 2: return run_move<uint16_t>(m, rows, arrays, s);
-    case 4: return run_move<uint32_t>(m, rows, arrays, s);
-    case 8: return run_move<uint2>(m, rows, arrays, s);
-    default: return run_move<uint4>(m, rows, arrays, s);
+    case 2: return run_move<uint16_t>(a, m, s);
+    case 4: return run_move<uint32_t>(a, m, s);
+    case 8: return run_move<uint2>(a, m, s);
+    default: return run_move<uint4>(a, m, s);
     }
 }
 

@@ -5,6 +5,7 @@
 #pragma once
 
 #include <cstdint>
+#include <type_traits>
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -91,6 +92,26 @@ __device__ __forceinline__ float pow2(float x)
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// The largest value of a piece; NaN counts for nothing.
+template <class T, int N>
+__device__ __forceinline__ float piece_max(const Piece<T, N> &p)
+{
+    if constexpr (sizeof(T) == 4) {
+        float r = p.v[0];
+#pragma unroll
+        for (int e = 1; e < N; ++e) r = fmaxf(r, p.v[e]);
+        return r;
+    } else {
+        // two at a time
+        using Pair = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
+        const Pair *q = reinterpret_cast<const Pair *>(p.v);
+        Pair r = q[0];
+#pragma unroll
+        for (int e = 1; e < N / 2; ++e) r = __hmax2(r, q[e]);
+        return fmaxf(row_to_float(T(r.x)), row_to_float(T(r.y)));
+    }
 }
 
 // Id i of an int32 or int64 array; any value outside [0, limit) becomes limit

@@ -100,26 +100,6 @@ struct Scale {
 // A sum of weights in units of 2^-40.
 __device__ __forceinline__ float from_fixed(uint64_t units) { return __ull2float_rn(units) * (1.0f / kFixed); }
 
-// The largest value of a piece; NaN counts for nothing.
-template <class T, int N>
-__device__ __forceinline__ float piece_max(const Piece<T, N> &p)
-{
-    if constexpr (sizeof(T) == 4) {
-        float r = p.v[0];
-#pragma unroll
-        for (int e = 1; e < N; ++e) r = fmaxf(r, p.v[e]);
-        return r;
-    } else {
-        // two at a time
-        using Pair = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
-        const Pair *q = reinterpret_cast<const Pair *>(p.v);
-        Pair r = q[0];
-#pragma unroll
-        for (int e = 1; e < N / 2; ++e) r = __hmax2(r, q[e]);
-        return fmaxf(row_to_float(T(r.x)), row_to_float(T(r.y)));
-    }
-}
-
 // A key to find the largest of and a weight to add up, reduced together.
 struct KeySum {
     uint64_t key;

@@ -15,6 +15,10 @@
 // then by sequence: where there are more than the GPU holds at a time, the
 // last chunk of a position decides it, and chunks of later positions of a
 // sequence that has stopped are not read.
+//
+// exp((x - m) / T) is 2^(x f - c) with f = log2(e) / T and c = m f rounded: one
+// multiply-add, whose only rounding is that of the exponent, since every weight
+// of a row carries the same 2^(m f - c) and p is a quotient of them.
 #include "gc_rows.cuh"
 #include "gc_rows_internal.h"
 
@@ -24,10 +28,15 @@ using namespace gcd;
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kBatch = 4;             // pieces of 16 bytes that a thread has under way
+constexpr int kBatch = 8;             // pieces of 16 bytes that a thread has under way
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr float kLargest = 3.402823466e38f;
 constexpr float kUniformLo = 0x1p-25f, kUniformHi = 1.0f - 0x1p-24f;
+
+// Chunks: 16 pieces per thread, 64 KB, where that makes more CTAs than the
+// GPU holds, else fewer.
+constexpr uint32_t kDrawWave = 4;          // CTAs per SM of the draw
+constexpr uint32_t kSteps = 16, kWave = 4;  // kWave: CTAs per SM
 
 // z = (x - m) / t as a power of two's exponent.
 __device__ __forceinline__ float power_of(float t)
@@ -63,7 +72,8 @@ struct Verify {
     Part *x_part, *d_part;      // [row][chunk]
     unsigned long long *best;   // per sequence: the draw so far
     uint32_t *drawn;            // per sequence: chunks that have drawn
-    uint32_t *stop, *arrived;   // per sequence: first rejected position; per position: chunks done; NULL: not kept
+    uint32_t *left, *arrived;   // per sequence: drafts from the first rejected one on; per position: chunks done; NULL: not kept
+    uint32_t draw, draws;       // pieces in a chunk of the draw, chunks
 
     // without random numbers every sequence is greedy
     __device__ __forceinline__ float t(uint32_t b) const
@@ -95,20 +105,41 @@ struct Pieces {
     }
 };
 
-__device__ __forceinline__ float batch_weight(float x, float m, float power)
+// Whether c = m * power can be taken off by a multiply-add.
+__device__ __forceinline__ bool plain(float c) { return fabsf(c) < 0x1p100f; }
+
+// The weight of a logit by a maximum, of any values.
+__device__ __forceinline__ float weight(float x, float m, float power)
 {
-    // NaN weighs nothing, +inf as much as the largest value
-    return pow2(fminf(fmaxf((sample_value(x) - m) * power, -INFINITY), 0.0f));
+    x = sample_value(x);
+    const float c = m * power;
+    return pow2(plain(c) ? fmaf(x, power, -c) : (x - m) * power);
 }
 
 // m and sum joined with another maximum and sum.
 __device__ __forceinline__ void join(float &m, float &sum, float m2, float sum2, float power)
 {
     const float top = fmaxf(m, m2);
+    if (!(top > -INFINITY)) return;
+    auto scale = [&](float from) {
+        const float c = from * power, d = top * power;
+        return pow2(plain(c) && plain(d) ? c - d : (from - top) * power);
+    };
+    sum = (m == top ? sum : sum * scale(m)) + (m2 == top ? sum2 : sum2 * scale(m2));
+    m = top;
+}
+
+// m and sum of all lanes, to all of them.
+__device__ __forceinline__ void join_lanes(float &m, float &sum, float power)
+{
+    const uint32_t bits = __reduce_max_sync(kFull, order_bits(m));
+    float top = order_value(bits), s = 0.0f;
     if (top > -INFINITY) {
-        sum = sum * pow2((m - top) * power) + sum2 * pow2((m2 - top) * power);
-        m = top;
+        join(top, s, m, sum, power);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
     }
+    m = top, sum = s;
 }
 
 // A chunk's maximum and sum, to lane 0 of warp 0.
@@ -125,51 +156,49 @@ __device__ __forceinline__ Part chunk_sum(const Pieces<T> &row, uint32_t first, 
             sum = m > -INFINITY ? 1.0f : 0.0f;
         }
     }
-    for (uint32_t base = first + threadIdx.x; base < end; base += kBatch * kThreads) {
-        Piece<T, kVec> v[kBatch];
-#pragma unroll
-        for (int q = 0; q < kBatch; ++q) {
-            const uint32_t j = base + q * kThreads;
-            if (j < end) {
-                v[q] = load_piece<T, kVec>(row.x + row.head + size_t(j) * kVec);
-            } else {
-#pragma unroll
-                for (uint32_t e = 0; e < kVec; ++e) v[q].v[e] = row_from_float<T>(-INFINITY);
-            }
-        }
+    auto add = [&](const Piece<T, kVec> *v, auto count) {
+        constexpr int kCount = decltype(count)::value;
         float top = m;
 #pragma unroll
-        for (int q = 0; q < kBatch; ++q)
-#pragma unroll
-            for (uint32_t e = 0; e < kVec; ++e) top = fmaxf(top, row_to_float(v[q].v[e]));
+        for (int q = 0; q < kCount; ++q) top = fmaxf(top, piece_max(v[q]));
         top = fminf(top, kLargest);
-        if (!(top > -INFINITY)) continue;
+        if (!(top > -INFINITY)) return;
+        const float c = top * power;
         float more = 0.0f;
 #pragma unroll
-        for (int q = 0; q < kBatch; ++q)
+        for (int q = 0; q < kCount; ++q)
 #pragma unroll
-            for (uint32_t e = 0; e < kVec; ++e) more += pow2((row_to_float(v[q].v[e]) - top) * power);
-        if (!(more <= float(kBatch * kVec))) {  // a NaN or an infinity
+            for (uint32_t e = 0; e < kVec; ++e) more += pow2(fmaf(row_to_float(v[q].v[e]), power, -c));
+        if (!(more <= 1.5f * kCount * kVec) || !plain(c)) {  // a NaN or an infinity among them
             more = 0.0f;
 #pragma unroll
-            for (int q = 0; q < kBatch; ++q)
+            for (int q = 0; q < kCount; ++q)
 #pragma unroll
-                for (uint32_t e = 0; e < kVec; ++e) more += batch_weight(row_to_float(v[q].v[e]), top, power);
+                for (uint32_t e = 0; e < kVec; ++e) more += weight(row_to_float(v[q].v[e]), top, power);
         }
-        sum = (m > -INFINITY ? sum * pow2((m - top) * power) : 0.0f) + more;
-        m = top;
-    }
+        join(m, sum, top, more, power);
+    };
+    uint32_t j = first + threadIdx.x;
+    const T *from = row.x + row.head;
+    for (; j + (kBatch - 1) * kThreads < end; j += kBatch * kThreads) {
+        Piece<T, kVec> v[kBatch];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) join(m, sum, __shfl_xor_sync(kFull, m, o), __shfl_xor_sync(kFull, sum, o), power);
+        for (int q = 0; q < kBatch; ++q) v[q] = load_piece<T, kVec>(from + size_t(j + q * kThreads) * kVec);
+        add(v, std::integral_constant<int, kBatch>());
+    }
+    for (; j < end; j += kThreads) {
+        const Piece<T, kVec> v = load_piece<T, kVec>(from + size_t(j) * kVec);
+        add(&v, std::integral_constant<int, 1>());
+    }
+    join_lanes(m, sum, power);
     Part p;
     p.m = m, p.sum = sum;
     if ((threadIdx.x & 31) == 0) s_part[threadIdx.x >> 5] = p;
     __syncthreads();
-    if (threadIdx.x < kWarps) {
-        m = s_part[threadIdx.x].m, sum = s_part[threadIdx.x].sum;
-#pragma unroll
-        for (int o = kWarps / 2; o > 0; o >>= 1)
-            join(m, sum, __shfl_xor_sync(0xffu, m, o), __shfl_xor_sync(0xffu, sum, o), power);
+    if (threadIdx.x < 32) {
+        const bool has = threadIdx.x < kWarps;
+        m = has ? s_part[threadIdx.x].m : -INFINITY, sum = has ? s_part[threadIdx.x].sum : 0.0f;
+        join_lanes(m, sum, power);
         p.m = m, p.sum = sum;
     }
     return p;
@@ -186,15 +215,16 @@ __device__ __forceinline__ Part chunk_first(const Pieces<T> &row, uint32_t first
         const uint32_t i = row.single(threadIdx.x);
         if (i < row.vocab) key = first_key(sample_value(row_to_float(row.x[i])), i);
     }
-    for (uint32_t base = first + threadIdx.x; base < end; base += kBatch * kThreads) {
-        Piece<T, kVec> v[kBatch];
+    constexpr int kAhead = kBatch / 2;
+    for (uint32_t base = first + threadIdx.x; base < end; base += kAhead * kThreads) {
+        Piece<T, kVec> v[kAhead];
 #pragma unroll
-        for (int q = 0; q < kBatch; ++q) {
+        for (int q = 0; q < kAhead; ++q) {
             const uint32_t j = base + q * kThreads;
             if (j < end) v[q] = load_piece<T, kVec>(row.x + row.head + size_t(j) * kVec);
         }
 #pragma unroll
-        for (int q = 0; q < kBatch; ++q) {
+        for (int q = 0; q < kAhead; ++q) {
             const uint32_t j = base + q * kThreads;
             if (j >= end) continue;
 #pragma unroll
@@ -248,8 +278,7 @@ __device__ __forceinline__ Part row_part(const Part *parts, uint32_t chunks, boo
         p.key = __ldcg(reinterpret_cast<const unsigned long long *>(parts + c));
         join(m, sum, p.m, p.sum, power);
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) join(m, sum, __shfl_xor_sync(kFull, m, o), __shfl_xor_sync(kFull, sum, o), power);
+    join_lanes(m, sum, power);
     r.m = m, r.sum = sum;
     return r;
 }
@@ -270,12 +299,12 @@ __device__ __forceinline__ bool decide(const Verify &a, uint32_t b, uint32_t j, 
     if (greedy) return uint32_t(target.key >> 32) > order_bits(-INFINITY) && uint32_t(~target.key) == id;
     const T *x = static_cast<const T *>(a.x) + row * a.x_stride;
     // u q < p, with p = w / sum: in 64 bits, where the products are exact enough
-    const double wp = batch_weight(row_to_float(x[id]), target.m, power);
+    const double wp = weight(row_to_float(x[id]), target.m, power);
     double wq = 1.0;
     if (a.d) {
         draft = row_part(a.d_part + at * a.chunks, a.chunks, false, power);
         const T *d = static_cast<const T *>(a.d) + at * a.d_stride;
-        wq = draft.sum > 0.0f ? batch_weight(row_to_float(d[id]), draft.m, power) : 0.0f;
+        wq = draft.sum > 0.0f ? weight(row_to_float(d[id]), draft.m, power) : 0.0f;
     }
     const double u = fminf(fmaxf(a.accept[at], kUniformLo), kUniformHi);
     return target.sum > 0.0f && u * wq * double(target.sum) < wp * (draft.sum > 0.0f ? double(draft.sum) : 1.0);
@@ -283,7 +312,7 @@ __device__ __forceinline__ bool decide(const Verify &a, uint32_t b, uint32_t j, 
 
 // One chunk of one row.
 template <class T>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kWave)
 verify_rows_kernel(Verify a)
 {
     __shared__ Part s_part[kWarps];
@@ -300,18 +329,22 @@ verify_rows_kernel(Verify a)
         unit /= kinds;
     }
     const uint32_t b = unit;
-    if (a.stop && *reinterpret_cast<volatile uint32_t *>(a.stop + b) < j) return;
-    if (j == 0 && kind == 0 && c == 0 && threadIdx.x == 0) {
-        a.best[b] = 0;
-        a.drawn[b] = 0;
+    const int32_t *ids = a.ids + size_t(b) * a.drafts;
+    if (a.left == nullptr) {
+        if (j == 0 && kind == 0 && c == 0 && threadIdx.x == 0) {
+            a.best[b] = 0;
+            a.drawn[b] = 0;
+        }
+    } else if (*reinterpret_cast<volatile uint32_t *>(a.left + b) > a.drafts - j) {
+        return;
     }
     const float t = a.t(b), power = power_of(t);
     const bool greedy = !(t > 0.0f);
     if (kind == 1 && greedy) return;
     // a position past the first drafted token that is none is not reached
-    const int32_t *ids = a.ids + size_t(b) * a.drafts;
-    for (uint32_t i = 0; i < j + kind; ++i)
-        if (!a.real(uint32_t(ids[i]))) return;
+    bool none = false;
+    for (uint32_t i = threadIdx.x & 31; i < j + kind; i += 32) none |= !a.real(uint32_t(ids[i]));
+    if (__any_sync(kFull, none)) return;
 
     const T *x = kind == 0 ? static_cast<const T *>(a.x) + (size_t(b) * (a.drafts + 1) + j) * a.x_stride
                            : static_cast<const T *>(a.d) + (size_t(b) * a.drafts + j) * a.d_stride;
@@ -322,7 +355,7 @@ verify_rows_kernel(Verify a)
     Part *to = kind == 0 ? a.x_part + (size_t(b) * (a.drafts + 1) + j) * a.chunks + c
                          : a.d_part + (size_t(b) * a.drafts + j) * a.chunks + c;
     if (threadIdx.x == 0) to->key = p.key;
-    if (a.stop == nullptr || j == a.drafts || threadIdx.x >= 32) return;
+    if (a.left == nullptr || j == a.drafts || threadIdx.x >= 32) return;
     uint32_t before = 0;
     if (threadIdx.x == 0) {
         __threadfence();
@@ -330,22 +363,37 @@ verify_rows_kernel(Verify a)
         __threadfence();
     }
     before = __shfl_sync(kFull, before, 0);
-    const bool none = !a.real(uint32_t(ids[j]));  // then the draft's row is not read
+    none = !a.real(uint32_t(ids[j]));  // then the draft's row is not read
     if (before + 1 != a.chunks * (greedy || none ? 1 : kinds)) return;
     Part target, draft;
-    if (!decide<T>(a, b, j, target, draft) && threadIdx.x == 0) atomicMin(a.stop + b, j);
+    if (!decide<T>(a, b, j, target, draft) && threadIdx.x == 0) atomicMax(a.left + b, a.drafts - j);
 }
 
 // Of the tokens offered, the largest r / -log v; equal ones, the lowest index.
+// A token can only be it if -log v < r / bound for any ratio `bound` already
+// seen, so v > 1 - r / bound: one multiply-add spares most tokens the logarithm.
 struct Best {
     float ratio = 0.0f;
     uint32_t index = ~0u;
+    float bound = 0.0f, slope = -kLargest;  // bound: the warp's; slope: -1 / bound and a little more
+    __device__ __forceinline__ bool open(float r, float v) const { return !(v < fmaf(r, slope, 0.9999995f)); }
     __device__ __forceinline__ void take(float r, float v, uint32_t i)
     {
+        if (!(r > 0.0f)) return;
         const float q = r / -logf(fminf(fmaxf(v, kUniformLo), kUniformHi));
         if (q > ratio || (q == ratio && i < index)) {
             ratio = q;
             index = i;
+        }
+    }
+    // All lanes together: the bound of the warp.  Ratios are not negative, so
+    // their bits are in order.
+    __device__ __forceinline__ void share()
+    {
+        const float b = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(ratio)));
+        if (b > bound) {
+            bound = b;
+            slope = -1.000001f / b;
         }
     }
     __device__ __forceinline__ uint64_t key() const
@@ -359,38 +407,49 @@ template <class T>
 struct Stop {
     const T *x, *d;     // d: NULL where nothing is taken off
     const float *u;
-    float m, inverse, dm, dinverse, power;
+    float m, inverse, dm, dinverse, power, c, dc;
     uint32_t without;   // a token that cannot be drawn
+    bool usual;         // multiply-adds do: no infinities
 
-    __device__ __forceinline__ float p(float v) const { return batch_weight(v, m, power) * inverse; }
-    __device__ __forceinline__ float q(float v) const { return batch_weight(v, dm, power) * dinverse; }
+    // p - q.  A NaN of the draft weighs nothing; one of the target makes a NaN,
+    // which is never taken.
+    __device__ __forceinline__ float r(float v, float w) const
+    {
+        float p, q;
+        if (usual) {
+            p = pow2(__fmaf_rn(v, power, -c));
+            q = pow2(__fmaf_rn(w, power, -dc));
+        } else {
+            p = weight(v, m, power);
+            q = weight(w, dm, power);
+        }
+        return __fmaf_rn(fmaxf(q, 0.0f), -dinverse, __fmul_rn(p, inverse));
+    }
     __device__ __forceinline__ float r(uint32_t i) const
     {
-        float w = p(row_to_float(x[i]));
-        if (d) w = fmaxf(w - q(row_to_float(d[i])), 0.0f);
-        return i == without ? 0.0f : w;
+        return r(row_to_float(x[i]), d ? row_to_float(d[i]) : -INFINITY);
     }
 };
 
+// A piece of the three rows on its way.
 template <class T>
-__device__ __forceinline__ Best chunk_draw(const Stop<T> &s, const Pieces<T> &row, uint32_t first, uint32_t end,
-                                           bool singles)
-{
-    constexpr uint32_t kVec = Pieces<T>::kVec;
-    Best best;
-    if (singles) {
-        const uint32_t i = row.single(threadIdx.x);
-        if (i < row.vocab) best.take(s.r(i), s.u[i], i);
-    }
-    const bool d_whole = s.d && ((reinterpret_cast<uintptr_t>(s.d + row.head)) & 15u) == 0;
-    const bool u_whole = ((reinterpret_cast<uintptr_t>(s.u + row.head)) & 15u) == 0;
-    for (uint32_t base = first; base < end; base += kThreads) {
-        const uint32_t j = base + threadIdx.x;
-        if (j >= end) break;
-        const uint32_t i = row.head + j * kVec;
-        const Piece<T, kVec> v = load_piece<T, kVec>(row.x + i);
-        Piece<T, kVec> w;
-        float u[kVec];
+struct DrawPiece {
+    static constexpr uint32_t kVec = 16 / sizeof(T);
+    Piece<T, kVec> v, w;
+    float u[kVec];
+
+    __device__ __forceinline__ void load(const Stop<T> &s, uint32_t i, bool there, bool d_whole, bool u_whole)
+    {
+#pragma unroll
+        for (uint32_t e = 0; e < kVec; ++e) {
+            w.v[e] = row_from_float<T>(-INFINITY);
+            u[e] = 0.0f;
+        }
+        if (!there) {  // weights and numbers that cannot win
+            v = w;
+            return;
+        }
+        v = load_piece<T, kVec>(s.x + i);
         if (d_whole) {
             w = load_piece<T, kVec>(s.d + i);
         } else if (s.d) {
@@ -400,19 +459,60 @@ __device__ __forceinline__ Best chunk_draw(const Stop<T> &s, const Pieces<T> &ro
 #pragma unroll
         for (uint32_t e = 0; e < kVec; e += 4) {
             if (u_whole) {
-                const float4 f = __ldcs(reinterpret_cast<const float4 *>(s.u + i + e));
+                const float4 f = *reinterpret_cast<const float4 *>(s.u + i + e);
                 u[e] = f.x, u[e + 1] = f.y, u[e + 2] = f.z, u[e + 3] = f.w;
             } else {
 #pragma unroll
-                for (uint32_t k = e; k < e + 4; ++k) u[k] = __ldcs(s.u + i + k);
+                for (uint32_t k = e; k < e + 4; ++k) u[k] = s.u[i + k];
             }
         }
+    }
+};
+
+// Every thread of the CTA takes part.  Tokens that can win are few, and are
+// read once more, so that their code is there once.
+template <class T>
+__device__ __forceinline__ Best chunk_draw(const Stop<T> &s, const Pieces<T> &row, uint32_t first, uint32_t end,
+                                           bool singles)
+{
+    constexpr uint32_t kVec = Pieces<T>::kVec;
+    Best best;
+    const bool d_whole = s.d && ((reinterpret_cast<uintptr_t>(s.d + row.head)) & 15u) == 0;
+    const bool u_whole = ((reinterpret_cast<uintptr_t>(s.u + row.head)) & 15u) == 0;
+    DrawPiece<T> next;
+    uint32_t lone = singles ? row.single(threadIdx.x) : row.vocab;
+    next.load(s, row.head + (first + threadIdx.x) * kVec, first + threadIdx.x < end, d_whole, u_whole);
+    for (uint32_t base = first;; base += kThreads) {
+        const DrawPiece<T> now = next;
+        const uint32_t j = base + threadIdx.x, i = row.head + j * kVec;
+        next.load(s, i + kThreads * kVec, j + kThreads < end, d_whole, u_whole);
+        float r[kVec];
+        uint32_t which = 0;
 #pragma unroll
-        for (uint32_t e = 0; e < kVec; ++e) {
-            float r = s.p(row_to_float(v.v[e]));
-            if (s.d) r = fmaxf(r - s.q(row_to_float(w.v[e])), 0.0f);
-            if (r > 0.0f && i + e != s.without) best.take(r, u[e], i + e);
+        for (uint32_t e = 0; e < kVec; ++e) r[e] = s.r(row_to_float(now.v.v[e]), row_to_float(now.w.v[e]));
+        if (best.bound == 0.0f) {  // in the whole warp
+            // a first bound by each thread's largest r, and its single element
+            float top = 0.0f;
+            uint32_t highest = row.vocab;
+#pragma unroll
+            for (uint32_t e = 0; e < kVec; ++e)
+                if (r[e] > top) top = r[e], highest = i + e;
+            for (int k = 0; k < 2; ++k) {
+                const uint32_t t = k == 0 ? lone : highest;
+                if (t < row.vocab && t != s.without) best.take(s.r(t), s.u[t], t);
+            }
+            lone = row.vocab;
+            best.share();
         }
+#pragma unroll
+        for (uint32_t e = 0; e < kVec; ++e)
+            if (best.open(r[e], now.u[e])) which |= 1u << e;
+        for (; which; which &= which - 1) {
+            const uint32_t t = i + __ffs(which) - 1;
+            if (t < row.vocab && t != s.without) best.take(s.r(t), s.u[t], t);
+        }
+        best.share();
+        if (base + kThreads >= end) break;
     }
     return best;
 }
@@ -435,7 +535,7 @@ __device__ __forceinline__ uint64_t cta_largest(uint64_t key, uint64_t *s_key)
 
 // One chunk of the row at which a sequence stops; the last one writes the results.
 template <class T>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kDrawWave)
 verify_draw_kernel(Verify a)
 {
     __shared__ Part s_target[GC_MAX_DRAFTS + 1], s_draft[GC_MAX_DRAFTS + 1];
@@ -443,25 +543,32 @@ verify_draw_kernel(Verify a)
     __shared__ uint64_t s_key[kWarps];
     __shared__ uint32_t s_stop, s_last;
     __shared__ int32_t s_token;
-    const uint32_t b = blockIdx.x / a.chunks, c = blockIdx.x % a.chunks;
+    const uint32_t b = blockIdx.x / a.draws, c = blockIdx.x % a.draws;
     const float t = a.t(b), power = power_of(t);
     const bool greedy = !(t > 0.0f);
     const int32_t *ids = a.ids + size_t(b) * a.drafts;
     if (greedy && c > 0) return;
     chain_wait();
-    for (uint32_t j = threadIdx.x >> 5; j <= a.drafts; j += kWarps) {
-        Part target, draft;
-        const bool ok = decide<T>(a, b, j, target, draft);
-        if ((threadIdx.x & 31) == 0) {
-            s_ok[j] = ok;
-            s_target[j] = target;
-            s_draft[j] = draft;
+    // Where the rows' kernel has decided, only the row at which the sequence
+    // stops is looked up now, the others by the CTA that writes the results.
+    const uint32_t decided = a.left ? a.drafts - a.left[b] : ~0u;
+    auto look = [&](uint32_t from, uint32_t to) {
+        for (uint32_t j = from + (threadIdx.x >> 5); j < to; j += kWarps) {
+            Part target, draft;
+            const bool ok = decide<T>(a, b, j, target, draft);
+            if ((threadIdx.x & 31) == 0) {
+                s_ok[j] = ok;
+                s_target[j] = target;
+                s_draft[j] = draft;
+            }
         }
-    }
-    __syncthreads();
+        __syncthreads();
+    };
+    if (decided <= a.drafts) look(decided, decided + 1);
+    else look(0, a.drafts + 1);
     if (threadIdx.x == 0) {
-        uint32_t j = 0;
-        while (j < a.drafts && s_ok[j]) ++j;
+        uint32_t j = decided <= a.drafts ? decided : 0;
+        while (decided > a.drafts && j < a.drafts && s_ok[j]) ++j;
         s_stop = j;
     }
     __syncthreads();
@@ -485,25 +592,32 @@ verify_draw_kernel(Verify a)
         s.power = power;
         s.without = rejected && !a.d ? uint32_t(ids[stop]) : ~0u;
         const Pieces<T> row(s.x, a.vocab);
-        const uint32_t first = min(c * a.chunk, row.count), end = min(first + a.chunk, row.count);
-        uint64_t key = cta_largest(chunk_draw(s, row, first, end, c == 0).key(), s_key);
-        if (threadIdx.x == 0) {
-            if (key) atomicMax(a.best + b, static_cast<unsigned long long>(key));
-            __threadfence();
-            s_last = atomicAdd(a.drawn + b, 1u) + 1 == a.chunks;
-            __threadfence();
-        }
-        __syncthreads();
-        if (!s_last) return;
-        key = *reinterpret_cast<volatile unsigned long long *>(a.best + b);
-        if (key == 0 && s.inverse > 0.0f) {
+        uint32_t first = min(c * a.draw, row.count), end = min(first + a.draw, row.count);
+        uint64_t key;
+        for (bool again = false;; again = true) {
+            if (!s.d) s.dm = 0.0f, s.dinverse = 0.0f;
+            s.c = s.m * power, s.dc = s.dm * power;
+            s.usual = plain(s.c) && s.m < kLargest && plain(s.dc) && s.dm < kLargest;
+            key = cta_largest(chunk_draw(s, row, first, end, again || c == 0).key(), s_key);
+            if (again) break;
+            if (threadIdx.x == 0) {
+                if (key) atomicMax(a.best + b, static_cast<unsigned long long>(key));
+                __threadfence();
+                s_last = atomicAdd(a.drawn + b, 1u) + 1 == a.draws;
+                __threadfence();
+            }
+            __syncthreads();
+            if (!s_last) return;
+            key = *reinterpret_cast<volatile unsigned long long *>(a.best + b);
+            if (key || s.inverse == 0.0f) break;
             // p - q rounds to nothing everywhere: p stands for it
             s.d = nullptr;
             s.without = ~0u;
-            key = cta_largest(chunk_draw(s, row, 0, row.count, true).key(), s_key);
+            first = 0, end = row.count;
         }
         if (threadIdx.x == 0) s_token = key ? int32_t(uint32_t(~key)) : -1;
     }
+    if (decided <= a.drafts) look(0, decided);
     __syncthreads();
     if (threadIdx.x == 0) a.accepted[b] = int32_t(stop);
     for (uint32_t j = threadIdx.x; j <= a.drafts; j += kThreads) {
@@ -513,16 +627,14 @@ verify_draw_kernel(Verify a)
         if (a.logprobs == nullptr) continue;
         float lp = token < 0 ? -INFINITY : 0.0f;
         if (token >= 0 && !greedy) {
-            const float z = (sample_value(row_to_float(x[j * a.x_stride + token])) - s_target[j].m) / t;
-            lp = z - logf(s_target[j].sum);
+            // log2 of the weight, less that of the sum
+            const float v = sample_value(row_to_float(x[j * a.x_stride + token])), m = s_target[j].m, o = m * power;
+            const float z = plain(o) ? fmaf(v, power, -o) : (v - m) * power;
+            lp = fmaf(z, 0.693147181f, -logf(s_target[j].sum));
         }
         a.logprobs[at] = lp;
     }
 }
-
-// Chunks: eight pieces per thread, 32 KB, where that makes more CTAs than the
-// GPU holds, else fewer.
-constexpr uint32_t kSteps = 8, kWave = 8;  // kWave: CTAs per SM
 
 struct Plan {
     uint32_t chunk, chunks;
@@ -540,7 +652,7 @@ Plan plan_of(size_t rows, size_t vocab, size_t elem)
 }
 
 struct Layout {
-    size_t x_part, d_part, best, drawn, stop, arrived, bytes;
+    size_t x_part, d_part, best, drawn, left, arrived, bytes;
 };
 
 Layout layout_of(size_t sequences, size_t drafts, uint32_t chunks)
@@ -554,9 +666,9 @@ Layout layout_of(size_t sequences, size_t drafts, uint32_t chunks)
     };
     l.x_part = take(sequences * (drafts + 1) * chunks * sizeof(Part));
     l.d_part = take(sequences * drafts * chunks * sizeof(Part));
-    l.best = take(sequences * 8);
+    l.best = take(sequences * 8);  // from here on: zeros where chunks decide
     l.drawn = take(sequences * 4);
-    l.stop = take(sequences * 4);
+    l.left = take(sequences * 4);
     l.arrived = take(sequences * drafts * 4);
     l.bytes = at;
     return l;
@@ -575,16 +687,21 @@ cudaError_t run_verify(Verify a, uint8_t *ws, cudaStream_t s)
     a.best = reinterpret_cast<unsigned long long *>(ws + l.best);
     a.drawn = reinterpret_cast<uint32_t *>(ws + l.drawn);
     if (plan.skip && a.drafts > 0) {
-        a.stop = reinterpret_cast<uint32_t *>(ws + l.stop);
+        a.left = reinterpret_cast<uint32_t *>(ws + l.left);
         a.arrived = reinterpret_cast<uint32_t *>(ws + l.arrived);
-        cudaError_t e = cudaMemsetAsync(a.stop, 0xff, size_t(a.sequences) * 4, s);
-        if (e == cudaSuccess) e = cudaMemsetAsync(a.arrived, 0, size_t(a.sequences) * a.drafts * 4, s);
+        const cudaError_t e = cudaMemsetAsync(ws + l.best, 0, l.bytes - l.best, s);
         if (e != cudaSuccess) return e;
     }
+    // The draw's chunks: as many CTAs as run at a time, a piece to a thread at least.
+    const uint32_t pieces = uint32_t(size_t(a.vocab) * sizeof(T) / 16 + 1);
+    const uint32_t most = uint32_t(gch::ceil_div(pieces, size_t(kThreads)));
+    a.draws = uint32_t(gch::kSms * kDrawWave / a.sequences);
+    a.draws = a.draws < 1 ? 1 : a.draws < most ? a.draws : most;
+    a.draw = uint32_t(gch::ceil_div(pieces, a.draws));
     verify_rows_kernel<T><<<uint32_t((target_rows + draft_rows) * plan.chunks), kThreads, 0, s>>>(a);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    return gch::launch_next(verify_draw_kernel<T>, dim3(a.sequences * plan.chunks), dim3(kThreads), 0, s, a);
+    return gch::launch_next(verify_draw_kernel<T>, dim3(a.sequences * a.draws), dim3(kThreads), 0, s, a);
 }
 
 }  // namespace

@@ -37,7 +37,7 @@ def relative(p, z):
 
 def terms(tokens, experts):
     """Additions of float32 in one thread's share of a sum over tokens, and after it."""
-    lanes = 1
+    lanes = 32 if experts > 32 else 1
     while lanes < 32 and lanes * 8 < experts:
         lanes *= 2
     groups = 256 // lanes
