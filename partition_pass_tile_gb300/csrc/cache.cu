@@ -312,14 +312,17 @@ struct Move {
 constexpr int kMoveThreads = 256;
 constexpr int kMoveAhead = 4;   // rows that a thread has under way
 
-// The kept rows: a row of threads per slot, kMoveAhead slots at a time.  The
-// last slots of all heads come first: they are the recent positions, which need
-// not wait for the selection.
+// The kept rows: a row of threads per slot, kMoveAhead slots at a time, head by
+// head.  Of `down` blocks of a head those that hold recent positions alone, the
+// `early` last, come first for all heads: they need not wait for the selection.
 template <class P>
-__global__ void __launch_bounds__(kMoveThreads)
-cache_move_kernel(Evict a, Move m, uint32_t down)
+__global__ void __launch_bounds__(kMoveThreads, 5)
+cache_move_kernel(Evict a, Move m, uint32_t down, uint32_t early)
 {
-    const uint32_t block = down - 1 - blockIdx.x / a.rows(), bh = blockIdx.x % a.rows();
+    const uint32_t ahead = early * a.rows(), late = down - early;
+    const bool is_early = blockIdx.x < ahead;
+    const uint32_t at_ = is_early ? blockIdx.x : blockIdx.x - ahead, each = is_early ? early : late;
+    const uint32_t bh = at_ / each, block = at_ % each + (is_early ? late : 0);
     const uint32_t b = bh / a.heads, h = bh % a.heads, w = blockIdx.y;
     const uint32_t n = clamp_length(a.lengths, b, a.length), kept = min(n, a.budget);
     const uint32_t slots = blockDim.y * kMoveAhead, first = block * slots + threadIdx.y;
@@ -379,8 +382,10 @@ cudaError_t run_move(const Evict &a, Move m, cudaStream_t s)
     uint32_t tx = kMoveAhead;  // so that a block has a thread to a slot
     while (tx < kMoveThreads && tx < most) tx <<= 1;
     const dim3 block(tx, kMoveThreads / tx);
-    const uint32_t down = uint32_t(gch::ceil_div(a.budget, block.y * kMoveAhead));
-    return gch::launch_next(cache_move_kernel<P>, dim3(down * a.batch * a.heads, m.arrays + 1), block, 0, s, a, m, down);
+    const uint32_t slots = block.y * kMoveAhead, down = uint32_t(gch::ceil_div(a.budget, slots));
+    const uint32_t early = down - uint32_t(gch::ceil_div(a.budget - a.recent, slots));
+    return gch::launch_next(cache_move_kernel<P>, dim3(down * a.batch * a.heads, m.arrays + 1), block, 0, s, a, m, down,
+                            early);
 }
 
 template <class T, int N>

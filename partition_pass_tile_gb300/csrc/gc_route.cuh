@@ -74,57 +74,74 @@ __device__ __forceinline__ float warp_sum(float v)
     return v;
 }
 
-// A warp's token: x[V] become its weights exp(x - m); returns their sum, 0 if no
-// expert is open, and the largest logit's order bits.
-template <int V, class X>
-__device__ __forceinline__ float warp_weights(const X &logits, float (&w)[V], Exponent &exponent, uint32_t &top, float &best)
+// A warp's token: w[V] are the weights exp(x - m) of its logits x[V]; returns
+// their sum, 0 if no expert is open, and the order bits of the largest logit of
+// the warp (top) and of the lane (best).  Logits that are not all finite and
+// small leave cleaned.
+template <int V>
+__device__ __forceinline__ float warp_weights(float (&x)[V], float (&w)[V], Exponent &exponent, uint32_t &top,
+                                              uint32_t &best)
 {
-    best = -INFINITY;
+    float most = -INFINITY;
 #pragma unroll
-    for (int v = 0; v < V; ++v) best = fmaxf(best, logits[v]);
-    top = __reduce_max_sync(kRouteFull, order_bits(best));
+    for (int v = 0; v < V; ++v) most = fmaxf(most, x[v]);
+    best = order_bits(most);
+    top = __reduce_max_sync(kRouteFull, best);
     exponent.m = order_value(top);
     exponent.c = exponent.m * kLog2e;
     exponent.usual = true;
     float total = 0.0f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        w[v] = pow2(fmaf(logits[v], kLog2e, -exponent.c));
+        w[v] = pow2(fmaf(x[v], kLog2e, -exponent.c));
         total += w[v];
     }
     total = warp_sum(total);
     if (total <= 1.5f * 32 * V && fabsf(exponent.c) < 0x1p100f) return total;
     // no expert, a NaN, an infinity or a very large logit
     exponent.usual = false;
-    best = fminf(best, 3.402823466e38f);
-    top = __reduce_max_sync(kRouteFull, order_bits(best));
-    if (top <= kRouteNone) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) w[v] = 0.0f;
-        return 0.0f;
-    }
-    exponent.m = order_value(top);
+    for (int v = 0; v < V; ++v) x[v] = sample_value(x[v]);
+    best = order_bits(fminf(most, 3.402823466e38f));
+    top = __reduce_max_sync(kRouteFull, best);
+    exponent.m = top > kRouteNone ? order_value(top) : 0.0f;
     total = 0.0f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        w[v] = exponent.weight(logits[v]);
+        w[v] = exponent.weight(x[v]);
         total += w[v];
     }
     return warp_sum(total);
 }
 
-// The sum over a CTA of W warps, of doubles; every thread calls it, thread 0 has it.
-template <int W>
-__device__ __forceinline__ double cta_sum(double v, double *s_warp)
+// 1 / x of a sum of weights, off by at most 2^-23 of itself.
+__device__ __forceinline__ float inverse_of(float x)
 {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kRouteFull, v, o);
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// The sums over a CTA of W warps, of whole numbers and of floats; every thread
+// calls them and has the result.
+template <int W>
+__device__ __forceinline__ uint32_t cta_count(uint32_t v, uint32_t *s_warp)
+{
+    v = __reduce_add_sync(kRouteFull, v);
     __syncthreads();
     if ((threadIdx.x & 31) == 0) s_warp[threadIdx.x >> 5] = v;
     __syncthreads();
-    if (threadIdx.x == 0)
-        for (int w = 1; w < W; ++w) v += s_warp[w];
-    return v;
+    return __reduce_add_sync(kRouteFull, (threadIdx.x & 31) < W ? s_warp[threadIdx.x & 31] : 0u);
+}
+
+template <int W>
+__device__ __forceinline__ float cta_sum(float v, uint32_t *s_warp)
+{
+    v = warp_sum(v);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) s_warp[threadIdx.x >> 5] = __float_as_uint(v);
+    __syncthreads();
+    return warp_sum((threadIdx.x & 31) < W ? __uint_as_float(s_warp[threadIdx.x & 31]) : 0.0f);
 }
 
 // A group of 1, 2 or 4 lanes.

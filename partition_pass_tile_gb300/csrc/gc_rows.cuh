@@ -184,9 +184,9 @@ __device__ __forceinline__ uint4 peer_load4(uint32_t at)
     return v;
 }
 
-__device__ __forceinline__ void peer_store(uint32_t at, double v)
+__device__ __forceinline__ void peer_store(uint32_t at, uint32_t v)
 {
-    asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(at), "d"(v) : "memory");
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
 }
 
 // Programmatic launches: a kernel launched by launch_next may start while the

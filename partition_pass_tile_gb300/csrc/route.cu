@@ -11,7 +11,7 @@
 // are few) holds the experts [l * V, (l + 1) * V) of a token in registers, so
 // that equal values go by lane and then by register; the lane's sums over
 // tokens of its experts' probabilities stay in registers until the end, CTAs
-// leave them in the workspace, and a cluster adds them up in double.
+// leave them in the workspace, and a cluster adds them up.
 #include "gc_route.cuh"
 
 namespace {
@@ -35,39 +35,42 @@ struct RouteOut {
     float *load, *loss;
 };
 
+// loss = experts * dot / pairs, dot the sum of counts * load.
+__device__ __forceinline__ float loss_of(uint32_t experts, float dot, uint32_t pairs)
+{
+    return pairs > 0 ? float(experts) * dot / float(pairs) : 0.0f;
+}
+
 // A CTA's sums: to the workspace, or, if it is the only one, to the results.
-// each(f) calls f(expert, sum, count) by some thread for every expert.
+// each(f) calls f(expert, sum, count) by some thread for every expert.  No
+// double here: that pipe makes a chain of reductions of one CTA take 10 us.
 template <int W, class Each>
 __device__ __forceinline__ void finish(uint32_t experts, uint32_t routed, const RouteOut &out, const Totals &part,
-                                       double *s_warp, const Each &each)
+                                       uint32_t *s_warp, const Each &each)
 {
+    const uint32_t n = cta_count<W>(routed, s_warp);
     if (gridDim.x > 1) {
         each([&](uint32_t e, float s, uint32_t c) {
             part.sums[size_t(blockIdx.x) * experts + e] = s;
             part.counts[size_t(blockIdx.x) * (experts + 1) + e] = c;
         });
-        const double n = cta_sum<W>(double(routed), s_warp);
-        if (threadIdx.x == 0) part.counts[size_t(blockIdx.x) * (experts + 1) + experts] = uint32_t(n);
+        if (threadIdx.x == 0) part.counts[size_t(blockIdx.x) * (experts + 1) + experts] = n;
         return;
     }
-    __shared__ double s_n;
-    const double mine = cta_sum<W>(double(routed), s_warp);
-    if (threadIdx.x == 0) s_n = mine;
-    __syncthreads();
-    const double n = s_n;
-    double pairs = 0.0, dot = 0.0;
+    uint32_t pairs = 0;
+    float dot = 0.0f;
     each([&](uint32_t e, float s, uint32_t c) {
-        const double load = n > 0.0 ? double(s) / n : 0.0;
+        const float load = n > 0 ? s / float(n) : 0.0f;
         out.counts[e] = int32_t(c);
-        if (out.load) out.load[e] = float(load);
-        pairs += double(c);
-        dot += double(c) * load;
+        if (out.load) out.load[e] = load;
+        pairs += c;
+        dot = fmaf(float(c), load, dot);
     });
-    pairs = cta_sum<W>(pairs, s_warp);
+    pairs = cta_count<W>(pairs, s_warp);
     dot = cta_sum<W>(dot, s_warp);
     if (threadIdx.x == 0) {
         out.counts[experts] = int32_t(n);
-        if (out.loss) *out.loss = pairs > 0.0 ? float(double(experts) * dot / pairs) : 0.0f;
+        if (out.loss) *out.loss = loss_of(experts, dot, pairs);
     }
 }
 
@@ -100,15 +103,16 @@ route_warp_kernel(const T *__restrict__ logits, size_t stride, uint32_t tokens, 
 {
     constexpr int kWarps = kWarpThreads<V> / 32;
     constexpr int kSlots = V < 8 ? V : 8;
-    __shared__ uint64_t s_list[kWarps][kCandidates];
+    __shared__ uint32_t s_id[kWarps][kCandidates];
+    __shared__ uint4 s_key[kWarps][kCandidates / 4];
     __shared__ float s_sum[kWarps][32 * kSlots];
     __shared__ uint32_t s_count[GC_MAX_EXPERTS];
-    __shared__ double s_warp[kWarps];
+    __shared__ uint32_t s_warp[kWarps];
     chain_start();
     const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5, first = lane * V;
     for (uint32_t e = threadIdx.x; e < experts; e += kWarpThreads<V>) s_count[e] = 0;
     __syncthreads();
-    uint64_t *list = s_list[warp];
+    uint32_t *id = s_id[warp], *key = reinterpret_cast<uint32_t *>(s_key[warp]);
     float sum[V];
     uint32_t routed = 0;
 #pragma unroll
@@ -122,12 +126,13 @@ route_warp_kernel(const T *__restrict__ logits, size_t stride, uint32_t tokens, 
     uint64_t t = uint64_t(blockIdx.x) * kWarps + warp;
     fetch(t);
     for (; t < tokens; t += step) {
-        const Logits<T, N, V> x = next;
+        float x[V], w[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) x[v] = next[v];
         fetch(t + step);
-        float w[V], best;
         Exponent exponent;
-        uint32_t top;
-        const float total = warp_weights(x, w, exponent, top, best);
+        uint32_t top, left;
+        const float total = warp_weights(x, w, exponent, top, left);
         int32_t *ids = out.ids + t * topk;
         float *weights = out.weights + t * topk;
         if (!(total > 0.0f)) {
@@ -135,55 +140,55 @@ route_warp_kernel(const T *__restrict__ logits, size_t stride, uint32_t tokens, 
             continue;
         }
         ++routed;
-        const float inverse = 1.0f / total;
+        const float inverse = inverse_of(total);
 #pragma unroll
         for (int v = 0; v < V; ++v) sum[v] = fmaf(w[v], inverse, sum[v]);
 
-        // NaN is never among what follows, +inf counts as the largest value
-        auto value = [&](int v) { return exponent.usual ? x[v] : sample_value(x[v]); };
-        uint32_t bound = top, left = order_bits(best);
+        // a bound that at least k logits reach
+        const uint32_t most = left;
+        uint32_t bound = top;
         for (uint32_t j = 1; j < topk && bound > kRouteNone; ++j) {
             left = left == bound ? 0u : left;
             bound = __reduce_max_sync(kRouteFull, left);
         }
-        bound = max(bound, kRouteNone + 1);
-        const float least = order_value(bound);
+        const float least = order_value(max(bound, kRouteNone + 1));
         using Mask = typename Bits<V>::Type;
         Mask which = 0;
 #pragma unroll
-        for (int v = 0; v < V; ++v) which |= value(v) >= least ? Mask(1) << v : Mask(0);
-        uint32_t n = __reduce_add_sync(kRouteFull, Bits<V>::count(which));
-        uint32_t rank = lane;
-        if (n <= 32) {
-            uint32_t base = 0;
-            while (true) {
-                const uint32_t have = __ballot_sync(kRouteFull, which != 0);
-                if (have == 0) break;
-                if (which) {
-                    const int at = Bits<V>::lowest(which);
-                    float v = 0.0f;
-                    if constexpr (V <= 8) {
+        for (int v = 0; v < V; ++v) which |= x[v] >= least ? Mask(1) << v : Mask(0);
+        const uint32_t mine = Bits<V>::count(which);
+        uint32_t upto = mine;
 #pragma unroll
-                        for (int i = 0; i < V; ++i)
-                            if (i == at) v = value(i);
-                    } else {
-                        v = sample_value(row_to_float(logits[t * stride + first + at]));
-                    }
-                    list[base + __popc(have & ((1u << lane) - 1u))] =
-                        (uint64_t(order_bits(v)) << 32) | uint32_t(~(first + at));
-                    which &= which - 1;
-                }
-                base += __popc(have);
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t y = __shfl_up_sync(kRouteFull, upto, o);
+            if (lane >= uint32_t(o)) upto += y;
+        }
+        uint32_t n = __shfl_sync(kRouteFull, upto, 31), rank = lane;
+        if (n <= 32) {
+            // listed by id; read again, which spares finding them among the registers
+            for (uint32_t at = upto - mine; which; which &= which - 1, ++at) id[at] = first + Bits<V>::lowest(which);
+            key[lane] = 0;
+            __syncwarp();
+            uint32_t own = 0;
+            if (lane < n) {
+                own = order_bits(sample_value(row_to_float(logits[t * stride + id[lane]])));
+                key[lane] = own;
             }
             __syncwarp();
-            const uint64_t mine = list[lane];
+            // before it: the larger ones, and the equal ones listed before it
             rank = 0;
-            for (uint32_t c = 0; c < n; ++c) rank += list[c] > mine;
+            for (uint32_t c = 0; c < n; c += 4) {
+                const uint4 k = s_key[warp][c / 4];
+                rank += k.x >= own + (c >= lane);
+                rank += k.y >= own + (c + 1 >= lane);
+                rank += k.z >= own + (c + 2 >= lane);
+                rank += k.w >= own + (c + 3 >= lane);
+            }
             if (lane >= n) rank = ~0u;
         } else {
             // one after another: a lane's largest, and which of its logits are left
             Mask rest = ~Mask(0);
-            left = order_bits(best);
+            left = most;
             for (n = 0; n < topk; ++n) {
                 if (n > 0) top = __reduce_max_sync(kRouteFull, left);
                 if (top <= kRouteNone) break;
@@ -193,13 +198,14 @@ route_warp_kernel(const T *__restrict__ logits, size_t stride, uint32_t tokens, 
 #pragma unroll
                     for (int v = 0; v < V; ++v) {
                         if (!(rest >> v & 1u)) continue;
-                        const uint32_t key = order_bits(value(v));
-                        if (!found && key == top) {
+                        const uint32_t k = order_bits(x[v]);
+                        if (!found && k == top) {
                             found = true;
                             rest &= ~(Mask(1) << v);
-                            list[n] = (uint64_t(top) << 32) | uint32_t(~(first + v));
+                            id[n] = first + v;
+                            key[n] = top;
                         } else {
-                            left = max(left, key);
+                            left = max(left, k);
                         }
                     }
                 }
@@ -208,23 +214,19 @@ route_warp_kernel(const T *__restrict__ logits, size_t stride, uint32_t tokens, 
         }
         // n listed, ranked or in order
         const uint32_t listed = n;
-        float chosen = 0.0f, mine[2] = {0.0f, 0.0f};
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const uint32_t r = h == 0 ? rank : lane + 32;
-            if (lane + 32 * h < listed && r < topk) mine[h] = exponent.weight(order_value(uint32_t(list[lane + 32 * h] >> 32)));
-            chosen += mine[h];
+        const bool own_one = lane < listed && rank < topk, other = lane + 32 < listed;
+        const float first_w = own_one ? exponent.weight(order_value(key[lane])) : 0.0f;
+        const float other_w = other ? exponent.weight(order_value(key[lane + 32])) : 0.0f;
+        const float scale = normalize ? inverse_of(warp_sum(first_w + other_w)) : inverse;
+        if (own_one) {
+            ids[rank] = int32_t(id[lane]);
+            weights[rank] = first_w * scale;
+            if (out.counts) atomicAdd(&s_count[id[lane]], 1u);
         }
-        chosen = normalize ? warp_sum(chosen) : total;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const uint32_t r = h == 0 ? rank : lane + 32;
-            if (lane + 32 * h < listed && r < topk) {
-                const uint32_t id = ~uint32_t(list[lane + 32 * h]);
-                ids[r] = int32_t(id);
-                weights[r] = mine[h] / chosen;
-                if (out.counts) atomicAdd(&s_count[id], 1u);
-            }
+        if (other) {
+            ids[lane + 32] = int32_t(id[lane + 32]);
+            weights[lane + 32] = other_w * scale;
+            if (out.counts) atomicAdd(&s_count[id[lane + 32]], 1u);
         }
         for (uint32_t j = listed + lane; j < topk; j += 32) ids[j] = -1, weights[j] = 0.0f;
         __syncwarp();
@@ -266,7 +268,7 @@ route_group_kernel(const T *__restrict__ logits, size_t stride, uint32_t tokens,
     __shared__ Pick s_pick[kGroupThreads * V];
     __shared__ float s_sum[kWarps][4 * V];
     __shared__ uint32_t s_count[kWarps][4 * V];
-    __shared__ double s_warp[kWarps];
+    __shared__ uint32_t s_warp[kWarps];
     chain_start();
     const Group g(lanes);
     const uint32_t first = g.lane * V, groups = kGroupThreads / lanes;
@@ -379,27 +381,26 @@ __global__ void __cluster_dims__(kJoinCluster, 1, 1) __launch_bounds__(kJoinThre
 route_join_kernel(Totals part, uint32_t parts, uint32_t experts, RouteOut out)
 {
     constexpr int kWarps = kJoinThreads / 32;
-    __shared__ double s_warp[kWarps];
-    __shared__ double s_sum[kWarps][32];
+    __shared__ uint32_t s_warp[kWarps];
+    __shared__ float s_sum[kWarps][32];
     __shared__ uint32_t s_count[kWarps][32];
-    __shared__ double s_got[2][kJoinCluster];
+    __shared__ float s_dot[kJoinCluster];
+    __shared__ uint32_t s_pairs[kJoinCluster];
     const uint32_t rank = cluster_rank(), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     chain_wait();
-    double n = 0.0;
-    for (uint32_t c = threadIdx.x; c < parts; c += kJoinThreads) n += double(part.counts[size_t(c) * (experts + 1) + experts]);
-    n = cta_sum<kWarps>(n, s_warp);
-    if (threadIdx.x == 0) s_warp[0] = n;
-    __syncthreads();
-    n = s_warp[0];
-    double pairs = 0.0, dot = 0.0;
+    uint32_t n = 0;
+    for (uint32_t c = threadIdx.x; c < parts; c += kJoinThreads) n += part.counts[size_t(c) * (experts + 1) + experts];
+    n = cta_count<kWarps>(n, s_warp);
+    uint32_t pairs = 0;
+    float dot = 0.0f;
     for (uint32_t e0 = rank * 32; e0 < experts; e0 += kJoinCluster * 32) {
         const uint32_t e = e0 + lane;
-        double s = 0.0;
+        float s = 0.0f;
         uint32_t k = 0;
         if (e < experts) {
-#pragma unroll 8
+#pragma unroll 10
             for (uint32_t c = warp; c < parts; c += kWarps) {
-                s += double(part.sums[size_t(c) * experts + e]);
+                s += part.sums[size_t(c) * experts + e];
                 k += part.counts[size_t(c) * (experts + 1) + e];
             }
         }
@@ -407,34 +408,36 @@ route_join_kernel(Totals part, uint32_t parts, uint32_t experts, RouteOut out)
         s_sum[warp][lane] = s;
         s_count[warp][lane] = k;
         __syncthreads();
-        if (warp == 0 && e < experts) {
-            for (int w = 1; w < kWarps; ++w) {
-                s += s_sum[w][lane];
-                k += s_count[w][lane];
+        // a warp to an expert
+        const uint32_t mine = e0 + warp;
+        if (mine < experts) {
+            s = warp_sum(s_sum[lane][warp]);
+            k = __reduce_add_sync(kRouteFull, s_count[lane][warp]);
+            if (lane == 0) {
+                const float load = n > 0 ? s / float(n) : 0.0f;
+                out.counts[mine] = int32_t(k);
+                if (out.load) out.load[mine] = load;
+                pairs += k;
+                dot = fmaf(float(k), load, dot);
             }
-            const double load = n > 0.0 ? s / n : 0.0;
-            out.counts[e] = int32_t(k);
-            if (out.load) out.load[e] = float(load);
-            pairs += double(k);
-            dot += double(k) * load;
         }
     }
-    pairs = cta_sum<kWarps>(pairs, s_warp);
+    pairs = cta_count<kWarps>(pairs, s_warp);
     dot = cta_sum<kWarps>(dot, s_warp);
     cluster_sync();  // every CTA of the cluster runs
     if (threadIdx.x == 0) {
-        peer_store(peer_address(&s_got[0][rank], 0), pairs);
-        peer_store(peer_address(&s_got[1][rank], 0), dot);
+        peer_store(peer_address(&s_dot[rank], 0), __float_as_uint(dot));
+        peer_store(peer_address(&s_pairs[rank], 0), pairs);
     }
     cluster_sync();
     if (rank == 0 && threadIdx.x == 0) {
-        pairs = dot = 0.0;
+        pairs = 0, dot = 0.0f;
         for (int c = 0; c < kJoinCluster; ++c) {
-            pairs += s_got[0][c];
-            dot += s_got[1][c];
+            pairs += s_pairs[c];
+            dot += s_dot[c];
         }
         out.counts[experts] = int32_t(n);
-        if (out.loss) *out.loss = pairs > 0.0 ? float(double(experts) * dot / pairs) : 0.0f;
+        if (out.loss) *out.loss = loss_of(experts, dot, pairs);
     }
 }
 

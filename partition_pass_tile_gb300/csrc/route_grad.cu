@@ -23,18 +23,14 @@ struct Grad {
 
 // dloss * experts / (n * pairs): a = factor * counts.  Every thread has it.
 template <int W>
-__device__ __forceinline__ float loss_factor(const Grad &a, double *s_warp, float *s_factor)
+__device__ __forceinline__ float loss_factor(const Grad &a, uint32_t *s_warp)
 {
     if (a.dloss == nullptr) return 0.0f;
-    double pairs = 0.0;
-    for (uint32_t e = threadIdx.x; e < a.experts; e += W * 32) pairs += double(max(a.counts[e], 0));
-    pairs = cta_sum<W>(pairs, s_warp);
-    if (threadIdx.x == 0) {
-        const double n = double(a.counts[a.experts]);
-        *s_factor = pairs > 0.0 && n > 0.0 ? float(double(*a.dloss) * double(a.experts) / (n * pairs)) : 0.0f;
-    }
-    __syncthreads();
-    return *s_factor;
+    uint32_t pairs = 0;
+    for (uint32_t e = threadIdx.x; e < a.experts; e += W * 32) pairs += uint32_t(max(a.counts[e], 0));
+    pairs = cta_count<W>(pairs, s_warp);
+    const int32_t n = a.counts[a.experts];
+    return pairs > 0 && n > 0 ? *a.dloss * float(a.experts) / float(n) / float(pairs) : 0.0f;
 }
 
 // ---------------------------------------------------------------- a warp to a token
@@ -50,11 +46,10 @@ __global__ void __launch_bounds__(kThreads, kResident<V>)
 route_grad_warp_kernel(const T *__restrict__ logits, T *__restrict__ dx, Grad a)
 {
     __shared__ Pick s_pick[kWarps][GC_MAX_TOPK];
-    __shared__ double s_warp[kWarps];
-    __shared__ float s_factor;
+    __shared__ uint32_t s_warp[kWarps];
     const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5, first = lane * V;
     Pick *pick = s_pick[warp];
-    const float factor = loss_factor<kWarps>(a, s_warp, &s_factor);
+    const float factor = loss_factor<kWarps>(a, s_warp);
     float share[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) share[v] = a.dloss && first + v < a.experts ? factor * float(a.counts[first + v]) : 0.0f;
@@ -75,16 +70,18 @@ route_grad_warp_kernel(const T *__restrict__ logits, T *__restrict__ dx, Grad a)
     };
     fetch(t);
     for (; t < a.tokens; t += step) {
-        const Logits<T, N, V> x = next;
+        float x[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) x[v] = next[v];
         const uint32_t id = next_id < a.experts ? next_id : ~0u;
         const float g = id != ~0u ? next_g : 0.0f;
         fetch(t + step);
         T *to = dx + t * a.dx_stride;
         const T *row = logits + t * a.stride;
         const bool live = __shfl_sync(kRouteFull, id, 0) != ~0u;
-        float w[V], best;
+        float w[V];
         Exponent exponent;
-        uint32_t top;
+        uint32_t top, best;
         float total = 0.0f;
         if (live) {
             total = warp_weights(x, w, exponent, top, best);
@@ -92,7 +89,7 @@ route_grad_warp_kernel(const T *__restrict__ logits, T *__restrict__ dx, Grad a)
 #pragma unroll
             for (int v = 0; v < V; ++v) w[v] = 0.0f;
         }
-        const float inverse = total > 0.0f ? 1.0f / total : 0.0f;
+        const float inverse = total > 0.0f ? inverse_of(total) : 0.0f;
         float dot = 0.0f;
         if (a.dloss) {
 #pragma unroll
@@ -106,7 +103,7 @@ route_grad_warp_kernel(const T *__restrict__ logits, T *__restrict__ dx, Grad a)
             if (id != ~0u) mine = exponent.weight(row_to_float(row[id])) * inverse;
             const float chosen = a.normalize ? warp_sum(mine) : 1.0f;
             float inner = warp_sum(mine * g);
-            const float scale = chosen > 0.0f ? 1.0f / chosen : 0.0f;
+            const float scale = chosen > 0.0f ? inverse_of(chosen) : 0.0f;
             if (a.normalize) {
                 inner *= scale;
                 part = mine * scale * (g - inner);
@@ -183,12 +180,11 @@ route_grad_group_kernel(const T *__restrict__ logits, T *__restrict__ dx, Grad a
 {
     constexpr int V = kGroupValues;
     __shared__ Pick s_pick[kThreads * V];
-    __shared__ double s_warp[kWarps];
-    __shared__ float s_factor;
+    __shared__ uint32_t s_warp[kWarps];
     const Group g(lanes);
     const uint32_t first = g.lane * V, groups = kThreads / lanes, experts = a.experts, topk = a.topk;
     Pick *pick = s_pick + (threadIdx.x - g.lane) * V;
-    const float factor = loss_factor<kWarps>(a, s_warp, &s_factor);
+    const float factor = loss_factor<kWarps>(a, s_warp);
     float share[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) share[v] = a.dloss && first + v < experts ? factor * float(a.counts[first + v]) : 0.0f;

@@ -6,7 +6,8 @@ y takes two roundings of its own and one of the constant, so 2^y is off by
 3 |z| e of itself, and 4 e more by the approximation of 2^y (2^-22); the sum by
 the mean of that over its terms, with at most 64 + 5 additions of e; the
 quotient by 3 e.  Weights over their sum: the same once more with at most 64
-additions.  Elements below 2^-126 may be 0."""
+additions.  Elements below 2^-126 may be 0.  Sums over tokens and experts: one 2^-24 for each addition on
+a term's way, of terms that are not negative."""
 
 import numpy as np
 import pytest
@@ -36,13 +37,13 @@ def relative(p, z):
 
 
 def terms(tokens, experts):
-    """Additions of float32 in one thread's share of a sum over tokens, and after it."""
-    lanes = 32 if experts > 32 else 1
-    while lanes < 32 and lanes * 8 < experts:
-        lanes *= 2
-    groups = 256 // lanes
-    grid = min(-(-tokens // groups), 456)
-    return -(-tokens // max(1, grid * groups)) + 5 + 8
+    """Additions of float32 on the way of a token to a sum over tokens: its thread's, its CTA's and the CTAs'."""
+    if experts > 32:
+        groups, most = (16, 304) if experts <= 256 else (8, 304) if experts <= 512 else (8, 152)
+    else:
+        groups, most = 256 // (1 if experts <= 8 else 2 if experts <= 16 else 4), 456
+    grid = min(-(-tokens // groups), most)
+    return -(-tokens // (grid * groups)) + 64
 
 
 def check_route(r, x64, topk, normalize, mask):
@@ -59,7 +60,8 @@ def check_route(r, x64, topk, normalize, mask):
     off = (p * rel).sum(0) / n + (terms(tokens, experts) + 1) * E * load + 2.0 ** -126
     assert np.all(np.abs(r.load.double().cpu().numpy() - load) <= off)
     share = counts[:experts] / max(counts[:experts].sum(), 1)
-    assert abs(float(r.loss) - loss) <= experts * float(share @ off) + E * loss
+    # its sum over the experts: at most 64 additions of one thread, 10 of its CTA, 8 of the CTAs', and three products
+    assert abs(float(r.loss) - loss) <= experts * float(share @ off) + 85 * E * loss
     return ids, counts
 
 
