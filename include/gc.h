@@ -549,7 +549,10 @@ gc_status gc_expert_combine_grad(const void *d_g, size_t g_stride, const void *d
                                  size_t topk, size_t width, gc_row_dtype dtype, void *d_dy,
                                  size_t dy_stride, float *d_dweights, cudaStream_t stream);
 
-/* Workspace bytes of gc_expert_route; 0 for arguments out of range. */
+/*
+ * Workspace bytes of gc_expert_route; 0 for arguments out of range.  256, or
+ * without d_counts: the call checks its workspace and does not touch it.
+ */
 size_t gc_expert_route_workspace_bytes(size_t tokens, uint32_t experts);
 
 /*

@@ -302,7 +302,7 @@ gc_status gc_expert_route(const void *d_logits, size_t logits_stride, size_t tok
         (d_counts == nullptr && (d_load || d_loss)) || d_ws == nullptr)
         return GC_ERR_INVALID_VALUE;
     if ((reinterpret_cast<uintptr_t>(d_ws) & 255u) != 0) return GC_ERR_MISALIGNED;
-    if (ws_bytes < expert_route_workspace_bytes(tokens, experts)) return GC_ERR_WORKSPACE_TOO_SMALL;
+    if (ws_bytes < (d_counts ? expert_route_workspace_bytes(tokens, experts) : 256)) return GC_ERR_WORKSPACE_TOO_SMALL;
     const gc_status st = check_spans({row_span(d_logits, tokens, logits_stride, experts, dtype, false),
                                       flat(d_mask, tokens, 1, false), flat(d_ids, tokens * topk, 4, true),
                                       flat(d_weights, tokens * topk, 4, true),

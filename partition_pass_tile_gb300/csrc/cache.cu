@@ -72,9 +72,12 @@ cache_score_kernel(const T *__restrict__ weights, Weights a, const float *scores
                     next();
                 }
 #pragma unroll
-                for (int i = 0; i < kScoreRows; ++i)
+                for (int i = 0; i < kScoreRows; ++i) {
+                    float x[N];
+                    piece_values(v[i], x);
 #pragma unroll
-                    for (int e = 0; e < N; ++e) acc[e] += row_to_float(v[i].v[e]);
+                    for (int e = 0; e < N; ++e) acc[e] += x[e];
+                }
             }
         } else {  // the end of the rows
             for (uint32_t r = threadIdx.y; r < rows; r += y, next())

@@ -52,6 +52,16 @@ struct Logits {
         }
     }
     __device__ __forceinline__ float operator[](int v) const { return row_to_float(p[v / N].v[v % N]); }
+    __device__ __forceinline__ void values(float (&x)[V]) const
+    {
+#pragma unroll
+        for (int i = 0; i < V / N; ++i) {
+            float y[N];
+            piece_values(p[i], y);
+#pragma unroll
+            for (int e = 0; e < N; ++e) x[i * N + e] = y[e];
+        }
+    }
 };
 
 // exp(x - m) as a power of two.  c = m log2(e) is taken off by a multiply-add,

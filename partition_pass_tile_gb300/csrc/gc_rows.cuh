@@ -94,6 +94,24 @@ __device__ __forceinline__ float pow2(float x)
     return y;
 }
 
+// The values of a piece.  bfloat16 are taken from their words by one instruction
+// each; one at a time they cost two.
+template <class T, int N>
+__device__ __forceinline__ void piece_values(const Piece<T, N> &p, float (&x)[N])
+{
+    if constexpr (std::is_same<T, __nv_bfloat16>::value && N % 2 == 0) {
+        const uint32_t *w = reinterpret_cast<const uint32_t *>(p.v);
+#pragma unroll
+        for (int e = 0; e < N; e += 2) {
+            x[e] = __uint_as_float(w[e / 2] << 16);
+            x[e + 1] = __uint_as_float(w[e / 2] & 0xffff0000u);
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < N; ++e) x[e] = row_to_float(p.v[e]);
+    }
+}
+
 // The largest value of a piece; NaN counts for nothing.
 template <class T, int N>
 __device__ __forceinline__ float piece_max(const Piece<T, N> &p)

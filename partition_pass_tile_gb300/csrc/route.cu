@@ -127,8 +127,7 @@ route_warp_kernel(const T *__restrict__ logits, size_t stride, uint32_t tokens, 
     fetch(t);
     for (; t < tokens; t += step) {
         float x[V], w[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) x[v] = next[v];
+        next.values(x);
         fetch(t + step);
         Exponent exponent;
         uint32_t top, left;

@@ -71,8 +71,7 @@ route_grad_warp_kernel(const T *__restrict__ logits, T *__restrict__ dx, Grad a)
     fetch(t);
     for (; t < a.tokens; t += step) {
         float x[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) x[v] = next[v];
+        next.values(x);
         const uint32_t id = next_id < a.experts ? next_id : ~0u;
         const float g = id != ~0u ? next_g : 0.0f;
         fetch(t + step);

@@ -28,7 +28,9 @@ using namespace gcd;
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kBatch = 8;             // pieces of 16 bytes that a thread has under way
+constexpr int kRing = 6;              // pieces of 16 bytes that a thread has under way
+constexpr int kAtOnce = 2;            // of them waited for and loaded again together
+constexpr int kDrawRing = 3;          // pieces of each of three rows in the draw
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr float kLargest = 3.402823466e38f;
 constexpr float kUniformLo = 0x1p-25f, kUniformHi = 1.0f - 0x1p-24f;
@@ -36,7 +38,7 @@ constexpr float kUniformLo = 0x1p-25f, kUniformHi = 1.0f - 0x1p-24f;
 // Chunks: 16 pieces per thread, 64 KB, where that makes more CTAs than the
 // GPU holds, else fewer.
 constexpr uint32_t kDrawWave = 4;          // CTAs per SM of the draw
-constexpr uint32_t kSteps = 16, kWave = 4;  // kWave: CTAs per SM
+constexpr uint32_t kSteps = 16, kWave = 6;  // kWave: CTAs per SM
 
 // z = (x - m) / t as a power of two's exponent.
 __device__ __forceinline__ float power_of(float t)
@@ -142,53 +144,96 @@ __device__ __forceinline__ void join_lanes(float &m, float &sum, float power)
     m = top, sum = s;
 }
 
-// A chunk's maximum and sum, to lane 0 of warp 0.
-template <class T>
-__device__ __forceinline__ Part chunk_sum(const Pieces<T> &row, uint32_t first, uint32_t end, bool singles, float power,
-                                          Part *s_part)
+__device__ __forceinline__ void copy_piece(void *to, const void *from, bool there)
+{
+    if (there)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(uint32_t(__cvta_generic_to_shared(to))), "l"(from)
+                     : "memory");
+}
+
+__device__ __forceinline__ void copy_float(void *to, const float *from)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(uint32_t(__cvta_generic_to_shared(to))), "l"(from)
+                 : "memory");
+}
+
+__device__ __forceinline__ void commit_copies() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+template <int N>
+__device__ __forceinline__ void wait_copies()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// A chunk's pieces to f, one after another, through a ring of asynchronous
+// copies, each thread its own: kRing of them are under way at any time.
+template <class T, class F>
+__device__ __forceinline__ void each_piece(const Pieces<T> &row, uint32_t first, uint32_t end, uint4 *ring, const F &f)
 {
     constexpr uint32_t kVec = Pieces<T>::kVec;
-    float m = -INFINITY, sum = 0.0f;
+    const T *from = row.x + row.head;
+    uint4 *mine = ring + threadIdx.x;
+    auto copy = [&](uint32_t j, int slot) {
+#pragma unroll
+        for (int q = 0; q < kAtOnce; ++q) copy_piece(mine + (slot + q) * kThreads, from + size_t(j + q * kThreads) * kVec, j + q * kThreads < end);
+        commit_copies();
+    };
+    constexpr uint32_t kStride = kAtOnce * kThreads;
+    uint32_t j = first + threadIdx.x;
+#pragma unroll
+    for (int q = 0; q < kRing; q += kAtOnce) copy(j + q * kThreads, q);
+    for (int slot = 0; j < end; j += kStride) {
+        wait_copies<kRing / kAtOnce - 1>();
+#pragma unroll
+        for (int q = 0; q < kAtOnce; ++q) {
+            if (j + q * kThreads >= end) break;
+            f(load_piece<T, kVec>(reinterpret_cast<const T *>(mine + (slot + q) * kThreads)), row.head + (j + q * kThreads) * kVec);
+        }
+        copy(j + kRing * kThreads, slot);
+        slot = slot + kAtOnce < kRing ? slot + kAtOnce : 0;
+    }
+    wait_copies<0>();
+}
+
+// A chunk's sum by a maximum, to lane 0 of warp 0.  The maximum is one of the
+// chunk's first logits: later ones may weigh up to 2^60, which spares looking
+// for the largest.
+template <class T>
+__device__ __forceinline__ Part chunk_sum(const Pieces<T> &row, uint32_t first, uint32_t end, bool singles, float power,
+                                          uint4 *ring, Part *s_part)
+{
+    constexpr uint32_t kVec = Pieces<T>::kVec;
+    float m = -INFINITY, c = 0.0f, sum = 0.0f;
+    bool usual = false;  // m is a logit and c can be taken off
+    auto base = [&](float top) {
+        top = fminf(fmaxf(top, m), kLargest);
+        if (!(top > -INFINITY)) return;
+        join(m, sum, top, 0.0f, power);
+        c = m * power;
+        usual = plain(c);
+    };
+    each_piece(row, first, end, ring, [&](const Piece<T, kVec> &v, uint32_t) {
+        if (!usual) base(piece_max(v));
+        float x[kVec], more = 0.0f;
+        piece_values(v, x);
+#pragma unroll
+        for (uint32_t e = 0; e < kVec; ++e) more += pow2(fmaf(x[e], power, -c));
+        if (usual && more <= 0x1p60f) {
+            sum += more;
+            return;
+        }
+        // no logit, a NaN, an infinity or a much larger one
+        base(piece_max(v));
+        if (!(m > -INFINITY)) return;
+#pragma unroll
+        for (uint32_t e = 0; e < kVec; ++e) sum += weight(x[e], m, power);
+    });
     if (singles) {
         const uint32_t i = row.single(threadIdx.x);
         if (i < row.vocab) {
-            m = sample_value(row_to_float(row.x[i]));
-            sum = m > -INFINITY ? 1.0f : 0.0f;
+            const float x = sample_value(row_to_float(row.x[i]));
+            if (x > -INFINITY) join(m, sum, x, 1.0f, power);
         }
-    }
-    auto add = [&](const Piece<T, kVec> *v, auto count) {
-        constexpr int kCount = decltype(count)::value;
-        float top = m;
-#pragma unroll
-        for (int q = 0; q < kCount; ++q) top = fmaxf(top, piece_max(v[q]));
-        top = fminf(top, kLargest);
-        if (!(top > -INFINITY)) return;
-        const float c = top * power;
-        float more = 0.0f;
-#pragma unroll
-        for (int q = 0; q < kCount; ++q)
-#pragma unroll
-            for (uint32_t e = 0; e < kVec; ++e) more += pow2(fmaf(row_to_float(v[q].v[e]), power, -c));
-        if (!(more <= 1.5f * kCount * kVec) || !plain(c)) {  // a NaN or an infinity among them
-            more = 0.0f;
-#pragma unroll
-            for (int q = 0; q < kCount; ++q)
-#pragma unroll
-                for (uint32_t e = 0; e < kVec; ++e) more += weight(row_to_float(v[q].v[e]), top, power);
-        }
-        join(m, sum, top, more, power);
-    };
-    uint32_t j = first + threadIdx.x;
-    const T *from = row.x + row.head;
-    for (; j + (kBatch - 1) * kThreads < end; j += kBatch * kThreads) {
-        Piece<T, kVec> v[kBatch];
-#pragma unroll
-        for (int q = 0; q < kBatch; ++q) v[q] = load_piece<T, kVec>(from + size_t(j + q * kThreads) * kVec);
-        add(v, std::integral_constant<int, kBatch>());
-    }
-    for (; j < end; j += kThreads) {
-        const Piece<T, kVec> v = load_piece<T, kVec>(from + size_t(j) * kVec);
-        add(&v, std::integral_constant<int, 1>());
     }
     join_lanes(m, sum, power);
     Part p;
@@ -207,31 +252,27 @@ __device__ __forceinline__ Part chunk_sum(const Pieces<T> &row, uint32_t first, 
 // The key of the first of a chunk's largest values, to lane 0 of warp 0.
 template <class T>
 __device__ __forceinline__ Part chunk_first(const Pieces<T> &row, uint32_t first, uint32_t end, bool singles,
-                                            Part *s_part)
+                                            uint4 *ring, Part *s_part)
 {
     constexpr uint32_t kVec = Pieces<T>::kVec;
     uint64_t key = first_key(-INFINITY, ~0u);
+    float top = -INFINITY;
+    each_piece(row, first, end, ring, [&](const Piece<T, kVec> &v, uint32_t i) {
+        if (!(piece_max(v) > top)) return;  // a thread's pieces come in order: equal values later count for nothing
+#pragma unroll
+        for (uint32_t e = 0; e < kVec; ++e) {
+            const float x = sample_value(row_to_float(v.v[e]));
+            if (x > top) {
+                top = x;
+                key = first_key(x, i + e);
+            }
+        }
+    });
     if (singles) {
         const uint32_t i = row.single(threadIdx.x);
-        if (i < row.vocab) key = first_key(sample_value(row_to_float(row.x[i])), i);
-    }
-    constexpr int kAhead = kBatch / 2;
-    for (uint32_t base = first + threadIdx.x; base < end; base += kAhead * kThreads) {
-        Piece<T, kVec> v[kAhead];
-#pragma unroll
-        for (int q = 0; q < kAhead; ++q) {
-            const uint32_t j = base + q * kThreads;
-            if (j < end) v[q] = load_piece<T, kVec>(row.x + row.head + size_t(j) * kVec);
-        }
-#pragma unroll
-        for (int q = 0; q < kAhead; ++q) {
-            const uint32_t j = base + q * kThreads;
-            if (j >= end) continue;
-#pragma unroll
-            for (uint32_t e = 0; e < kVec; ++e) {
-                const uint64_t k = first_key(sample_value(row_to_float(v[q].v[e])), row.head + j * kVec + e);
-                key = k > key ? k : key;
-            }
+        if (i < row.vocab) {
+            const uint64_t k = first_key(sample_value(row_to_float(row.x[i])), i);
+            key = k > key ? k : key;
         }
     }
     auto reduce = [&](uint32_t mask, int o) {
@@ -316,19 +357,12 @@ __global__ void __launch_bounds__(kThreads, kWave)
 verify_rows_kernel(Verify a)
 {
     __shared__ Part s_part[kWarps];
+    __shared__ uint4 s_ring[kRing * kThreads];
     chain_start();
-    // unit -> position, sequence, target or draft, chunk
-    const uint32_t kinds = a.d ? 2 : 1, each = a.sequences * kinds * a.chunks;
-    uint32_t unit = blockIdx.x, j = unit / each, kind = 0;
-    if (j >= a.drafts) j = a.drafts;
-    unit -= j * each;
-    const uint32_t c = unit % a.chunks;
-    unit /= a.chunks;
-    if (j < a.drafts) {
-        kind = unit % kinds;
-        unit /= kinds;
-    }
-    const uint32_t b = unit;
+    // positions first, then sequences, target or draft, chunks
+    const uint32_t j = blockIdx.z, kinds = a.d ? 2 : 1, c = blockIdx.x % a.chunks, unit = blockIdx.x / a.chunks;
+    const uint32_t kind = a.d ? unit & 1u : 0u, b = a.d ? unit >> 1 : unit;
+    if (kind == 1 && j == a.drafts) return;
     const int32_t *ids = a.ids + size_t(b) * a.drafts;
     if (a.left == nullptr) {
         if (j == 0 && kind == 0 && c == 0 && threadIdx.x == 0) {
@@ -350,8 +384,8 @@ verify_rows_kernel(Verify a)
                            : static_cast<const T *>(a.d) + (size_t(b) * a.drafts + j) * a.d_stride;
     const Pieces<T> row(x, a.vocab);
     const uint32_t first = min(c * a.chunk, row.count), end = min(first + a.chunk, row.count);
-    const Part p = greedy ? chunk_first(row, first, end, c == 0, s_part)
-                          : chunk_sum(row, first, end, c == 0, power, s_part);
+    const Part p = greedy ? chunk_first(row, first, end, c == 0, s_ring, s_part)
+                          : chunk_sum(row, first, end, c == 0, power, s_ring, s_part);
     Part *to = kind == 0 ? a.x_part + (size_t(b) * (a.drafts + 1) + j) * a.chunks + c
                          : a.d_part + (size_t(b) * a.drafts + j) * a.chunks + c;
     if (threadIdx.x == 0) to->key = p.key;
@@ -413,17 +447,15 @@ struct Stop {
 
     // p - q.  A NaN of the draft weighs nothing; one of the target makes a NaN,
     // which is never taken.
+    __device__ __forceinline__ float usual_r(float v, float w) const
+    {
+        const float p = pow2(__fmaf_rn(v, power, -c)), q = pow2(__fmaf_rn(w, power, -dc));
+        return __fmaf_rn(fmaxf(q, 0.0f), -dinverse, __fmul_rn(p, inverse));
+    }
     __device__ __forceinline__ float r(float v, float w) const
     {
-        float p, q;
-        if (usual) {
-            p = pow2(__fmaf_rn(v, power, -c));
-            q = pow2(__fmaf_rn(w, power, -dc));
-        } else {
-            p = weight(v, m, power);
-            q = weight(w, dm, power);
-        }
-        return __fmaf_rn(fmaxf(q, 0.0f), -dinverse, __fmul_rn(p, inverse));
+        if (usual) return usual_r(v, w);
+        return __fmaf_rn(weight(w, dm, power), -dinverse, __fmul_rn(weight(v, m, power), inverse));
     }
     __device__ __forceinline__ float r(uint32_t i) const
     {
@@ -431,65 +463,80 @@ struct Stop {
     }
 };
 
-// A piece of the three rows on its way.
+// The rings of the draw, in shared memory.
 template <class T>
-struct DrawPiece {
-    static constexpr uint32_t kVec = 16 / sizeof(T);
-    Piece<T, kVec> v, w;
-    float u[kVec];
-
-    __device__ __forceinline__ void load(const Stop<T> &s, uint32_t i, bool there, bool d_whole, bool u_whole)
-    {
-#pragma unroll
-        for (uint32_t e = 0; e < kVec; ++e) {
-            w.v[e] = row_from_float<T>(-INFINITY);
-            u[e] = 0.0f;
-        }
-        if (!there) {  // weights and numbers that cannot win
-            v = w;
-            return;
-        }
-        v = load_piece<T, kVec>(s.x + i);
-        if (d_whole) {
-            w = load_piece<T, kVec>(s.d + i);
-        } else if (s.d) {
-#pragma unroll
-            for (uint32_t e = 0; e < kVec; ++e) w.v[e] = s.d[i + e];
-        }
-#pragma unroll
-        for (uint32_t e = 0; e < kVec; e += 4) {
-            if (u_whole) {
-                const float4 f = *reinterpret_cast<const float4 *>(s.u + i + e);
-                u[e] = f.x, u[e + 1] = f.y, u[e + 2] = f.z, u[e + 3] = f.w;
-            } else {
-#pragma unroll
-                for (uint32_t k = e; k < e + 4; ++k) u[k] = s.u[i + k];
-            }
-        }
-    }
+struct DrawRing {
+    static constexpr int kWords = 4 / sizeof(T);  // of 16 bytes of random numbers per piece
+    uint4 x[kDrawRing][kThreads], d[kDrawRing][kThreads];
+    float4 u[kDrawRing][kWords][kThreads];
 };
 
 // Every thread of the CTA takes part.  Tokens that can win are few, and are
 // read once more, so that their code is there once.
 template <class T>
 __device__ __forceinline__ Best chunk_draw(const Stop<T> &s, const Pieces<T> &row, uint32_t first, uint32_t end,
-                                           bool singles)
+                                           bool singles, DrawRing<T> &ring)
 {
     constexpr uint32_t kVec = Pieces<T>::kVec;
     Best best;
     const bool d_whole = s.d && ((reinterpret_cast<uintptr_t>(s.d + row.head)) & 15u) == 0;
     const bool u_whole = ((reinterpret_cast<uintptr_t>(s.u + row.head)) & 15u) == 0;
-    DrawPiece<T> next;
     uint32_t lone = singles ? row.single(threadIdx.x) : row.vocab;
-    next.load(s, row.head + (first + threadIdx.x) * kVec, first + threadIdx.x < end, d_whole, u_whole);
-    for (uint32_t base = first;; base += kThreads) {
-        const DrawPiece<T> now = next;
-        const uint32_t j = base + threadIdx.x, i = row.head + j * kVec;
-        next.load(s, i + kThreads * kVec, j + kThreads < end, d_whole, u_whole);
-        float r[kVec];
-        uint32_t which = 0;
+    auto copy = [&](uint32_t j, int slot) {
+        if (j < end) {
+            const uint32_t i = row.head + j * kVec;
+            copy_piece(&ring.x[slot][threadIdx.x], s.x + i, true);
+            copy_piece(&ring.d[slot][threadIdx.x], s.d + i, d_whole);
 #pragma unroll
-        for (uint32_t e = 0; e < kVec; ++e) r[e] = s.r(row_to_float(now.v.v[e]), row_to_float(now.w.v[e]));
+            for (int q = 0; q < DrawRing<T>::kWords; ++q) {
+                float4 *to = &ring.u[slot][q][threadIdx.x];
+                if (u_whole) {
+                    copy_piece(to, s.u + i + 4 * q, true);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) copy_float(reinterpret_cast<float *>(to) + e, s.u + i + 4 * q + e);
+                }
+            }
+        }
+        commit_copies();
+    };
+#pragma unroll
+    for (int q = 0; q < kDrawRing; ++q) copy(first + threadIdx.x + q * kThreads, q);
+    int slot = 0;
+    for (uint32_t base = first;; base += kThreads) {
+        const uint32_t j = base + threadIdx.x, i = row.head + j * kVec;
+        float r[kVec], u[kVec];
+        uint32_t which = 0;
+        wait_copies<kDrawRing - 1>();
+#pragma unroll
+        for (uint32_t e = 0; e < kVec; ++e) r[e] = u[e] = 0.0f;
+        if (j < end) {
+            const Piece<T, kVec> v = load_piece<T, kVec>(reinterpret_cast<const T *>(&ring.x[slot][threadIdx.x]));
+            Piece<T, kVec> w;
+            if (d_whole) {
+                w = load_piece<T, kVec>(reinterpret_cast<const T *>(&ring.d[slot][threadIdx.x]));
+            } else {
+#pragma unroll
+                for (uint32_t e = 0; e < kVec; ++e) w.v[e] = s.d ? s.d[i + e] : row_from_float<T>(-INFINITY);
+            }
+#pragma unroll
+            for (uint32_t e = 0; e < kVec; e += 4) {
+                const float4 f = ring.u[slot][e / 4][threadIdx.x];
+                u[e] = f.x, u[e + 1] = f.y, u[e + 2] = f.z, u[e + 3] = f.w;
+            }
+            float x[kVec], d[kVec];
+            piece_values(v, x);
+            piece_values(w, d);
+            if (s.usual) {
+#pragma unroll
+                for (uint32_t e = 0; e < kVec; ++e) r[e] = s.usual_r(x[e], d[e]);
+            } else {
+#pragma unroll
+                for (uint32_t e = 0; e < kVec; ++e) r[e] = s.r(x[e], d[e]);
+            }
+        }
+        copy(j + kDrawRing * kThreads, slot);
+        slot = slot + 1 < kDrawRing ? slot + 1 : 0;
         if (best.bound == 0.0f) {  // in the whole warp
             // a first bound by each thread's largest r, and its single element
             float top = 0.0f;
@@ -506,7 +553,7 @@ __device__ __forceinline__ Best chunk_draw(const Stop<T> &s, const Pieces<T> &ro
         }
 #pragma unroll
         for (uint32_t e = 0; e < kVec; ++e)
-            if (best.open(r[e], now.u[e])) which |= 1u << e;
+            if (best.open(r[e], u[e])) which |= 1u << e;
         for (; which; which &= which - 1) {
             const uint32_t t = i + __ffs(which) - 1;
             if (t < row.vocab && t != s.without) best.take(s.r(t), s.u[t], t);
@@ -514,6 +561,7 @@ __device__ __forceinline__ Best chunk_draw(const Stop<T> &s, const Pieces<T> &ro
         best.share();
         if (base + kThreads >= end) break;
     }
+    wait_copies<0>();
     return best;
 }
 
@@ -543,6 +591,8 @@ verify_draw_kernel(Verify a)
     __shared__ uint64_t s_key[kWarps];
     __shared__ uint32_t s_stop, s_last;
     __shared__ int32_t s_token;
+    extern __shared__ uint4 s_rings[];
+    DrawRing<T> &ring = *reinterpret_cast<DrawRing<T> *>(s_rings);
     const uint32_t b = blockIdx.x / a.draws, c = blockIdx.x % a.draws;
     const float t = a.t(b), power = power_of(t);
     const bool greedy = !(t > 0.0f);
@@ -551,27 +601,35 @@ verify_draw_kernel(Verify a)
     chain_wait();
     // Where the rows' kernel has decided, only the row at which the sequence
     // stops is looked up now, the others by the CTA that writes the results.
-    const uint32_t decided = a.left ? a.drafts - a.left[b] : ~0u;
-    auto look = [&](uint32_t from, uint32_t to) {
-        for (uint32_t j = from + (threadIdx.x >> 5); j < to; j += kWarps) {
-            Part target, draft;
-            const bool ok = decide<T>(a, b, j, target, draft);
-            if ((threadIdx.x & 31) == 0) {
-                s_ok[j] = ok;
-                s_target[j] = target;
-                s_draft[j] = draft;
-            }
+    const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    auto target_row = [&](uint32_t j) {
+        return row_part(a.x_part + (size_t(b) * (a.drafts + 1) + j) * a.chunks, a.chunks, greedy, power);
+    };
+    if (a.left) {
+        const uint32_t j = a.drafts - a.left[b];
+        if (warp == 0) {
+            const Part part = target_row(j);
+            if (lane == 0) s_target[j] = part, s_stop = j;
+        } else if (warp == 1 && a.d && !greedy && j < a.drafts) {
+            // of use only if the drafted token is one
+            const Part part = row_part(a.d_part + (size_t(b) * a.drafts + j) * a.chunks, a.chunks, false, power);
+            if (lane == 0) s_draft[j] = part;
         }
         __syncthreads();
-    };
-    if (decided <= a.drafts) look(decided, decided + 1);
-    else look(0, a.drafts + 1);
-    if (threadIdx.x == 0) {
-        uint32_t j = decided <= a.drafts ? decided : 0;
-        while (decided > a.drafts && j < a.drafts && s_ok[j]) ++j;
-        s_stop = j;
+    } else {
+        for (uint32_t j = warp; j <= a.drafts; j += kWarps) {
+            Part target, draft;
+            const bool ok = decide<T>(a, b, j, target, draft);
+            if (lane == 0) s_ok[j] = ok, s_target[j] = target, s_draft[j] = draft;
+        }
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            uint32_t j = 0;
+            while (j < a.drafts && s_ok[j]) ++j;
+            s_stop = j;
+        }
+        __syncthreads();
     }
-    __syncthreads();
     const uint32_t stop = s_stop;
     const T *x = static_cast<const T *>(a.x) + size_t(b) * (a.drafts + 1) * a.x_stride;
     if (greedy) {
@@ -587,8 +645,10 @@ verify_draw_kernel(Verify a)
         s.u = a.uniform + size_t(b) * a.u_stride;
         s.m = s_target[stop].m;
         s.inverse = s_target[stop].sum > 0.0f ? 1.0f / s_target[stop].sum : 0.0f;
-        s.dm = s_draft[stop].m;
-        s.dinverse = s_draft[stop].sum > 0.0f ? 1.0f / s_draft[stop].sum : 0.0f;
+        if (s.d) {
+            s.dm = s_draft[stop].m;
+            s.dinverse = s_draft[stop].sum > 0.0f ? 1.0f / s_draft[stop].sum : 0.0f;
+        }
         s.power = power;
         s.without = rejected && !a.d ? uint32_t(ids[stop]) : ~0u;
         const Pieces<T> row(s.x, a.vocab);
@@ -598,7 +658,7 @@ verify_draw_kernel(Verify a)
             if (!s.d) s.dm = 0.0f, s.dinverse = 0.0f;
             s.c = s.m * power, s.dc = s.dm * power;
             s.usual = plain(s.c) && s.m < kLargest && plain(s.dc) && s.dm < kLargest;
-            key = cta_largest(chunk_draw(s, row, first, end, again || c == 0).key(), s_key);
+            key = cta_largest(chunk_draw(s, row, first, end, again || c == 0, ring).key(), s_key);
             if (again) break;
             if (threadIdx.x == 0) {
                 if (key) atomicMax(a.best + b, static_cast<unsigned long long>(key));
@@ -617,7 +677,11 @@ verify_draw_kernel(Verify a)
         }
         if (threadIdx.x == 0) s_token = key ? int32_t(uint32_t(~key)) : -1;
     }
-    if (decided <= a.drafts) look(0, decided);
+    if (a.left)
+        for (uint32_t j = warp; j < stop; j += kWarps) {
+            const Part part = target_row(j);
+            if (lane == 0) s_target[j] = part;
+        }
     __syncthreads();
     if (threadIdx.x == 0) a.accepted[b] = int32_t(stop);
     for (uint32_t j = threadIdx.x; j <= a.drafts; j += kThreads) {
@@ -698,10 +762,14 @@ cudaError_t run_verify(Verify a, uint8_t *ws, cudaStream_t s)
     a.draws = uint32_t(gch::kSms * kDrawWave / a.sequences);
     a.draws = a.draws < 1 ? 1 : a.draws < most ? a.draws : most;
     a.draw = uint32_t(gch::ceil_div(pieces, a.draws));
-    verify_rows_kernel<T><<<uint32_t((target_rows + draft_rows) * plan.chunks), kThreads, 0, s>>>(a);
-    const cudaError_t e = cudaGetLastError();
+    const dim3 grid(a.sequences * (a.d ? 2 : 1) * plan.chunks, 1, a.drafts + 1);
+    verify_rows_kernel<T><<<grid, kThreads, 0, s>>>(a);
+    cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    return gch::launch_next(verify_draw_kernel<T>, dim3(a.sequences * a.draws), dim3(kThreads), 0, s, a);
+    constexpr size_t kSmem = sizeof(DrawRing<T>);
+    e = cudaFuncSetAttribute(verify_draw_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmem));
+    if (e != cudaSuccess) return e;
+    return gch::launch_next(verify_draw_kernel<T>, dim3(a.sequences * a.draws), dim3(kThreads), kSmem, s, a);
 }
 
 }  // namespace

@@ -613,7 +613,8 @@ def _scratch(ws: torch.Tensor | None, nbytes: int, device, stream) -> torch.Tens
     return ws if ws is not None else _new(max(nbytes, 256), torch.uint8, device, stream)
 
 
-# gc_expert_workspace_bytes of a dispatch whose workspace is checked and not touched.
+# gc_expert_workspace_bytes and gc_expert_route_workspace_bytes of calls whose
+# workspace is checked and not touched.
 EXPERT_WORKSPACE_UNUSED = 256
 
 
@@ -835,13 +836,24 @@ def sample(logits: torch.Tensor, uniform: torch.Tensor | None = None, temperatur
 def _rows3(t: torch.Tensor, what: str) -> tuple[int, int]:
     """(pointer, row stride) of a [n, m, width] tensor whose rows are one row array."""
     _on_device(t)
-    shape, stride = t.shape, t.stride()
-    if len(shape) == 3 and t.numel() == 0:
-        return t.data_ptr(), shape[2]
-    if len(shape) != 3 or (stride[2] != 1 and shape[2] > 1) or \
-            (shape[0] > 1 and shape[1] > 1 and stride[0] != shape[1] * stride[1]):
-        raise ValueError(f"{what} is a 3-D tensor of contiguous rows, the same distance apart throughout")
-    return t.data_ptr(), stride[1] if shape[1] > 1 else stride[0] if shape[0] > 1 else shape[2]
+    if t.dim() == 3:
+        n, m, width = t.shape
+        outer, row, inner = t.stride()
+        if (inner == 1 or width == 1) and (n == 1 or m == 1 or outer == m * row):
+            return t.data_ptr(), row if m > 1 else outer if n > 1 else width
+        if t.numel() == 0:
+            return t.data_ptr(), width
+    raise ValueError(f"{what} is a 3-D tensor of contiguous rows, the same distance apart throughout")
+
+
+def _out(t: torch.Tensor | None, shape, dtype: torch.dtype, device, stream, what: str) -> tuple[torch.Tensor, int]:
+    """The caller's contiguous output, checked, or a new one; and its pointer."""
+    if t is None:
+        t = _new(shape, dtype, device, stream)
+        return t, t.data_ptr()
+    if t.shape != shape or t.dtype != dtype:
+        raise ValueError(f"{what} is a {dtype} tensor of shape {tuple(shape)}")
+    return t, _ptr(t)
 
 
 class Routing(NamedTuple):
@@ -851,6 +863,9 @@ class Routing(NamedTuple):
     counts: torch.Tensor | None   # [experts + 1] int32: pairs of each expert; tokens with a choice
     load: torch.Tensor | None     # [experts] float32, mean probabilities
     loss: torch.Tensor | None     # [1] float32
+
+
+_NO_ROUTING = Routing(None, None, None, None, None)
 
 
 @lru_cache(maxsize=1024)
@@ -874,19 +889,21 @@ def expert_route(logits: torch.Tensor, topk: int, normalize: bool = True, mask: 
     dev = logits.device
     if not 0 < topk <= experts:
         raise ValueError(f"topk is a number of [1, {experts}]")
-    o = out if out is not None else Routing(None, None, None, None, None)
-    ids = _like(o.ids, (tokens, topk), torch.int32, dev, stream, "out.ids")
-    weights = _like(o.weights, (tokens, topk), torch.float32, dev, stream, "out.weights")
-    counts = means = loss = None
+    o = out if out is not None else _NO_ROUTING
+    ids, ip = _out(o.ids, (tokens, topk), torch.int32, dev, stream, "out.ids")
+    weights, wp = _out(o.weights, (tokens, topk), torch.float32, dev, stream, "out.weights")
+    counts = means = loss = cp = mp = sp = None
     if balance:
-        counts = _like(o.counts, (experts + 1,), torch.int32, dev, stream, "out.counts")
-        means = _like(o.load, (experts,), torch.float32, dev, stream, "out.load")
-        loss = _like(o.loss, (1,), torch.float32, dev, stream, "out.loss")
-    ws = _scratch(ws, expert_route_workspace_bytes(tokens, experts), dev, stream)
+        counts, cp = _out(o.counts, (experts + 1,), torch.int32, dev, stream, "out.counts")
+        means, mp = _out(o.load, (experts,), torch.float32, dev, stream, "out.load")
+        loss, sp = _out(o.loss, (1,), torch.float32, dev, stream, "out.loss")
+    if ws is None:
+        need = expert_route_workspace_bytes(tokens, experts) if balance else EXPERT_WORKSPACE_UNUSED
+        ws = _untouched(dev) if need == EXPERT_WORKSPACE_UNUSED else _scratch(None, need, dev, stream)
     _check(load().gc_expert_route(
         lp, ls, tokens, experts, row_dtype_code(logits.dtype), topk, int(normalize),
-        _typed(mask, torch.bool, tokens, "mask"), _ptr(ids), _ptr(weights), _ptr(counts), _ptr(means), _ptr(loss),
-        _ptr(ws), ws.numel(), _handle(stream, dev)), "gc_expert_route")
+        None if mask is None else _typed(mask, torch.bool, tokens, "mask"), ip, wp, cp, mp, sp, _ptr(ws), ws.numel(),
+        _handle(stream, dev)), "gc_expert_route")
     return Routing(ids, weights, counts, means, loss)
 
 
@@ -939,30 +956,30 @@ def sample_verify(logits: torch.Tensor, drafts: torch.Tensor, accept: torch.Tens
     sequences, places, vocab = logits.shape
     n = places - 1
     dev = logits.device
-    if n < 0 or drafts.dim() != 2 or tuple(drafts.shape) != (sequences, n):
+    if n < 0 or drafts.shape != (sequences, n):
         raise ValueError("logits is [sequences, drafts + 1, vocab] and drafts [sequences, drafts]")
     dp, ds = None, 0
     if draft_logits is not None:
-        if draft_logits.dtype != logits.dtype or tuple(draft_logits.shape) != (sequences, n, vocab):
+        if draft_logits.dtype != logits.dtype or draft_logits.shape != (sequences, n, vocab):
             raise ValueError(f"draft_logits is a {logits.dtype} tensor of shape {(sequences, n, vocab)}")
         dp, ds = _rows3(draft_logits, "draft_logits")
     up, us = None, 0
     if (accept is None) != (uniform is None):
         raise ValueError("accept and uniform come together")
     if uniform is not None:
-        if uniform.dtype != torch.float32 or tuple(uniform.shape) != (sequences, vocab):
+        if uniform.dtype != torch.float32 or uniform.shape != (sequences, vocab):
             raise ValueError(f"uniform is a float32 tensor of shape {(sequences, vocab)}")
         up, us = _rows(uniform)
     temperature = _per_row(temperature, torch.float32, sequences, dev, stream)
-    tokens = _like(tokens, (sequences, places), torch.int32, dev, stream, "tokens")
-    accepted = _like(accepted, (sequences,), torch.int32, dev, stream, "accepted")
-    logprobs = _like(logprobs, (sequences, places), torch.float32, dev, stream, "logprobs")
+    tokens, tp = _out(tokens, (sequences, places), torch.int32, dev, stream, "tokens")
+    accepted, np = _out(accepted, (sequences,), torch.int32, dev, stream, "accepted")
+    logprobs, pp = _out(logprobs, (sequences, places), torch.float32, dev, stream, "logprobs")
     ws = _scratch(ws, sample_verify_workspace_bytes(sequences, n, vocab), dev, stream)
     _check(load().gc_sample_verify(
         lp, ls, dp, ds, sequences, n, vocab, row_dtype_code(logits.dtype),
         _typed(drafts, torch.int32, sequences * n, "drafts"), _typed(accept, torch.float32, sequences * n, "accept"),
-        up, us, _typed(temperature, torch.float32, sequences, "temperature"), _ptr(tokens), _ptr(accepted),
-        _ptr(logprobs), _ptr(ws), ws.numel(), _handle(stream, dev)), "gc_sample_verify")
+        up, us, _typed(temperature, torch.float32, sequences, "temperature"), tp, np, pp, _ptr(ws), ws.numel(),
+        _handle(stream, dev)), "gc_sample_verify")
     return tokens, accepted, logprobs
 
 
@@ -981,11 +998,12 @@ def cache_score(weights: torch.Tensor, scores: torch.Tensor | None, heads: int |
         raise ValueError("weights is a 4-D tensor [batch, query heads, queries, length] of contiguous rows")
     _on_device(weights)
     batch, query_heads, count, length = weights.shape
+    sb, sh, sq, _ = weights.stride()
     if scores is not None:
         if heads not in (None, scores.size(1)):
             raise ValueError(f"scores has {scores.size(1)} heads, not {heads}")
         heads = scores.size(1)
-        if scores.dtype != torch.float32 or tuple(scores.shape) != (batch, heads, length):
+        if scores.dtype != torch.float32 or scores.shape != (batch, heads, length):
             raise ValueError(f"scores is a float32 tensor of shape {(batch, heads, length)}")
     if not heads or query_heads % heads or not query_heads:
         raise ValueError(f"{query_heads} query heads share {heads} heads of a cache")
@@ -993,9 +1011,8 @@ def cache_score(weights: torch.Tensor, scores: torch.Tensor | None, heads: int |
     out = _like(out, (batch, heads, length), torch.float32, dev, stream, "out")
     sp, ss = (None, 0) if scores is None else _rows3(scores, "scores")
     op, os = _rows3(out, "out")
-    strides = [s if n > 1 else 0 for s, n in zip(weights.stride(), weights.shape)]
     _check(load().gc_cache_score(
-        weights.data_ptr(), *strides[:3], row_dtype_code(weights.dtype), batch, heads, query_heads // heads, count,
+        weights.data_ptr(), sb if batch > 1 else 0, sh if query_heads > 1 else 0, sq if count > 1 else 0, row_dtype_code(weights.dtype), batch, heads, query_heads // heads, count,
         length, sp, ss, decay, _typed(lengths, torch.int32, batch, "lengths"),
         _typed(queries, torch.int32, batch, "queries"), op, os, _handle(stream, dev)), "gc_cache_score")
     return out
@@ -1018,13 +1035,18 @@ def cache_evict_workspace_bytes(batch: int, heads: int, budget: int) -> int:
 def _cache_rows(t: torch.Tensor) -> CacheRows:
     """A [batch, heads, length, width] tensor whose rows are contiguous."""
     _on_device(t)
-    shape, stride = t.shape, t.stride()
-    if len(shape) == 4 and t.numel() == 0:
-        return CacheRows(t.data_ptr(), 0, 0, shape[3], shape[3])
-    if len(shape) != 4 or (stride[3] != 1 and shape[3] > 1):
-        raise ValueError("libgc takes 4-D caches [batch, heads, length, width] whose rows are contiguous")
-    return CacheRows(t.data_ptr(), *(s if n > 1 else 0 for s, n in zip(stride[:2], shape)),
-                     stride[2] if shape[2] > 1 else shape[3], shape[3])
+    if t.dim() == 4:
+        batch, heads, length, width = t.shape
+        outer, head, row, inner = t.stride()
+        if inner == 1 or width == 1:
+            return CacheRows(t.data_ptr(), outer if batch > 1 else 0, head if heads > 1 else 0,
+                             row if length > 1 else width, width)
+        if t.numel() == 0:
+            return CacheRows(t.data_ptr(), 0, 0, width, width)
+    raise ValueError("libgc takes 4-D caches [batch, heads, length, width] whose rows are contiguous")
+
+
+_NOTHING_KEPT = KeptCache(None, None, None, None, None)
 
 
 def cache_evict(keys: torch.Tensor, values: torch.Tensor | None, scores: torch.Tensor, budget: int, sinks: int = 0,
@@ -1043,23 +1065,26 @@ def cache_evict(keys: torch.Tensor, values: torch.Tensor | None, scores: torch.T
     kr = _cache_rows(keys)
     batch, heads, length, width = shape
     dev = keys.device
-    if scores.dtype != torch.float32 or tuple(scores.shape) != (batch, heads, length):
+    if scores.dtype != torch.float32 or scores.shape != (batch, heads, length):
         raise ValueError(f"scores is a float32 tensor of shape {(batch, heads, length)}")
     if budget < 1 or sinks < 0 or recent < 0 or sinks + recent > budget:
         raise ValueError("budget is at least 1, and sinks and recent fit into it")
     sp, ss = _rows3(scores, "scores")
     pp, ps = None, 0
     if positions is not None:
-        if positions.dtype != torch.int32 or tuple(positions.shape) != (batch, heads, length):
+        if positions.dtype != torch.int32 or positions.shape != (batch, heads, length):
             raise ValueError(f"positions is an int32 tensor of shape {(batch, heads, length)}")
         pp, ps = _rows3(positions, "positions")
     fill = 0 if lengths is not None or length < budget else None
-    o = out if out is not None else KeptCache(None, None, None, None, None)
+    o = out if out is not None else _NOTHING_KEPT
 
     def rows(mine, t, what):
+        size = (batch, heads, budget, t.size(3))
         if mine is None:
-            return _new((batch, heads, budget, t.size(3)), t.dtype, dev, stream, fill)
-        return _like(mine, (batch, heads, budget, t.size(3)), t.dtype, dev, stream, what)
+            return _new(size, t.dtype, dev, stream, fill)
+        if mine.shape != size or mine.dtype != t.dtype:
+            raise ValueError(f"{what} is a {t.dtype} tensor of shape {size}")
+        return mine
 
     kept_keys = rows(o.keys, keys, "out.keys")
     vr = kvr = kept_values = None
@@ -1069,12 +1094,13 @@ def cache_evict(keys: torch.Tensor, values: torch.Tensor | None, scores: torch.T
         vr = _cache_rows(values)
         kept_values = rows(o.values, values, "out.values")
         kvr = _cache_rows(kept_values)
-    kept_scores = _like(o.scores, (batch, heads, budget), torch.float32, dev, stream, "out.scores")
-    kept_positions = _like(o.positions, (batch, heads, budget), torch.int32, dev, stream, "out.positions")
-    kept_lengths = _like(o.lengths, (batch,), torch.int32, dev, stream, "out.lengths")
+    kept_scores, ksp = _out(o.scores, (batch, heads, budget), torch.float32, dev, stream, "out.scores")
+    kept_positions, kpp = _out(o.positions, (batch, heads, budget), torch.int32, dev, stream, "out.positions")
+    kept_lengths, klp = _out(o.lengths, (batch,), torch.int32, dev, stream, "out.lengths")
     ws = _scratch(ws, cache_evict_workspace_bytes(batch, heads, budget), dev, stream)
     _check(load().gc_cache_evict(
-        kr, vr, row_dtype_code(keys.dtype), sp, ss, pp, ps, _typed(lengths, torch.int32, batch, "lengths"), batch,
-        heads, length, budget, sinks, recent, _cache_rows(kept_keys), kvr, _ptr(kept_scores), _ptr(kept_positions),
-        _ptr(kept_lengths), _ptr(ws), ws.numel(), _handle(stream, dev)), "gc_cache_evict")
+        kr, vr, row_dtype_code(keys.dtype), sp, ss, pp, ps,
+        None if lengths is None else _typed(lengths, torch.int32, batch, "lengths"), batch, heads, length, budget,
+        sinks, recent, _cache_rows(kept_keys), kvr, ksp, kpp, klp, _ptr(ws), ws.numel(), _handle(stream, dev)),
+        "gc_cache_evict")
     return KeptCache(kept_keys, kept_values, kept_scores, kept_positions, kept_lengths)
