@@ -6,6 +6,8 @@
 // cache's head.  Eviction is a stable select-if whose predicate is "among the
 // first or the last positions, or among the highest scores between them", with
 // a row of keys and one of values attached to each element.
+#include <atomic>
+
 #include "gc_rows.cuh"
 #include "gc_rows_internal.h"
 
@@ -197,10 +199,23 @@ cache_select_kernel(Evict a)
     constexpr uint32_t kChunk = K * kEvictThreads;
     const bool once = end - first <= kChunk;
     uint32_t key[K];  // 0: no position
+    extern __shared__ uint32_t s_turn[];
+    // Read across the warp and turned in shared memory (rows of K + 1 words, so
+    // that neither way meets a bank twice): K neighbouring positions to a lane.
     auto load = [&](uint32_t at) {
+        uint32_t *mine = s_turn + warp * (32 * (K + 1));
         const uint32_t from = at + warp * (32 * K) + lane;
 #pragma unroll
         for (int k = 0; k < K; ++k) key[k] = from + 32 * k < end ? score_key(scores[from + 32 * k]) : 0u;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const uint32_t i = 32 * k + lane;
+            mine[i / K * (K + 1) + i % K] = key[k];
+        }
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < K; ++k) key[k] = mine[lane * (K + 1) + k];
+        __syncwarp();
     };
     if (want == 0) return;
     if (once) load(first);
@@ -245,22 +260,30 @@ cache_select_kernel(Evict a)
     }
 
     // `rest` of the scores at the cut are kept: how many of either kind lie before this CTA's
-    uint32_t up = 0, eq = 0;
+    auto compare = [&](uint32_t &above, uint32_t &equal) {
+        above = equal = 0;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            above |= uint32_t(key[k] > cut) << k;
+            equal |= uint32_t(key[k] == cut) << k;
+        }
+    };
+    uint32_t up = 0, eq = 0, above, equal;
     if (team > 1) {
-        uint32_t above = 0, equal = 0;
+        uint32_t more = 0, same = 0;
         for (uint32_t at = first; at < end; at += kChunk) {
             if (!once) load(at);
-#pragma unroll
-            for (int k = 0; k < K; ++k) above += key[k] > cut, equal += key[k] == cut;
+            compare(above, equal);
+            more += __popc(above), same += __popc(equal);
         }
-        above = __reduce_add_sync(kFull, above);
-        equal = __reduce_add_sync(kFull, equal);
-        if (lane == 0) sm.warp[warp] = above, sm.equals[warp] = equal;
+        more = __reduce_add_sync(kFull, more);
+        same = __reduce_add_sync(kFull, same);
+        if (lane == 0) sm.warp[warp] = more, sm.equals[warp] = same;
         __syncthreads();
         if (warp == 0) {
-            above = __reduce_add_sync(kFull, sm.warp[lane]);
-            equal = __reduce_add_sync(kFull, sm.equals[lane]);
-            if (lane == 0) sm.above = above, sm.equal = equal;
+            more = __reduce_add_sync(kFull, sm.warp[lane]);
+            same = __reduce_add_sync(kFull, sm.equals[lane]);
+            if (lane == 0) sm.above = more, sm.equal = same;
         }
         cluster_sync();
         for (uint32_t q = 0; q < rank; ++q) {
@@ -269,34 +292,34 @@ cache_select_kernel(Evict a)
         }
         cluster_sync();  // nobody looks into another CTA any more
     }
-    const uint32_t below = (1u << lane) - 1u;
     for (uint32_t at = first; at < end; at += kChunk) {
         if (!once) load(at);
-        uint32_t above = 0, equal = 0;
+        compare(above, equal);
+        // of either kind before this lane's: in the low and the high half, in this warp at most K * 32
+        const uint32_t mine = uint32_t(__popc(above)) | uint32_t(__popc(equal)) << 16;
+        uint32_t upto = mine;
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            above += __popc(__ballot_sync(kFull, key[k] > cut));
-            equal += __popc(__ballot_sync(kFull, key[k] == cut));
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t y = __shfl_up_sync(kFull, upto, o);
+            if (lane >= uint32_t(o)) upto += y;
         }
         __syncthreads();
-        if (lane == 0) sm.warp[warp] = above, sm.equals[warp] = equal;
+        if (lane == 31) sm.warp[warp] = upto & 0xffffu, sm.equals[warp] = upto >> 16;
         __syncthreads();
-        uint32_t my_up = up + __reduce_add_sync(kFull, lane < warp ? sm.warp[lane] : 0u);
-        uint32_t my_eq = eq + __reduce_add_sync(kFull, lane < warp ? sm.equals[lane] : 0u);
+        uint32_t my_up = up + __reduce_add_sync(kFull, lane < warp ? sm.warp[lane] : 0u) + ((upto - mine) & 0xffffu);
+        uint32_t my_eq = eq + __reduce_add_sync(kFull, lane < warp ? sm.equals[lane] : 0u) + ((upto - mine) >> 16);
         up += __reduce_add_sync(kFull, sm.warp[lane]);
         eq += __reduce_add_sync(kFull, sm.equals[lane]);
-        const uint32_t from = at + warp * (32 * K) + lane;
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const bool is_above = key[k] > cut, is_equal = key[k] == cut;
-            const uint32_t ma = __ballot_sync(kFull, is_above), me_ = __ballot_sync(kFull, is_equal);
-            const uint32_t e = my_eq + __popc(me_ & below);
-            if (is_above || (is_equal && e < rest)) {
-                const uint32_t slot = a.sinks + my_up + __popc(ma & below) + min(e, rest);
-                if (slot < a.budget) list[slot] = int32_t(from + 32 * k);  // beyond it only if the scores change meanwhile
+        const uint32_t from = at + warp * (32 * K) + lane * K;
+        for (uint32_t both = above | equal; both; both &= both - 1) {
+            const uint32_t k = __ffs(both) - 1;
+            const bool is_equal = equal >> k & 1u;
+            if (!is_equal || my_eq < rest) {
+                const uint32_t slot = a.sinks + my_up + min(my_eq, rest);
+                if (slot < a.budget) list[slot] = int32_t(from + k);  // beyond it only if the scores change meanwhile
             }
-            my_up += __popc(ma);
-            my_eq += __popc(me_);
+            my_up += !is_equal;
+            my_eq += is_equal;
         }
     }
 }
@@ -372,6 +395,23 @@ cache_move_kernel(Evict a, Move m, uint32_t down, uint32_t early)
                 reinterpret_cast<P *>(to + size_t(first + k * blockDim.y) * m.to[w].row)[c] = v[k];
     }
     if (known) chain_wait();  // the launch is done when both kernels are
+}
+
+template <int K>
+cudaError_t run_select(cudaLaunchConfig_t cfg, const Evict &a)
+{
+    cfg.dynamicSmemBytes = kEvictWarps * 32 * (K + 1) * sizeof(uint32_t);
+    // the attribute lasts as long as the process: set once for each device
+    static std::atomic<uint64_t> set{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    const uint64_t bit = uint64_t(1) << (dev & 63);
+    if (e == cudaSuccess && (dev > 63 || !(set.load(std::memory_order_relaxed) & bit))) {
+        e = cudaFuncSetAttribute(cache_select_kernel<K>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 int(cfg.dynamicSmemBytes));
+        if (e == cudaSuccess) set.fetch_or(bit, std::memory_order_relaxed);
+    }
+    return e == cudaSuccess ? cudaLaunchKernelEx(&cfg, cache_select_kernel<K>, a) : e;
 }
 
 template <class P>
@@ -458,8 +498,7 @@ cudaError_t launch_cache_evict(const gc_cache_rows *keys, const gc_cache_rows *v
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    cudaError_t e = length <= team * 4 * kEvictThreads ? cudaLaunchKernelEx(&cfg, cache_select_kernel<4>, a)
-                                                       : cudaLaunchKernelEx(&cfg, cache_select_kernel<32>, a);
+    cudaError_t e = length <= team * 4 * kEvictThreads ? run_select<4>(cfg, a) : run_select<32>(cfg, a);
     if (e != cudaSuccess) return e;
 
     Move m{};

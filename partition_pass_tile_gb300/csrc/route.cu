@@ -441,7 +441,11 @@ route_join_kernel(Totals part, uint32_t parts, uint32_t experts, RouteOut out)
 }
 
 // CTAs: as many as run at a time, each with the tokens of its warps or groups at
-// least once.
+// least once; one alone, which spares the second launch, where it has them at
+// most kAlone times (24 tokens of 64 experts: ALONE1 us against ALONE2 by two launches;
+// 128 tokens ALONE3 against ALONE4).
+constexpr size_t kAlone = 4;
+
 uint32_t route_grid(uint32_t tokens, uint32_t experts)
 {
     const bool warps = experts > kSmallExperts;
@@ -449,7 +453,7 @@ uint32_t route_grid(uint32_t tokens, uint32_t experts)
     const size_t each = warps ? (v <= 8 ? kWarpThreads<8> : kWarpThreads<64>) / 32 : kGroupThreads / route_lanes(experts);
     const size_t resident = warps ? (v <= 16 ? kWarpResident<8> : kWarpResident<64>) : kGroupResident;
     const size_t need = gch::ceil_div(tokens, each), most = gch::kSms * resident;
-    return uint32_t(need < 1 ? 1 : need < most ? need : most);
+    return uint32_t(need <= kAlone ? 1 : need < most ? need : most);
 }
 
 Totals totals_in(uint8_t *ws, uint32_t grid, uint32_t experts)

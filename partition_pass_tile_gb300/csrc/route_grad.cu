@@ -39,7 +39,7 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 
 template <int V>
-constexpr int kResident = V <= 8 ? 4 : V == 16 ? 3 : 1;  // CTAs per SM
+constexpr int kResident = V <= 8 ? 3 : V == 16 ? 2 : 1;  // CTAs per SM
 
 template <class T, int N, int V>
 __global__ void __launch_bounds__(kThreads, kResident<V>)

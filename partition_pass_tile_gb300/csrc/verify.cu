@@ -19,6 +19,8 @@
 // exp((x - m) / T) is 2^(x f - c) with f = log2(e) / T and c = m f rounded: one
 // multiply-add, whose only rounding is that of the exponent, since every weight
 // of a row carries the same 2^(m f - c) and p is a quotient of them.
+#include <atomic>
+
 #include "gc_rows.cuh"
 #include "gc_rows_internal.h"
 
@@ -766,8 +768,16 @@ cudaError_t run_verify(Verify a, uint8_t *ws, cudaStream_t s)
     verify_rows_kernel<T><<<grid, kThreads, 0, s>>>(a);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
+    // the attribute lasts as long as the process: set once for each device
     constexpr size_t kSmem = sizeof(DrawRing<T>);
-    e = cudaFuncSetAttribute(verify_draw_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmem));
+    static std::atomic<uint64_t> set{0};
+    int dev = 0;
+    e = cudaGetDevice(&dev);
+    const uint64_t bit = uint64_t(1) << (dev & 63);
+    if (e == cudaSuccess && (dev > 63 || !(set.load(std::memory_order_relaxed) & bit))) {
+        e = cudaFuncSetAttribute(verify_draw_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmem));
+        if (e == cudaSuccess) set.fetch_or(bit, std::memory_order_relaxed);
+    }
     if (e != cudaSuccess) return e;
     return gch::launch_next(verify_draw_kernel<T>, dim3(a.sequences * a.draws), dim3(kThreads), kSmem, s, a);
 }
