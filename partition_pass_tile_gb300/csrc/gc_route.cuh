@@ -13,25 +13,15 @@ constexpr uint32_t kRouteNone = 0x007fffffu;  // order_bits(-inf): no expert
 constexpr float kLog2e = 1.44269504f;
 
 // Up to kSmallExperts experts a token belongs to a group of 1, 2 or 4 lanes with
-// eight each, more of them to a warp with V each: 131072 tokens of 32 experts,
-// top-4, take GROUP us by groups and WARP by warps, of 64 GROUP64 and WARP64.
+// eight each, more of them to a team of 8, 16 or 32 lanes.
 constexpr uint32_t kSmallExperts = 32;
 constexpr int kGroupValues = 8;
 
 inline uint32_t route_lanes(uint32_t experts)
 {
-    if (experts > kSmallExperts) return 32;
     uint32_t lanes = 1;
     while (lanes * kGroupValues < experts) lanes *= 2;
     return lanes;
-}
-
-// Experts of a lane of a warp.
-inline int route_values(uint32_t experts)
-{
-    for (int v : {2, 4, 8, 16})
-        if (experts <= 32u * uint32_t(v)) return v;
-    return 64;
 }
 
 // This lane's logits of a token, -inf where there is none.
@@ -84,19 +74,48 @@ __device__ __forceinline__ float warp_sum(float v)
     return v;
 }
 
-// A warp's token: w[V] are the weights exp(x - m) of its logits x[V]; returns
+// A team of G lanes; all lanes of the warp call these together.
+template <int G>
+__device__ __forceinline__ float team_sum(float v)
+{
+#pragma unroll
+    for (int o = G / 2; o > 0; o >>= 1) v += __shfl_xor_sync(kRouteFull, v, o);
+    return v;
+}
+
+template <int G>
+__device__ __forceinline__ uint32_t team_max(uint32_t v)
+{
+    if constexpr (G == 32) {
+        return __reduce_max_sync(kRouteFull, v);
+    } else {
+#pragma unroll
+        for (int o = G / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(kRouteFull, v, o));
+        return v;
+    }
+}
+
+template <int G>
+__device__ __forceinline__ uint32_t team_ballot(bool p)
+{
+    const uint32_t b = __ballot_sync(kRouteFull, p);
+    if constexpr (G == 32) return b;
+    else return (b >> (threadIdx.x & 31 & ~(G - 1))) & ((1u << G) - 1u);
+}
+
+// A team's token: w[V] are the weights exp(x - m) of its logits x[V]; returns
 // their sum, 0 if no expert is open, and the order bits of the largest logit of
-// the warp (top) and of the lane (best).  Logits that are not all finite and
+// the team (top) and of the lane (best).  Logits that are not all finite and
 // small leave cleaned.
-template <int V>
-__device__ __forceinline__ float warp_weights(float (&x)[V], float (&w)[V], Exponent &exponent, uint32_t &top,
+template <int G, int V>
+__device__ __forceinline__ float team_weights(float (&x)[V], float (&w)[V], Exponent &exponent, uint32_t &top,
                                               uint32_t &best)
 {
     float most = -INFINITY;
 #pragma unroll
     for (int v = 0; v < V; ++v) most = fmaxf(most, x[v]);
     best = order_bits(most);
-    top = __reduce_max_sync(kRouteFull, best);
+    top = team_max<G>(best);
     exponent.m = order_value(top);
     exponent.c = exponent.m * kLog2e;
     exponent.usual = true;
@@ -106,22 +125,25 @@ __device__ __forceinline__ float warp_weights(float (&x)[V], float (&w)[V], Expo
         w[v] = pow2(fmaf(x[v], kLog2e, -exponent.c));
         total += w[v];
     }
-    total = warp_sum(total);
-    if (total <= 1.5f * 32 * V && fabsf(exponent.c) < 0x1p100f) return total;
-    // no expert, a NaN, an infinity or a very large logit
-    exponent.usual = false;
+    total = team_sum<G>(total);
+    const bool odd = !(total <= 1.5f * G * V && fabsf(exponent.c) < 0x1p100f);
+    if (!__any_sync(kRouteFull, odd)) return total;
+    // a team without an expert, or with a NaN, an infinity or a very large logit: the others keep what they have
+    const uint32_t clean_best = order_bits(fminf(most, 3.402823466e38f)), clean_top = team_max<G>(clean_best);
+    float again = 0.0f;
+    if (odd) {
+        best = clean_best, top = clean_top;
+        exponent.usual = false;
+        exponent.m = top > kRouteNone ? order_value(top) : 0.0f;
 #pragma unroll
-    for (int v = 0; v < V; ++v) x[v] = sample_value(x[v]);
-    best = order_bits(fminf(most, 3.402823466e38f));
-    top = __reduce_max_sync(kRouteFull, best);
-    exponent.m = top > kRouteNone ? order_value(top) : 0.0f;
-    total = 0.0f;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        w[v] = exponent.weight(x[v]);
-        total += w[v];
+        for (int v = 0; v < V; ++v) {
+            x[v] = sample_value(x[v]);
+            w[v] = exponent.weight(x[v]);
+            again += w[v];
+        }
     }
-    return warp_sum(total);
+    again = team_sum<G>(again);
+    return odd ? again : total;
 }
 
 // 1 / x of a sum of weights, off by at most 2^-23 of itself.
@@ -179,22 +201,28 @@ struct Pick {
 };
 
 // Pieces of 16 bytes (or of a lane's share) where pointers, strides and experts
-// allow it, else elements.  CALL(T, N) for groups, CALL_WARP(T, N, V) for warps.
-#define GC_ROUTE_BY_VALUES(T, values, whole, CALL_WARP)                                             \
-    switch (values) {                                                                               \
-    case 2: if (whole) { return CALL_WARP(T, 2, 2); } return CALL_WARP(T, 1, 2);                    \
-    case 4: if (whole) { return CALL_WARP(T, 4, 4); } return CALL_WARP(T, 1, 4);                    \
-    case 8: if (whole) { return CALL_WARP(T, int(16 / sizeof(T)), 8); } return CALL_WARP(T, 1, 8);  \
-    case 16: if (whole) { return CALL_WARP(T, int(16 / sizeof(T)), 16); } return CALL_WARP(T, 1, 16); \
-    default: if (whole) { return CALL_WARP(T, int(16 / sizeof(T)), 64); } return CALL_WARP(T, 1, 64); \
+// allow it, else elements.  CALL(T, N) for groups, CALL_TEAM(T, N, V, G) for
+// teams: 16 lanes up to 256 experts if `half`, else the whole warp.
+#define GC_ROUTE_TEAM(T, whole, V, G, CALL_TEAM)                                            \
+    {                                                                                       \
+        constexpr int kMost = 16 / int(sizeof(T)), kPiece = V < kMost ? V : kMost;          \
+        if (whole) return CALL_TEAM(T, kPiece, V, G);                                       \
+        return CALL_TEAM(T, 1, V, G);                                                       \
     }
-#define GC_ROUTE_BY_SIZE(T, experts, whole, CALL, CALL_WARP)                        \
-    if (experts > kSmallExperts) { GC_ROUTE_BY_VALUES(T, route_values(experts), whole, CALL_WARP) } \
-    if (whole) { return CALL(T, int(16 / sizeof(T))); }                             \
-    return CALL(T, 1);
-#define GC_ROUTE_BY_DTYPE(dt, experts, whole, CALL, CALL_WARP)                                  \
-    if (dt == GC_ROW_F32) { GC_ROUTE_BY_SIZE(float, experts, whole, CALL, CALL_WARP) }          \
-    if (dt == GC_ROW_BF16) { GC_ROUTE_BY_SIZE(__nv_bfloat16, experts, whole, CALL, CALL_WARP) } \
-    GC_ROUTE_BY_SIZE(__half, experts, whole, CALL, CALL_WARP)
+#define GC_ROUTE_BY_SIZE(T, experts, half, whole, CALL, CALL_TEAM)                          \
+    if (experts <= kSmallExperts) {                                                         \
+        if (whole) return CALL(T, int(16 / sizeof(T)));                                     \
+        return CALL(T, 1);                                                                  \
+    }                                                                                       \
+    if (half && experts <= 64) GC_ROUTE_TEAM(T, whole, 4, 16, CALL_TEAM)                    \
+    if (half && experts <= 128) GC_ROUTE_TEAM(T, whole, 8, 16, CALL_TEAM)                   \
+    if (half && experts <= 256) GC_ROUTE_TEAM(T, whole, 16, 16, CALL_TEAM)                  \
+    if (experts <= 256) GC_ROUTE_TEAM(T, whole, 8, 32, CALL_TEAM)                           \
+    if (experts <= 512) GC_ROUTE_TEAM(T, whole, 16, 32, CALL_TEAM)                          \
+    GC_ROUTE_TEAM(T, whole, 64, 32, CALL_TEAM)
+#define GC_ROUTE_BY_DTYPE(dt, experts, half, whole, CALL, CALL_TEAM)                                  \
+    if (dt == GC_ROW_F32) { GC_ROUTE_BY_SIZE(float, experts, half, whole, CALL, CALL_TEAM) }          \
+    if (dt == GC_ROW_BF16) { GC_ROUTE_BY_SIZE(__nv_bfloat16, experts, half, whole, CALL, CALL_TEAM) } \
+    GC_ROUTE_BY_SIZE(__half, experts, half, whole, CALL, CALL_TEAM)
 
 }  // namespace gcd

@@ -7,8 +7,8 @@
 // choice, c[e] the pairs of expert e and f = c / sum c:
 //     load = sum p / n,   loss = experts * sum f load.
 //
-// One read of the logits.  Lane l of a warp (of a group of lanes where experts
-// are few) holds the experts [l * V, (l + 1) * V) of a token in registers, so
+// One read of the logits.  Lane l of a team of 16 or 32 (of a smaller group
+// where experts are few) holds the experts [l * V, (l + 1) * V) of a token in registers, so
 // that equal values go by lane and then by register; the lane's sums over
 // tokens of its experts' probabilities stay in registers until the end, CTAs
 // leave them in the workspace, and a cluster adds them up.
@@ -74,13 +74,16 @@ __device__ __forceinline__ void finish(uint32_t experts, uint32_t routed, const 
     }
 }
 
-// ---------------------------------------------------------------- a warp to a token
+// ---------------------------------------------------------------- a team to a token
 
 template <int V>
-constexpr int kWarpThreads = V <= 8 ? 512 : 256;
+constexpr int kTeamThreads = V <= 8 ? 512 : 256;
 template <int V>
-constexpr int kWarpResident = V <= 16 ? 2 : 1;  // CTAs per SM
+constexpr int kTeamResident = V <= 16 ? 2 : 1;  // CTAs per SM
 constexpr uint32_t kCandidates = 64;
+// Choices that a team of 16 lanes makes: the bound below is one of its lanes'
+// largest, and the candidates have to be hardly more than the lanes.
+constexpr uint32_t kHalfTopk = 12;
 
 // A bit for each of a lane's experts.
 template <int V>
@@ -90,108 +93,137 @@ struct Bits {
     static __device__ __forceinline__ int lowest(Type b) { return (V > 32 ? __ffsll(b) : __ffs(uint32_t(b))) - 1; }
 };
 
+// The k-th largest of a team's values, k <= G: of 16 lanes by sorting them (ten
+// exchanges), of 32 by taking the largest off k - 1 times.
+template <int G>
+__device__ __forceinline__ uint32_t kth_largest(uint32_t v, uint32_t top, uint32_t k)
+{
+    if constexpr (G == 32) {
+        uint32_t bound = top;
+        for (uint32_t j = 1; j < k && bound > kRouteNone; ++j) {
+            v = v == bound ? 0u : v;
+            bound = __reduce_max_sync(kRouteFull, v);
+        }
+        return bound;
+    } else {
+        const uint32_t lane = threadIdx.x & (G - 1);
+#pragma unroll
+        for (uint32_t size = 2; size <= G; size <<= 1)
+#pragma unroll
+            for (uint32_t o = size / 2; o > 0; o >>= 1) {
+                const uint32_t other = __shfl_xor_sync(kRouteFull, v, o);
+                // in descending order at the end
+                v = ((lane & o) != 0) == ((lane & size) != 0) ? max(v, other) : min(v, other);
+            }
+        return __shfl_sync(kRouteFull, v, k - 1, G);
+    }
+}
+
 // The choices.  A lower bound of the k-th largest logit is the k-th largest of
-// the lanes' largest: k warp-wide maxima.  The logits not below it, hardly more
-// than k, are listed, one to a lane, and ranked by comparing each with all.
-// Where they are more than a warp (many closed experts, equal values, large k)
-// the choices are taken one after another.  131072 tokens of 256 float32, top-8:
-// TIME us, against 162 one after another.
-template <class T, int N, int V>
-__global__ void __launch_bounds__(kWarpThreads<V>, kWarpResident<V>)
-route_warp_kernel(const T *__restrict__ logits, size_t stride, uint32_t tokens, uint32_t experts, uint32_t topk,
+// the lanes' largest.  The logits not below it, hardly more than k, are listed,
+// one to a lane, and ranked by comparing each with all.  Where they are more
+// than the lanes (many closed experts, equal values, large k) the choices are
+// taken one after another.  131072 tokens of 256 float32, top-8: FWD256 us, bound by
+// instructions; by whole warps 76, one after another 162.
+template <class T, int N, int V, int G>
+__global__ void __launch_bounds__(kTeamThreads<V>, kTeamResident<V>)
+route_team_kernel(const T *__restrict__ logits, size_t stride, uint32_t tokens, uint32_t experts, uint32_t topk,
                   bool normalize, const uint8_t *__restrict__ mask, RouteOut out, Totals part)
 {
-    constexpr int kWarps = kWarpThreads<V> / 32;
+    constexpr int kWarps = kTeamThreads<V> / 32, kTeams = kTeamThreads<V> / G;
     constexpr int kSlots = V < 8 ? V : 8;
-    __shared__ uint32_t s_id[kWarps][kCandidates];
-    __shared__ uint4 s_key[kWarps][kCandidates / 4];
-    __shared__ float s_sum[kWarps][32 * kSlots];
+    __shared__ uint32_t s_id[kTeams][kCandidates];
+    __shared__ uint4 s_key[kTeams][kCandidates / 4];
+    __shared__ float s_sum[kWarps][G * kSlots];
     __shared__ uint32_t s_count[GC_MAX_EXPERTS];
     __shared__ uint32_t s_warp[kWarps];
     chain_start();
-    const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5, first = lane * V;
-    for (uint32_t e = threadIdx.x; e < experts; e += kWarpThreads<V>) s_count[e] = 0;
+    const uint32_t lane = threadIdx.x & (G - 1), team = threadIdx.x / G, warp = threadIdx.x >> 5, first = lane * V;
+    for (uint32_t e = threadIdx.x; e < experts; e += kTeamThreads<V>) s_count[e] = 0;
     __syncthreads();
-    uint32_t *id = s_id[warp], *key = reinterpret_cast<uint32_t *>(s_key[warp]);
+    uint32_t *id = s_id[team], *key = reinterpret_cast<uint32_t *>(s_key[team]);
     float sum[V];
     uint32_t routed = 0;
 #pragma unroll
     for (int v = 0; v < V; ++v) sum[v] = 0.0f;
 
-    const uint64_t step = uint64_t(gridDim.x) * kWarps;
+    const uint64_t step = uint64_t(gridDim.x) * kTeams;
     Logits<T, N, V> next;
     auto fetch = [&](uint64_t t) {
         next.load(logits + t * stride, first, experts, t < tokens && (mask == nullptr || mask[t] != 0));
     };
-    uint64_t t = uint64_t(blockIdx.x) * kWarps + warp;
-    fetch(t);
-    for (; t < tokens; t += step) {
+    fetch(uint64_t(blockIdx.x) * kTeams + team);
+    // all lanes of a warp go round together, whatever their teams find
+    for (uint64_t base = uint64_t(blockIdx.x) * kTeams; base < tokens; base += step) {
+        const uint64_t t = base + team;
+        const bool inside = t < tokens;
         float x[V], w[V];
         next.values(x);
         fetch(t + step);
         Exponent exponent;
         uint32_t top, left;
-        const float total = warp_weights(x, w, exponent, top, left);
+        const float total = team_weights<G>(x, w, exponent, top, left);
+        const T *row = logits + t * stride;
         int32_t *ids = out.ids + t * topk;
         float *weights = out.weights + t * topk;
-        if (!(total > 0.0f)) {
-            for (uint32_t j = lane; j < topk; j += 32) ids[j] = -1, weights[j] = 0.0f;
-            continue;
-        }
-        ++routed;
-        const float inverse = inverse_of(total);
+        const bool any = total > 0.0f;
+        routed += any;
+        const float inverse = any ? inverse_of(total) : 0.0f;
 #pragma unroll
         for (int v = 0; v < V; ++v) sum[v] = fmaf(w[v], inverse, sum[v]);
 
-        // a bound that at least k logits reach
-        const uint32_t most = left;
-        uint32_t bound = top;
-        for (uint32_t j = 1; j < topk && bound > kRouteNone; ++j) {
-            left = left == bound ? 0u : left;
-            bound = __reduce_max_sync(kRouteFull, left);
-        }
-        const float least = order_value(max(bound, kRouteNone + 1));
+        const float least = order_value(max(topk <= G ? kth_largest<G>(left, top, topk) : 0u, kRouteNone + 1));
         using Mask = typename Bits<V>::Type;
         Mask which = 0;
 #pragma unroll
         for (int v = 0; v < V; ++v) which |= x[v] >= least ? Mask(1) << v : Mask(0);
-        const uint32_t mine = Bits<V>::count(which);
-        uint32_t upto = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t y = __shfl_up_sync(kRouteFull, upto, o);
-            if (lane >= uint32_t(o)) upto += y;
+        // listed before this lane's: by lanes with one candidate or more, two or more, ...
+        const uint32_t mine = Bits<V>::count(which), below = (1u << lane) - 1u;
+        uint32_t n = 0, at = 0;
+        for (uint32_t more = 0; __any_sync(kRouteFull, mine > more); ++more) {
+            const uint32_t have = team_ballot<G>(mine > more);
+            n += __popc(have);
+            at += __popc(have & below);
         }
-        uint32_t n = __shfl_sync(kRouteFull, upto, 31), rank = lane;
-        if (n <= 32) {
+        const uint32_t largest_n = __reduce_max_sync(kRouteFull, n);
+        if (largest_n <= G) {
             // listed by id; read again, which spares finding them among the registers
-            for (uint32_t at = upto - mine; which; which &= which - 1, ++at) id[at] = first + Bits<V>::lowest(which);
+            for (; which; which &= which - 1, ++at) id[at] = first + Bits<V>::lowest(which);
             key[lane] = 0;
             __syncwarp();
-            uint32_t own = 0;
+            uint32_t own = 0, e = 0;
             if (lane < n) {
-                own = order_bits(sample_value(row_to_float(logits[t * stride + id[lane]])));
+                e = id[lane];
+                own = order_bits(sample_value(row_to_float(row[e])));
                 key[lane] = own;
             }
             __syncwarp();
             // before it: the larger ones, and the equal ones listed before it
-            rank = 0;
-            for (uint32_t c = 0; c < n; c += 4) {
-                const uint4 k = s_key[warp][c / 4];
+            uint32_t rank = 0;
+            for (uint32_t c = 0; c < largest_n; c += 4) {
+                const uint4 k = s_key[team][c / 4];
                 rank += k.x >= own + (c >= lane);
                 rank += k.y >= own + (c + 1 >= lane);
                 rank += k.z >= own + (c + 2 >= lane);
                 rank += k.w >= own + (c + 3 >= lane);
             }
-            if (lane >= n) rank = ~0u;
+            const bool chosen = lane < n && rank < topk;
+            const float mine_w = chosen ? exponent.weight(order_value(own)) : 0.0f;
+            const float scale = normalize ? inverse_of(team_sum<G>(mine_w)) : inverse;
+            if (chosen) {
+                ids[rank] = int32_t(e);
+                weights[rank] = mine_w * scale;
+                if (out.counts) atomicAdd(&s_count[e], 1u);
+            }
         } else {
             // one after another: a lane's largest, and which of its logits are left
             Mask rest = ~Mask(0);
-            left = most;
-            for (n = 0; n < topk; ++n) {
-                if (n > 0) top = __reduce_max_sync(kRouteFull, left);
-                if (top <= kRouteNone) break;
-                if (lane == uint32_t(__ffs(__ballot_sync(kRouteFull, left == top)) - 1)) {
+            n = 0;
+            for (uint32_t j = 0; j < topk; ++j) {
+                if (j > 0) top = team_max<G>(left);
+                const uint32_t have = team_ballot<G>(left == top && top > kRouteNone);
+                n += have != 0;
+                if (have != 0 && lane == uint32_t(__ffs(have) - 1)) {
                     left = 0;
                     bool found = false;
 #pragma unroll
@@ -201,8 +233,8 @@ route_warp_kernel(const T *__restrict__ logits, size_t stride, uint32_t tokens, 
                         if (!found && k == top) {
                             found = true;
                             rest &= ~(Mask(1) << v);
-                            id[n] = first + v;
-                            key[n] = top;
+                            id[j] = first + v;
+                            key[j] = top;
                         } else {
                             left = max(left, k);
                         }
@@ -210,24 +242,17 @@ route_warp_kernel(const T *__restrict__ logits, size_t stride, uint32_t tokens, 
                 }
             }
             __syncwarp();
+            float chosen = 0.0f;
+            for (uint32_t j = lane; j < n; j += G) chosen += exponent.weight(order_value(key[j]));
+            const float scale = normalize ? inverse_of(team_sum<G>(chosen)) : inverse;
+            for (uint32_t j = lane; j < n; j += G) {
+                ids[j] = int32_t(id[j]);
+                weights[j] = exponent.weight(order_value(key[j])) * scale;
+                if (out.counts) atomicAdd(&s_count[id[j]], 1u);
+            }
         }
-        // n listed, ranked or in order
-        const uint32_t listed = n;
-        const bool own_one = lane < listed && rank < topk, other = lane + 32 < listed;
-        const float first_w = own_one ? exponent.weight(order_value(key[lane])) : 0.0f;
-        const float other_w = other ? exponent.weight(order_value(key[lane + 32])) : 0.0f;
-        const float scale = normalize ? inverse_of(warp_sum(first_w + other_w)) : inverse;
-        if (own_one) {
-            ids[rank] = int32_t(id[lane]);
-            weights[rank] = first_w * scale;
-            if (out.counts) atomicAdd(&s_count[id[lane]], 1u);
-        }
-        if (other) {
-            ids[lane + 32] = int32_t(id[lane + 32]);
-            weights[lane + 32] = other_w * scale;
-            if (out.counts) atomicAdd(&s_count[id[lane + 32]], 1u);
-        }
-        for (uint32_t j = listed + lane; j < topk; j += 32) ids[j] = -1, weights[j] = 0.0f;
+        if (inside)
+            for (uint32_t j = n + lane; j < topk; j += G) ids[j] = -1, weights[j] = 0.0f;
         __syncwarp();
     }
     if (out.counts == nullptr) return;
@@ -236,11 +261,15 @@ route_warp_kernel(const T *__restrict__ logits, size_t stride, uint32_t tokens, 
         for (int base = 0; base < V; base += kSlots) {
             __syncthreads();
 #pragma unroll
-            for (int v = 0; v < V; ++v)
-                if (v >= base && v < base + kSlots) s_sum[warp][lane * kSlots + (v & (kSlots - 1))] = sum[v];
+            for (int v = 0; v < V; ++v) {
+                if (v < base || v >= base + kSlots) continue;
+                float s = sum[v];
+                if (G == 16) s += __shfl_xor_sync(kRouteFull, s, 16);
+                if ((threadIdx.x & 31) < G) s_sum[warp][lane * kSlots + (v & (kSlots - 1))] = s;
+            }
             __syncthreads();
             const uint32_t e = threadIdx.x / kSlots * V + base + threadIdx.x % kSlots;
-            if (threadIdx.x < 32 * kSlots && e < experts) {
+            if (threadIdx.x < G * kSlots && e < experts) {
                 float s = 0.0f;
                 for (int w = 0; w < kWarps; ++w) s += s_sum[w][threadIdx.x];
                 f(e, s, s_count[e]);
@@ -446,12 +475,8 @@ route_join_kernel(Totals part, uint32_t parts, uint32_t experts, RouteOut out)
 // 128 tokens ALONE3 against ALONE4).
 constexpr size_t kAlone = 4;
 
-uint32_t route_grid(uint32_t tokens, uint32_t experts)
+uint32_t grid_of(uint32_t tokens, size_t each, size_t resident)
 {
-    const bool warps = experts > kSmallExperts;
-    const int v = route_values(experts);
-    const size_t each = warps ? (v <= 8 ? kWarpThreads<8> : kWarpThreads<64>) / 32 : kGroupThreads / route_lanes(experts);
-    const size_t resident = warps ? (v <= 16 ? kWarpResident<8> : kWarpResident<64>) : kGroupResident;
     const size_t need = gch::ceil_div(tokens, each), most = gch::kSms * resident;
     return uint32_t(need <= kAlone ? 1 : need < most ? need : most);
 }
@@ -474,21 +499,21 @@ template <class T, int N>
 cudaError_t run_group(const void *logits, size_t stride, uint32_t tokens, uint32_t experts, uint32_t topk,
                       bool normalize, const uint8_t *mask, const RouteOut &out, uint8_t *ws, cudaStream_t s)
 {
-    const uint32_t grid = route_grid(tokens, experts);
+    const uint32_t lanes = route_lanes(experts), grid = grid_of(tokens, kGroupThreads / lanes, kGroupResident);
     const Totals part = totals_in(ws, grid, experts);
     route_group_kernel<T, N><<<grid, kGroupThreads, 0, s>>>(static_cast<const T *>(logits), stride, tokens, experts,
-                                                            topk, normalize, mask, route_lanes(experts), out, part);
+                                                            topk, normalize, mask, lanes, out, part);
     return join(part, grid, experts, out, s);
 }
 
-template <class T, int N, int V>
-cudaError_t run_warp(const void *logits, size_t stride, uint32_t tokens, uint32_t experts, uint32_t topk,
+template <class T, int N, int V, int G>
+cudaError_t run_team(const void *logits, size_t stride, uint32_t tokens, uint32_t experts, uint32_t topk,
                      bool normalize, const uint8_t *mask, const RouteOut &out, uint8_t *ws, cudaStream_t s)
 {
-    const uint32_t grid = route_grid(tokens, experts);
+    const uint32_t grid = grid_of(tokens, kTeamThreads<V> / G, kTeamResident<V>);
     const Totals part = totals_in(ws, grid, experts);
-    route_warp_kernel<T, N, V><<<grid, kWarpThreads<V>, 0, s>>>(static_cast<const T *>(logits), stride, tokens,
-                                                                experts, topk, normalize, mask, out, part);
+    route_team_kernel<T, N, V, G><<<grid, kTeamThreads<V>, 0, s>>>(static_cast<const T *>(logits), stride, tokens,
+                                                                   experts, topk, normalize, mask, out, part);
     return join(part, grid, experts, out, s);
 }
 
@@ -498,7 +523,12 @@ namespace gch {
 
 size_t expert_route_workspace_bytes(size_t tokens, uint32_t experts)
 {
-    const uint32_t grid = route_grid(uint32_t(tokens), experts);
+    // whichever kernel the number of choices will take: no more CTAs than this
+    const uint32_t n = uint32_t(tokens);
+    uint32_t grid;
+    if (experts <= kSmallExperts) grid = grid_of(n, kGroupThreads / route_lanes(experts), kGroupResident);
+    else if (experts <= 256) grid = grid_of(n, kTeamThreads<16> / 16, kTeamResident<8>);  // 16 tokens, as 512 threads of whole warps
+    else grid = grid_of(n, kTeamThreads<64> / 32, kTeamResident<16>);
     if (grid == 1) return 256;
     return align_up(size_t(grid) * experts * 4, 256) + align_up(size_t(grid) * (experts + 1) * 4, 256);
 }
@@ -511,8 +541,9 @@ cudaError_t launch_expert_route(const void *logits, size_t stride, uint32_t toke
     const bool whole = ((uintptr_t(logits) | elem * (stride | experts)) & 15u) == 0;
     const RouteOut out{ids, weights, counts, load, loss};
 #define GC_ROUTE_CALL(T, N) run_group<T, N>(logits, stride, tokens, experts, topk, normalize, mask, out, ws, s)
-#define GC_ROUTE_CALL_WARP(T, N, V) run_warp<T, N, V>(logits, stride, tokens, experts, topk, normalize, mask, out, ws, s)
-    GC_ROUTE_BY_DTYPE(dt, experts, whole, GC_ROUTE_CALL, GC_ROUTE_CALL_WARP)
+#define GC_ROUTE_CALL_TEAM(T, N, V, G) \
+    run_team<T, N, V, G>(logits, stride, tokens, experts, topk, normalize, mask, out, ws, s)
+    GC_ROUTE_BY_DTYPE(dt, experts, topk <= kHalfTopk, whole, GC_ROUTE_CALL, GC_ROUTE_CALL_TEAM)
 }
 
 }  // namespace gch

@@ -33,31 +33,36 @@ __device__ __forceinline__ float loss_factor(const Grad &a, uint32_t *s_warp)
     return pairs > 0 && n > 0 ? *a.dloss * float(a.experts) / float(n) / float(pairs) : 0.0f;
 }
 
-// ---------------------------------------------------------------- a warp to a token
+// ---------------------------------------------------------------- a team to a token
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 
 template <int V>
-constexpr int kResident = V <= 8 ? 3 : V == 16 ? 2 : 1;  // CTAs per SM
+constexpr int kResident = V <= 4 ? 4 : V == 8 ? 3 : V == 16 ? 2 : 1;  // CTAs per SM
 
-template <class T, int N, int V>
+// The next token's logits and choices are on their way while one is computed.
+// 131072 tokens of 64, 128 and 256 float32 by teams of 16: FIG64, FIG128 and FIG256 us;
+// by whole warps, which pay for every token what does not depend on its
+// experts, 59, 66 and 63.
+template <class T, int N, int V, int G>
 __global__ void __launch_bounds__(kThreads, kResident<V>)
-route_grad_warp_kernel(const T *__restrict__ logits, T *__restrict__ dx, Grad a)
+route_grad_team_kernel(const T *__restrict__ logits, T *__restrict__ dx, Grad a)
 {
-    __shared__ Pick s_pick[kWarps][GC_MAX_TOPK];
+    constexpr int kTeams = 32 / G;
+    __shared__ Pick s_pick[kWarps * kTeams][GC_MAX_TOPK];
     __shared__ uint32_t s_warp[kWarps];
-    const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5, first = lane * V;
-    Pick *pick = s_pick[warp];
+    const uint32_t lane = threadIdx.x & (G - 1), team = threadIdx.x / G, first = lane * V;
+    Pick *pick = s_pick[team];
     const float factor = loss_factor<kWarps>(a, s_warp);
     float share[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) share[v] = a.dloss && first + v < a.experts ? factor * float(a.counts[first + v]) : 0.0f;
+    const bool few = a.topk <= G;  // a choice to a lane
 
-    const uint64_t step = uint64_t(gridDim.x) * kWarps;
-    uint64_t t = uint64_t(blockIdx.x) * kWarps + warp;
+    const uint64_t step = uint64_t(gridDim.x) * kWarps * kTeams;
+    uint64_t base = uint64_t(blockIdx.x) * kWarps * kTeams;
     Logits<T, N, V> next;
-    // a lane's choice: its id and the gradient of its weight
     uint32_t next_id = ~0u;
     float next_g = 0.0f;
     auto fetch = [&](uint64_t at) {
@@ -68,8 +73,10 @@ route_grad_warp_kernel(const T *__restrict__ logits, T *__restrict__ dx, Grad a)
             if (a.dweights) next_g = a.dweights[at * a.topk + lane];
         }
     };
-    fetch(t);
-    for (; t < a.tokens; t += step) {
+    fetch(base + team);
+    for (; base < a.tokens; base += step) {
+        const uint64_t t = base + team;
+        const bool inside = t < a.tokens;
         float x[V];
         next.values(x);
         const uint32_t id = next_id < a.experts ? next_id : ~0u;
@@ -77,86 +84,82 @@ route_grad_warp_kernel(const T *__restrict__ logits, T *__restrict__ dx, Grad a)
         fetch(t + step);
         T *to = dx + t * a.dx_stride;
         const T *row = logits + t * a.stride;
-        const bool live = __shfl_sync(kRouteFull, id, 0) != ~0u;
+        // a token without a choice has a row of zeros
+        const bool live = __shfl_sync(kRouteFull, id, 0, G) != ~0u;
         float w[V];
         Exponent exponent;
         uint32_t top, best;
-        float total = 0.0f;
-        if (live) {
-            total = warp_weights(x, w, exponent, top, best);
-        } else {
-#pragma unroll
-            for (int v = 0; v < V; ++v) w[v] = 0.0f;
-        }
-        const float inverse = total > 0.0f ? inverse_of(total) : 0.0f;
+        const float total = team_weights<G>(x, w, exponent, top, best);
+        const float inverse = live && total > 0.0f ? inverse_of(total) : 0.0f;
         float dot = 0.0f;
         if (a.dloss) {
 #pragma unroll
             for (int v = 0; v < V; ++v) dot = fmaf(w[v], share[v], dot);
-            dot = warp_sum(dot) * inverse;
+            dot = team_sum<G>(dot) * inverse;
         }
         // the choices' weights, and what they add to their elements
-        const bool parts = a.dweights && live;
         float mine = 0.0f, part = 0.0f;
-        if (parts && a.topk <= 32) {
-            if (id != ~0u) mine = exponent.weight(row_to_float(row[id])) * inverse;
-            const float chosen = a.normalize ? warp_sum(mine) : 1.0f;
-            float inner = warp_sum(mine * g);
-            const float scale = chosen > 0.0f ? inverse_of(chosen) : 0.0f;
+        if (a.dweights && few) {
+            if (live && id != ~0u) mine = exponent.weight(row_to_float(row[id])) * inverse;
+            float inner = team_sum<G>(mine * g);
             if (a.normalize) {
-                inner *= scale;
-                part = mine * scale * (g - inner);
+                const float chosen = team_sum<G>(mine), scale = chosen > 0.0f ? inverse_of(chosen) : 0.0f;
+                part = mine * scale * (g - inner * scale);
             } else {
                 dot += inner;
                 part = mine * g;
             }
-        } else if (parts) {
+        } else if (a.dweights) {
             float chosen = 0.0f, inner = 0.0f;
-            for (uint32_t j = lane; j < a.topk; j += 32) {
-                const uint32_t e = uint32_t(a.ids[t * a.topk + j]);
+            for (uint32_t j = lane; j < a.topk; j += G) {
+                const uint32_t e = live ? uint32_t(a.ids[t * a.topk + j]) : ~0u;
                 Pick c{0.0f, -1};
                 if (e < a.experts) c = Pick{exponent.weight(row_to_float(row[e])) * inverse, int32_t(e)};
                 pick[j] = c;
                 chosen += c.x;
                 if (c.id >= 0) inner += c.x * a.dweights[t * a.topk + j];
             }
-            chosen = a.normalize ? warp_sum(chosen) : 1.0f;
-            inner = warp_sum(inner);
-            const float scale = chosen > 0.0f ? 1.0f / chosen : 0.0f;
+            chosen = team_sum<G>(chosen);
+            inner = team_sum<G>(inner);
+            const float scale = chosen > 0.0f ? inverse_of(chosen) : 0.0f;
             if (a.normalize) inner *= scale;
             else dot += inner;
-            for (uint32_t j = lane; j < a.topk; j += 32)
+            for (uint32_t j = lane; j < a.topk; j += G)
                 if (pick[j].id >= 0)
                     pick[j].x *= a.normalize ? scale * (a.dweights[t * a.topk + j] - inner) : a.dweights[t * a.topk + j];
         }
+        if (inside) {
 #pragma unroll
-        for (int i = 0; i < V; i += N) {
-            if (first + i >= a.experts) break;
-            Piece<T, N> o;
+            for (int i = 0; i < V; i += N) {
+                if (first + i >= a.experts) break;
+                Piece<T, N> o;
 #pragma unroll
-            for (int e = 0; e < N; ++e) o.v[e] = row_from_float<T>(w[i + e] * inverse * (share[i + e] - dot));
-            store_piece<T, N>(to + first + i, o);
+                for (int e = 0; e < N; ++e)
+                    o.v[e] = row_from_float<T>(live ? w[i + e] * inverse * (share[i + e] - dot) : 0.0f);
+                store_piece<T, N>(to + first + i, o);
+            }
         }
-        if (!parts) continue;
+        if (!a.dweights) continue;
         __syncwarp();
         // An id that occurs twice has both choices' parts, and both lanes write the same.
-        if (a.topk <= 32) {
-            const uint32_t same = __match_any_sync(kRouteFull, id != ~0u ? id : 0x80000000u | lane);
-            if (__any_sync(kRouteFull, same != 1u << lane)) {
+        if (few) {
+            const bool has = live && id != ~0u;
+            const uint32_t same = __match_any_sync(kRouteFull, has ? (threadIdx.x & 31 & ~(G - 1)) << 16 | id : 0x80000000u | lane);
+            if (__any_sync(kRouteFull, has && (same & (same - 1)) != 0)) {
                 const float own = part;
                 part = 0.0f;
-                for (uint32_t q = 0; q < 32; ++q) {
+                for (int q = 0; q < 32; ++q) {
                     const float other = __shfl_sync(kRouteFull, own, q);
                     if (same >> q & 1u) part += other;
                 }
             }
-            if (id != ~0u) {
+            if (has) {
                 const float c = a.dloss ? factor * float(a.counts[id]) : 0.0f;
                 to[id] = row_from_float<T>(mine * (c - dot) + part);
             }
         } else {
-            for (uint32_t j = lane; j < a.topk; j += 32) {
-                const int32_t e = pick[j].id;
+            for (uint32_t j = lane; j < a.topk; j += G) {
+                const int32_t e = live ? pick[j].id : -1;
                 if (e < 0) continue;
                 float both = 0.0f;
                 for (uint32_t q = 0; q < a.topk; ++q)
@@ -280,10 +283,10 @@ cudaError_t run_group(const void *logits, void *dx, const Grad &a, cudaStream_t 
     return cudaGetLastError();
 }
 
-template <class T, int N, int V>
-cudaError_t run_warp(const void *logits, void *dx, const Grad &a, cudaStream_t s)
+template <class T, int N, int V, int G>
+cudaError_t run_team(const void *logits, void *dx, const Grad &a, cudaStream_t s)
 {
-    route_grad_warp_kernel<T, N, V><<<grid_of(a.tokens, kWarps, kResident<V>), kThreads, 0, s>>>(
+    route_grad_team_kernel<T, N, V, G><<<grid_of(a.tokens, kThreads / G, kResident<V>), kThreads, 0, s>>>(
         static_cast<const T *>(logits), static_cast<T *>(dx), a);
     return cudaGetLastError();
 }
@@ -301,8 +304,8 @@ cudaError_t launch_expert_route_grad(const void *logits, size_t stride, uint32_t
     const bool whole = ((uintptr_t(logits) | uintptr_t(dx) | elem * (stride | dx_stride | experts)) & 15u) == 0;
     const Grad a{tokens, experts, topk, stride, dx_stride, normalize, ids, counts, dweights, dloss};
 #define GC_ROUTE_GRAD_CALL(T, N) run_group<T, N>(logits, dx, a, s)
-#define GC_ROUTE_GRAD_CALL_WARP(T, N, V) run_warp<T, N, V>(logits, dx, a, s)
-    GC_ROUTE_BY_DTYPE(dt, experts, whole, GC_ROUTE_GRAD_CALL, GC_ROUTE_GRAD_CALL_WARP)
+#define GC_ROUTE_GRAD_CALL_TEAM(T, N, V, G) run_team<T, N, V, G>(logits, dx, a, s)
+    GC_ROUTE_BY_DTYPE(dt, experts, true, whole, GC_ROUTE_GRAD_CALL, GC_ROUTE_GRAD_CALL_TEAM)
 }
 
 }  // namespace gch

@@ -42,6 +42,8 @@ def terms(tokens, experts):
         groups, most = (16, 304) if experts <= 256 else (8, 304) if experts <= 512 else (8, 152)
     else:
         groups, most = 256 // (1 if experts <= 8 else 2 if experts <= 16 else 4), 456
+    # one CTA alone takes up to four times its tokens
+    groups = groups if -(-tokens // groups) > 4 else max(1, groups // 4)
     grid = min(-(-tokens // groups), most)
     return -(-tokens // (grid * groups)) + 64
 
@@ -84,6 +86,13 @@ ROUTE = [
     (70, 2048, 64, "bf16", True, 0.1, 0.9, 0, 0),
     (40, 2047, 64, "f32", False, 0.0, 0.0, 0, 0),
     (20000, 4, 2, "bf16", True, 0.1, 0.0, 0, 0),
+    (2001, 33, 12, "f32", True, 0.0, 0.0, 0, 0),
+    (500, 64, 13, "bf16", False, 0.1, 0.0, 0, 0),
+    (1777, 65, 6, "f16", True, 0.0, 0.4, 0, 0),
+    (3001, 128, 8, "bf16", True, 0.0, 0.0, 0, 0),
+    (600, 129, 2, "f32", False, 0.3, 0.9, 3, 1),
+    (800, 256, 12, "bf16", True, 0.0, 0.99, 0, 0),
+    (300, 200, 16, "f32", True, 0.0, 0.0, 0, 0),
     (9000, 32, 4, "f32", False, 0.0, 0.0, 0, 0),
 ]
 
