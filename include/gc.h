@@ -582,9 +582,8 @@ size_t gc_expert_route_workspace_bytes(size_t tokens, uint32_t experts);
  *
  * Roundings: p by exp2 of (x - max) * log2(e), off by at most (6 + 3/2 |x -
  * max|) * 2^-23 of itself; a token's sums are float32 trees.  load adds up in
- * float32: the tokens of one thread in their order, at most tokens / 2432 (of
- * warps, more than 32 experts) or tokens / 29184 of them and one more, then at
- * most 64 such sums.
+ * float32: at most tokens / 1216 + 2 tokens one after another, then at most 64
+ * such sums.
  */
 gc_status gc_expert_route(const void *d_logits, size_t logits_stride, size_t tokens, uint32_t experts,
                           gc_row_dtype dtype, size_t topk, int normalize, const uint8_t *d_mask,

@@ -35,7 +35,10 @@ __device__ __forceinline__ uint32_t clamp_length(const int32_t *lengths, uint32_
 }
 
 // Pieces across, the rows (queries of the group's heads, head by head) down the
-// threads of a block, whose sums are then joined in their order.  `whole`: the
+// threads of a block, whose sums are then joined in their order.  Bound by HBM:
+// 32 heads of 256 rows of 16384 bf16, 273 MB, take 46 us, 87% of the copy rate;
+// with a row's address from two products and eight rows in local memory, as a
+// tail of variable length left them, 98.  `whole`: the
 // scores and the result move in 16 bytes too.
 template <class T, int N>
 __global__ void __launch_bounds__(kScoreThreads, 4)
@@ -176,7 +179,9 @@ struct SelectSmem {
 // at a time, K to a lane, as ordered bits in registers.  The cut is the score of
 // rank m between the sinks and the recent positions, found by three histograms
 // of those bits, 12, 10 and 10 of them; of the scores at the cut the first are
-// kept.  A share of at most K * 1024 positions is read once.
+// kept.  A share of at most K * 1024 positions is read once.  128 heads of 32768
+// scores to 2048: 18 us, bound by instructions (about 60 a score); with four CTAs
+// to a head that read their scores from L2 five times, 43.
 template <int K>
 __global__ void __launch_bounds__(kEvictThreads)
 cache_select_kernel(Evict a)
@@ -341,6 +346,8 @@ constexpr int kMoveAhead = 4;   // rows that a thread has under way
 // The kept rows: a row of threads per slot, kMoveAhead slots at a time, head by
 // head.  Of `down` blocks of a head those that hold recent positions alone, the
 // `early` last, come first for all heads: they need not wait for the selection.
+// 128 heads of 2048 rows of 2 x 256 bytes: 47 us behind the selection's 18, for
+// 268 MB (40 at the copy rate), each row a place of its own in HBM.
 template <class P>
 __global__ void __launch_bounds__(kMoveThreads, 5)
 cache_move_kernel(Evict a, Move m, uint32_t down, uint32_t early)

@@ -79,7 +79,7 @@ __device__ __forceinline__ void finish(uint32_t experts, uint32_t routed, const 
 template <int V>
 constexpr int kTeamThreads = V <= 8 ? 512 : 256;
 template <int V>
-constexpr int kTeamResident = V <= 16 ? 2 : 1;  // CTAs per SM
+constexpr int kTeamResident = V <= 8 ? 2 : V == 16 ? 3 : 1;  // CTAs per SM
 constexpr uint32_t kCandidates = 64;
 // Choices that a team of 16 lanes makes: the bound below is one of its lanes'
 // largest, and the candidates have to be hardly more than the lanes.
@@ -123,8 +123,10 @@ __device__ __forceinline__ uint32_t kth_largest(uint32_t v, uint32_t top, uint32
 // the lanes' largest.  The logits not below it, hardly more than k, are listed,
 // one to a lane, and ranked by comparing each with all.  Where they are more
 // than the lanes (many closed experts, equal values, large k) the choices are
-// taken one after another.  131072 tokens of 256 float32, top-8: FWD256 us, bound by
-// instructions; by whole warps 76, one after another 162.
+// taken one after another.  131072 tokens of 256 float32, top-8: 70 us against 21
+// for the bytes, bound by instructions (about 400 a token, half of them on the
+// pipe of comparisons and integers); by whole warps 76, one after another 162.
+// Of 64 experts, top-4, 37 us (warps 56), of 128 bf16, top-8, 49 (73).
 template <class T, int N, int V, int G>
 __global__ void __launch_bounds__(kTeamThreads<V>, kTeamResident<V>)
 route_team_kernel(const T *__restrict__ logits, size_t stride, uint32_t tokens, uint32_t experts, uint32_t topk,
@@ -469,11 +471,11 @@ route_join_kernel(Totals part, uint32_t parts, uint32_t experts, RouteOut out)
     }
 }
 
-// CTAs: as many as run at a time, each with the tokens of its warps or groups at
-// least once; one alone, which spares the second launch, where it has them at
-// most kAlone times (24 tokens of 64 experts: ALONE1 us against ALONE2 by two launches;
-// 128 tokens ALONE3 against ALONE4).
-constexpr size_t kAlone = 4;
+// CTAs: as many as run at a time, each with the tokens of its teams or groups at
+// least once; one alone, which spares the second launch, where that has them at
+// most kAlone times (of 64 experts 24 tokens 3.3 us, 64 tokens 4.7, by two
+// launches 7.2 and 7.0; 128 tokens, four times, 7.1 against 6.7).
+constexpr size_t kAlone = 2;
 
 uint32_t grid_of(uint32_t tokens, size_t each, size_t resident)
 {
@@ -527,7 +529,7 @@ size_t expert_route_workspace_bytes(size_t tokens, uint32_t experts)
     const uint32_t n = uint32_t(tokens);
     uint32_t grid;
     if (experts <= kSmallExperts) grid = grid_of(n, kGroupThreads / route_lanes(experts), kGroupResident);
-    else if (experts <= 256) grid = grid_of(n, kTeamThreads<16> / 16, kTeamResident<8>);  // 16 tokens, as 512 threads of whole warps
+    else if (experts <= 256) grid = grid_of(n, kTeamThreads<16> / 16, kTeamResident<16>);  // 16 tokens, as 512 threads of whole warps
     else grid = grid_of(n, kTeamThreads<64> / 32, kTeamResident<16>);
     if (grid == 1) return 256;
     return align_up(size_t(grid) * experts * 4, 256) + align_up(size_t(grid) * (experts + 1) * 4, 256);

@@ -19,6 +19,14 @@
 // exp((x - m) / T) is 2^(x f - c) with f = log2(e) / T and c = m f rounded: one
 // multiply-add, whose only rounding is that of the exponent, since every weight
 // of a row carries the same 2^(m f - c) and p is a quotient of them.
+//
+// Measured, kernels alone: 192 sequences of 5 drafts by a model, 128000 bf16, four
+// in five positions accepted: 118 us.  The rows take 72 of it, 356 MB at 5.1 TB/s,
+// where 316 MB would do (the rest was under way when its sequence stopped), bound
+// by the exponentials and their four instructions a logit; reading all 540 MB
+// takes 104.  The draw takes 46: 98 MB of random numbers and two rows of each
+// sequence once more.  One sequence of 4 drafts, 32768 float32: 11 us, two
+// launches' chains of dependent reads.
 #include <atomic>
 
 #include "gc_rows.cuh"
@@ -37,7 +45,8 @@ constexpr uint32_t kFull = 0xffffffffu;
 constexpr float kLargest = 3.402823466e38f;
 constexpr float kUniformLo = 0x1p-25f, kUniformHi = 1.0f - 0x1p-24f;
 
-// Chunks: 16 pieces per thread, 64 KB, where that makes more CTAs than the
+// Chunks: 16 pieces per thread, 64 KB (8 a thread take 131 us at the size above,
+// for what every CTA does once; 32 take 118, with 50 MB more under way), where that makes more CTAs than the
 // GPU holds, else fewer.
 constexpr uint32_t kDrawWave = 4;          // CTAs per SM of the draw
 constexpr uint32_t kSteps = 16, kWave = 6;  // kWave: CTAs per SM
@@ -168,33 +177,55 @@ __device__ __forceinline__ void wait_copies()
 }
 
 // A chunk's pieces to f, one after another, through a ring of asynchronous
-// copies, each thread its own: kRing of them are under way at any time.
+// copies, each thread its own: kRing of them are under way at any time.  A round
+// of the ring is unrolled, so that its places and the copies' addresses are
+// constants.
 template <class T, class F>
 __device__ __forceinline__ void each_piece(const Pieces<T> &row, uint32_t first, uint32_t end, uint4 *ring, const F &f)
 {
     constexpr uint32_t kVec = Pieces<T>::kVec;
-    const T *from = row.x + row.head;
+    const uint32_t j = first + threadIdx.x;
+    const int left = j < end ? int((end - j + kThreads - 1) / kThreads) : 0;  // of this thread
+    const T *from = row.x + row.head + size_t(j) * kVec;
+    uint32_t at = row.head + j * kVec;
     uint4 *mine = ring + threadIdx.x;
-    auto copy = [&](uint32_t j, int slot) {
 #pragma unroll
-        for (int q = 0; q < kAtOnce; ++q) copy_piece(mine + (slot + q) * kThreads, from + size_t(j + q * kThreads) * kVec, j + q * kThreads < end);
-        commit_copies();
-    };
-    constexpr uint32_t kStride = kAtOnce * kThreads;
-    uint32_t j = first + threadIdx.x;
+    for (int q = 0; q < kRing; ++q) {
+        copy_piece(mine + q * kThreads, from + q * kThreads * kVec, q < left);
+        if (q % kAtOnce == kAtOnce - 1) commit_copies();
+    }
+    for (int i = 0; i < left; i += kRing) {
+        from += kRing * kThreads * kVec;
 #pragma unroll
-    for (int q = 0; q < kRing; q += kAtOnce) copy(j + q * kThreads, q);
-    for (int slot = 0; j < end; j += kStride) {
-        wait_copies<kRing / kAtOnce - 1>();
-#pragma unroll
-        for (int q = 0; q < kAtOnce; ++q) {
-            if (j + q * kThreads >= end) break;
-            f(load_piece<T, kVec>(reinterpret_cast<const T *>(mine + (slot + q) * kThreads)), row.head + (j + q * kThreads) * kVec);
+        for (int q = 0; q < kRing; ++q) {
+            if (q % kAtOnce == 0) wait_copies<kRing / kAtOnce - 1>();
+            if (i + q < left) f(mine + q * kThreads, at + q * kThreads * kVec);
+            copy_piece(mine + q * kThreads, from + q * kThreads * kVec, i + q + kRing < left);
+            if (q % kAtOnce == kAtOnce - 1) commit_copies();
         }
-        copy(j + kRing * kThreads, slot);
-        slot = slot + kAtOnce < kRing ? slot + kAtOnce : 0;
+        at += kRing * kThreads * kVec;
     }
     wait_copies<0>();
+}
+
+// A piece that holds the first logits, a NaN, an infinity or a logit far above
+// m: the new (m, sum).  Out of line, with the piece still in shared memory.
+template <class T>
+__device__ __noinline__ float2 rare_piece(const uint4 *at, float m, float sum, float power)
+{
+    constexpr int kVec = 16 / sizeof(T);
+    float x[kVec];
+    piece_values(load_piece<T, kVec>(reinterpret_cast<const T *>(at)), x);
+    float top = m;
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) top = fmaxf(top, x[e]);
+    top = fminf(top, kLargest);
+    if (top > -INFINITY) {
+        join(m, sum, top, 0.0f, power);
+#pragma unroll 1
+        for (int e = 0; e < kVec; ++e) sum += weight(row_to_float(reinterpret_cast<const T *>(at)[e]), m, power);
+    }
+    return make_float2(m, sum);
 }
 
 // A chunk's sum by a maximum, to lane 0 of warp 0.  The maximum is one of the
@@ -205,30 +236,19 @@ __device__ __forceinline__ Part chunk_sum(const Pieces<T> &row, uint32_t first, 
                                           uint4 *ring, Part *s_part)
 {
     constexpr uint32_t kVec = Pieces<T>::kVec;
-    float m = -INFINITY, c = 0.0f, sum = 0.0f;
-    bool usual = false;  // m is a logit and c can be taken off
-    auto base = [&](float top) {
-        top = fminf(fmaxf(top, m), kLargest);
-        if (!(top > -INFINITY)) return;
-        join(m, sum, top, 0.0f, power);
-        c = m * power;
-        usual = plain(c);
-    };
-    each_piece(row, first, end, ring, [&](const Piece<T, kVec> &v, uint32_t) {
-        if (!usual) base(piece_max(v));
+    float m = -INFINITY, sum = 0.0f, c = INFINITY;  // no reference yet: the first piece is rare
+    each_piece(row, first, end, ring, [&](const uint4 *at, uint32_t) {
         float x[kVec], more = 0.0f;
-        piece_values(v, x);
+        piece_values(load_piece<T, kVec>(reinterpret_cast<const T *>(at)), x);
 #pragma unroll
         for (uint32_t e = 0; e < kVec; ++e) more += pow2(fmaf(x[e], power, -c));
-        if (usual && more <= 0x1p60f) {
+        if (more <= 0x1p60f && c < 0x1p100f) {
             sum += more;
-            return;
+        } else {
+            const float2 r = rare_piece<T>(at, m, sum, power);
+            m = r.x, sum = r.y;
+            c = m > -INFINITY && plain(m * power) ? m * power : INFINITY;
         }
-        // no logit, a NaN, an infinity or a much larger one
-        base(piece_max(v));
-        if (!(m > -INFINITY)) return;
-#pragma unroll
-        for (uint32_t e = 0; e < kVec; ++e) sum += weight(x[e], m, power);
     });
     if (singles) {
         const uint32_t i = row.single(threadIdx.x);
@@ -259,7 +279,8 @@ __device__ __forceinline__ Part chunk_first(const Pieces<T> &row, uint32_t first
     constexpr uint32_t kVec = Pieces<T>::kVec;
     uint64_t key = first_key(-INFINITY, ~0u);
     float top = -INFINITY;
-    each_piece(row, first, end, ring, [&](const Piece<T, kVec> &v, uint32_t i) {
+    each_piece(row, first, end, ring, [&](const uint4 *at, uint32_t i) {
+        const Piece<T, kVec> v = load_piece<T, kVec>(reinterpret_cast<const T *>(at));
         if (!(piece_max(v) > top)) return;  // a thread's pieces come in order: equal values later count for nothing
 #pragma unroll
         for (uint32_t e = 0; e < kVec; ++e) {
@@ -361,9 +382,9 @@ verify_rows_kernel(Verify a)
     __shared__ Part s_part[kWarps];
     __shared__ uint4 s_ring[kRing * kThreads];
     chain_start();
-    // positions first, then sequences, target or draft, chunks
-    const uint32_t j = blockIdx.z, kinds = a.d ? 2 : 1, c = blockIdx.x % a.chunks, unit = blockIdx.x / a.chunks;
-    const uint32_t kind = a.d ? unit & 1u : 0u, b = a.d ? unit >> 1 : unit;
+    // positions first, then chunks, sequences, target or draft
+    const uint32_t j = blockIdx.z, c = blockIdx.y, kinds = a.d ? 2 : 1;
+    const uint32_t kind = a.d ? blockIdx.x & 1u : 0u, b = a.d ? blockIdx.x >> 1 : blockIdx.x;
     if (kind == 1 && j == a.drafts) return;
     const int32_t *ids = a.ids + size_t(b) * a.drafts;
     if (a.left == nullptr) {
@@ -764,7 +785,7 @@ cudaError_t run_verify(Verify a, uint8_t *ws, cudaStream_t s)
     a.draws = uint32_t(gch::kSms * kDrawWave / a.sequences);
     a.draws = a.draws < 1 ? 1 : a.draws < most ? a.draws : most;
     a.draw = uint32_t(gch::ceil_div(pieces, a.draws));
-    const dim3 grid(a.sequences * (a.d ? 2 : 1) * plan.chunks, 1, a.drafts + 1);
+    const dim3 grid(a.sequences * (a.d ? 2 : 1), plan.chunks, a.drafts + 1);
     verify_rows_kernel<T><<<grid, kThreads, 0, s>>>(a);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;

@@ -42,8 +42,8 @@ def terms(tokens, experts):
         groups, most = (16, 304) if experts <= 256 else (8, 304) if experts <= 512 else (8, 152)
     else:
         groups, most = 256 // (1 if experts <= 8 else 2 if experts <= 16 else 4), 456
-    # one CTA alone takes up to four times its tokens
-    groups = groups if -(-tokens // groups) > 4 else max(1, groups // 4)
+    # one CTA alone takes up to twice its tokens
+    groups = groups if -(-tokens // groups) > 2 else max(1, groups // 2)
     grid = min(-(-tokens // groups), most)
     return -(-tokens // (grid * groups)) + 64
 
