@@ -711,8 +711,8 @@ size_t gc_sample_verify_workspace_bytes(size_t sequences, size_t drafts, size_t 
  *
  * Roundings: p and q are exp2 of (x - max) * (log2(e) / T) in float32, off by
  * at most (4 + 5/4 |z|) * 2^-22 of themselves, |z| = (max - x) / T; sums are
- * float32 trees over at most 2^-12 of the vocabulary per thread; the
- * comparison is in double.  The result is that of these p and q: a position
+ * float32, at most 128 logits of one thread and vocab / 131072 of its chunks one
+ * after another; the comparison is in double.  The result is that of these p and q: a position
  * whose u q and p agree to that many bits may be decided either way.
  *
  * d_logits: sequences * (drafts + 1) rows of `vocab`, d_draft_logits:

@@ -57,7 +57,7 @@ struct Logits {
 
 // exp(x - m) as a power of two.  c = m log2(e) is taken off by a multiply-add,
 // whose only rounding is the exponent's (every weight of a token carries the
-// same 2^(m log2(e) - c)), unless the logits are not all finite and small.
+// same 2^(m log2(e) - c), near 1), unless the logits are not all finite or large.
 struct Exponent {
     float m, c;
     bool usual;
@@ -127,7 +127,7 @@ __device__ __forceinline__ float team_weights(float (&x)[V], float (&w)[V], Expo
         total += w[v];
     }
     total = team_sum<G>(total);
-    const bool odd = !(total <= 1.5f * G * V && fabsf(exponent.c) < 0x1p100f);
+    const bool odd = !(total <= 1.5f * G * V && fabsf(exponent.c) < 0x1p24f);
     if (!__any_sync(kRouteFull, odd)) return total;
     // a team without an expert, or with a NaN, an infinity or a very large logit: the others keep what they have
     const uint32_t clean_best = order_bits(fminf(most, 3.402823466e38f)), clean_top = team_max<G>(clean_best);

@@ -118,8 +118,9 @@ struct Pieces {
     }
 };
 
-// Whether c = m * power can be taken off by a multiply-add.
-__device__ __forceinline__ bool plain(float c) { return fabsf(c) < 0x1p100f; }
+// Whether c = m * power can be taken off by a multiply-add: every weight then
+// carries 2^(m * power - c), which has to stay near 1.
+__device__ __forceinline__ bool plain(float c) { return fabsf(c) < 0x1p24f; }
 
 // The weight of a logit by a maximum, of any values.
 __device__ __forceinline__ float weight(float x, float m, float power)
@@ -129,14 +130,16 @@ __device__ __forceinline__ float weight(float x, float m, float power)
     return pow2(plain(c) ? fmaf(x, power, -c) : (x - m) * power);
 }
 
-// m and sum joined with another maximum and sum.
+// m and sum joined with another maximum and sum.  Each sum's weights are by its
+// own m: less c where that is plain, less the exact product where not.
 __device__ __forceinline__ void join(float &m, float &sum, float m2, float sum2, float power)
 {
     const float top = fmaxf(m, m2);
     if (!(top > -INFINITY)) return;
     auto scale = [&](float from) {
         const float c = from * power, d = top * power;
-        return pow2(plain(c) && plain(d) ? c - d : (from - top) * power);
+        if (plain(c)) return pow2(plain(d) ? c - d : fmaf(-top, power, c));
+        return pow2(plain(d) ? fmaf(from, power, -d) : (from - top) * power);
     };
     sum = (m == top ? sum : sum * scale(m)) + (m2 == top ? sum2 : sum2 * scale(m2));
     m = top;
@@ -242,7 +245,7 @@ __device__ __forceinline__ Part chunk_sum(const Pieces<T> &row, uint32_t first, 
         piece_values(load_piece<T, kVec>(reinterpret_cast<const T *>(at)), x);
 #pragma unroll
         for (uint32_t e = 0; e < kVec; ++e) more += pow2(fmaf(x[e], power, -c));
-        if (more <= 0x1p60f && c < 0x1p100f) {
+        if (more <= 0x1p60f && c < INFINITY) {
             sum += more;
         } else {
             const float2 r = rare_piece<T>(at, m, sum, power);

@@ -118,6 +118,11 @@ EVICT = [
     (1, 1, 70001, 8, 8, 60000, 5, 7, "f16", None, "head", "few", 0),
     (40, 16, 300, 32, 32, 100, 4, 10, "bf16", "some", "token", "any", 0),
     (2, 2, 64, 128, 128, 500, 4, 10, "bf16", "some", "head", "any", 0),
+    # a CTA's share of more positions than it holds at a time, one CTA to a head, and 32 positions to a thread
+    (1, 1, 300001, 4, None, 200, 4, 10, "bf16", None, "head", "any", 0),
+    (1, 2, 270000, 4, None, 150000, 4, 10, "bf16", None, "head", "few", 0),
+    (8, 20, 9000, 8, None, 700, 2, 64, "bf16", "some", "token", "any", 0),
+    (1, 3, 40000, 8, 16, 39000, 0, 0, "bf16", None, "token", "wild", 0),
 ]
 
 
@@ -171,6 +176,14 @@ def test_evict_offsets_past_32_bits():
     for b in range(2):
         at = torch.from_numpy(ref.kept(s[b, 0].cpu().numpy(), 50, 10, 0, 0)).cuda()
         assert torch.equal(got.keys[b, 0], k[b, 0, at])
+
+
+def test_score_offsets_past_32_bits():
+    big = torch.empty((1 << 32) + 4096, dtype=torch.bfloat16, device="cuda")
+    w = big.as_strided((2, 1, 3, 64), (1 << 32, 0, 64, 1))
+    w.copy_(torch.rand(2, 1, 3, 64, device="cuda"))
+    s = torch.rand(2, 1, 64, device="cuda")
+    assert torch.equal(gc.cache_score(w, s), gc.cache_score(w.contiguous(), s))
 
 
 def test_evict_nothing():

@@ -93,6 +93,9 @@ ROUTE = [
     (600, 129, 2, "f32", False, 0.3, 0.9, 3, 1),
     (800, 256, 12, "bf16", True, 0.0, 0.99, 0, 0),
     (300, 200, 16, "f32", True, 0.0, 0.0, 0, 0),
+    (20000, 256, 8, "f32", True, 0.05, 0.0, 0, 0),
+    (15000, 100, 4, "bf16", False, 0.0, 0.1, 0, 0),
+    (12000, 300, 3, "f16", True, 0.0, 0.0, 0, 0),
     (9000, 32, 4, "f32", False, 0.0, 0.0, 0, 0),
 ]
 
@@ -252,6 +255,20 @@ def test_repeats_streams_and_graphs():
         assert all(torch.equal(a, b) for a, b in zip(r, want))
         assert torch.equal(d, gc.expert_route_grad(x, want.ids, want.counts, dweights=g, dloss=dl))
     assert torch.equal(dx, dx)
+
+
+def test_offsets_past_32_bits():
+    big = torch.empty(20 << 28, dtype=torch.bfloat16, device="cuda")
+    far = big.as_strided((20, 40), (1 << 28, 1))
+    x = torch.randn(20, 40, device="cuda").bfloat16()
+    far.copy_(x)
+    near, there = gc.expert_route(x, 3), gc.expert_route(far, 3)
+    assert all(torch.equal(a, b) for a, b in zip(near, there))
+    dw, dl = torch.randn(20, 3, device="cuda"), torch.ones(1, device="cuda")
+    want = gc.expert_route_grad(x, near.ids, near.counts, dweights=dw, dloss=dl)
+    assert torch.equal(want, gc.expert_route_grad(far, near.ids, near.counts, dweights=dw, dloss=dl))
+    gc.expert_route_grad(x, near.ids, near.counts, dweights=dw, dloss=dl, out=far)
+    assert torch.equal(want, far.contiguous())
 
 
 def test_refusals():

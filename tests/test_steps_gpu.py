@@ -185,3 +185,29 @@ def test_example_drafts():
     assert tokens.shape == (90, 4) and accepted.shape == (90,)
     for row, a in zip(tokens.tolist(), accepted.tolist()):
         assert 0 <= a <= 3 and all(0 <= t < 300 for t in row[:a + 1]) and row[a + 1:] == [-1] * (3 - a)
+
+
+def test_calls_on_two_streams_at_once():
+    # every operator twice, on streams of their own, with nothing waited for in between
+    g = torch.Generator(device="cuda").manual_seed(4)
+    scores = torch.randn(5000, 64, generator=g, device="cuda")
+    logits, drafted = (torch.randn(40, n, 9000, generator=g, device="cuda") for n in (4, 3))
+    drafts = drafted.argmax(2).int()
+    accept, uniform = torch.rand(40, 3, generator=g, device="cuda"), torch.rand(40, 9000, generator=g, device="cuda")
+    w, keys = torch.rand(3, 8, 4, 6000, generator=g, device="cuda"), torch.randn(3, 2, 6000, 32, generator=g, device="cuda")
+
+    def all_of(stream=None):
+        r = gc.expert_route(scores, 4, stream=stream)
+        d = gc.expert_route_grad(scores, r.ids, r.counts, dweights=r.weights, dloss=r.loss, stream=stream)
+        v = gc.sample_verify(logits, drafts, accept, uniform, draft_logits=drafted, stream=stream)
+        s = gc.cache_score(w, None, heads=2, stream=stream)
+        k = gc.cache_evict(keys, None, s, 900, 4, 50, stream=stream)
+        return [*r, d, *v, s, *(t for t in k if t is not None)]
+    want = all_of()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(10):
+        got = [all_of(s) for s in streams]
+        torch.cuda.synchronize()
+        for one in got:
+            assert all(torch.equal(a, b) for a, b in zip(want, one))

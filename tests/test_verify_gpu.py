@@ -87,6 +87,10 @@ VERIFY = [
     (3, 2, 131072, "bf16", True, 0, 0, 0.0, 0.0),
     (2, 1, 200001, "f32", False, 0, 0, 0.0, 0.0),
     (700, 2, 64, "f32", True, 0, 0, 0.0, 0.1),
+    # more rows than CTAs at a time: positions are decided on the way
+    (400, 3, 3001, "f16", False, 1, 0, 0.1, 0.3),
+    (330, 2, 1500, "bf16", True, 0, 0, 0.0, 0.2),
+    (1300, 0, 40, "bf16", False, 0, 0, 0.0, 0.0),
 ]
 
 
@@ -195,6 +199,65 @@ def test_differences_that_round_to_nothing_still_draw():
                                            draft_logits=d)
     assert bool(((tokens[:, 0] >= 0) & (tokens[:, 0] < 3)).all())
     assert bool((tokens[accepted == 1, 1] >= 0).all()) and bool((tokens[accepted == 0, 1] == -1).all())
+
+
+def test_offsets_past_32_bits():
+    (x, x64), (d, d64), ids, accept, uniform, t = setup(3, 3, 2, 64, "bf16", True)
+    big = torch.empty(9 << 29, dtype=torch.bfloat16, device="cuda")
+    far = big.as_strided((3, 3, 64), (3 << 29, 1 << 29, 1))
+    far.copy_(x)
+    drafts, acc, uni, temp = (torch.from_numpy(a).cuda() for a in (ids.astype(np.int32), accept, uniform, t))
+    for draft in (d, None):
+        want = gc.sample_verify(x, drafts, acc, uni, draft_logits=draft, temperature=temp)
+        got = gc.sample_verify(far, drafts, acc, uni, draft_logits=draft, temperature=temp)
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+@pytest.mark.parametrize("temperature", [1e-45, 1e-30, 1e30, float("inf"), float("nan"), -1.0])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_temperatures_at_their_ends(dtype, temperature):
+    # next to 0 the largest logit is all there is, at infinity every open token weighs the same
+    g = torch.Generator(device="cuda").manual_seed(2)
+    x = (3 * torch.randn(50, 2, 777, generator=g, device="cuda")).to(DTYPES[dtype])
+    top = x.float().argmax(2)
+    drafts = top[:, :1].int()
+    drafts[25:] = (drafts[25:] + 1) % 777
+    accept, uniform = torch.full((50, 1), 0.5, device="cuda"), torch.rand(50, 777, generator=g, device="cuda")
+    tokens, accepted, logprobs = gc.sample_verify(x, drafts, accept, uniform, temperature=temperature)
+    if temperature > 1:
+        assert not accepted.any() and bool(((tokens[:, 0] >= 0) & (tokens[:, 0] != drafts[:, 0])).all())
+        # off by |z| of at most 1e-28, the sum's 777 additions and its logarithm
+        assert bool(((logprobs[:, 0] + np.log(777)).abs() <= 800 * 2.0 ** -24).all())
+        return
+    first = (x.float() == x.float().amax(2, keepdim=True)).float().argmax(2)
+    unique = (x.float() == x.float().amax(2, keepdim=True)).sum(2) == 1
+    sure = unique.all(1)
+    assert sure.sum() > 20
+    assert bool((accepted[:25][sure[:25]] == 1).all()) and bool((accepted[25:][sure[25:]] == 0).all())
+    assert torch.equal(tokens[:25][sure[:25]], first[:25][sure[:25]].int())
+    assert torch.equal(tokens[25:, 0][sure[25:]], first[25:, 0][sure[25:]].int())
+    assert bool((logprobs[:, 0][sure] == 0).all())
+
+
+def test_logits_of_any_size():
+    # values whose difference, or product with log2(e) / T, leaves float32
+    for big in (3e38, 1e30, 1e25):
+        x = torch.full((4, 2, 100), -big, device="cuda")
+        x[0, :, 3] = big                      # one far above the rest
+        x[1, :, 3], x[1, :, 4] = big, big     # two
+        x[2, :, 50:] = big                    # half
+        drafts = torch.tensor([[3], [4], [60], [0]], dtype=torch.int32, device="cuda")
+        accept, uniform = torch.full((4, 1), 0.001, device="cuda"), torch.rand(4, 100, device="cuda")
+        for t in (1.0, 1e-3, 1e3):
+            tokens, accepted, lp = gc.sample_verify(x, drafts, accept, uniform, draft_logits=torch.zeros(4, 1, 100, device="cuda"), temperature=t)
+            assert accepted.tolist() == [1, 1, 1, 1]
+            assert tokens[0].tolist() == [3, 3] and int(tokens[1, 1]) in (3, 4) and int(tokens[2, 1]) >= 50
+            want = torch.log(torch.tensor([1.0, 0.5, 1 / 50, 1 / 100], device="cuda"))
+            assert bool(((lp[:, 0] - want).abs() <= 2.0 ** -18).all())
+            r = gc.expert_route(x[:, 0], 3)
+            assert r.ids[0, 0] == 3 and r.ids[1].tolist()[:2] == [3, 4] and r.ids[2].tolist() == [50, 51, 52]
+            assert torch.equal(r.ids[3], torch.arange(3, dtype=torch.int32, device="cuda"))
+            assert bool(((r.weights.sum(1) - 1).abs() <= 8 * 2.0 ** -24).all())
 
 
 def test_nothing_to_verify():
