@@ -717,10 +717,14 @@ verify_draw_kernel(Verify a)
         if (a.logprobs == nullptr) continue;
         float lp = token < 0 ? -INFINITY : 0.0f;
         if (token >= 0 && !greedy) {
-            // log2 of the weight, less that of the sum
+            // log(w / sum) with sum = 2^k f, 1 <= f < 2: the exponent of w less k, without the roundings of either
+            // (the reference may lie far from both), and log f
             const float v = sample_value(row_to_float(x[j * a.x_stride + token])), m = s_target[j].m, o = m * power;
-            const float z = plain(o) ? fmaf(v, power, -o) : (v - m) * power;
-            lp = fmaf(z, 0.693147181f, -logf(s_target[j].sum));
+            const int bits = __float_as_int(s_target[j].sum), k = (bits >> 23) - 127;
+            const float f = __int_as_float((bits & 0x7fffff) | 0x3f800000), product = v * power;
+            float z = (v - m) * power - float(k);
+            if (plain(o)) z = product - o - float(k) + fmaf(v, power, -product);
+            lp = z * 0.693147181f - logf(f);
         }
         a.logprobs[at] = lp;
     }
