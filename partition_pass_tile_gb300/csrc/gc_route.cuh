@@ -25,17 +25,24 @@ inline uint32_t route_lanes(uint32_t experts)
     return lanes;
 }
 
-// This lane's logits of a token, -inf where there is none.
-template <class T, int N, int V>
+// This lane's logits of a token, -inf where there is none: pieces of N, each G
+// pieces behind the one before, so that the G lanes of a team read side by side
+// (G = 1: a lane's experts are neighbours).
+template <class T, int N, int V, int G>
 struct Logits {
     Piece<T, N> p[V / N];
 
+    // The expert of a lane's element v.
+    static __device__ __forceinline__ uint32_t expert(uint32_t first, int v)
+    {
+        return first + uint32_t(v / N * (G * N) + v % N);
+    }
     __device__ __forceinline__ void load(const T *__restrict__ row, uint32_t first, uint32_t experts, bool live)
     {
 #pragma unroll
         for (int i = 0; i < V / N; ++i) {
-            if (live && first + i * N < experts) {
-                p[i] = load_piece<T, N>(row + first + i * N);
+            if (live && first + i * G * N < experts) {
+                p[i] = load_piece<T, N>(row + first + i * G * N);
             } else {
 #pragma unroll
                 for (int e = 0; e < N; ++e) p[i].v[e] = row_from_float<T>(-INFINITY);

@@ -7,11 +7,10 @@
 // choice, c[e] the pairs of expert e and f = c / sum c:
 //     load = sum p / n,   loss = experts * sum f load.
 //
-// One read of the logits.  Lane l of a team of 16 or 32 (of a smaller group
-// where experts are few) holds the experts [l * V, (l + 1) * V) of a token in registers, so
-// that equal values go by lane and then by register; the lane's sums over
-// tokens of its experts' probabilities stay in registers until the end, CTAs
-// leave them in the workspace, and a cluster adds them up.
+// One read of the logits.  A token's experts lie in the registers of a team of 16
+// or 32 lanes, or of a smaller group where experts are few; the lanes' sums over
+// tokens of their experts' probabilities stay there until the end, CTAs leave
+// them in the workspace, and a cluster adds them up.
 #include "gc_route.cuh"
 
 namespace {
@@ -123,10 +122,12 @@ __device__ __forceinline__ uint32_t kth_largest(uint32_t v, uint32_t top, uint32
 // the lanes' largest.  The logits not below it, hardly more than k, are listed,
 // one to a lane, and ranked by comparing each with all.  Where they are more
 // than the lanes (many closed experts, equal values, large k) the choices are
-// taken one after another.  131072 tokens of 256 float32, top-8: 70 us against 21
-// for the bytes, bound by instructions (about 400 a token, half of them on the
-// pipe of comparisons and integers); by whole warps 76, one after another 162.
-// Of 64 experts, top-4, 37 us (warps 56), of 128 bf16, top-8, 49 (73).
+// taken one after another.  131072 tokens of 256 float32, top-8: 66 us against 21
+// for the bytes, bound by instructions (about 320 a token, most of them on the
+// pipes of comparisons, integers and shuffles); by whole warps 76, with a lane's
+// experts neighbours, which read every second 16 bytes or fewer at a time, 72,
+// one after another 162.  Of 64 experts, top-4, 37 us (warps 56), of 128 bf16,
+// top-8, 48 (73).
 template <class T, int N, int V, int G>
 __global__ void __launch_bounds__(kTeamThreads<V>, kTeamResident<V>)
 route_team_kernel(const T *__restrict__ logits, size_t stride, uint32_t tokens, uint32_t experts, uint32_t topk,
@@ -134,23 +135,23 @@ route_team_kernel(const T *__restrict__ logits, size_t stride, uint32_t tokens, 
 {
     constexpr int kWarps = kTeamThreads<V> / 32, kTeams = kTeamThreads<V> / G;
     constexpr int kSlots = V < 8 ? V : 8;
-    __shared__ uint32_t s_id[kTeams][kCandidates];
-    __shared__ uint4 s_key[kTeams][kCandidates / 4];
+    __shared__ uint4 s_id[kTeams][kCandidates / 4], s_key[kTeams][kCandidates / 4];
     __shared__ float s_sum[kWarps][G * kSlots];
     __shared__ uint32_t s_count[GC_MAX_EXPERTS];
     __shared__ uint32_t s_warp[kWarps];
     chain_start();
-    const uint32_t lane = threadIdx.x & (G - 1), team = threadIdx.x / G, warp = threadIdx.x >> 5, first = lane * V;
+    const uint32_t lane = threadIdx.x & (G - 1), team = threadIdx.x / G, warp = threadIdx.x >> 5, first = lane * N;
+    using Row = Logits<T, N, V, G>;
     for (uint32_t e = threadIdx.x; e < experts; e += kTeamThreads<V>) s_count[e] = 0;
     __syncthreads();
-    uint32_t *id = s_id[team], *key = reinterpret_cast<uint32_t *>(s_key[team]);
+    uint32_t *id = reinterpret_cast<uint32_t *>(s_id[team]), *key = reinterpret_cast<uint32_t *>(s_key[team]);
     float sum[V];
     uint32_t routed = 0;
 #pragma unroll
     for (int v = 0; v < V; ++v) sum[v] = 0.0f;
 
     const uint64_t step = uint64_t(gridDim.x) * kTeams;
-    Logits<T, N, V> next;
+    Row next;
     auto fetch = [&](uint64_t t) {
         next.load(logits + t * stride, first, experts, t < tokens && (mask == nullptr || mask[t] != 0));
     };
@@ -190,7 +191,7 @@ route_team_kernel(const T *__restrict__ logits, size_t stride, uint32_t tokens, 
         const uint32_t largest_n = __reduce_max_sync(kRouteFull, n);
         if (largest_n <= G) {
             // listed by id; read again, which spares finding them among the registers
-            for (; which; which &= which - 1, ++at) id[at] = first + Bits<V>::lowest(which);
+            for (; which; which &= which - 1, ++at) id[at] = Row::expert(first, Bits<V>::lowest(which));
             key[lane] = 0;
             __syncwarp();
             uint32_t own = 0, e = 0;
@@ -200,14 +201,13 @@ route_team_kernel(const T *__restrict__ logits, size_t stride, uint32_t tokens, 
                 key[lane] = own;
             }
             __syncwarp();
-            // before it: the larger ones, and the equal ones listed before it
+            // before it: the larger ones, and the equal ones of a lower expert
+            const uint64_t order = uint64_t(own) << 32 | uint32_t(~e);
+            auto before = [&](uint32_t k, uint32_t i) { return uint32_t((uint64_t(k) << 32 | uint32_t(~i)) > order); };
             uint32_t rank = 0;
             for (uint32_t c = 0; c < largest_n; c += 4) {
-                const uint4 k = s_key[team][c / 4];
-                rank += k.x >= own + (c >= lane);
-                rank += k.y >= own + (c + 1 >= lane);
-                rank += k.z >= own + (c + 2 >= lane);
-                rank += k.w >= own + (c + 3 >= lane);
+                const uint4 k = s_key[team][c / 4], i = s_id[team][c / 4];
+                rank += before(k.x, i.x) + before(k.y, i.y) + before(k.z, i.z) + before(k.w, i.w);
             }
             const bool chosen = lane < n && rank < topk;
             const float mine_w = chosen ? exponent.weight(order_value(own)) : 0.0f;
@@ -218,29 +218,31 @@ route_team_kernel(const T *__restrict__ logits, size_t stride, uint32_t tokens, 
                 if (out.counts) atomicAdd(&s_count[e], 1u);
             }
         } else {
-            // one after another: a lane's largest, and which of its logits are left
+            // one after another: a lane's largest with its expert, and which of its logits are left
             Mask rest = ~Mask(0);
+            uint32_t whose = 0;
+            auto largest_left = [&] {
+                left = 0;
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    const uint32_t k = order_bits(x[v]);
+                    if ((rest >> v & 1u) && k > left) left = k, whose = uint32_t(v);
+                }
+            };
+            largest_left();
             n = 0;
             for (uint32_t j = 0; j < topk; ++j) {
-                if (j > 0) top = team_max<G>(left);
-                const uint32_t have = team_ballot<G>(left == top && top > kRouteNone);
-                n += have != 0;
-                if (have != 0 && lane == uint32_t(__ffs(have) - 1)) {
-                    left = 0;
-                    bool found = false;
-#pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        if (!(rest >> v & 1u)) continue;
-                        const uint32_t k = order_bits(x[v]);
-                        if (!found && k == top) {
-                            found = true;
-                            rest &= ~(Mask(1) << v);
-                            id[j] = first + v;
-                            key[j] = top;
-                        } else {
-                            left = max(left, k);
-                        }
-                    }
+                top = team_max<G>(left);
+                // of equal ones the lowest expert
+                const uint32_t e = Row::expert(first, 0) + whose / N * (G * N) + whose % N;
+                const uint32_t low = ~team_max<G>(left == top ? ~e : 0u);
+                if (top <= kRouteNone) continue;
+                ++n;
+                if (left == top && e == low) {
+                    id[j] = e;
+                    key[j] = top;
+                    rest &= ~(Mask(1) << whose);
+                    largest_left();
                 }
             }
             __syncwarp();
@@ -270,7 +272,8 @@ route_team_kernel(const T *__restrict__ logits, size_t stride, uint32_t tokens, 
                 if ((threadIdx.x & 31) < G) s_sum[warp][lane * kSlots + (v & (kSlots - 1))] = s;
             }
             __syncthreads();
-            const uint32_t e = threadIdx.x / kSlots * V + base + threadIdx.x % kSlots;
+            const uint32_t v = base + threadIdx.x % kSlots;
+            const uint32_t e = threadIdx.x / kSlots * N + v / N * (G * N) + v % N;
             if (threadIdx.x < G * kSlots && e < experts) {
                 float s = 0.0f;
                 for (int w = 0; w < kWarps; ++w) s += s_sum[w][threadIdx.x];
@@ -311,7 +314,7 @@ route_group_kernel(const T *__restrict__ logits, size_t stride, uint32_t tokens,
     for (uint64_t base = uint64_t(blockIdx.x) * groups; base < tokens; base += uint64_t(gridDim.x) * groups) {
         const uint64_t t = base + threadIdx.x / lanes;
         const bool inside = t < tokens;
-        Logits<T, N, V> row;
+        Logits<T, N, V, 1> row;
         row.load(logits + t * stride, first, experts, inside && (mask == nullptr || mask[t] != 0));
         float x[V];
         uint32_t key[V], best = 0;

@@ -43,7 +43,7 @@ constexpr int kResident = V <= 4 ? 4 : V == 8 ? 3 : V == 16 ? 2 : 1;  // CTAs pe
 
 // The next token's logits and choices are on their way while one is computed.
 // 131072 tokens of 64 float32, 128 bf16 and 256 float32 by teams of 16: 24, 29
-// and 56 us (the last 72% of the copy rate); by whole warps, which pay for every
+// and 54 us (the last 75% of the copy rate); by whole warps, which pay for every
 // token what does not depend on its experts, 59, 70 and 64.
 template <class T, int N, int V, int G>
 __global__ void __launch_bounds__(kThreads, kResident<V>)
@@ -52,17 +52,21 @@ route_grad_team_kernel(const T *__restrict__ logits, T *__restrict__ dx, Grad a)
     constexpr int kTeams = 32 / G;
     __shared__ Pick s_pick[kWarps * kTeams][GC_MAX_TOPK];
     __shared__ uint32_t s_warp[kWarps];
-    const uint32_t lane = threadIdx.x & (G - 1), team = threadIdx.x / G, first = lane * V;
+    const uint32_t lane = threadIdx.x & (G - 1), team = threadIdx.x / G, first = lane * N;
+    using Row = Logits<T, N, V, G>;
     Pick *pick = s_pick[team];
     const float factor = loss_factor<kWarps>(a, s_warp);
     float share[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) share[v] = a.dloss && first + v < a.experts ? factor * float(a.counts[first + v]) : 0.0f;
+    for (int v = 0; v < V; ++v) {
+        const uint32_t e = Row::expert(first, v);
+        share[v] = a.dloss && e < a.experts ? factor * float(a.counts[e]) : 0.0f;
+    }
     const bool few = a.topk <= G;  // a choice to a lane
 
     const uint64_t step = uint64_t(gridDim.x) * kWarps * kTeams;
     uint64_t base = uint64_t(blockIdx.x) * kWarps * kTeams;
-    Logits<T, N, V> next;
+    Row next;
     uint32_t next_id = ~0u;
     float next_g = 0.0f;
     auto fetch = [&](uint64_t at) {
@@ -131,12 +135,13 @@ route_grad_team_kernel(const T *__restrict__ logits, T *__restrict__ dx, Grad a)
         if (inside) {
 #pragma unroll
             for (int i = 0; i < V; i += N) {
-                if (first + i >= a.experts) break;
+                const uint32_t at = Row::expert(first, i);
+                if (at >= a.experts) break;
                 Piece<T, N> o;
 #pragma unroll
                 for (int e = 0; e < N; ++e)
                     o.v[e] = row_from_float<T>(live ? w[i + e] * inverse * (share[i + e] - dot) : 0.0f);
-                store_piece<T, N>(to + first + i, o);
+                store_piece<T, N>(to + at, o);
             }
         }
         if (!a.dweights) continue;
@@ -196,7 +201,7 @@ route_grad_group_kernel(const T *__restrict__ logits, T *__restrict__ dx, Grad a
         const bool inside = t < a.tokens;
         const bool live = inside && uint32_t(a.ids[t * topk]) < experts;
         const T *row = logits + t * a.stride;
-        Logits<T, N, V> x;
+        Logits<T, N, V, 1> x;
         x.load(row, first, experts, live);
         float p[V], m = -INFINITY;
 #pragma unroll
