@@ -12,7 +12,7 @@
 // each chunk's maximum m and sum of exp((x - m) / T) (greedy sequences: the
 // first of the largest values).  The second reads one row of each sequence
 // again, the one at which it stops, and draws.  Chunks go by position first,
-// then by sequence: where there are more than the GPU holds at a time, the
+// then by sequence: where there are many more than the GPU holds at a time, the
 // last chunk of a position decides it, and chunks of later positions of a
 // sequence that has stopped are not read.
 //
@@ -23,8 +23,7 @@
 // Measured, kernels alone: 192 sequences of 5 drafts by a model, 128000 bf16, four
 // in five positions accepted: 118 us.  The rows take 72 of it, 356 MB at 5.1 TB/s,
 // where 316 MB would do (the rest was under way when its sequence stopped), bound
-// by the exponentials and their four instructions a logit; reading all 540 MB
-// takes 104.  The draw takes 46: 98 MB of random numbers and two rows of each
+// by the exponentials and their four instructions a logit.  The draw takes 46: 98 MB of random numbers and two rows of each
 // sequence once more.  One sequence of 4 drafts, 32768 float32: 11 us, two
 // launches' chains of dependent reads.
 #include <atomic>
@@ -49,7 +48,11 @@ constexpr float kUniformLo = 0x1p-25f, kUniformHi = 1.0f - 0x1p-24f;
 // for what every CTA does once; 32 take 118, with 50 MB more under way), where that makes more CTAs than the
 // GPU holds, else fewer.
 constexpr uint32_t kDrawWave = 4;          // CTAs per SM of the draw
-constexpr uint32_t kSteps = 16, kWave = 6;  // kWave: CTAs per SM
+constexpr uint32_t kSteps = 16, kWave = 6;
+// Positions are decided on the way where chunks are more than this many times
+// what the GPU holds at a time.  Of 5 drafts of 128000 bf16, 32 sequences take 43 us
+// so and 38 without, 96 take 76 and 76, 128 take 89 and 96, 192 take 120 and 136.
+constexpr size_t kSkipWaves = 5;  // kWave: CTAs per SM
 
 // z = (x - m) / t as a power of two's exponent.
 __device__ __forceinline__ float power_of(float t)
@@ -741,7 +744,7 @@ Plan plan_of(size_t rows, size_t vocab, size_t elem)
     uint32_t steps = kSteps;
     while (steps > 1 && rows * gch::ceil_div(pieces, size_t(steps) * kThreads) < wave) steps /= 2;
     Plan p{steps * kThreads, uint32_t(gch::ceil_div(pieces, size_t(steps) * kThreads)), false};
-    p.skip = rows * p.chunks > wave;
+    p.skip = rows * p.chunks > kSkipWaves * wave;
     return p;
 }
 
