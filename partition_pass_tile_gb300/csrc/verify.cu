@@ -398,8 +398,8 @@ verify_rows_kernel(Verify a)
             a.best[b] = 0;
             a.drawn[b] = 0;
         }
-    } else if (*reinterpret_cast<volatile uint32_t *>(a.left + b) > a.drafts - j) {
-        return;
+    } else if (__syncthreads_or(threadIdx.x == 0 && *reinterpret_cast<volatile uint32_t *>(a.left + b) > a.drafts - j)) {
+        return;  // read once: the word may change between two threads' reads
     }
     const float t = a.t(b), power = power_of(t);
     const bool greedy = !(t > 0.0f);
