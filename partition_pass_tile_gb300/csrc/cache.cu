@@ -182,8 +182,8 @@ struct SelectSmem {
 // kept.  A share of at most K * 1024 positions is read once.  128 heads of 32768
 // scores to 2048: 18 us, bound by instructions (about 60 a score); with four CTAs
 // to a head that read their scores from L2 five times, 43.
-template <int K>
-__global__ void __launch_bounds__(kEvictThreads)
+template <int K, int B>
+__global__ void __launch_bounds__(kEvictThreads, B)
 cache_select_kernel(Evict a)
 {
     __shared__ SelectSmem sm;
@@ -404,7 +404,7 @@ cache_move_kernel(Evict a, Move m, uint32_t down, uint32_t early)
     if (known) chain_wait();  // the launch is done when both kernels are
 }
 
-template <int K>
+template <int K, int B>
 cudaError_t run_select(cudaLaunchConfig_t cfg, const Evict &a)
 {
     cfg.dynamicSmemBytes = kEvictWarps * 32 * (K + 1) * sizeof(uint32_t);
@@ -414,11 +414,11 @@ cudaError_t run_select(cudaLaunchConfig_t cfg, const Evict &a)
     cudaError_t e = cudaGetDevice(&dev);
     const uint64_t bit = uint64_t(1) << (dev & 63);
     if (e == cudaSuccess && (dev > 63 || !(set.load(std::memory_order_relaxed) & bit))) {
-        e = cudaFuncSetAttribute(cache_select_kernel<K>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        e = cudaFuncSetAttribute(cache_select_kernel<K, B>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  int(cfg.dynamicSmemBytes));
         if (e == cudaSuccess) set.fetch_or(bit, std::memory_order_relaxed);
     }
-    return e == cudaSuccess ? cudaLaunchKernelEx(&cfg, cache_select_kernel<K>, a) : e;
+    return e == cudaSuccess ? cudaLaunchKernelEx(&cfg, cache_select_kernel<K, B>, a) : e;
 }
 
 template <class P>
@@ -491,10 +491,12 @@ cudaError_t launch_cache_evict(const gc_cache_rows *keys, const gc_cache_rows *v
                   lengths, kept_scores, kept_positions, kept_lengths, reinterpret_cast<int32_t *>(ws)};
     const uint32_t rows = batch * heads;
     // A cluster per head: as many CTAs as read its positions once, 32 to a
-    // thread, and more where all of them still run at a time.
+    // thread, and up to four with 16 to a thread where all of them still run at a
+    // time.  More meet too often: 8 heads of 32768 take 17 us by two CTAs each and
+    // 25 by eight, of 131072 25 by four and 31 by eight.
     uint32_t team = 1;
     while (team < kMaxTeam && length > team * 32 * kEvictThreads) team *= 2;
-    while (team < kMaxTeam && size_t(rows) * team * 2 <= kSms && length > team * 4 * kEvictThreads) team *= 2;
+    while (team < 4 && size_t(rows) * team * 2 <= kSms && length > team * 16 * kEvictThreads) team *= 2;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(rows * team);
     cfg.blockDim = dim3(kEvictThreads);
@@ -505,7 +507,16 @@ cudaError_t launch_cache_evict(const gc_cache_rows *keys, const gc_cache_rows *v
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    cudaError_t e = length <= team * 4 * kEvictThreads ? run_select<4>(cfg, a) : run_select<32>(cfg, a);
+    const uint32_t each = uint32_t(ceil_div(length, size_t(team) * kEvictThreads));
+    // No more positions to a thread than the length needs (256 heads of 8000: 27 us
+    // with 8, 42 with 32), and two CTAs to an SM, with half the registers, where
+    // there are more than SMs (1024 heads of 5000: 65 us, 117 with 32 and one).
+    const bool crowd = size_t(rows) * team > kSms;
+    cudaError_t e;
+    if (each <= 4) e = crowd ? run_select<4, 2>(cfg, a) : run_select<4, 1>(cfg, a);
+    else if (each <= 8) e = crowd ? run_select<8, 2>(cfg, a) : run_select<8, 1>(cfg, a);
+    else if (each <= 16) e = run_select<16, 1>(cfg, a);
+    else e = run_select<32, 1>(cfg, a);
     if (e != cudaSuccess) return e;
 
     Move m{};

@@ -849,7 +849,7 @@ def _rows3(t: torch.Tensor, what: str) -> tuple[int, int]:
 def _out(t: torch.Tensor | None, shape, dtype: torch.dtype, device, stream, what: str) -> tuple[torch.Tensor, int]:
     """The caller's contiguous output, checked, or a new one; and its pointer."""
     if t is None:
-        t = _new(shape, dtype, device, stream)
+        t = torch.empty(shape, dtype=dtype, device=device) if stream is None else _new(shape, dtype, device, stream)
         return t, t.data_ptr()
     if t.shape != shape or t.dtype != dtype:
         raise ValueError(f"{what} is a {dtype} tensor of shape {tuple(shape)}")
@@ -972,13 +972,13 @@ def sample_verify(logits: torch.Tensor, drafts: torch.Tensor, accept: torch.Tens
         up, us = _rows(uniform)
     temperature = _per_row(temperature, torch.float32, sequences, dev, stream)
     tokens, tp = _out(tokens, (sequences, places), torch.int32, dev, stream, "tokens")
-    accepted, np = _out(accepted, (sequences,), torch.int32, dev, stream, "accepted")
+    accepted, ap = _out(accepted, (sequences,), torch.int32, dev, stream, "accepted")
     logprobs, pp = _out(logprobs, (sequences, places), torch.float32, dev, stream, "logprobs")
     ws = _scratch(ws, sample_verify_workspace_bytes(sequences, n, vocab), dev, stream)
     _check(load().gc_sample_verify(
         lp, ls, dp, ds, sequences, n, vocab, row_dtype_code(logits.dtype),
         _typed(drafts, torch.int32, sequences * n, "drafts"), _typed(accept, torch.float32, sequences * n, "accept"),
-        up, us, _typed(temperature, torch.float32, sequences, "temperature"), tp, np, pp, _ptr(ws), ws.numel(),
+        up, us, _typed(temperature, torch.float32, sequences, "temperature"), tp, ap, pp, _ptr(ws), ws.numel(),
         _handle(stream, dev)), "gc_sample_verify")
     return tokens, accepted, logprobs
 
