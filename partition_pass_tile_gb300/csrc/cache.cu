@@ -336,31 +336,59 @@ struct RowArray {
 
 struct Move {
     RowArray from[2], to[2];    // keys, values
-    uint32_t pieces[2];         // of sizeof(P) bytes
-    uint32_t arrays;
+    uint32_t pieces[2];         // of a row
+    uint32_t piece[2];          // bytes of one: 2, 4, 8 or 16
+    uint32_t across[2];         // threads to a row
+    uint32_t arrays, slots;     // slots of a block
 };
 
 constexpr int kMoveThreads = 256;
 constexpr int kMoveAhead = 4;   // rows that a thread has under way
 
-// The kept rows: a row of threads per slot, kMoveAhead slots at a time, head by
-// head.  Of `down` blocks of a head those that hold recent positions alone, the
-// `early` last, come first for all heads: they need not wait for the selection.
-// 128 heads of 2048 rows of 2 x 256 bytes: 47 us behind the selection's 18, for
-// 268 MB (40 at the copy rate), each row a place of its own in HBM.
-template <class P>
-__global__ void __launch_bounds__(kMoveThreads, 5)
+// A block's slots of one array, each thread kMoveAhead rows at a time.
+// position(slot) is a position, or `none`.
+template <class P, class F>
+__device__ __forceinline__ void move_rows(const uint8_t *from, size_t from_row, uint8_t *to, size_t to_row,
+                                          uint32_t pieces, uint32_t across, uint32_t first, uint32_t end,
+                                          uint32_t none, const F &position)
+{
+    const uint32_t down = kMoveThreads / across, x = threadIdx.x & (across - 1), y = threadIdx.x / across;
+    for (uint32_t slot = first + y; slot < end; slot += kMoveAhead * down) {
+        uint32_t at[kMoveAhead];
+#pragma unroll
+        for (int k = 0; k < kMoveAhead; ++k) at[k] = slot + k * down < end ? position(slot + k * down) : none;
+        for (uint32_t c = x; c < pieces; c += across) {
+            P v[kMoveAhead];
+#pragma unroll
+            for (int k = 0; k < kMoveAhead; ++k)
+                if (at[k] < none) v[k] = reinterpret_cast<const P *>(from + size_t(at[k]) * from_row)[c];
+#pragma unroll
+            for (int k = 0; k < kMoveAhead; ++k)
+                if (at[k] < none) reinterpret_cast<P *>(to + size_t(slot + k * down) * to_row)[c] = v[k];
+        }
+    }
+}
+
+// The kept rows, head by head; each array by the largest pieces that its own
+// addresses allow.  Of `down` blocks of a head those that hold recent positions
+// alone, the `early` last, come first for all heads: they need not wait for the
+// selection.  128 heads of 2048 rows of 2 x 256 bytes: 44 us behind the
+// selection's 18, for 268 MB (40 at the copy rate), each row a place of its own
+// in HBM.  Blocks on an SM count for more than registers: with 4, 5, 6 and 8 of
+// them 72, 67, 64 and 62 us altogether, though 8 spill 60 bytes; two rows at a
+// time instead of four also 62, and 69 to 59 where rows have 66 bytes.
+__global__ void __launch_bounds__(kMoveThreads, 8)
 cache_move_kernel(Evict a, Move m, uint32_t down, uint32_t early)
 {
     const uint32_t ahead = early * a.rows(), late = down - early;
     const bool is_early = blockIdx.x < ahead;
-    const uint32_t at_ = is_early ? blockIdx.x : blockIdx.x - ahead, each = is_early ? early : late;
-    const uint32_t bh = at_ / each, block = at_ % each + (is_early ? late : 0);
+    const uint32_t unit = is_early ? blockIdx.x : blockIdx.x - ahead, each = is_early ? early : late;
+    const uint32_t bh = unit / each, block = unit % each + (is_early ? late : 0);
     const uint32_t b = bh / a.heads, h = bh % a.heads, w = blockIdx.y;
     const uint32_t n = clamp_length(a.lengths, b, a.length), kept = min(n, a.budget);
-    const uint32_t slots = blockDim.y * kMoveAhead, first = block * slots + threadIdx.y;
+    const uint32_t first = block * m.slots, end = min(first + m.slots, a.budget);
     // slots whose positions are known beforehand: those of the recent ones, of the sinks, and all of a short sequence
-    const bool known = n <= a.budget || block * slots >= a.budget - a.recent || (block + 1) * slots <= a.sinks;
+    const bool known = n <= a.budget || first >= a.budget - a.recent || end <= a.sinks;
     if (!known) chain_wait();
     const int32_t *list = a.list + size_t(bh) * a.budget;
     // the position of a slot, or a.length
@@ -371,8 +399,8 @@ cache_move_kernel(Evict a, Move m, uint32_t down, uint32_t early)
         return min(uint32_t(list[slot]), a.length);
     };
     if (w == m.arrays) {  // scores and positions, a thread to a slot
-        const uint32_t me = threadIdx.y * blockDim.x + threadIdx.x, slot = block * slots + me;
-        if (me < slots && slot < a.budget) {
+        const uint32_t slot = first + threadIdx.x;
+        if (slot < end) {
             const uint32_t i = position(slot);
             float score = 0.0f;
             int32_t at = -1;
@@ -383,23 +411,19 @@ cache_move_kernel(Evict a, Move m, uint32_t down, uint32_t early)
             a.kept_scores[size_t(bh) * a.budget + slot] = score;
             a.kept_positions[size_t(bh) * a.budget + slot] = at;
         }
-        if (known) chain_wait();
-        return;
-    }
-    const uint8_t *from = m.from[w].p + size_t(b) * m.from[w].batch + size_t(h) * m.from[w].head;
-    uint8_t *to = m.to[w].p + size_t(b) * m.to[w].batch + size_t(h) * m.to[w].head;
-    uint32_t at[kMoveAhead];
-#pragma unroll
-    for (int k = 0; k < kMoveAhead; ++k) at[k] = position(first + k * blockDim.y);
-    for (uint32_t c = threadIdx.x; c < m.pieces[w]; c += blockDim.x) {
-        P v[kMoveAhead];
-#pragma unroll
-        for (int k = 0; k < kMoveAhead; ++k)
-            if (at[k] < a.length) v[k] = reinterpret_cast<const P *>(from + size_t(at[k]) * m.from[w].row)[c];
-#pragma unroll
-        for (int k = 0; k < kMoveAhead; ++k)
-            if (at[k] < a.length)
-                reinterpret_cast<P *>(to + size_t(first + k * blockDim.y) * m.to[w].row)[c] = v[k];
+    } else {
+        const uint8_t *from = m.from[w].p + size_t(b) * m.from[w].batch + size_t(h) * m.from[w].head;
+        uint8_t *to = m.to[w].p + size_t(b) * m.to[w].batch + size_t(h) * m.to[w].head;
+        auto move = [&](auto piece) {
+            move_rows<decltype(piece)>(from, m.from[w].row, to, m.to[w].row, m.pieces[w], m.across[w], first, end,
+                                       a.length, position);
+        };
+        switch (m.piece[w]) {
+        case 2: move(uint16_t()); break;
+        case 4: move(uint32_t()); break;
+        case 8: move(uint2()); break;
+        default: move(uint4()); break;
+        }
     }
     if (known) chain_wait();  // the launch is done when both kernels are
 }
@@ -419,23 +443,6 @@ cudaError_t run_select(cudaLaunchConfig_t cfg, const Evict &a)
         if (e == cudaSuccess) set.fetch_or(bit, std::memory_order_relaxed);
     }
     return e == cudaSuccess ? cudaLaunchKernelEx(&cfg, cache_select_kernel<K, B>, a) : e;
-}
-
-template <class P>
-cudaError_t run_move(const Evict &a, Move m, cudaStream_t s)
-{
-    uint32_t most = 1;
-    for (uint32_t w = 0; w < m.arrays; ++w) {
-        m.pieces[w] /= sizeof(P);
-        most = m.pieces[w] > most ? m.pieces[w] : most;
-    }
-    uint32_t tx = kMoveAhead;  // so that a block has a thread to a slot
-    while (tx < kMoveThreads && tx < most) tx <<= 1;
-    const dim3 block(tx, kMoveThreads / tx);
-    const uint32_t slots = block.y * kMoveAhead, down = uint32_t(gch::ceil_div(a.budget, slots));
-    const uint32_t early = down - uint32_t(gch::ceil_div(a.budget - a.recent, slots));
-    return gch::launch_next(cache_move_kernel<P>, dim3(down * a.batch * a.heads, m.arrays + 1), block, 0, s, a, m, down,
-                            early);
 }
 
 template <class T, int N>
@@ -521,10 +528,10 @@ cudaError_t launch_cache_evict(const gc_cache_rows *keys, const gc_cache_rows *v
 
     Move m{};
     const size_t elem = dt == GC_ROW_F32 ? 4 : 2;
-    const uint32_t arrays = m.arrays = values ? 2 : 1;
-    uint64_t bits = 0;
     const gc_cache_rows *from[2] = {keys, values}, *to[2] = {kept_keys, kept_values};
-    for (uint32_t w = 0; w < arrays; ++w) {
+    m.arrays = values ? 2 : 1;
+    for (uint32_t w = 0; w < m.arrays; ++w) {
+        uint64_t bits = 0;
         auto put = [&](const gc_cache_rows &r) {
             const RowArray t{static_cast<uint8_t *>(r.d_rows), r.batch_stride * elem, r.head_stride * elem,
                              r.row_stride * elem};
@@ -533,14 +540,15 @@ cudaError_t launch_cache_evict(const gc_cache_rows *keys, const gc_cache_rows *v
         };
         m.from[w] = put(*from[w]);
         m.to[w] = put(*to[w]);
-        m.pieces[w] = uint32_t(from[w]->width * elem);
+        m.piece[w] = uint32_t(piece_elems(bits, 2)) * 2;
+        m.pieces[w] = uint32_t(from[w]->width * elem / m.piece[w]);
+        for (m.across[w] = 1; m.across[w] < uint32_t(kMoveThreads) && m.across[w] < m.pieces[w];) m.across[w] *= 2;
     }
-    switch (piece_elems(bits, 2) * 2) {
-    case 2: return run_move<uint16_t>(a, m, s);
-    case 4: return run_move<uint32_t>(a, m, s);
-    case 8: return run_move<uint2>(a, m, s);
-    default: return run_move<uint4>(a, m, s);
-    }
+    // 64 slots to a block, fewer where that would leave SMs without one
+    m.slots = 64;
+    while (m.slots > 16 && size_t(rows) * ceil_div(budget, m.slots) < kSms * 4) m.slots /= 2;
+    const uint32_t down = uint32_t(ceil_div(budget, m.slots)), early = down - uint32_t(ceil_div(budget - recent, m.slots));
+    return launch_next(cache_move_kernel, dim3(down * rows, m.arrays + 1), dim3(kMoveThreads), 0, s, a, m, down, early);
 }
 
 }  // namespace gch
