@@ -259,8 +259,9 @@ __device__ __forceinline__ Part chunk_sum(const Pieces<T> &row, uint32_t first, 
     if (singles) {
         const uint32_t i = row.single(threadIdx.x);
         if (i < row.vocab) {
+            // by itself, with the rounding that its own product with `power` leaves in every weight by it
             const float x = sample_value(row_to_float(row.x[i]));
-            if (x > -INFINITY) join(m, sum, x, 1.0f, power);
+            if (x > -INFINITY) join(m, sum, x, weight(x, x, power), power);
         }
     }
     join_lanes(m, sum, power);

@@ -1,0 +1,72 @@
+"""Verification of drafted tokens where its arithmetic is at its ends: elements
+outside a row's 16-byte pieces, logits far above those met first, random numbers
+below 0, rows without a draft's probabilities.
+
+Tolerances of a log probability, e = 2^-24, with z the distance of its logit
+from the largest over T and Z the mean of z over the row's probabilities.  Terms
+of z: log2(e) / T is off by 2.3 e, a weight's exponent by e z, the logarithm's
+product and conversion by 2 e z: 8 e (z + Z) at most.  Constant ones of a row of
+one chunk: 4 e for a weight's approximation; three joins of sums by different
+maxima (single elements, lanes, warps), 6 e each; 18 additions; 4 e for the
+logarithm and what is added to it: 44 e, taken as 64 e."""
+
+import numpy as np
+import pytest
+import torch
+
+import more_rows_ref as ref
+from partition_pass_tile_gb300 import gc
+from test_verify_gpu import DTYPES, check, rows_of, setup
+
+pytestmark = pytest.mark.gpu
+
+E = 2.0 ** -24
+
+
+def log_p(x64, temperature):
+    """-> log probabilities in 64 bits, z, the mean of z."""
+    z = (x64.max(-1, keepdims=True) - x64) / float(np.float32(temperature))
+    w = np.exp(-np.minimum(z, 800.0))
+    total = w.sum(-1, keepdims=True)
+    return -z - np.log(total), z, (w / total * np.minimum(z, 800.0)).sum(-1, keepdims=True)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("temperature,size", [(1.0, 10.0), (0.1, 10.0), (0.01, 10.0), (1e-3, 10.0), (1e-4, 10.0),
+                                              (1.0, 4000.0), (0.1, 4000.0), (1e-4, 4000.0)])
+def test_largest_logit_outside_the_pieces(dtype, temperature, size):
+    # rows of odd length an odd distance apart start at every alignment; the largest logit is one of the first or last
+    rng = np.random.default_rng(int(size) + round(1 / temperature))
+    n, vocab = 48, 1003
+    x = size * (0.5 + 0.1 * rng.standard_normal((n, 2, vocab)))
+    at = rng.choice([0, 1, 2, 6, 500, vocab - 7, vocab - 3, vocab - 2, vocab - 1], (n, 2))
+    np.put_along_axis(x, at[:, :, None], size * (1.2 + 0.3 * rng.random((n, 2, 1))), 2)
+    xt, x64 = rows_of(x.astype(np.float32), dtype, 2)
+    drafts = torch.from_numpy(at[:, :1].astype(np.int32)).cuda()
+    uniform = torch.from_numpy(rng.random((n, vocab)).astype(np.float32)).cuda()
+    tokens, accepted, logprobs = gc.sample_verify(xt, drafts, torch.zeros(n, 1, device="cuda"), uniform,
+                                                  temperature=temperature)
+    assert accepted.tolist() == [1] * n
+    lp, z, mean = log_p(x64, temperature)
+    tokens = tokens.cpu().numpy()[:, :, None].astype(np.int64)
+    assert np.array_equal(tokens[:, 0, 0], at[:, 0])
+    want, bound = np.take_along_axis(lp, tokens, 2), (64 + 8 * (np.take_along_axis(z, tokens, 2) + mean)) * E
+    assert np.all(np.abs(logprobs.double().cpu().numpy()[:, :, None] - want) <= bound)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("temperature,size", [(1.0, 10.0), (0.01, 10.0), (1e-4, 10.0), (1.0, 4000.0)])
+def test_a_certain_token_outside_the_pieces_is_accepted(dtype, temperature, size):
+    # p = 1 is above every u q, u at most 1 - 2^-24
+    rng = np.random.default_rng(int(size) + round(1 / temperature))
+    n, vocab = 48, 77
+    x = np.full((n, 2, vocab), -np.inf)
+    at = rng.choice([0, 1, 2, 40, vocab - 3, vocab - 2, vocab - 1], (n, 2))
+    np.put_along_axis(x, at[:, :, None], size * (1 + rng.random((n, 2, 1))), 2)
+    xt, _ = rows_of(x.astype(np.float32), dtype, 2)
+    drafts = torch.from_numpy(at[:, :1].astype(np.int32)).cuda()
+    tokens, accepted, logprobs = gc.sample_verify(xt, drafts, torch.ones(n, 1, device="cuda"),
+                                                  torch.rand(n, vocab, device="cuda"), temperature=temperature)
+    assert accepted.tolist() == [1] * n and tokens.tolist() == at.tolist()
+    # twice the weight's approximation, 4 e, at most
+    assert bool((logprobs.abs() <= 8 * E).all())
