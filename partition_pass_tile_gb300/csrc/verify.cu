@@ -728,7 +728,7 @@ verify_draw_kernel(Verify a)
             const float f = __int_as_float((bits & 0x7fffff) | 0x3f800000), product = v * power;
             float z = (v - m) * power - float(k);
             if (plain(o)) z = product - o - float(k) + fmaf(v, power, -product);
-            lp = z * 0.693147181f - logf(f);
+            lp = fminf(z * 0.693147181f - logf(f), 0.0f);  // what is above 0 is roundings
         }
         a.logprobs[at] = lp;
     }

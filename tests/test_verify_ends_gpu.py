@@ -70,3 +70,17 @@ def test_a_certain_token_outside_the_pieces_is_accepted(dtype, temperature, size
     assert accepted.tolist() == [1] * n and tokens.tolist() == at.tolist()
     # twice the weight's approximation, 4 e, at most
     assert bool((logprobs.abs() <= 8 * E).all())
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_no_log_probability_is_above_zero(dtype):
+    # one token outweighs all others: its log probability is 0 but for roundings, which must not show as p > 1
+    rng = np.random.default_rng(8)
+    n, vocab = 600, 2003
+    x = 3 * rng.standard_normal((n, 1, vocab))
+    x[np.arange(n), 0, rng.integers(0, vocab, n)] = 40 + 10 * rng.random(n)
+    xt, _ = rows_of(x.astype(np.float32), dtype, 2)
+    none = torch.empty(n, 0, dtype=torch.int32, device="cuda")
+    for temperature in (1.3, 1.0, 0.7, 0.05):
+        logprobs = gc.sample_verify(xt, none, none.float(), torch.rand(n, vocab, device="cuda"), temperature=temperature)[2]
+        assert bool((logprobs <= 0).all())
