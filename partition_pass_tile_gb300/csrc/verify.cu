@@ -436,6 +436,7 @@ verify_rows_kernel(Verify a)
 // Of the tokens offered, the largest r / -log v; equal ones, the lowest index.
 // A token can only be it if -log v < r / bound for any ratio `bound` already
 // seen, so v > 1 - r / bound: one multiply-add spares most tokens the logarithm.
+// v is one that counts: numbers below 2^-25 and NaN are 2^-25.
 struct Best {
     float ratio = 0.0f;
     uint32_t index = ~0u;
@@ -583,7 +584,7 @@ __device__ __forceinline__ Best chunk_draw(const Stop<T> &s, const Pieces<T> &ro
         }
 #pragma unroll
         for (uint32_t e = 0; e < kVec; ++e)
-            if (best.open(r[e], u[e])) which |= 1u << e;
+            if (best.open(r[e], fmaxf(u[e], kUniformLo))) which |= 1u << e;
         for (; which; which &= which - 1) {
             const uint32_t t = i + __ffs(which) - 1;
             if (t < row.vocab && t != s.without) best.take(s.r(t), s.u[t], t);

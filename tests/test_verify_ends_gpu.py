@@ -84,3 +84,21 @@ def test_no_log_probability_is_above_zero(dtype):
     for temperature in (1.3, 1.0, 0.7, 0.05):
         logprobs = gc.sample_verify(xt, none, none.float(), torch.rand(n, vocab, device="cuda"), temperature=temperature)[2]
         assert bool((logprobs <= 0).all())
+
+
+@pytest.mark.parametrize("number", [-100.0, -float("inf"), -2.0 ** -30, float("nan")])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_random_numbers_below_zero_draw(dtype, number):
+    # They count as 2^-25.  The token that has one weighs about 50 times each of the others, whose numbers are 0.5: its
+    # ratio is 50 / 17.3, theirs 1 / 0.69, which is half of it.  With many sequences a thread has several pieces of a
+    # row, and the token's is none of the first.
+    for n, vocab in ((1, 1500), (3, 40001), (700, 9000)):
+        x = torch.zeros(n, 1, vocab, dtype=DTYPES[dtype], device="cuda")
+        uniform = torch.full((n, vocab), 0.5, device="cuda")
+        rows = torch.arange(n, device="cuda")
+        at = rows % 500 + vocab - 600
+        x[rows, 0, at] = 3.9
+        uniform[rows, at] = number
+        none = torch.empty(n, 0, dtype=torch.int32, device="cuda")
+        tokens, _, _ = gc.sample_verify(x, none, none.float(), uniform)
+        assert torch.equal(tokens[:, 0].long(), at), (n, vocab)
