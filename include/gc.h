@@ -771,7 +771,7 @@ size_t gc_cache_evict_workspace_bytes(size_t batch, size_t heads, size_t budget)
  * lengths[b] positions of head h of sequence b all if n <= budget, else
  *   - the first `sinks`, and the last `recent`,
  *   - of those between, the budget - sinks - recent with the highest scores,
- *     equal scores (-0 and +0 are equal) the lower position, NaN below all.
+ *     equal scores the lower position; -0 and +0 are equal, NaN counts as -inf.
  * They keep their order: kept row i is that of the i-th of them.
  *
  * keys, values: the cache's rows, batch x heads x length of dtype; values may

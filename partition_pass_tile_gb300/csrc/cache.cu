@@ -148,7 +148,7 @@ struct Evict {
     __host__ __device__ __forceinline__ uint32_t rows() const { return batch * heads; }
 };
 
-// Ascends with the score; NaN is the least.
+// Ascends with the score; NaN counts as -inf.
 __device__ __forceinline__ uint32_t score_key(float x) { return order_bits(fmaxf(x, -INFINITY)); }
 
 // Exclusive sum over the threads of a CTA.
