@@ -709,11 +709,16 @@ size_t gc_sample_verify_workspace_bytes(size_t sequences, size_t drafts, size_t 
  * Filters (top-k, top-p, min-p) are applied to the logits beforehand, by -inf
  * in the target's and the draft's.
  *
- * Roundings: p and q are exp2 of (x - max) * (log2(e) / T) in float32, off by
- * at most (4 + 5/4 |z|) * 2^-22 of themselves, |z| = (max - x) / T; sums are
- * float32, at most 128 logits of one thread and vocab / 131072 of its chunks one
- * after another; the comparison is in double.  The result is that of these p and q: a position
- * whose u q and p agree to that many bits may be decided either way.
+ * Roundings, with z = (max - x) / T: the weight exp(-z) of a logit is a power
+ * of two by a maximum of the logits met so far, which later ones may exceed by
+ * up to 2^60; it is off by at most (7 + 5/4 z) * 2^-22 of itself.  Sums are
+ * float32: at most 128 logits of one thread one after another, threads by
+ * trees, then at most vocab / 32768 + 2 of the row's chunks one after another.
+ * Each join of sums by different maxima adds at most 2^-20: on a logit's way
+ * at most one for each piece of its thread (16) and each of those chunks, and
+ * four more; usually fewer than six.  The comparison of u q with p is in
+ * double.  The result is that of these p and q: a position whose u q and p
+ * agree to that many bits may be decided either way.
  *
  * d_logits: sequences * (drafts + 1) rows of `vocab`, d_draft_logits:
  * sequences * drafts rows of the same type; d_drafts: int32, sequences *

@@ -102,3 +102,25 @@ def test_random_numbers_below_zero_draw(dtype, number):
         none = torch.empty(n, 0, dtype=torch.int32, device="cuda")
         tokens, _, _ = gc.sample_verify(x, none, none.float(), uniform)
         assert torch.equal(tokens[:, 0].long(), at), (n, vocab)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_logits_far_above_the_first_of_a_thread(dtype):
+    # Each thread's first piece of a row is low, some of the later ones are 25 to 40 above it, less than 2^60.
+    # Beyond the constant terms above: exponents of up to 60 round by 22 e of the weight, in the sum, in p and twice in
+    # the logarithm; one join of maxima as far apart, 42 e; up to three more joins, 6 e each, and 24 more additions:
+    # 64 + 88 + 42 + 18 + 24, taken as 240 e.
+    rng = np.random.default_rng(11)
+    n, vocab = 40, 131072
+    piece = 4 if dtype == "f32" else 8
+    x = rng.standard_normal((n, 1, vocab)).astype(np.float32)
+    number = np.arange(vocab) // (256 * piece)                  # of a thread's piece among its pieces
+    later = (number % 2 == 1) & (rng.random((n, 1, vocab)) < 0.001)
+    x[later] += rng.uniform(25, 40, int(later.sum())).astype(np.float32)
+    xt, x64 = rows_of(x, dtype)
+    none = torch.empty(n, 0, dtype=torch.int32, device="cuda")
+    tokens, _, logprobs = gc.sample_verify(xt, none, none.float(), torch.rand(n, vocab, device="cuda"))
+    lp, z, mean = log_p(x64, 1.0)
+    tokens = tokens.cpu().numpy()[:, :, None].astype(np.int64)
+    want, bound = np.take_along_axis(lp, tokens, 2), (240 + 8 * (np.take_along_axis(z, tokens, 2) + mean)) * E
+    assert np.all(np.abs(logprobs.double().cpu().numpy()[:, :, None] - want) <= bound)
