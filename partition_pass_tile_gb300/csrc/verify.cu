@@ -427,6 +427,7 @@ verify_rows_kernel(Verify a)
         __threadfence();
     }
     before = __shfl_sync(kFull, before, 0);
+    __syncwarp();  // a shuffle orders nothing: the other lanes read the parts behind lane 0's fence
     none = !a.real(uint32_t(ids[j]));  // then the draft's row is not read
     if (before + 1 != a.chunks * (greedy || none ? 1 : kinds)) return;
     Part target, draft;
