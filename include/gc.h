@@ -786,7 +786,7 @@ size_t gc_cache_evict_workspace_bytes(size_t batch, size_t heads, size_t budget)
  * batch x heads x budget rows of the same widths; rows from the sequence's new
  * length on are left as they were.  d_kept_scores, d_kept_positions: batch *
  * heads * budget, from the new length on 0 and -1.  d_kept_lengths: min(n,
- * budget) per sequence.  sinks + recent <= budget, budget >= 1.
+ * budget) per sequence.  sinks + recent <= budget, budget >= 1, heads >= 1.
  */
 gc_status gc_cache_evict(const gc_cache_rows *keys, const gc_cache_rows *values, gc_row_dtype dtype,
                          const float *d_scores, size_t scores_stride, const int32_t *d_positions,

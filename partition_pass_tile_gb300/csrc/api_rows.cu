@@ -411,7 +411,8 @@ gc_status gc_cache_score(const void *d_weights, size_t batch_stride, size_t head
 
 size_t gc_cache_evict_workspace_bytes(size_t batch, size_t heads, size_t budget)
 {
-    if (batch > GC_MAX_ELEMENTS || heads > GC_MAX_ELEMENTS || !valid_grid(batch, heads) || budget < 1 ||
+    // without a head no kernel would write the sequences' new lengths
+    if (batch > GC_MAX_ELEMENTS || heads < 1 || heads > GC_MAX_ELEMENTS || !valid_grid(batch, heads) || budget < 1 ||
         budget > GC_MAX_ROW_WIDTH || !valid_grid(batch * heads, budget))
         return 0;
     return cache_evict_workspace_bytes(batch * heads, budget);
