@@ -1000,21 +1000,24 @@ def cache_score(weights: torch.Tensor, scores: torch.Tensor | None, heads: int |
     batch, query_heads, count, length = weights.shape
     sb, sh, sq, _ = weights.stride()
     if scores is not None:
+        if scores.dim() != 3:
+            raise ValueError("scores is a float32 tensor [batch, heads, length]")
         if heads not in (None, scores.size(1)):
             raise ValueError(f"scores has {scores.size(1)} heads, not {heads}")
         heads = scores.size(1)
         if scores.dtype != torch.float32 or scores.shape != (batch, heads, length):
             raise ValueError(f"scores is a float32 tensor of shape {(batch, heads, length)}")
-    if not heads or query_heads % heads or not query_heads:
+    if heads is None or heads < 1 or query_heads % heads or not query_heads:
         raise ValueError(f"{query_heads} query heads share {heads} heads of a cache")
     dev = weights.device
     out = _like(out, (batch, heads, length), torch.float32, dev, stream, "out")
     sp, ss = (None, 0) if scores is None else _rows3(scores, "scores")
     op, os = _rows3(out, "out")
     _check(load().gc_cache_score(
-        weights.data_ptr(), sb if batch > 1 else 0, sh if query_heads > 1 else 0, sq if count > 1 else 0, row_dtype_code(weights.dtype), batch, heads, query_heads // heads, count,
-        length, sp, ss, decay, _typed(lengths, torch.int32, batch, "lengths"),
-        _typed(queries, torch.int32, batch, "queries"), op, os, _handle(stream, dev)), "gc_cache_score")
+        weights.data_ptr(), sb if batch > 1 else 0, sh if query_heads > 1 else 0, sq if count > 1 else 0,
+        row_dtype_code(weights.dtype), batch, heads, query_heads // heads, count, length, sp, ss, decay,
+        _typed(lengths, torch.int32, batch, "lengths"), _typed(queries, torch.int32, batch, "queries"), op, os,
+        _handle(stream, dev)), "gc_cache_score")
     return out
 
 

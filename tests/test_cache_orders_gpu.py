@@ -1,4 +1,4 @@
-"""Eviction on the GPU with scores that are not numbers."""
+"""Eviction on the GPU with scores that are not numbers, and refusals of scores."""
 
 import numpy as np
 import pytest
@@ -45,3 +45,13 @@ def test_scores_that_are_not_numbers_count_as_the_least():
     assert gc.cache_evict(k, None, s, 2).positions.tolist() == [[[0, 3], [0, 1], [0, 1], [2, 3]]]
     assert gc.cache_evict(k, None, s, 1).positions.tolist() == [[[3], [0], [1], [2]]]
     check(k, s, [4], 3, 0, 0)
+
+
+def test_scores_of_other_shapes_are_refused():
+    w = torch.zeros(2, 6, 1, 20, device="cuda")
+    for call in (lambda: gc.cache_score(w, None, heads=-1), lambda: gc.cache_score(w, None, heads=0),
+                 lambda: gc.cache_score(w, torch.zeros(20, device="cuda")),
+                 lambda: gc.cache_score(w, torch.zeros(2, 20, device="cuda")),
+                 lambda: gc.cache_score(w, torch.zeros(2, 3, 20, device="cuda"), heads=2)):
+        with pytest.raises(ValueError):
+            call()
