@@ -210,27 +210,29 @@ struct Pick {
 
 // Pieces of 16 bytes (or of a lane's share) where pointers, strides and experts
 // allow it, else elements.  CALL(T, N) for groups, CALL_TEAM(T, N, V, G) for
-// teams: 16 lanes up to 256 experts if `half`, else the whole warp.
+// teams: 16 lanes up to 256 experts, else the whole warp.  WARP(T, whole): what
+// comes before the teams of 16 lanes; GC_ROUTE_NO_WARP where they do always.
 #define GC_ROUTE_TEAM(T, whole, V, G, CALL_TEAM)                                            \
     {                                                                                       \
         constexpr int kMost = 16 / int(sizeof(T)), kPiece = V < kMost ? V : kMost;          \
         if (whole) return CALL_TEAM(T, kPiece, V, G);                                       \
         return CALL_TEAM(T, 1, V, G);                                                       \
     }
-#define GC_ROUTE_BY_SIZE(T, experts, half, whole, CALL, CALL_TEAM)                          \
+#define GC_ROUTE_NO_WARP(T, whole)
+#define GC_ROUTE_BY_SIZE(T, experts, whole, CALL, CALL_TEAM, WARP)                          \
     if (experts <= kSmallExperts) {                                                         \
         if (whole) return CALL(T, int(16 / sizeof(T)));                                     \
         return CALL(T, 1);                                                                  \
     }                                                                                       \
-    if (half && experts <= 64) GC_ROUTE_TEAM(T, whole, 4, 16, CALL_TEAM)                    \
-    if (half && experts <= 128) GC_ROUTE_TEAM(T, whole, 8, 16, CALL_TEAM)                   \
-    if (half && experts <= 256) GC_ROUTE_TEAM(T, whole, 16, 16, CALL_TEAM)                  \
-    if (experts <= 256) GC_ROUTE_TEAM(T, whole, 8, 32, CALL_TEAM)                           \
+    WARP(T, whole)                                                                          \
+    if (experts <= 64) GC_ROUTE_TEAM(T, whole, 4, 16, CALL_TEAM)                            \
+    if (experts <= 128) GC_ROUTE_TEAM(T, whole, 8, 16, CALL_TEAM)                           \
+    if (experts <= 256) GC_ROUTE_TEAM(T, whole, 16, 16, CALL_TEAM)                          \
     if (experts <= 512) GC_ROUTE_TEAM(T, whole, 16, 32, CALL_TEAM)                          \
     GC_ROUTE_TEAM(T, whole, 64, 32, CALL_TEAM)
-#define GC_ROUTE_BY_DTYPE(dt, experts, half, whole, CALL, CALL_TEAM)                                  \
-    if (dt == GC_ROW_F32) { GC_ROUTE_BY_SIZE(float, experts, half, whole, CALL, CALL_TEAM) }          \
-    if (dt == GC_ROW_BF16) { GC_ROUTE_BY_SIZE(__nv_bfloat16, experts, half, whole, CALL, CALL_TEAM) } \
-    GC_ROUTE_BY_SIZE(__half, experts, half, whole, CALL, CALL_TEAM)
+#define GC_ROUTE_BY_DTYPE(dt, experts, whole, CALL, CALL_TEAM, WARP)                                  \
+    if (dt == GC_ROW_F32) { GC_ROUTE_BY_SIZE(float, experts, whole, CALL, CALL_TEAM, WARP) }          \
+    if (dt == GC_ROW_BF16) { GC_ROUTE_BY_SIZE(__nv_bfloat16, experts, whole, CALL, CALL_TEAM, WARP) } \
+    GC_ROUTE_BY_SIZE(__half, experts, whole, CALL, CALL_TEAM, WARP)
 
 }  // namespace gcd

@@ -548,7 +548,10 @@ cudaError_t launch_expert_route(const void *logits, size_t stride, uint32_t toke
 #define GC_ROUTE_CALL(T, N) run_group<T, N>(logits, stride, tokens, experts, topk, normalize, mask, out, ws, s)
 #define GC_ROUTE_CALL_TEAM(T, N, V, G) \
     run_team<T, N, V, G>(logits, stride, tokens, experts, topk, normalize, mask, out, ws, s)
-    GC_ROUTE_BY_DTYPE(dt, experts, topk <= kHalfTopk, whole, GC_ROUTE_CALL, GC_ROUTE_CALL_TEAM)
+    // more choices than a team of 16 lanes makes
+#define GC_ROUTE_WARP(T, whole) \
+    if (experts <= 256 && topk > kHalfTopk) GC_ROUTE_TEAM(T, whole, 8, 32, GC_ROUTE_CALL_TEAM)
+    GC_ROUTE_BY_DTYPE(dt, experts, whole, GC_ROUTE_CALL, GC_ROUTE_CALL_TEAM, GC_ROUTE_WARP)
 }
 
 }  // namespace gch

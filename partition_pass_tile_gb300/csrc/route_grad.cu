@@ -310,7 +310,7 @@ cudaError_t launch_expert_route_grad(const void *logits, size_t stride, uint32_t
     const Grad a{tokens, experts, topk, stride, dx_stride, normalize, ids, counts, dweights, dloss};
 #define GC_ROUTE_GRAD_CALL(T, N) run_group<T, N>(logits, dx, a, s)
 #define GC_ROUTE_GRAD_CALL_TEAM(T, N, V, G) run_team<T, N, V, G>(logits, dx, a, s)
-    GC_ROUTE_BY_DTYPE(dt, experts, true, whole, GC_ROUTE_GRAD_CALL, GC_ROUTE_GRAD_CALL_TEAM)
+    GC_ROUTE_BY_DTYPE(dt, experts, whole, GC_ROUTE_GRAD_CALL, GC_ROUTE_GRAD_CALL_TEAM, GC_ROUTE_NO_WARP)
 }
 
 }  // namespace gch
