@@ -124,3 +124,40 @@ def test_logits_far_above_the_first_of_a_thread(dtype):
     tokens = tokens.cpu().numpy()[:, :, None].astype(np.int64)
     want, bound = np.take_along_axis(lp, tokens, 2), (240 + 8 * (np.take_along_axis(z, tokens, 2) + mean)) * E
     assert np.all(np.abs(logprobs.double().cpu().numpy()[:, :, None] - want) <= bound)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_a_draft_without_an_open_token_whose_token_is_closed(dtype):
+    # u q < p is 0 < 0: rejected, and what is drawn from max(p - q, 0) is drawn from p
+    rng = np.random.default_rng(4)
+    for n, vocab in ((30, 301), (2, 20011), (800, 1003)):
+        x = 2 * rng.standard_normal((n, 2, vocab)).astype(np.float32)
+        ids = rng.integers(0, vocab, (n, 1))
+        np.put_along_axis(x[:, :1], ids[:, :, None], -np.inf, 2)
+        xt, x64 = rows_of(x, dtype, 3)
+        d = torch.full((n, 1, vocab), -float("inf"), dtype=DTYPES[dtype], device="cuda")
+        accept, uniform = rng.random((n, 1)).astype(np.float32), rng.random((n, vocab)).astype(np.float32)
+        got = gc.sample_verify(xt, torch.from_numpy(ids.astype(np.int32)).cuda(), torch.from_numpy(accept).cuda(),
+                               torch.from_numpy(uniform).cuda(), draft_logits=d)
+        assert not got[1].any()
+        compared = 0
+        for b in range(n):
+            want, a, lp, _ = ref.verify(x64[b], ids[b], accept[b], uniform[b], np.full((1, vocab), -np.inf), 1.0)
+            # the first of the ratios is clear of the second by 2^-16 of it
+            p, _ = ref.softmax(x64[b, 0])
+            ratio = np.sort(p / -np.log(np.clip(uniform[b].astype(np.float64), ref.U_LO, ref.U_HI)))
+            if ratio[-1] * (1 - 2.0 ** -16) > ratio[-2]:
+                compared += 1
+                assert a == 0 and got[0][b].tolist() == want.tolist()
+        assert compared >= 0.9 * n
+
+
+# sequences alone, at seeds for which the 64-bit form's decisions are clear
+@pytest.mark.parametrize("seed,k,vocab,dtype,drafted", [
+    (1, 0, 1, "f32", False), (2, 1, 1, "bf16", True), (1, 4, 4096, "f32", True), (3, 4, 4096, "f32", True),
+    (7, 4, 4096, "f32", True), (3, 6, 30001, "bf16", True), (6, 6, 30001, "bf16", True), (4, 3, 999, "f16", False)])
+def test_one_sequence(seed, k, vocab, dtype, drafted):
+    (x, x64), (d, d64), ids, accept, uniform, _ = setup(seed, 1, k, vocab, dtype, drafted)
+    drafts, acc, uni = (torch.from_numpy(a).cuda() for a in (ids.astype(np.int32), accept, uniform))
+    got = gc.sample_verify(x, drafts, acc, uni, draft_logits=d)
+    assert check(got, x64, d64, ids, accept, uniform, np.ones(1)) == 1
