@@ -581,7 +581,8 @@ size_t gc_expert_route_workspace_bytes(size_t tokens, uint32_t experts);
  * two have to be NULL.
  *
  * Roundings: p by exp2 of (x - max) * log2(e), off by at most (6 + 3/2 |x -
- * max|) * 2^-23 of itself; a token's sums are float32 trees.  load adds up in
+ * max|) * 2^-23 of itself, and 0 where that is below 2^-126; a token's sums are
+ * float32 trees.  load adds up in
  * float32: at most tokens / 1216 + 2 tokens one after another, then at most 64
  * such sums.
  */
@@ -711,14 +712,15 @@ size_t gc_sample_verify_workspace_bytes(size_t sequences, size_t drafts, size_t 
  *
  * Roundings, with z = (max - x) / T: the weight exp(-z) of a logit is a power
  * of two by a maximum of the logits met so far, which later ones may exceed by
- * up to 2^60; it is off by at most (7 + 5/4 z) * 2^-22 of itself.  Sums are
- * float32: at most 128 logits of one thread one after another, threads by
- * trees, then at most vocab / 32768 + 2 of the row's chunks one after another.
- * Each join of sums by different maxima adds at most 2^-20: on a logit's way
- * at most one for each piece of its thread (16) and each of those chunks, and
- * four more; usually fewer than six.  The comparison of u q with p is in
- * double.  The result is that of these p and q: a position whose u q and p
- * agree to that many bits may be decided either way.
+ * up to 2^60; it is off by at most (7 + 5/4 z) * 2^-22 of itself, and 0 where
+ * it is below 2^-126.  Sums are float32: at most 128 logits of one thread one
+ * after another, threads by trees, then at most vocab / 32768 + 2 of the row's
+ * chunks one after another.  Each join of sums by different maxima adds at most
+ * 2^-20: on a logit's way at most one for each piece of its thread (16) and
+ * each of those chunks, and four more; usually fewer than six.  The comparison
+ * of u q with p is in double.  The result is that of these p and q: a position
+ * whose u q and p agree to that many bits may be decided either way, and one
+ * with p and q both 0 is rejected.
  *
  * d_logits: sequences * (drafts + 1) rows of `vocab`, d_draft_logits:
  * sequences * drafts rows of the same type; d_drafts: int32, sequences *

@@ -161,3 +161,18 @@ def test_one_sequence(seed, k, vocab, dtype, drafted):
     drafts, acc, uni = (torch.from_numpy(a).cuda() for a in (ids.astype(np.int32), accept, uniform))
     got = gc.sample_verify(x, drafts, acc, uni, draft_logits=d)
     assert check(got, x64, d64, ids, accept, uniform, np.ones(1)) == 1
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_weights_below_the_least_are_none(dtype):
+    # exp(-80) is above 2^-126, exp(-100) below it: with q = 0 the first is accepted, the second is p = 0 and is not
+    x = torch.zeros(2, 2, 50, dtype=DTYPES[dtype], device="cuda")
+    x[0, 0, 20], x[1, 0, 20] = -80.0, -100.0
+    d = torch.zeros(2, 1, 50, dtype=DTYPES[dtype], device="cuda")
+    d[:, :, 20] = -float("inf")
+    drafts = torch.full((2, 1), 20, dtype=torch.int32, device="cuda")
+    tokens, accepted, logprobs = gc.sample_verify(x, drafts, torch.full((2, 1), 0.5, device="cuda"),
+                                                  torch.rand(2, 50, device="cuda"), draft_logits=d)
+    assert accepted.tolist() == [1, 0] and int(tokens[0, 0]) == 20 and int(tokens[1, 0]) not in (-1, 20)
+    # 49 weights of 1: z and its product with ln 2 round by 3 e z, the rest as above
+    assert abs(float(logprobs[0, 0]) + 80 + np.log(49.0)) <= (64 + 8 * 80) * E
