@@ -180,8 +180,10 @@ struct SelectSmem {
 // rank m between the sinks and the recent positions, found by three histograms
 // of those bits, 12, 10 and 10 of them; of the scores at the cut the first are
 // kept.  A share of at most K * 1024 positions is read once.  128 heads of 32768
-// scores to 2048: 18 us, bound by instructions (about 60 a score); with four CTAs
-// to a head that read their scores from L2 five times, 43.
+// scores to 2048: 18 us, bound by instructions (62 of a warp for 32 scores, and 107
+// with two CTAs to a head) between barriers, 52% of the issue slots; with four
+// CTAs to a head that read their scores from L2 five times, 43.  All scores equal,
+// each an atomic on one word three times: 22.
 template <int K, int B>
 __global__ void __launch_bounds__(kEvictThreads, B)
 cache_select_kernel(Evict a)

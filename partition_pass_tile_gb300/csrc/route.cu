@@ -123,8 +123,9 @@ __device__ __forceinline__ uint32_t kth_largest(uint32_t v, uint32_t top, uint32
 // one to a lane, and ranked by comparing each with all.  Where they are more
 // than the lanes (many closed experts, equal values, large k) the choices are
 // taken one after another.  131072 tokens of 256 float32, top-8: 66 us against 21
-// for the bytes, bound by instructions (about 320 a token, most of them on the
-// pipes of comparisons, integers and shuffles); by whole warps 76, with a lane's
+// for the bytes, bound by instructions (319 a token, 65% of the issue slots, 52% of
+// the pipe of comparisons and integers, with 33% of the warps; 80 registers, for
+// which 72 bytes are spilled); by whole warps 76, with a lane's
 // experts neighbours, which read every second 16 bytes or fewer at a time, 72,
 // one after another 162.  Of 64 experts, top-4, 37 us (warps 56), of 128 bf16,
 // top-8, 48 (73).

@@ -21,11 +21,14 @@
 // of a row carries the same 2^(m f - c) and p is a quotient of them.
 //
 // Measured, kernels alone: 192 sequences of 5 drafts by a model, 128000 bf16, four
-// in five positions accepted: 118 us.  The rows take 72 of it, 356 MB at 5.1 TB/s,
+// in five positions accepted: 119 us.  The rows take 72 of it, 356 MB at 5.1 TB/s,
 // where 316 MB would do (the rest was under way when its sequence stopped), bound
-// by the exponentials and their four instructions a logit.  The draw takes 46: 98 MB of random numbers and two rows of each
-// sequence once more.  One sequence of 4 drafts, 32768 float32: 11 us, two
-// launches' chains of dependent reads.
+// by instructions: 11 a logit, 79 to 87% of the issue slots (of 48 and 96
+// sequences), 35% of the pipe of exponentials.  The draw takes 46: 98 MB of
+// random numbers and two rows of each sequence once more.  Where filters have
+// left 50 tokens of each row, 146 us, 15 instructions a logit (rare_piece), against
+// 123 of the same rows whole; greedy sequences 62.  One sequence of 4 drafts, 32768
+// float32: 12 us, two launches' chains of dependent reads.
 #include <atomic>
 
 #include "gc_rows.cuh"
@@ -47,12 +50,12 @@ constexpr float kUniformLo = 0x1p-25f, kUniformHi = 1.0f - 0x1p-24f;
 // Chunks: 16 pieces per thread, 64 KB (8 a thread take 131 us at the size above,
 // for what every CTA does once; 32 take 118, with 50 MB more under way), where that makes more CTAs than the
 // GPU holds, else fewer.
-constexpr uint32_t kDrawWave = 4;          // CTAs per SM of the draw
-constexpr uint32_t kSteps = 16, kWave = 6;
+constexpr uint32_t kDrawWave = 4;  // CTAs per SM of the draw
+constexpr uint32_t kSteps = 16, kWave = 6;  // kWave: CTAs per SM of the rows
 // Positions are decided on the way where chunks are more than this many times
 // what the GPU holds at a time.  Of 5 drafts of 128000 bf16, 32 sequences take 43 us
 // so and 38 without, 96 take 76 and 76, 128 take 89 and 96, 192 take 120 and 136.
-constexpr size_t kSkipWaves = 5;  // kWave: CTAs per SM
+constexpr size_t kSkipWaves = 5;
 
 // z = (x - m) / t as a power of two's exponent.
 __device__ __forceinline__ float power_of(float t)
@@ -214,8 +217,9 @@ __device__ __forceinline__ void each_piece(const Pieces<T> &row, uint32_t first,
     wait_copies<0>();
 }
 
-// A piece that holds the first logits, a NaN, an infinity or a logit far above
-// m: the new (m, sum).  Out of line, with the piece still in shared memory.
+// A piece that holds a thread's first open logits (or, before them, none), a NaN,
+// an infinity or a logit far above m: the new (m, sum).  Out of line, with the
+// piece still in shared memory.
 template <class T>
 __device__ __noinline__ float2 rare_piece(const uint4 *at, float m, float sum, float power)
 {
